@@ -134,9 +134,10 @@ def prepare(case, seed):
     if case["tail"]:  # the teacher's whole log-sum-exp, a little more than its top entries give
         tail = torch.logsumexp(teacher.to(f32) / case["T"], dim=1) + 0.2 * torch.rand(N, device="cuda", generator=gen)
     s = dict(case=case, hidden=hidden, W=W, targets=targets if case["hard"] else None, ids=ids.contiguous(), teacher=teacher,
-             teacher_lse=tail, lse=torch.empty(N, device="cuda"), logp_top=torch.empty(N, K, device="cuda"))
+             teacher_lse=tail, logp=torch.zeros(N, device="cuda") if case["hard"] else None, lse=torch.empty(N, device="cuda"),
+             logp_top=torch.empty(N, K, device="cuda"))
     if case["op"] == "distill_fwd":
-        s |= dict(kl=torch.empty(N, device="cuda"), logp=torch.empty(N, device="cuda") if case["hard"] else None)
+        s |= dict(kl=torch.empty(N, device="cuda"))
         return s
     Wf = W.to(f32)
     for r in range(0, N, 2048):  # the forward pass's values
@@ -146,6 +147,9 @@ def prepare(case, seed):
         top = z.gather(1, i.clamp(0, V - 1).long()) - lse[:, None]
         s["logp_top"][r:r + 2048] = torch.where(i >= 0, top, 0.0)
         s["lse"][r:r + 2048] = torch.where(padded[r:r + 2048], 0.0, lse)
+        if case["hard"]:
+            t = targets[r:r + 2048]
+            s["logp"][r:r + 2048] = torch.where(t >= 0, z.gather(1, t.clamp(0, V - 1).long()[:, None])[:, 0] - lse, 0.0)
     s |= dict(g_kl=0.5 + torch.rand(N, device="cuda", generator=gen), g_logp=-0.3 * torch.rand(N, device="cuda", generator=gen) if case["hard"] else None,
               dh=torch.empty(N, H, device="cuda", dtype=torch.bfloat16), dW=torch.empty(V, H, device="cuda", dtype=torch.bfloat16))
     return s
@@ -181,7 +185,8 @@ def _framework(s):
     if op == "distill_fwd":
         lm.lmhead_logps_distill_fwd(*given, s["kl"], s["logp"], s["lse"], s["logp_top"], s["workspace"])
         return _some(kl=s["kl"], logp=s["logp"], lse=s["lse"], logp_top=s["logp_top"])
-    lm.lmhead_logps_distill_bwd(*given, s["lse"], s["logp_top"], s["g_kl"], s["g_logp"], s["dh"], s["dW"], 0, s["workspace"])
+    lm.lmhead_logps_distill_bwd(*given, s["logp"], s["lse"], s["logp_top"], s["g_kl"], s["g_logp"], s["dh"], s["dW"], 0,
+                                s["workspace"])
     return dict(dh=s["dh"], dW=s["dW"])
 
 
