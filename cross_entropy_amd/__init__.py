@@ -21,14 +21,22 @@ Entry points mirror the C ABI:
                          (the head over vocabulary shards, partials merged by log-sum-exp)
     lmhead_logps_fwd_noalloc  (tempered forward without a workspace, for callers
                          that cannot allocate; its scratch is a fixed device array)
-two allocating helpers, ``forward`` and ``backward`` (``temperature=``
+    lmhead_logps_distill_fwd / lmhead_logps_distill_bwd  (KL to a teacher's top
+                         logits, and the log-prob of a hard target beside it)
+    lmhead_logps_norm_fwd / lmhead_logps_norm_bwd  (the layer or RMS norm in
+                         front of the head)
+with allocating helpers for the last two pairs (``distill_forward``,
+``distill_backward``, ``norm_forward``, ``norm_backward``) and autograd front
+ends (``lmhead_distill``, ``lmhead_norm``);
+two allocating helpers for the head, ``forward`` and ``backward`` (``temperature=``
 selects the tempered calls, ``dh=`` / ``dW=`` with ``accumulate=`` add into
 caller buffers), and ``lmhead_logps``, a ``torch.autograd.Function`` front
-end for training code.
+end for training code. ``lmhead_logps`` and ``lmhead_distill`` take the final
+norm too (``norm=Norm(...)``: hidden is then the stream in front of it).
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import Any, NamedTuple, Optional, Tuple
 
 from . import _native
 from ._native import LmheadError, load, version  # noqa: F401
@@ -46,9 +54,25 @@ __all__ = [
     "lmhead_logps_merge_shards",
     "lmhead_logps_bwd_shard",
     "lmhead_logps_fwd_noalloc",
+    "lmhead_logps_distill_workspace_bytes",
+    "lmhead_logps_distill_fwd",
+    "lmhead_logps_distill_bwd",
+    "lmhead_logps_norm_workspace_bytes",
+    "lmhead_logps_norm_fwd",
+    "lmhead_logps_norm_bwd",
     "lmhead_logps",
+    "lmhead_distill",
+    "lmhead_norm",
+    "Norm",
     "forward",
     "backward",
+    "distill_forward",
+    "distill_backward",
+    "norm_forward",
+    "norm_backward",
+    "workspace_for",
+    "distill_workspace_for",
+    "norm_workspace_for",
     "version",
 ]
 
@@ -337,6 +361,265 @@ def backward(hidden, W, targets, chunk_size: int, lse, entropy, g_logp, g_ent: O
     return dh, dW
 
 
+def _enqueue(dev, raw, *args):
+    """Call ``raw`` with the tensors' device current (a launch goes to the
+    current device where the stream is the default one) and check its status."""
+    torch = _torch()
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _native.check(raw(*args))
+    else:
+        with torch.cuda.device(dev):
+            _native.check(raw(*args))
+
+
+def lmhead_logps_distill_workspace_bytes(N: int, H: int, V: int, K: int, chunk_size: int, with_backward=True) -> int:
+    """Workspace bytes of the distillation calls; with_backward as for
+    ``lmhead_logps_workspace_bytes``."""
+    return _native.raw_distill_workspace_bytes(N, H, V, K, chunk_size, _ws_kind(with_backward))
+
+
+def _type_of(t, name):
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return _native.TYPE_F32
+    if t.dtype in _bf16_types():
+        return _native.TYPE_BF16
+    raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+
+
+def _any_types():
+    return (_torch().float32,) + _bf16_types()
+
+
+def _distill_args(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature):
+    torch = _torch()
+    if hidden.dim() != 2 or W.dim() != 2 or hidden.shape[1] != W.shape[1]:
+        raise ValueError(f"hidden [N,H] and W [V,H] must share H: {tuple(hidden.shape)} vs {tuple(W.shape)}")
+    N, H = hidden.shape
+    V = W.shape[0]
+    if ids.dim() != 2 or ids.shape[0] != N or teacher.shape != ids.shape:
+        raise ValueError(f"ids and teacher must be [{N}, K]: {tuple(ids.shape)} and {tuple(teacher.shape)}")
+    K = ids.shape[1]
+    dev = hidden.device
+    return dev, N, K, (
+        _ptr(hidden, "hidden", _bf16_types(), dev), _ptr(W, "W", _bf16_types(), dev),
+        _ptr(targets, "targets", (torch.int32,), dev, N, optional=True), _ptr(ids, "ids", (torch.int32,), dev),
+        _ptr(teacher, "teacher", _any_types(), dev), _type_of(teacher, "teacher"),
+        _ptr(teacher_lse, "teacher_lse", (torch.float32,), dev, N, optional=True), N, H, V, K, chunk_size, temperature)
+
+
+def lmhead_logps_distill_fwd(hidden, W, targets, ids, teacher, teacher_lse, chunk_size: int, temperature: float, kl,
+                             logp, lse, logp_top, workspace, stream=None) -> None:
+    """Enqueue the distillation forward: kl [N], logp [N] (or None), lse [N]
+    and logp_top [N, K] (float32). ``targets`` (int32 [N]) and ``teacher_lse``
+    (float32 [N]) may be None; ``ids`` is int32 [N, K], ``teacher`` float32 or
+    bfloat16 [N, K]."""
+    f32 = (_torch().float32,)
+    dev, N, K, args = _distill_args(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature)
+    _enqueue(
+        dev, _native.raw_distill_fwd, *args, _ptr(kl, "kl", f32, dev, N), _ptr(logp, "logp", f32, dev, N, optional=True), _ptr(lse, "lse", f32, dev, N),
+        _ptr(logp_top, "logp_top", f32, dev, N * K), _ptr(workspace, "workspace", (_torch().uint8,), dev),
+        workspace.numel(), _stream(dev, stream))
+
+
+def lmhead_logps_distill_bwd(hidden, W, targets, ids, teacher, teacher_lse, chunk_size: int, temperature: float, logp,
+                             lse, logp_top, g_kl, g_logp, dh, dW, flags: int, workspace, stream=None) -> None:
+    """Enqueue the distillation backward into dh [N, H] / dW [V, H], both
+    float32 or both bfloat16; ``flags`` as for ``lmhead_logps_bwd_ex``; the
+    workspace is that of ``distill_workspace_for`` (True or "bf16")."""
+    f32 = (_torch().float32,)
+    dev, N, K, args = _distill_args(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature)
+    if dh.shape != hidden.shape or dW.shape != W.shape:
+        raise ValueError("dh must be [N,H] and dW [V,H]")
+    if dh.dtype != dW.dtype:
+        raise TypeError(f"dh and dW must have one dtype, got {dh.dtype} and {dW.dtype}")
+    _enqueue(
+        dev, _native.raw_distill_bwd, *args, _ptr(logp, "logp", f32, dev, N, optional=True), _ptr(lse, "lse", f32, dev, N),
+        _ptr(logp_top, "logp_top", f32, dev, N * K), _ptr(g_kl, "g_kl", f32, dev, N, optional=True),
+        _ptr(g_logp, "g_logp", f32, dev, N, optional=True), _ptr(dh, "dh", _any_types(), dev),
+        _ptr(dW, "dW", _any_types(), dev), _type_of(dh, "dh"), flags,
+        _ptr(workspace, "workspace", (_torch().uint8,), dev), workspace.numel(), _stream(dev, stream))
+
+
+def distill_workspace_for(hidden, W, ids, chunk_size: int, with_backward=True):
+    """Allocate a workspace for the distillation calls (with_backward as for
+    ``workspace_for``)."""
+    torch = _torch()
+    nbytes = lmhead_logps_distill_workspace_bytes(hidden.shape[0], hidden.shape[1], W.shape[0], ids.shape[1],
+                                                  chunk_size, with_backward)
+    return torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
+
+
+def distill_forward(hidden, W, targets, ids, teacher, chunk_size: int, teacher_lse=None, workspace=None, stream=None,
+                    temperature: float = 1.0) -> Tuple:
+    """Allocate outputs and run the distillation forward: (kl, logp | None,
+    lse, logp_top); ``targets`` may be None."""
+    torch = _torch()
+    N, K = ids.shape
+    dev = hidden.device
+    kl, lse = (torch.empty(N, dtype=torch.float32, device=dev) for _ in range(2))
+    logp = None if targets is None else torch.empty(N, dtype=torch.float32, device=dev)
+    logp_top = torch.empty((N, K), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = distill_workspace_for(hidden, W, ids, chunk_size, with_backward=False)
+    lmhead_logps_distill_fwd(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature, kl, logp, lse,
+                             logp_top, workspace, stream)
+    return kl, logp, lse, logp_top
+
+
+def distill_backward(hidden, W, targets, ids, teacher, chunk_size: int, logp, lse, logp_top, g_kl, g_logp=None,
+                     teacher_lse=None, workspace=None, stream=None, temperature: float = 1.0, dh=None, dW=None,
+                     accumulate: bool = False, grad_dtype=None) -> Tuple:
+    """Run the distillation backward: (dh, dW), float32 (or bfloat16 with
+    ``grad_dtype=torch.bfloat16``); the rest as for ``backward``."""
+    torch = _torch()
+    if grad_dtype is None:
+        grad_dtype = dh.dtype if dh is not None else torch.float32
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
+    if accumulate and (dh is None or dW is None):
+        raise ValueError("accumulate needs both dh and dW buffers")
+    if dh is None:
+        dh = torch.empty(hidden.shape, dtype=grad_dtype, device=hidden.device)
+    if dW is None:
+        dW = torch.empty(W.shape, dtype=grad_dtype, device=hidden.device)
+    if workspace is None:
+        workspace = distill_workspace_for(hidden, W, ids, chunk_size,
+                                          with_backward="bf16" if grad_dtype == torch.bfloat16 else True)
+    flags = (_native.BWD_ACCUMULATE_DH | _native.BWD_ACCUMULATE_DW) if accumulate else 0
+    lmhead_logps_distill_bwd(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature, logp, lse,
+                             logp_top, g_kl, g_logp, dh, dW, flags, workspace, stream)
+    return dh, dW
+
+
+class Norm(NamedTuple):
+    """A norm over the last dimension: weight and bias [H] (or None), eps, and
+    kind "layer" or "rms"."""
+    weight: Any = None
+    bias: Any = None
+    eps: float = 1e-6
+    kind: str = "layer"
+
+
+_NORM_KINDS = {"layer": _native.NORM_LAYER, "rms": _native.NORM_RMS}
+
+
+def _norm_kind(kind):
+    if kind not in _NORM_KINDS:
+        raise ValueError(f"kind must be 'layer' or 'rms', got {kind!r}")
+    return _NORM_KINDS[kind]
+
+
+def _norm_shape(x):
+    if x.dim() < 1:
+        raise ValueError("x must have a last dimension to normalise")
+    H = x.shape[-1]
+    if H < 1:
+        raise ValueError("the last dimension of x must not be empty")
+    return x.numel() // H, H
+
+
+def lmhead_logps_norm_workspace_bytes(N: int, H: int) -> int:
+    """Workspace bytes of the norm's backward."""
+    return _native.raw_norm_workspace_bytes(N, H)
+
+
+def _vector_type(a, b, names):
+    """The one type of two optional vectors (float32 if there is neither)."""
+    if a is not None and b is not None and a.dtype != b.dtype:
+        raise TypeError(f"{names[0]} and {names[1]} must have one dtype, got {a.dtype} and {b.dtype}")
+    some = a if a is not None else b
+    return _native.TYPE_F32 if some is None else _type_of(some, names[0] if a is not None else names[1])
+
+
+def lmhead_logps_norm_fwd(x, weight, bias, eps: float, kind: str, y, mean, rstd, stream=None) -> None:
+    """Enqueue the norm of x [..., H] into y (x's shape; bfloat16, or float32
+    where x is). weight and bias [H] may be None, and mean / rstd (float32,
+    one per row, for the backward) too; kind is "layer" or "rms"."""
+    f32 = (_torch().float32,)
+    N, H = _norm_shape(x)
+    dev = x.device
+    if y.shape != x.shape:
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+    _enqueue(
+        dev, _native.raw_norm_fwd, _ptr(x, "x", _any_types(), dev), _type_of(x, "x"), _ptr(weight, "weight", _any_types(), dev, H, optional=True),
+        _ptr(bias, "bias", _any_types(), dev, H, optional=True), _vector_type(weight, bias, ("weight", "bias")), N, H,
+        eps, _norm_kind(kind), _ptr(y, "y", _any_types(), dev), _type_of(y, "y"),
+        _ptr(mean, "mean", f32, dev, N, optional=True), _ptr(rstd, "rstd", f32, dev, N, optional=True),
+        _stream(dev, stream))
+
+
+def lmhead_logps_norm_bwd(x, weight, kind: str, mean, rstd, dy, dx, dweight, dbias, flags: int, workspace,
+                          stream=None) -> None:
+    """Enqueue the norm's backward into dx (x's dtype) and, unless None,
+    dweight and dbias [H] (float32 or bfloat16); ``flags`` 0 or
+    ``_native.BWD_ACCUMULATE_DW`` (add into dweight and dbias). The workspace
+    may be None where neither is wanted."""
+    f32 = (_torch().float32,)
+    N, H = _norm_shape(x)
+    dev = x.device
+    if dy.shape != x.shape or dx.shape != x.shape:
+        raise ValueError(f"dy and dx must have x's shape {tuple(x.shape)}, got {tuple(dy.shape)} and {tuple(dx.shape)}")
+    if _type_of(dx, "dx") != _type_of(x, "x"):
+        raise TypeError(f"dx must have x's dtype {x.dtype}, got {dx.dtype}")
+    _enqueue(
+        dev, _native.raw_norm_bwd, _ptr(x, "x", _any_types(), dev), _type_of(x, "x"), _ptr(weight, "weight", _any_types(), dev, H, optional=True),
+        _vector_type(weight, None, ("weight", "")), N, H, _norm_kind(kind),
+        _ptr(mean, "mean", f32, dev, N, optional=True), _ptr(rstd, "rstd", f32, dev, N),
+        _ptr(dy, "dy", _any_types(), dev), _type_of(dy, "dy"), _ptr(dx, "dx", _any_types(), dev),
+        _ptr(dweight, "dweight", _any_types(), dev, H, optional=True),
+        _ptr(dbias, "dbias", _any_types(), dev, H, optional=True),
+        _vector_type(dweight, dbias, ("dweight", "dbias")), flags,
+        _ptr(workspace, "workspace", (_torch().uint8,), dev, optional=True),
+        0 if workspace is None else workspace.numel(), _stream(dev, stream))
+
+
+def norm_workspace_for(x):
+    """Allocate a workspace for the norm's backward."""
+    torch = _torch()
+    N, H = _norm_shape(x)
+    return torch.empty(lmhead_logps_norm_workspace_bytes(N, H), dtype=torch.uint8, device=x.device)
+
+
+def norm_forward(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "layer", out_dtype=None,
+                 stream=None) -> Tuple:
+    """Allocate outputs and run the norm: (y, mean | None, rstd). ``out_dtype``
+    (default: x's) may be bfloat16 for a float32 x."""
+    torch = _torch()
+    N, _ = _norm_shape(x)
+    y = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
+    mean = torch.empty_like(rstd) if kind == "layer" else None
+    lmhead_logps_norm_fwd(x, weight, bias, eps, kind, y, mean, rstd, stream)
+    return y, mean, rstd
+
+
+def norm_backward(x, weight, mean, rstd, dy, kind: str = "layer", with_weight: bool = True, with_bias: bool = False,
+                  workspace=None, stream=None, dweight=None, dbias=None, accumulate: bool = False,
+                  grad_dtype=None) -> Tuple:
+    """Run the norm's backward: (dx, dweight | None, dbias | None).
+    ``with_weight`` / ``with_bias`` allocate those gradients (in ``grad_dtype``,
+    default the weight's dtype or float32) unless buffers are given; with
+    ``accumulate`` the given buffers are added into."""
+    torch = _torch()
+    _, H = _norm_shape(x)
+    dx = torch.empty_like(x)
+    if accumulate and ((with_weight and dweight is None) or (with_bias and dbias is None)):
+        raise ValueError("accumulate needs the gradient buffers that are wanted")
+    if grad_dtype is None:
+        given = dweight if dweight is not None else dbias if dbias is not None else weight
+        grad_dtype = torch.float32 if given is None else given.dtype
+    if dweight is None and with_weight:
+        dweight = torch.empty(H, dtype=grad_dtype, device=x.device)
+    if dbias is None and with_bias:
+        dbias = torch.empty(H, dtype=grad_dtype, device=x.device)
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = norm_workspace_for(x)
+    flags = _native.BWD_ACCUMULATE_DW if accumulate else 0
+    lmhead_logps_norm_bwd(x, weight, kind, mean, rstd, dy, dx, dweight, dbias, flags, workspace, stream)
+    return dx, dweight, dbias
+
+
 def _autograd_function():
     torch = _torch()
 
@@ -379,16 +662,111 @@ def _autograd_function():
     return _LmheadLogps
 
 
+def _distill_function():
+    torch = _torch()
+
+    class _LmheadDistill(torch.autograd.Function):
+        """kl (and logp) of the head with its backward through the library;
+        keeps lse, logp and the student's log-probs at the teacher's ids."""
+
+        @staticmethod
+        def forward(ctx, hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature):
+            kl, logp, lse, logp_top = distill_forward(hidden, W, targets, ids, teacher, chunk_size, teacher_lse,
+                                                      temperature=temperature)
+            ctx.chunk_size = chunk_size
+            ctx.temperature = temperature
+            ctx.save_for_backward(hidden, W, targets, ids, teacher, teacher_lse, logp, lse, logp_top)
+            return kl if logp is None else (kl, logp)
+
+        @staticmethod
+        def backward(ctx, g_kl, g_logp=None):
+            hidden, W, targets, ids, teacher, teacher_lse, logp, lse, logp_top = ctx.saved_tensors
+            gk = None if g_kl is None else g_kl.detach().contiguous().float()
+            gl = None if (g_logp is None or logp is None) else g_logp.detach().contiguous().float()
+            bf16 = hidden.dtype == torch.bfloat16 and W.dtype == torch.bfloat16
+            dh, dW = distill_backward(hidden, W, targets, ids, teacher, ctx.chunk_size, logp, lse, logp_top, gk, gl,
+                                      teacher_lse, temperature=ctx.temperature,
+                                      grad_dtype=torch.bfloat16 if bf16 else torch.float32)
+            return (dh.to(hidden.dtype) if ctx.needs_input_grad[0] else None,
+                    dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
+                    None, None, None, None, None, None)
+
+    return _LmheadDistill
+
+
+def _norm_function():
+    torch = _torch()
+
+    class _LmheadNorm(torch.autograd.Function):
+        """The norm with its backward through the library; keeps x and the
+        rows' statistics."""
+
+        @staticmethod
+        def forward(ctx, x, weight, bias, eps, kind, out_dtype):
+            y, mean, rstd = norm_forward(x, weight, bias, eps, kind, out_dtype)
+            ctx.kind = kind
+            ctx.bias = None if bias is None else bias.dtype
+            ctx.save_for_backward(x, weight, mean, rstd)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, weight, mean, rstd = ctx.saved_tensors
+            want_w, want_b = ctx.needs_input_grad[1], ctx.needs_input_grad[2]
+            dx, dw, db = norm_backward(x, weight, mean, rstd, dy.detach().contiguous(), ctx.kind, with_weight=want_w,
+                                       with_bias=want_b, grad_dtype=ctx.bias if weight is None else weight.dtype)
+            return dx if ctx.needs_input_grad[0] else None, dw, db, None, None, None
+
+    return _LmheadNorm
+
+
 _FN = None
+_DISTILL_FN = None
+_NORM_FN = None
 
 
-def lmhead_logps(hidden, W, targets, chunk_size: int, temperature: Optional[float] = None, with_entropy: bool = True):
+def lmhead_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "layer", out_dtype=None):
+    """Differentiable norm in front of the head: x [..., H] bfloat16 or
+    float32 (``out_dtype=torch.bfloat16`` gives the head its dtype from a
+    float32 stream); gradients flow to x, weight and bias. A row whose incoming
+    gradient is 0 (a token that the head masks) adds nothing to any gradient,
+    whatever it holds."""
+    global _NORM_FN
+    if _NORM_FN is None:
+        _NORM_FN = _norm_function()
+    return _NORM_FN.apply(x, weight, bias, eps, kind, out_dtype)
+
+
+def _normed(hidden, norm):
+    if norm is None:
+        return hidden
+    return lmhead_norm(hidden, norm.weight, norm.bias, norm.eps, norm.kind, out_dtype=_torch().bfloat16)
+
+
+def lmhead_logps(hidden, W, targets, chunk_size: int, temperature: Optional[float] = None, with_entropy: bool = True,
+                 norm: Optional[Norm] = None):
     """Differentiable head for training code: returns ``(logp, entropy)``
     (or ``logp`` alone without entropy). ``hidden`` [N, H] and ``W`` [V, H]
     are bfloat16 tensors on one GPU; a backward through either output runs
     ``lmhead_logps_bwd`` on the saved lse / entropy (the logits are recomputed,
-    never stored). Masked targets (outside [0, V)) give zeros."""
+    never stored). Masked targets (outside [0, V)) give zeros. With ``norm``,
+    hidden is the stream in front of the final norm (bfloat16 or float32), and
+    gradients flow to it and to the norm's weight and bias."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()
-    return _FN.apply(hidden, W, targets, chunk_size, temperature, with_entropy)
+    return _FN.apply(_normed(hidden, norm), W, targets, chunk_size, temperature, with_entropy)
+
+
+def lmhead_distill(hidden, W, ids, teacher, chunk_size: int, targets=None, teacher_lse=None,
+                   temperature: float = 1.0, norm: Optional[Norm] = None):
+    """Differentiable distillation loss per token against a teacher's top
+    logits: ``kl`` [N], or ``(kl, logp)`` with hard ``targets``. ``ids`` (int32)
+    and ``teacher`` (bfloat16 or float32) are [N, K]; ids outside [0, V) are
+    missing entries. Gradients flow to hidden and W (and, with ``norm`` as for
+    ``lmhead_logps``, to the norm's weight and bias); the teacher gets none.
+    Multiply kl by temperature squared for gradients of temperature 1's size."""
+    global _DISTILL_FN
+    if _DISTILL_FN is None:
+        _DISTILL_FN = _distill_function()
+    return _DISTILL_FN.apply(_normed(hidden, norm), W, targets, ids, teacher, teacher_lse, chunk_size, temperature)

@@ -36,6 +36,12 @@ EXPORTED = (
     "lmhead_logps_merge_shards",
     "lmhead_logps_bwd_shard",
     "lmhead_logps_fwd_noalloc",
+    "lmhead_logps_distill_workspace_bytes",
+    "lmhead_logps_distill_fwd",
+    "lmhead_logps_distill_bwd",
+    "lmhead_logps_norm_workspace_bytes",
+    "lmhead_logps_norm_fwd",
+    "lmhead_logps_norm_bwd",
     "lmhead_logps_last_error",
     "lmhead_logps_version",
     "lmhead_logps_trace_enable",
@@ -109,6 +115,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.lmhead_logps_bwd_shard.restype = ctypes.c_int
     lib.lmhead_logps_fwd_noalloc.argtypes = [p, p, p, i64, i64, i64, i64, f32, p, p, p, p]
     lib.lmhead_logps_fwd_noalloc.restype = ctypes.c_int
+    i32 = ctypes.c_int
+    lib.lmhead_logps_distill_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i32, ctypes.POINTER(sz)]
+    lib.lmhead_logps_distill_workspace_bytes.restype = ctypes.c_int
+    lib.lmhead_logps_distill_fwd.argtypes = [p, p, p, p, p, i32, p, i64, i64, i64, i64, i64, f32, p, p, p, p, p, sz, p]
+    lib.lmhead_logps_distill_fwd.restype = ctypes.c_int
+    lib.lmhead_logps_distill_bwd.argtypes = [p, p, p, p, p, i32, p, i64, i64, i64, i64, i64, f32, p, p, p, p, p, p, p,
+                                             i32, ctypes.c_uint, p, sz, p]
+    lib.lmhead_logps_distill_bwd.restype = ctypes.c_int
+    lib.lmhead_logps_norm_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    lib.lmhead_logps_norm_workspace_bytes.restype = ctypes.c_int
+    lib.lmhead_logps_norm_fwd.argtypes = [p, i32, p, p, i32, i64, i64, f32, i32, p, i32, p, p, p]
+    lib.lmhead_logps_norm_fwd.restype = ctypes.c_int
+    lib.lmhead_logps_norm_bwd.argtypes = [p, i32, p, i32, i64, i64, i32, p, p, p, i32, p, p, p, i32, ctypes.c_uint, p,
+                                          sz, p]
+    lib.lmhead_logps_norm_bwd.restype = ctypes.c_int
     lib.lmhead_logps_last_error.argtypes = []
     lib.lmhead_logps_last_error.restype = ctypes.c_char_p
     lib.lmhead_logps_version.argtypes = []
@@ -233,8 +254,69 @@ def raw_fwd_noalloc(hidden, W, targets, N, H, V, chunk_size, temperature, logp, 
                                            lse or None, stream or None)
 
 
+TYPE_BF16, TYPE_F32 = 0, 1
+DISTILL_MAX_K = 1024
+
+
+def raw_distill_workspace_bytes(N: int, H: int, V: int, K: int, chunk_size: int, with_backward) -> int:
+    """with_backward: WS_FWD, WS_BWD or WS_BWD_BF16."""
+    out = ctypes.c_size_t(0)
+    check(load().lmhead_logps_distill_workspace_bytes(int(N), int(H), int(V), int(K), int(chunk_size),
+                                                      int(with_backward), ctypes.byref(out)))
+    return int(out.value)
+
+
+def raw_distill_fwd(hidden, W, targets, ids, teacher, teacher_type, teacher_lse, N, H, V, K, chunk_size, temperature,
+                    kl, logp, lse, logp_top, workspace, workspace_bytes, stream) -> int:
+    """Call lmhead_logps_distill_fwd with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_distill_fwd(hidden or None, W or None, targets or None, ids or None, teacher or None,
+                                           int(teacher_type), teacher_lse or None, int(N), int(H), int(V), int(K),
+                                           int(chunk_size), float(temperature), kl or None, logp or None, lse or None,
+                                           logp_top or None, workspace or None, int(workspace_bytes), stream or None)
+
+
+def raw_distill_bwd(hidden, W, targets, ids, teacher, teacher_type, teacher_lse, N, H, V, K, chunk_size, temperature,
+                    logp, lse, logp_top, g_kl, g_logp, dh, dW, grad_type, flags, workspace, workspace_bytes,
+                    stream) -> int:
+    """Call lmhead_logps_distill_bwd with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_distill_bwd(hidden or None, W or None, targets or None, ids or None, teacher or None,
+                                           int(teacher_type), teacher_lse or None, int(N), int(H), int(V), int(K),
+                                           int(chunk_size), float(temperature), logp or None, lse or None,
+                                           logp_top or None, g_kl or None, g_logp or None, dh or None, dW or None,
+                                           int(grad_type), int(flags), workspace or None, int(workspace_bytes),
+                                           stream or None)
+
+
+NORM_LAYER, NORM_RMS = 0, 1
+NORM_MAX_H = 16384
+
+
+def raw_norm_workspace_bytes(N: int, H: int) -> int:
+    out = ctypes.c_size_t(0)
+    check(load().lmhead_logps_norm_workspace_bytes(int(N), int(H), ctypes.byref(out)))
+    return int(out.value)
+
+
+def raw_norm_fwd(x, x_type, weight, bias, w_type, N, H, eps, kind, y, y_type, mean, rstd, stream) -> int:
+    """Call lmhead_logps_norm_fwd with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_norm_fwd(x or None, int(x_type), weight or None, bias or None, int(w_type), int(N),
+                                        int(H), float(eps), int(kind), y or None, int(y_type), mean or None,
+                                        rstd or None, stream or None)
+
+
+def raw_norm_bwd(x, x_type, weight, w_type, N, H, kind, mean, rstd, dy, y_type, dx, dweight, dbias, g_type, flags,
+                 workspace, workspace_bytes, stream) -> int:
+    """Call lmhead_logps_norm_bwd with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_norm_bwd(x or None, int(x_type), weight or None, int(w_type), int(N), int(H), int(kind),
+                                        mean or None, rstd or None, dy or None, int(y_type), dx or None,
+                                        dweight or None, dbias or None, int(g_type), int(flags), workspace or None,
+                                        int(workspace_bytes), stream or None)
+
+
 TRACE_KERNELS = ("fwd_stats_kernel", "fwd_merge_kernel", "bwd_step_kernel", "transpose_kernel",
-                 "fill_zero_kernel", "pad_rows_kernel", "bwd_step_bf16_kernel")
+                 "fill_zero_kernel", "pad_rows_kernel", "bwd_step_bf16_kernel", "distill_top_kernel",
+                 "distill_prep_kernel", "distill_scatter_kernel", "norm_fwd_kernel", "norm_bwd_kernel",
+                 "norm_reduce_kernel")
 
 
 def trace_enable(on: bool) -> None:

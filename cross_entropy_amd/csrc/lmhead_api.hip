@@ -390,12 +390,22 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
 
 namespace {
 
+// The distillation's part of a backward: its per-token preparation, launched
+// before everything else, and the special entries that overwrite each
+// cotangent block once it is formed. `bytes` is the whole workspace it needs.
+struct DistillHook {
+  lmh::DistillPrepArgs prep;
+  size_t bytes;
+};
+
 // The backward of W's rows [voff, voff + V) of a vocabulary of Vtot ids.
 // dh / dW are float32 (bf16_out false) or bf16 gradients (bf16_out true).
+// With `distill`, targets and g_logp are what its preparation writes.
 int bwd_impl(const char* who, const uint16_t* hidden, const uint16_t* W, const int32_t* targets, int64_t N,
              int64_t H, int64_t V, int64_t voff, int64_t Vtot, int64_t chunk_size, float temperature,
              const float* lse, const float* entropy, const float* g_logp, const float* g_ent, void* dh,
-             void* dW, unsigned flags, bool bf16_out, void* workspace, size_t workspace_bytes, void* stream) {
+             void* dW, unsigned flags, bool bf16_out, void* workspace, size_t workspace_bytes, void* stream,
+             const DistillHook* distill = nullptr) {
   int rc = check_shape(N, H, V, chunk_size);
   if (rc != LMH_OK) return rc;
   rc = check_shard(V, voff, Vtot);
@@ -426,7 +436,7 @@ int bwd_impl(const char* who, const uint16_t* hidden, const uint16_t* W, const i
   if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(workspace, 16) || !aligned(dh, 16))
     return fail(LMH_ERR_UNSUPPORTED, "%s: hidden, W, dh and workspace need 16-byte alignment", who);
   const lmh::BwdPlan p = lmh::plan_backward(N, H, V, chunk_size);
-  const size_t need = bf16_out ? p.bytes_bf16 : p.bytes;
+  const size_t need = distill ? distill->bytes : bf16_out ? p.bytes_bf16 : p.bytes;
   if (workspace_bytes < need)
     return fail(LMH_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
   char* ws = static_cast<char*>(workspace);
@@ -441,6 +451,7 @@ int bwd_impl(const char* who, const uint16_t* hidden, const uint16_t* W, const i
   // the cotangent-tile counters start at zero (a fill kernel, not a memset:
   // the call may be captured into a graph)
   hipError_t te = lmh::launch_fill_zero(reinterpret_cast<float*>(ctr), (nb + 1) * 8, s);
+  if (te == hipSuccess && distill) te = lmh::launch_distill_prep(distill->prep, s);
   if (te == hipSuccess)
     te = lmh::launch_transpose(hidden, H, N, H, p.N_pad, p.H_pad, targets, Vtot, ht, p.ld_ht, s);
   if (te == hipSuccess && v_tail < V) te = lmh::launch_pad_rows(W + v_tail * H, V - v_tail, H, 64, W_tail, s);
@@ -537,7 +548,12 @@ int bwd_impl(const char* who, const uint16_t* hidden, const uint16_t* W, const i
       st.z_dz = nullptr;
       st.z_ntt = st.z_nvt = 0;
     }
-    const hipError_t e = bf16_out ? lmh::launch_bwd_step_bf16(st, s) : lmh::launch_bwd_step(st, s);
+    hipError_t e = bf16_out ? lmh::launch_bwd_step_bf16(st, s) : lmh::launch_bwd_step(st, s);
+    if (e == hipSuccess && distill && j < nb) {
+      const lmh::DistillPrepArgs& d = distill->prep;
+      e = lmh::launch_distill_scatter({d.ent_id, d.ent_val, d.K + 1, st.z_dz, p.ld_dz, st.z_t0, st.z_Ct, st.z_v0,
+                                       st.z_Vb}, s);
+    }
     if (e != hipSuccess) return fail(LMH_ERR_HIP, "%s: launch failed: %s", who, hipGetErrorString(e));
   }
   return ok();
@@ -596,6 +612,251 @@ int lmhead_logps_bwd(const uint16_t* hidden, const uint16_t* W, const int32_t* t
                      float* dW, void* workspace, size_t workspace_bytes, void* stream) {
   return lmhead_logps_bwd_ex(hidden, W, targets, N, H, V, chunk_size, 1.0f, lse, entropy, g_logp,
                              g_ent, dh, dW, 0u, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Distillation from a teacher's top logits.
+namespace {
+
+static_assert(lmh::kDistillMaxK == LMH_DISTILL_MAX_K && lmh::kNormMaxH == LMH_NORM_MAX_H, "limits in the header");
+
+bool known_type(int type) { return type == LMH_TYPE_BF16 || type == LMH_TYPE_F32; }
+uintptr_t type_size(int type) { return type == LMH_TYPE_F32 ? 4 : 2; }
+
+int check_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size) {
+  const int rc = check_shape(N, H, V, chunk_size);
+  if (rc != LMH_OK) return rc;
+  if (K < 1 || K > LMH_DISTILL_MAX_K)
+    return fail(LMH_ERR_SHAPE, "K must be in [1, %d], got %lld", LMH_DISTILL_MAX_K, (long long)K);
+  return LMH_OK;
+}
+
+// Where the distillation's arrays lie behind the head's own workspace.
+struct DistillPlan {
+  size_t off_rec = 0, fwd_bytes = 0;                                   // forward: merged records [N][4]
+  size_t off_tgt = 0, off_ga = 0, off_id = 0, off_val = 0, bytes = 0;  // backward
+};
+
+DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size, int kind) {
+  DistillPlan d;
+  const int64_t n = std::max<int64_t>(N, 1);
+  auto room = [](int64_t bytes) { return (size_t)lmh::round_up(bytes, 256); };
+  d.off_rec = lmh::plan_forward(N, H, V).bytes;
+  d.fwd_bytes = d.off_rec + room(n * 16);
+  if (kind == LMH_WS_FWD) {
+    d.bytes = d.fwd_bytes;
+    return d;
+  }
+  const lmh::BwdPlan p = lmh::plan_backward(N, H, V, chunk_size);
+  d.off_tgt = kind == LMH_WS_BWD_BF16 ? p.bytes_bf16 : p.bytes;
+  d.off_ga = d.off_tgt + room(n * 4);
+  d.off_id = d.off_ga + room(n * 4);
+  d.off_val = d.off_id + room(n * (K + 1) * 4);
+  d.bytes = d.off_val + room(n * (K + 1) * 2);
+  return d;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lmhead_logps_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size,
+                                         int with_backward, size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(LMH_ERR_NULL, "bytes_out is NULL");
+  int rc = check_distill(N, H, V, K, chunk_size);
+  if (rc != LMH_OK) return rc;
+  if (with_backward < 0 || with_backward > LMH_WS_BWD_BF16)
+    return fail(LMH_ERR_ARGS, "with_backward must be 0, 1 or 2, got %d", with_backward);
+  if (with_backward && (rc = check_backward_size(N, V)) != LMH_OK) return rc;
+  const DistillPlan d = plan_distill(N, H, V, K, chunk_size, with_backward);
+  *bytes_out = std::max(d.fwd_bytes, d.bytes);
+  return ok();
+}
+
+int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const int32_t* targets, const int32_t* ids,
+                             const void* teacher, int teacher_type, const float* teacher_lse, int64_t N, int64_t H,
+                             int64_t V, int64_t K, int64_t chunk_size, float temperature, float* kl, float* logp,
+                             float* lse, float* logp_top, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_distill(N, H, V, K, chunk_size);
+  if (rc != LMH_OK) return rc;
+  rc = check_temperature(temperature);
+  if (rc != LMH_OK) return rc;
+  if (!known_type(teacher_type)) return fail(LMH_ERR_ARGS, "distill_fwd: unknown teacher_type %d", teacher_type);
+  if (logp != nullptr && targets == nullptr) return fail(LMH_ERR_ARGS, "distill_fwd: logp asked for without targets");
+  if (N == 0) return ok();
+  if (!hidden || !W || !ids || !teacher || !kl || !lse || !logp_top || !workspace)
+    return fail(LMH_ERR_NULL,
+                "distill_fwd: hidden, W, ids, teacher, kl, lse, logp_top and workspace must be non-NULL");
+  if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(workspace, 16) || !aligned(targets, 4) || !aligned(ids, 4) ||
+      !aligned(teacher, type_size(teacher_type)) || !aligned(teacher_lse, 4) || !aligned(kl, 4) || !aligned(logp, 4) ||
+      !aligned(lse, 4) || !aligned(logp_top, 4))
+    return fail(LMH_ERR_UNSUPPORTED,
+                "distill_fwd: hidden, W and workspace need 16-byte alignment, the others that of their elements");
+  const DistillPlan d = plan_distill(N, H, V, K, chunk_size, LMH_WS_FWD);
+  if (workspace_bytes < d.bytes)
+    return fail(LMH_ERR_WORKSPACE, "distill_fwd: workspace of %zu bytes, %zu needed", workspace_bytes, d.bytes);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float* rec = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.off_rec);
+  const lmh::FwdPlan p = lmh::plan_forward(N, H, V);
+  const float sc = temper_scale(temperature);
+  // without hard targets the tile kernel still reads N ids to pick a logit by:
+  // any will do, the pick is not used
+  lmh::FwdArgs a{hidden, W, targets != nullptr ? targets : ids, N, H, V, p.S, p.n_tt, p.n_vt, 0, V, sc,
+                 inv_temperature(temperature), workspace, p.part_ld, nullptr, nullptr, nullptr, rec};
+  hipError_t e = lmh::launch_fwd(a, s);
+  const double back = 1.0 / ((double)sc * (double)temperature);
+  const float back_hi = (float)back;
+  if (e == hipSuccess)
+    e = lmh::launch_distill_top({hidden, W, targets, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
+                                 (int)H, (int)V, (int)K, temperature, back_hi, (float)(back - (double)back_hi), rec,
+                                 kl, logp, lse, logp_top}, s);
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "distill_fwd: launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const int32_t* targets, const int32_t* ids,
+                             const void* teacher, int teacher_type, const float* teacher_lse, int64_t N, int64_t H,
+                             int64_t V, int64_t K, int64_t chunk_size, float temperature, const float* logp,
+                             const float* lse, const float* logp_top, const float* g_kl, const float* g_logp,
+                             void* dh, void* dW, int grad_type, unsigned flags, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  int rc = check_distill(N, H, V, K, chunk_size);
+  if (rc != LMH_OK) return rc;
+  rc = check_temperature(temperature);
+  if (rc != LMH_OK) return rc;
+  rc = check_backward_size(N, V);
+  if (rc != LMH_OK) return rc;
+  if (!known_type(teacher_type) || !known_type(grad_type))
+    return fail(LMH_ERR_ARGS, "distill_bwd: unknown teacher_type %d or grad_type %d", teacher_type, grad_type);
+  if (g_logp != nullptr && (targets == nullptr || logp == nullptr))
+    return fail(LMH_ERR_ARGS, "distill_bwd: g_logp given without targets or without the forward's logp");
+  const bool bf16 = grad_type == LMH_TYPE_BF16;
+  DistillHook hook{};
+  const int32_t* tgt = nullptr;
+  const float* ga = nullptr;
+  if (N > 0) {
+    if (!ids || !teacher || !logp_top || !workspace || !dh)
+      return fail(LMH_ERR_NULL, "distill_bwd: ids, teacher, logp_top, dh and workspace must be non-NULL");
+    if (!aligned(targets, 4) || !aligned(ids, 4) || !aligned(teacher, type_size(teacher_type)) ||
+        !aligned(teacher_lse, 4) || !aligned(logp, 4) || !aligned(lse, 4) || !aligned(logp_top, 4) ||
+        !aligned(g_kl, 4) || !aligned(g_logp, 4) || !aligned(workspace, 16) || !aligned(dW, 16))
+      return fail(LMH_ERR_UNSUPPORTED, "distill_bwd: a misaligned pointer");
+    const DistillPlan d = plan_distill(N, H, V, K, chunk_size, bf16 ? LMH_WS_BWD_BF16 : LMH_WS_BWD);
+    char* ws = static_cast<char*>(workspace);
+    int32_t* w_tgt = reinterpret_cast<int32_t*>(ws + d.off_tgt);
+    float* w_ga = reinterpret_cast<float*>(ws + d.off_ga);
+    // a hard target without a cotangent takes no part
+    hook.prep = {g_logp != nullptr ? targets : nullptr, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
+                 (int)V, (int)K, temperature, inv_temperature(temperature), logp, logp_top, g_kl, g_logp, w_tgt, w_ga,
+                 reinterpret_cast<int32_t*>(ws + d.off_id), reinterpret_cast<uint16_t*>(ws + d.off_val)};
+    hook.bytes = d.bytes;
+    tgt = w_tgt;
+    ga = w_ga;
+  }
+  return bwd_impl("distill_bwd", hidden, W, tgt, N, H, V, 0, V, chunk_size, temperature, lse, nullptr, ga, nullptr,
+                  dh, dW, flags, bf16, workspace, workspace_bytes, stream, N > 0 ? &hook : nullptr);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The norm in front of the head.
+namespace {
+
+int check_norm(const char* who, int64_t N, int64_t H) {
+  if (N < 0 || N >= (int64_t(1) << 31))
+    return fail(LMH_ERR_SHAPE, "%s: N must be in [0, 2^31), got %lld", who, (long long)N);
+  if (H <= 0) return fail(LMH_ERR_SHAPE, "%s: H must be > 0, got %lld", who, (long long)H);
+  if (H > LMH_NORM_MAX_H)
+    return fail(LMH_ERR_UNSUPPORTED, "%s: H must be at most %d, got %lld", who, LMH_NORM_MAX_H, (long long)H);
+  return LMH_OK;
+}
+
+int check_norm_types(const char* who, int kind, int x_type, int y_type, int w_type) {
+  if (kind != LMH_NORM_LAYER && kind != LMH_NORM_RMS) return fail(LMH_ERR_ARGS, "%s: unknown kind %d", who, kind);
+  if (!known_type(x_type) || !known_type(y_type) || !known_type(w_type))
+    return fail(LMH_ERR_ARGS, "%s: unknown type among x %d, y %d, weight %d", who, x_type, y_type, w_type);
+  if (y_type == LMH_TYPE_F32 && x_type != LMH_TYPE_F32)
+    return fail(LMH_ERR_ARGS, "%s: float32 y needs float32 x", who);
+  return LMH_OK;
+}
+
+size_t norm_part_bytes(int64_t N, int64_t H) { return (size_t)lmh::norm_bwd_blocks(N, H) * 2 * (size_t)H * 4; }
+
+}  // namespace
+
+extern "C" {
+
+int lmhead_logps_norm_workspace_bytes(int64_t N, int64_t H, size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(LMH_ERR_NULL, "bytes_out is NULL");
+  const int rc = check_norm("norm", N, H);
+  if (rc != LMH_OK) return rc;
+  *bytes_out = norm_part_bytes(N, H);
+  return ok();
+}
+
+int lmhead_logps_norm_fwd(const void* x, int x_type, const void* weight, const void* bias, int w_type, int64_t N,
+                          int64_t H, float eps, int kind, void* y, int y_type, float* mean, float* rstd,
+                          void* stream) {
+  int rc = check_norm("norm_fwd", N, H);
+  if (rc != LMH_OK) return rc;
+  rc = check_norm_types("norm_fwd", kind, x_type, y_type, w_type);
+  if (rc != LMH_OK) return rc;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(LMH_ERR_ARGS, "norm_fwd: eps must be finite and >= 0, got %g", (double)eps);
+  if (N == 0) return ok();
+  if (!x || !y) return fail(LMH_ERR_NULL, "norm_fwd: x and y must be non-NULL");
+  if (!aligned(x, type_size(x_type)) || !aligned(y, type_size(y_type)) || !aligned(weight, type_size(w_type)) ||
+      !aligned(bias, type_size(w_type)) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(LMH_ERR_UNSUPPORTED, "norm_fwd: a pointer is not aligned to its elements");
+  const hipError_t e = lmh::launch_norm_fwd({x, weight, bias, x_type == LMH_TYPE_F32, y_type == LMH_TYPE_F32,
+                                             w_type == LMH_TYPE_F32, kind == LMH_NORM_RMS, N, (int)H, eps, y, mean,
+                                             rstd}, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "norm_fwd: launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_type, int64_t N, int64_t H, int kind,
+                          const float* mean, const float* rstd, const void* dy, int y_type, void* dx, void* dweight,
+                          void* dbias, int g_type, unsigned flags, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int rc = check_norm("norm_bwd", N, H);
+  if (rc != LMH_OK) return rc;
+  rc = check_norm_types("norm_bwd", kind, x_type, y_type, w_type);
+  if (rc != LMH_OK) return rc;
+  if (!known_type(g_type)) return fail(LMH_ERR_ARGS, "norm_bwd: unknown g_type %d", g_type);
+  if (flags & ~(unsigned)LMH_BWD_ACCUMULATE_DW) return fail(LMH_ERR_ARGS, "norm_bwd: unknown flags 0x%x", flags);
+  const bool accumulate = (flags & LMH_BWD_ACCUMULATE_DW) != 0;
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  if (!aligned(dweight, type_size(g_type)) || !aligned(dbias, type_size(g_type)))
+    return fail(LMH_ERR_UNSUPPORTED, "norm_bwd: a pointer is not aligned to its elements");
+  const lmh::NormReduceArgs empty{nullptr, 0, (int)H, g_type == LMH_TYPE_F32, accumulate, dweight, dbias};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (N == 0) {
+    if (!sums || accumulate) return ok();
+    const hipError_t e = lmh::launch_norm_reduce(empty, s);
+    if (e != hipSuccess) return fail(LMH_ERR_HIP, "norm_bwd: launch failed: %s", hipGetErrorString(e));
+    return ok();
+  }
+  if (!x || !rstd || !dy || !dx || (kind == LMH_NORM_LAYER && !mean) || (sums && !workspace))
+    return fail(LMH_ERR_NULL, "norm_bwd: x, mean (layer norm), rstd, dy, dx and workspace (for dweight, dbias) must be non-NULL");
+  if (!aligned(x, type_size(x_type)) || !aligned(dx, type_size(x_type)) || !aligned(dy, type_size(y_type)) ||
+      !aligned(weight, type_size(w_type)) || !aligned(mean, 4) || !aligned(rstd, 4) || (sums && !aligned(workspace, 16)))
+    return fail(LMH_ERR_UNSUPPORTED, "norm_bwd: a pointer is not aligned to its elements (workspace: 16 bytes)");
+  const size_t need = sums ? norm_part_bytes(N, H) : 0;
+  if (workspace_bytes < need)
+    return fail(LMH_ERR_WORKSPACE, "norm_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  float* part = sums ? static_cast<float*>(workspace) : nullptr;
+  lmh::NormReduceArgs red = empty;
+  red.part = part;
+  red.blocks = lmh::norm_bwd_blocks(N, H);
+  hipError_t e = lmh::launch_norm_bwd({x, weight, mean, rstd, dy, x_type == LMH_TYPE_F32, y_type == LMH_TYPE_F32,
+                                       w_type == LMH_TYPE_F32, kind == LMH_NORM_RMS, N, (int)H, dx, part},
+                                      red.blocks, s);
+  if (e == hipSuccess && sums) e = lmh::launch_norm_reduce(red, s);
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "norm_bwd: launch failed: %s", hipGetErrorString(e));
+  return ok();
 }
 
 }  // extern "C"

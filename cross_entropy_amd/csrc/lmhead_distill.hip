@@ -1,0 +1,295 @@
+// lmhead_distill.hip -- distillation from a teacher's top logits on the head's
+// never-stored logits, for gfx950: the parts beside the head's own tile
+// kernels (lmhead_kernels.hip).
+//
+// With z = W h / T, lse = log sum exp z and, for the K teacher entries
+// (id_k, t_k) of a token, s_k = z[id_k] - lse and q_k = softmax(t / T)_k over
+// the live entries (or exp(t_k / T - teacher_lse)):
+//
+//   kl   = sum_k q_k (log q_k - s_k),   Q = sum_k q_k
+//   dz_v = [ g_kl (Q p_v - sum_{id_k = v} q_k) + g_logp (1[v = target] - p_v) ] / T
+//
+// Away from the teacher's ids and the target, dz_v = -(g_logp - g_kl Q) p_v / T:
+// the head's own cotangent under the log-prob cotangent g_logp - g_kl Q. So
+// the forward takes the head's log-sum-exp record and adds K dot products a
+// token (0.04% of its products at K = 64, V = 152k), and the backward runs the
+// head's tiles with that combined cotangent and then overwrites the K + 1
+// special entries of each token in the cotangent block, each formed in
+// float32 and rounded to bf16 once (added to the tile's rounded entry instead,
+// Q p - q would keep only the digits that bf16 left in p).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "lmhead_internal.h"
+
+namespace lmh {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+__device__ __forceinline__ float teacher_at(const void* t, bool f32, int64_t i) {
+  return f32 ? static_cast<const float*>(t)[i] : widen(static_cast<const uint16_t*>(t)[i]);
+}
+
+// NaN-propagating max
+__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) v += __shfl_xor(v, x);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) v = nan_max(v, __shfl_xor(v, x));
+  return v;
+}
+
+// A token's log q over its live entries is t_k / T - shift (a true division:
+// t_k / T reaches the loss in full where the teacher's log-sum-exp is given,
+// and a rounded reciprocal would add its error to it): shift is the
+// teacher's own log-sum-exp, or that of the live entries (0 if none has any
+// mass, whose q are then all 0). One wave; `t_of(k)` gives t_k / T, -inf for
+// an entry that is not live.
+template <class F>
+__device__ __forceinline__ float teacher_shift(const float* teacher_lse, int64_t tok, int K, F t_of) {
+  if (teacher_lse != nullptr) return teacher_lse[tok];
+  const int lane = threadIdx.x & 63;
+  float m = -INFINITY;
+  for (int k = lane; k < K; k += 64) m = nan_max(m, t_of(k));
+  m = wave_max(m);
+  if (m == -INFINITY) return 0.0f;
+  float s = 0.0f;
+  for (int k = lane; k < K; k += 64) s += expf(t_of(k) - m);
+  return m + logf(wave_sum(s));
+}
+
+// q of one entry: 0 at t = -inf whatever the shift is.
+__device__ __forceinline__ float teacher_q(float t, float shift) { return t == -INFINITY ? 0.0f : expf(t - shift); }
+
+// The K dot products W[id_k] . h of a token into s_z: a workgroup's waves take
+// them eight at a time. Lane l holds 16-byte chunks l, l + 64, ... of the row;
+// one load of h serves eight rows of W.
+constexpr int kDotRows = 8;
+__device__ __forceinline__ void distill_dots(const DistillTopArgs& a, int64_t tok, int lane, int wave, int n_waves,
+                                             float* s_z) {
+  const int K = a.K, H = a.H, V = a.V;
+  const int32_t* ids = a.ids + tok * K;
+  const uint4* h = reinterpret_cast<const uint4*>(a.hidden + tok * H);
+  for (int k0 = wave * kDotRows; k0 < K; k0 += n_waves * kDotRows) {
+    const uint4* w[kDotRows];
+    float acc[kDotRows];
+#pragma unroll
+    for (int e = 0; e < kDotRows; ++e) {
+      int id = ids[min(k0 + e, K - 1)];
+      id = (id >= 0 && id < V) ? id : 0;   // a dead entry's dot product is not used
+      w[e] = reinterpret_cast<const uint4*>(a.W + (int64_t)id * H);
+      acc[e] = 0.0f;
+    }
+    for (int c = lane; c < H / 8; c += 64) {
+      const uint4 x = h[c];
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+      uint4 y[kDotRows];
+#pragma unroll
+      for (int e = 0; e < kDotRows; ++e) y[e] = w[e][c];
+#pragma unroll
+      for (int e = 0; e < kDotRows; ++e) {
+        const uint32_t ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[e] = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), acc[e]);
+          acc[e] = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), acc[e]);
+        }
+      }
+    }
+    // eight sums over 64 lanes: each of the first three steps halves the
+    // number of rows a lane still carries, so they cost 7 exchanges and not 24
+#pragma unroll
+    for (int x = 32, n = 4; n >= 1; x >>= 1, n >>= 1) {
+      const bool hi = (lane & x) != 0;
+#pragma unroll
+      for (int e = 0; e < n; ++e) {
+        const float give = hi ? acc[e] : acc[e + n];
+        const float keep = hi ? acc[e + n] : acc[e];
+        acc[e] = keep + __shfl_xor(give, x);
+      }
+    }
+    float z = acc[0];
+#pragma unroll
+    for (int x = 4; x >= 1; x >>= 1) z += __shfl_xor(z, x);
+    // lane bits 5, 4, 3 now name the row
+    const int e = ((lane >> 5) & 1) * 4 + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
+    if ((lane & 7) == 0 && k0 + e < K) s_z[k0 + e] = z;
+  }
+}
+
+// The outputs of one token from its dot products and its log-sum-exp record.
+__device__ __forceinline__ void distill_token(const DistillTopArgs& a, int64_t tok, int lane, const float* s_z) {
+  const int K = a.K, V = a.V;
+  const int32_t* ids = a.ids + tok * K;
+  const float4 rec = reinterpret_cast<const float4*>(a.rec)[tok];   // (m2, s1, s2, zt)
+  // The record is in base 2 of logits scaled by the float32 sc ~ log2(e) / T:
+  // back = 1 / (sc T) in two words takes the max back to natural units of z / T
+  // without sc's rounding, which a loss of the size of the max's last digits
+  // would show. A +inf logit (and no NaN) leaves m = +inf and s1 = NaN.
+  const float lse = rec.x == INFINITY ? INFINITY : fmaf(rec.x, a.back_hi, fmaf(rec.x, a.back_lo, kLn2 * log2f(rec.y)));
+  auto live_of = [&](int k) { return ids[k] >= 0 && ids[k] < V; };
+  auto t_of = [&](int k) { return live_of(k) ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY; };
+  const float shift = teacher_shift(a.teacher_lse, tok, K, t_of);
+  float kl = 0.0f;
+  bool any = false;
+  for (int k = lane; k < K; k += 64) {
+    const bool live = live_of(k);
+    any |= live;
+    const float top = live ? s_z[k] / a.T - lse : 0.0f;
+    const float t = t_of(k);
+    const float q = teacher_q(t, shift);
+    if (q != 0.0f) kl += q * ((t - shift) - top);
+    a.logp_top[tok * K + k] = top;
+  }
+  kl = wave_sum(kl);
+  const bool some = __any(any);
+  if (lane == 0) {
+    const int t = a.targets != nullptr ? a.targets[tok] : -1;
+    const bool hard = t >= 0 && t < V;
+    a.kl[tok] = kl;
+    a.lse[tok] = (hard || some) ? lse : 0.0f;
+    if (a.logp != nullptr) a.logp[tok] = hard ? rec.w / a.T - lse : 0.0f;
+  }
+}
+
+// Forward tail, a workgroup per token. Bound by the fetch of the K rows of W (2 H bytes each),
+// from the last-level cache where teachers agree on frequent ids.
+__global__ __launch_bounds__(256) void distill_top_kernel(const DistillTopArgs a) {
+  __shared__ float s_z[kDistillMaxK];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n_waves = blockDim.x >> 6;
+  for (int64_t tok = blockIdx.x; tok < a.N; tok += gridDim.x) {
+    distill_dots(a, tok, lane, wave, n_waves, s_z);
+    __syncthreads();
+    if (wave == 0) distill_token(a, tok, lane, s_z);
+    __syncthreads();   // s_z is read before the next token's dot products
+  }
+}
+
+// Backward, before the tiles. A wave per token forms what the head's tiles
+// read (the combined log-prob cotangent and a target id, one of the special
+// entries or -1 for a token without any) and the token's special entries:
+// (id, cotangent in bf16), K + 1 of them, id -1 where there is none. An id
+// that the teacher lists twice is formed once, at its first place, with the
+// sum of its q in list order.
+__global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t tok = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (tok >= a.N) return;
+  const int K = a.K, V = a.V;
+  const int32_t* ids = a.ids + tok * K;
+  const int target = a.targets != nullptr ? a.targets[tok] : -1;
+  const bool hard = target >= 0 && target < V;
+  const float g_kl = a.g_kl != nullptr ? a.g_kl[tok] : 0.0f;
+  const float g_logp = (hard && a.g_logp != nullptr) ? a.g_logp[tok] : 0.0f;
+  auto live_of = [&](int k) { return ids[k] >= 0 && ids[k] < V; };
+  auto t_of = [&](int k) { return live_of(k) ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY; };
+  // a token whose loss term has no cotangent forms none of it (selected, so a
+  // NaN in the teacher's row under g_kl = 0 stays out)
+  const bool kd = g_kl != 0.0f;
+  const float shift = kd ? teacher_shift(a.teacher_lse, tok, K, t_of) : 0.0f;
+  float Q = 0.0f;
+  int first = K;   // the first live entry
+  bool listed = false;
+  for (int k = lane; k < K; k += 64) {
+    if (!live_of(k)) continue;
+    first = min(first, k);
+    listed |= hard && ids[k] == target;
+    if (kd) Q += teacher_q(t_of(k), shift);
+  }
+  Q = wave_sum(Q);
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) first = min(first, __shfl_xor(first, x));
+  listed = __any(listed);
+  const float gQ = kd ? g_kl * Q : 0.0f;
+  auto cotangent = [&](float s, float q, bool is_target) {
+    const float p = expf(s);
+    float x = 0.0f;
+    if (p != 0.0f) x = (kd ? g_kl * fmaf(Q, p, -q) : 0.0f) - g_logp * p;   // an entry of probability 0 has no such term
+    else if (kd) x = -g_kl * q;
+    return __builtin_bit_cast(uint16_t, (__bf16)((is_target ? x + g_logp : x) * a.invT));
+  };
+  int32_t* e_id = a.ent_id + tok * (K + 1);
+  uint16_t* e_val = a.ent_val + tok * (K + 1);
+  for (int k = lane; k < K; k += 64) {
+    const int id = live_of(k) ? ids[k] : -1;
+    int out = id;
+    uint16_t val = 0;
+    if (id >= 0) {
+      float q = 0.0f;
+      for (int j = 0; j < K; ++j) {
+        if (ids[j] != id) continue;
+        if (j < k) out = -1;
+        if (kd) q += teacher_q(t_of(j), shift);
+      }
+      val = cotangent(a.logp_top[tok * K + k], q, hard && id == target);
+    }
+    e_id[k] = out;
+    e_val[k] = val;
+  }
+  if (lane == 0) {
+    const bool extra = hard && !listed;
+    e_id[K] = extra ? target : -1;
+    e_val[K] = extra ? cotangent(a.logp != nullptr ? a.logp[tok] : 0.0f, 0.0f, true) : (uint16_t)0;
+    a.tgt[tok] = hard ? target : (first < K ? ids[first] : -1);
+    a.ga[tok] = g_logp - gQ;
+  }
+}
+
+// Overwrites the special entries of tokens [t0, t0 + Ct) and vocabulary rows
+// [v0, v0 + Vb) in their cotangent block, after the launch that formed it.
+__global__ __launch_bounds__(256) void distill_scatter_kernel(const DistillScatterArgs a) {
+  const int64_t n = (int64_t)a.Ct * a.K1;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    const int64_t at = (int64_t)a.t0 * a.K1 + i;
+    const int v = a.ent_id[at] - a.v0;   // id -1 falls below every block
+    if (v >= 0 && v < a.Vb && a.ent_id[at] >= 0) a.dz[i / a.K1 * a.ld_dz + v] = a.ent_val[at];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_distill_top(const DistillTopArgs& a, hipStream_t stream) {
+  const int waves = std::max(1, std::min(4, (a.K + kDotRows - 1) / kDotRows));
+  const double N = (double)a.N, K = (double)a.K, H = (double)a.H;
+  trace_begin(stream);
+  hipLaunchKernelGGL(distill_top_kernel, dim3((unsigned)std::min<int64_t>(a.N, 1 << 20)), dim3(64 * waves), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kDistillTop, stream, 2.0 * N * K * H, 2.0 * N * (K + 1) * H + N * K * (8 + (a.t_f32 ? 4 : 2)) + 32.0 * N);
+  return hipSuccess;
+}
+
+hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream) {
+  const double N = (double)a.N, K = (double)a.K;
+  trace_begin(stream);
+  hipLaunchKernelGGL(distill_prep_kernel, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kDistillPrep, stream, 0.0, N * K * (14 + (a.t_f32 ? 4 : 2)) + 24.0 * N);
+  return hipSuccess;
+}
+
+hipError_t launch_distill_scatter(const DistillScatterArgs& a, hipStream_t stream) {
+  const int64_t n = (int64_t)a.Ct * a.K1;
+  trace_begin(stream);
+  hipLaunchKernelGGL(distill_scatter_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kDistillScatter, stream, 0.0, 4.0 * (double)n);
+  return hipSuccess;
+}
+
+}  // namespace lmh

@@ -1,5 +1,6 @@
 // lmhead_internal.h -- launch descriptors shared by the C ABI (lmhead_api.hip)
-// and the kernels (lmhead_kernels.hip). Not part of the public interface.
+// and the kernels (lmhead_kernels.hip, lmhead_distill.hip, lmhead_norm.hip).
+// Not part of the public interface.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -119,8 +120,104 @@ struct BwdStep {
   int dh_dead_zero;
 };
 
+// Distillation (lmhead_distill.hip). K entries per token: ids [N][K], teacher
+// logits [N][K] (float32 or bf16).
+constexpr int kDistillMaxK = 1024;
+
+struct DistillTopArgs {
+  const uint16_t* hidden;
+  const uint16_t* W;
+  const int32_t* targets;     // or NULL
+  const int32_t* ids;
+  const void* teacher;
+  bool t_f32;
+  const float* teacher_lse;   // or NULL: softmax over the live entries
+  int64_t N;
+  int H, V, K;
+  float T;
+  float back_hi, back_lo;     // 1 / (sc T) in two words (sc = the base-2 scale of the records)
+  const float* rec;           // merged records [N][4] of the forward
+  float* kl;
+  float* logp;                // or NULL
+  float* lse;
+  float* logp_top;            // [N][K]
+};
+
+// What the backward forms per token before the tiles run: the combined
+// log-prob cotangent ga and target id tgt that the tiles read, and K + 1
+// special entries (id or -1, cotangent in bf16) that overwrite the tiles'.
+struct DistillPrepArgs {
+  const int32_t* targets;     // or NULL
+  const int32_t* ids;
+  const void* teacher;
+  bool t_f32;
+  const float* teacher_lse;
+  int64_t N;
+  int V, K;
+  float T, invT;
+  const float* logp;          // of the target; read where it is not among the ids
+  const float* logp_top;
+  const float* g_kl;          // or NULL
+  const float* g_logp;        // or NULL
+  int32_t* tgt;               // [N]
+  float* ga;                  // [N]
+  int32_t* ent_id;            // [N][K + 1]
+  uint16_t* ent_val;          // [N][K + 1]
+};
+
+struct DistillScatterArgs {
+  const int32_t* ent_id;
+  const uint16_t* ent_val;
+  int K1;                     // K + 1
+  uint16_t* dz;
+  int64_t ld_dz;
+  int t0, Ct, v0, Vb;
+};
+
+// The norm in front of the head (lmhead_norm.hip); rows of H elements.
+constexpr int kNormMaxH = 16384;
+
+struct NormFwdArgs {
+  const void* x;
+  const void* w;      // or NULL: ones
+  const void* b;      // or NULL: zeros
+  bool x_f32, y_f32, w_f32, rms;
+  int64_t N;
+  int H;
+  float eps;
+  void* y;
+  float* mean;        // or NULL
+  float* rstd;        // or NULL
+};
+
+struct NormBwdArgs {
+  const void* x;
+  const void* w;      // or NULL: ones
+  const float* mean;  // not read for RMS
+  const float* rstd;
+  const void* dy;
+  bool x_f32, y_f32, w_f32, rms;
+  int64_t N;
+  int H;
+  void* dx;
+  float* part;        // [blocks][2][H] partial sums of dw and db, or NULL: neither is wanted
+};
+
+struct NormReduceArgs {
+  const float* part;
+  int blocks, H;
+  bool g_f32, accumulate;
+  void* dw;           // or NULL
+  void* db;           // or NULL
+};
+
+int norm_bwd_blocks(int64_t N, int64_t H);   // workgroups (partial rows) of the norm's backward
+
 // Kernel ids of the tracing facility (lmhead_trace.hip).
-enum KernelId { kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16, kNumKernels };
+enum KernelId {
+  kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
+  kDistillTop, kDistillPrep, kDistillScatter, kNormFwd, kNormBwd, kNormReduce, kNumKernels
+};
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);
 
@@ -136,5 +233,11 @@ hipError_t launch_pad_rows(const uint16_t* in, int64_t R, int64_t C, int64_t R_p
 hipError_t launch_transpose(const uint16_t* in, int64_t ld_in, int64_t R, int64_t C, int64_t R_pad,
                             int64_t C_pad, const int32_t* tgt, int64_t V, uint16_t* out,
                             int64_t ld_out, hipStream_t stream);
+hipError_t launch_distill_top(const DistillTopArgs& a, hipStream_t stream);
+hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream);
+hipError_t launch_distill_scatter(const DistillScatterArgs& a, hipStream_t stream);
+hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int blocks, hipStream_t stream);
+hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t stream);
 
 }  // namespace lmh

@@ -94,7 +94,7 @@ extern "C" {
 
 #define LMH_OK 0
 #define LMH_ERR_NULL (-1)        /* a required pointer is NULL */
-#define LMH_ERR_SHAPE (-2)       /* N < 0, H <= 0, V <= 0 or V >= 2^31 */
+#define LMH_ERR_SHAPE (-2)       /* N < 0, H <= 0, V <= 0 or V >= 2^31; K out of range */
 #define LMH_ERR_CHUNK (-3)       /* chunk_size <= 0 */
 #define LMH_ERR_WORKSPACE (-4)   /* workspace smaller than the queried size */
 #define LMH_ERR_ARGS (-5)        /* g_ent given without entropy; bad temperature */
@@ -304,6 +304,120 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
                              int64_t N, int64_t H, int64_t V, int64_t chunk_size, float temperature,
                              float* logp, float* entropy, float* lse, void* stream);
 
+/*
+ * Distillation from a teacher's top logits. Per token, the teacher gives K
+ * entries (id_k, t_k); with the tempered logits z / T of the head, their
+ * log-sum-exp lse and s_k = z[id_k] / T - lse,
+ *   kl   = sum_k q_k (log q_k - s_k)         (terms with q_k = 0 are 0)
+ *   q_k  = softmax over the entries of t_k / T, or, with teacher_lse,
+ *          exp(t_k / T - teacher_lse): the teacher's own probabilities, of
+ *          which the entries hold Q = sum_k q_k <= 1
+ * and, beside it from the same pass, logp = z[target] / T - lse of a hard
+ * target. Neither call holds the [tokens, vocab] logits. kl is the loss at
+ * temperature T without the customary factor T^2 (the caller's cotangent
+ * carries it).
+ *   targets      int32 [N]    hard targets, or NULL for none; outside [0, V)
+ *                             the token has none (logp 0)
+ *   ids          int32 [N,K]  teacher's ids; an id outside [0, V) marks a
+ *                             missing entry (a shorter list, padding), whose
+ *                             teacher logit is not used. An id may repeat:
+ *                             its q add up in the gradient
+ *   teacher      [N,K]        teacher's logits of those ids, of type
+ *                             teacher_type (LMH_TYPE_BF16 or LMH_TYPE_F32).
+ *                             t_k / T = -inf gives q_k = 0
+ *   teacher_lse  f32 [N]      log-sum-exp of the teacher's whole logits / T,
+ *                             or NULL: the entries' softmax
+ *   kl           f32 [N]      out
+ *   logp         f32 [N]      out: needs targets; may be NULL
+ *   lse          f32 [N]      out: of the student, kept for the backward
+ *   logp_top     f32 [N,K]    out: s_k, the student's log-probs at the ids (0
+ *                             for a missing entry), kept for the backward
+ * A token without any entry and without a hard target is masked: its outputs
+ * are 0, its dh row is 0 (unchanged when adding) and it adds nothing to dW,
+ * whatever its hidden row holds. A row whose entries all have q = 0 has kl 0
+ * and no gradient of it. NaN or +inf teacher logits make that row's kl NaN;
+ * otherwise non-finite values follow IEEE evaluation as for the head.
+ *
+ * lmhead_logps_distill_bwd: dh and dW of L = sum_i g_kl_i kl_i + g_logp_i
+ * logp_i (the teacher's logits get no gradient), through
+ *   dz_v = [g_kl (Q p_v - sum_{id_k = v} q_k) + g_logp (1[v = target] - p_v)] / T.
+ *   g_kl         f32 [N] or NULL (zeros); a token with g_kl = 0 does not form
+ *                        the term, whatever its teacher row holds
+ *   g_logp       f32 [N] or NULL (zeros); needs targets and the forward's logp
+ *   dh, dW       [N,H] and [V,H], 16-byte aligned, of type grad_type
+ *                (LMH_TYPE_F32, or LMH_TYPE_BF16 through float32 sums)
+ *   flags        LMH_BWD_ACCUMULATE_DH / _DW, as for lmhead_logps_bwd_ex and
+ *                lmhead_logps_bwd_bf16
+ * The workspace holds the head's backward workspace (chunk_size bounds the
+ * cotangent block as there) and 8 N + 6 N (K + 1) bytes of the tokens' special
+ * entries. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
+ * LMH_WS_FWD, LMH_WS_BWD or LMH_WS_BWD_BF16. A smaller size than the query
+ * gives is refused. Results do not depend on anything but the arguments:
+ * no atomics take part in sums.
+ * Errors: those of the head's calls, plus LMH_ERR_SHAPE when K is not in [1,
+ * LMH_DISTILL_MAX_K] and LMH_ERR_ARGS for an unknown type, logp or g_logp
+ * without targets, or g_logp without logp.
+ */
+#define LMH_TYPE_BF16 0
+#define LMH_TYPE_F32 1
+#define LMH_DISTILL_MAX_K 1024
+int lmhead_logps_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size,
+                                         int with_backward, size_t* bytes_out);
+int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const int32_t* targets,
+                             const int32_t* ids, const void* teacher, int teacher_type, const float* teacher_lse,
+                             int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size, float temperature,
+                             float* kl, float* logp, float* lse, float* logp_top,
+                             void* workspace, size_t workspace_bytes, void* stream);
+int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const int32_t* targets,
+                             const int32_t* ids, const void* teacher, int teacher_type, const float* teacher_lse,
+                             int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size, float temperature,
+                             const float* logp, const float* lse, const float* logp_top,
+                             const float* g_kl, const float* g_logp,
+                             void* dh, void* dW, int grad_type, unsigned flags,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The norm in front of the head, over rows of H:
+ *   kind LMH_NORM_LAYER: mu = mean x, rstd = 1 / sqrt(mean (x - mu)^2 + eps)
+ *   kind LMH_NORM_RMS:   mu = 0,      rstd = 1 / sqrt(mean x^2 + eps)
+ *   y = (x - mu) rstd weight + bias
+ * and its backward: with xh = (x - mu) rstd and g = dy weight,
+ *   dx = rstd (g - mean g - xh mean(g xh))    (RMS: without mean g)
+ *   dweight = sum_i dy_i xh_i,   dbias = sum_i dy_i.
+ *   x       [N,H] of x_type; y and dy [N,H] of y_type; dx [N,H] of x_type.
+ *           LMH_TYPE_F32 y needs LMH_TYPE_F32 x (bf16 x gives bf16 y)
+ *   weight  [H] of w_type, or NULL for ones; bias [H] of w_type, or NULL
+ *   mean    f32 [N]  out of the forward and read by the backward (LAYER); may
+ *                    be NULL in the forward, is not used for RMS
+ *   rstd    f32 [N]  likewise (both kinds)
+ *   dweight, dbias   [H] of g_type, either may be NULL (not wanted); with
+ *           flags LMH_BWD_ACCUMULATE_DW they are added into
+ *   H in [1, LMH_NORM_MAX_H], odd sizes too; every pointer aligned to its
+ *   elements (the workspace to 16). eps >= 0. Outputs must not overlap inputs.
+ * Statistics and sums are float32; bf16 outputs are rounded once. dweight and
+ * dbias are summed in an order that N and H fix. An element of dy that is 0
+ * contributes 0 whatever x, the statistics and the weight hold there, so a
+ * masked token (dy row 0) gets dx = 0 and adds nothing even where its x is
+ * NaN. The backward's workspace (lmhead_logps_norm_workspace_bytes; needed
+ * only where dweight or dbias is wanted) holds the partial sums.
+ * N = 0: the forward does nothing, the backward writes dweight = dbias = 0
+ * (unless adding). Errors: LMH_ERR_NULL, LMH_ERR_SHAPE (N < 0, H < 1),
+ * LMH_ERR_ARGS (unknown kind, type or flag; float32 y from bf16 x; eps < 0 or
+ * not finite), LMH_ERR_WORKSPACE, LMH_ERR_UNSUPPORTED (H > LMH_NORM_MAX_H, a
+ * misaligned pointer), LMH_ERR_HIP. Stream semantics as for every call here.
+ */
+#define LMH_NORM_LAYER 0
+#define LMH_NORM_RMS 1
+#define LMH_NORM_MAX_H 16384
+int lmhead_logps_norm_workspace_bytes(int64_t N, int64_t H, size_t* bytes_out);
+int lmhead_logps_norm_fwd(const void* x, int x_type, const void* weight, const void* bias, int w_type,
+                          int64_t N, int64_t H, float eps, int kind,
+                          void* y, int y_type, float* mean, float* rstd, void* stream);
+int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_type, int64_t N, int64_t H, int kind,
+                          const float* mean, const float* rstd, const void* dy, int y_type,
+                          void* dx, void* dweight, void* dbias, int g_type, unsigned flags,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Thread-local message of the calling thread's last failing call ("" if none). */
 const char* lmhead_logps_last_error(void);
 
@@ -322,6 +436,12 @@ const char* lmhead_logps_version(void);
  *   4 fill_zero_kernel
  *   5 pad_rows_kernel   (W's last V % 64 rows, zero-padded to 64)
  *   6 bwd_step_bf16_kernel (bwd_step_kernel writing bf16 gradients)
+ *   7 distill_top_kernel   (distillation: student's log-probs at the teacher's ids, loss)
+ *   8 distill_prep_kernel  (distillation backward: per-token cotangents and special entries)
+ *   9 distill_scatter_kernel (distillation backward: special entries into a cotangent block)
+ *  10 norm_fwd_kernel
+ *  11 norm_bwd_kernel
+ *  12 norm_reduce_kernel   (dweight and dbias from their partial sums)
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch
