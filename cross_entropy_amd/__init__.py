@@ -77,12 +77,25 @@ __all__ = [
 ]
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t, name, dtypes, device, numel=None, optional=False):
+    # the usual case first: small calls are bound by what is done here
+    try:
+        if (t.dtype in dtypes and t.is_cuda and t.device == device and t.is_contiguous()
+                and (numel is None or t.numel() == numel)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     torch = _torch()
     if t is None:
         if optional:
@@ -95,7 +108,7 @@ def _ptr(t, name, dtypes, device, numel=None, optional=False):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() != numel:
@@ -103,14 +116,23 @@ def _ptr(t, name, dtypes, device, numel=None, optional=False):
     return t.data_ptr()
 
 
+_BF16_TYPES = ()
+
+
 def _bf16_types():
-    torch = _torch()
-    return (torch.bfloat16, torch.int16, torch.uint16)
+    global _BF16_TYPES
+    if not _BF16_TYPES:
+        torch = _torch()
+        _BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)
+    return _BF16_TYPES
 
 
 def _stream(device, stream):
-    torch = _torch()
     if stream is None:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without building a Stream object
+        if raw is not None and device.index is not None:
+            return raw(device.index)
         return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
@@ -379,16 +401,21 @@ def lmhead_logps_distill_workspace_bytes(N: int, H: int, V: int, K: int, chunk_s
 
 
 def _type_of(t, name):
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return _native.TYPE_F32
-    if t.dtype in _bf16_types():
-        return _native.TYPE_BF16
-    raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    code = _any_types().get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    return code
+
+
+_ANY_TYPES = {}
 
 
 def _any_types():
-    return (_torch().float32,) + _bf16_types()
+    """dtype -> type code of what holds float32 or bfloat16 values."""
+    if not _ANY_TYPES:
+        _ANY_TYPES.update({t: _native.TYPE_BF16 for t in _bf16_types()})
+        _ANY_TYPES[_torch().float32] = _native.TYPE_F32
+    return _ANY_TYPES
 
 
 def _distill_args(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature):

@@ -21,21 +21,9 @@
 namespace lmh {
 namespace {
 
-constexpr int kBlock = 256;   // 4 waves
-
 // v_mul_legacy_f32: +0 when either factor is 0 (NaN and inf included), else IEEE
 extern "C" __device__ float lmh_norm_fmul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
 __device__ __forceinline__ float mul0(float a, float b) { return lmh_norm_fmul_legacy(a, b); }
-
-// 16-byte accesses at element alignment: rows of an odd length start off any
-// larger boundary, which global memory accepts (a split access costs a second
-// request, where element-wide loads would cost eight).
-struct __attribute__((packed, aligned(2))) Raw8h {
-  uint32_t w[4];
-};
-struct __attribute__((packed, aligned(4))) Raw4f {
-  float f[4];
-};
 
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t narrow(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
@@ -43,177 +31,195 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return (uint32_t)narrow(lo) | ((uint32_t)narrow(hi) << 16);
 }
 
-// A row of H elements over TPR threads, widened: thread t holds NV chunks of 8
-// elements, v[i] being row chunk i * TPR + t, 0 past the row's end. Every
-// thread issues all its loads before it uses any (chunks past the last whole
-// one reread that one and are dropped): a branch per chunk would wait for each
-// load in turn. A last chunk of less than 8 is read by elements afterwards.
-template <bool F32, int TPR, int NV>
-__device__ __forceinline__ void load_row(const void* row, int H, int t, float (&v)[NV][8]) {
-  const int whole = H >> 3;
-  if (whole > 0) {
-    if (F32) {
-      Raw4f a[NV], b[NV];
+// Accesses of 8 and 16 bytes at element alignment: rows of an odd length
+// start off any larger boundary, which global memory accepts (a split access
+// costs a second request, where element-wide ones would cost up to eight).
+template <int WORDS>
+struct __attribute__((packed, aligned(2))) Raw {
+  uint32_t w[WORDS];
+};
+
+// How a row of H elements lies over its threads: in groups of G elements,
+// group i * threads + t being thread t's i-th, so that each load of a wave
+// covers one piece of memory. G is 8 (16 bytes of bf16) where x is bf16 and 4
+// (16 bytes) where it is float32; a thread holds 8 NV elements either way.
+template <bool F32, int G>
+struct Group {
+  Raw<G * (F32 ? 4 : 2) / 4> raw;
+  __device__ __forceinline__ float at(int k) const {
+    if (F32) return __uint_as_float(raw.w[k]);
+    const uint32_t w = raw.w[k / 2];
+    return __uint_as_float((k & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  }
+  __device__ __forceinline__ void set(const float (&v)[G]) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Raw4f* p = reinterpret_cast<const Raw4f*>(static_cast<const float*>(row) + 8 * min(i * TPR + t, whole - 1));
-        a[i] = p[0];
-        b[i] = p[1];
+    for (int k = 0; k < G; k += F32 ? 1 : 2) raw.w[F32 ? k : k / 2] = F32 ? __float_as_uint(v[k]) : narrow2(v[k], v[k + 1]);
+  }
+};
+
+// A thread's part of a row as it lies in memory. Every thread issues all its
+// loads before it uses any (groups past the last whole one reread that one;
+// zero() drops them): a branch per group would wait for each load in turn. A
+// last group of fewer elements is read by elements.
+template <bool F32, int G, int NG>
+struct Part {
+  Group<F32, G> g[NG];
+  __device__ __forceinline__ void load(const void* base, int64_t row, int H, int t, int threads) {
+    const int whole = H / G;
+    const char* p = static_cast<const char*>(base) + row * H * (F32 ? 4 : 2);
+    constexpr int bytes = G * (F32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int c = min(i * threads + t, whole - 1);
+      if (whole > 0) g[i].raw = *reinterpret_cast<const decltype(g[i].raw)*>(p + (int64_t)c * bytes);
+    }
+    if (H % G != 0) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        if (i * threads + t != whole) continue;
+        float v[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          v[k] = 0.0f;
+          if (k < H % G) v[k] = F32 ? reinterpret_cast<const float*>(p)[whole * G + k]
+                                    : widen(reinterpret_cast<const uint16_t*>(p)[whole * G + k]);
+        }
+        g[i].set(v);
       }
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[i][k] = a[i].f[k];
-          v[i][4 + k] = b[i].f[k];
-        }
-    } else {
-      Raw8h a[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        a[i] = *reinterpret_cast<const Raw8h*>(static_cast<const uint16_t*>(row) + 8 * min(i * TPR + t, whole - 1));
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[i][2 * k] = __uint_as_float(a[i].w[k] << 16);
-          v[i][2 * k + 1] = __uint_as_float(a[i].w[k] & 0xFFFF0000u);
-        }
     }
   }
+  __device__ __forceinline__ void fill(float x) {
+    float v[G];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int k = 0; k < G; ++k) v[k] = x;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[i][k] = i * TPR + t < whole ? v[i][k] : 0.0f;
-  if ((H & 7) != 0) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i * TPR + t != whole) continue;
-#pragma unroll
-      for (int k = 0; k < 7; ++k)
-        if (k < (H & 7)) v[i][k] = F32 ? static_cast<const float*>(row)[8 * whole + k]
-                                       : widen(static_cast<const uint16_t*>(row)[8 * whole + k]);
-    }
+    for (int i = 0; i < NG; ++i) g[i].set(v);
   }
-}
+};
 
-template <bool F32, int TPR, int NV>
-__device__ __forceinline__ void store_row(void* row, int H, int t, const float (&v)[NV][8]) {
-  const int whole = H >> 3;
+template <bool F32, int G, int NG>
+__device__ __forceinline__ void store_part(void* base, int64_t row, int H, int t, int threads, const float (&v)[NG][G]) {
+  const int whole = H / G;
+  char* p = static_cast<char*>(base) + row * H * (F32 ? 4 : 2);
+  constexpr int bytes = G * (F32 ? 4 : 2);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * TPR + t;
-    if (c >= whole) continue;
-    if (F32) {
-      Raw4f a, b;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        a.f[k] = v[i][k];
-        b.f[k] = v[i][4 + k];
-      }
-      Raw4f* p = reinterpret_cast<Raw4f*>(static_cast<float*>(row) + 8 * c);
-      p[0] = a;
-      p[1] = b;
-    } else {
-      Raw8h a;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) a.w[k] = narrow2(v[i][2 * k], v[i][2 * k + 1]);
-      *reinterpret_cast<Raw8h*>(static_cast<uint16_t*>(row) + 8 * c) = a;
-    }
+  for (int i = 0; i < NG; ++i) {
+    const int c = i * threads + t;
+    Group<F32, G> o;
+    o.set(v[i]);
+    if (c < whole) *reinterpret_cast<decltype(o.raw)*>(p + (int64_t)c * bytes) = o.raw;
   }
-  if ((H & 7) != 0) {
+  if (H % G != 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i * TPR + t != whole) continue;
+    for (int i = 0; i < NG; ++i) {
+      if (i * threads + t != whole) continue;
 #pragma unroll
-      for (int k = 0; k < 7; ++k)
-        if (k < (H & 7)) {
-          if (F32) static_cast<float*>(row)[8 * whole + k] = v[i][k];
-          else static_cast<uint16_t*>(row)[8 * whole + k] = narrow(v[i][k]);
+      for (int k = 0; k < G - 1; ++k)
+        if (k < H % G) {
+          if (F32) reinterpret_cast<float*>(p)[whole * G + k] = v[i][k];
+          else reinterpret_cast<uint16_t*>(p)[whole * G + k] = narrow(v[i][k]);
         }
     }
   }
 }
 
-// The weights of a thread's columns, in either type; `fill` where there are none.
-template <int TPR, int NV>
-__device__ __forceinline__ void load_weights(const void* w, bool f32, float fill, int H, int t, float (&v)[NV][8]) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = fill;
-  } else if (f32) {
-    load_row<true, TPR, NV>(w, H, t, v);
-  } else {
-    load_row<false, TPR, NV>(w, H, t, v);
-  }
+// Sum over a wave in a fixed order, on the vector unit alone (data-parallel
+// moves within rows of 16 lanes, then across rows; lane 63 holds the total).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false);
+  return v + __int_as_float(o);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0xB1, 0xF>(v);    // lanes ^ 1
+  v = dpp_add<0x4E, 0xF>(v);    // lanes ^ 2
+  v = dpp_add<0x141, 0xF>(v);   // the other four of eight
+  v = dpp_add<0x140, 0xF>(v);   // the other eight of the row
+  v = dpp_add<0x142, 0xA>(v);   // rows 1 and 3 add rows 0 and 2
+  v = dpp_add<0x143, 0xC>(v);   // rows 2 and 3 add row 1's
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sums of two values over the threads of a row, in a fixed order: the wave by
-// butterflies, then (a block per row) the four waves' sums through LDS. The
-// two halves of `s` alternate between calls, so one barrier a call is enough.
-template <int TPR>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float (*s)[4][2], int& turn) {
-#pragma unroll
-  for (int x = 32; x >= 1; x >>= 1) {
-    a += __shfl_xor(a, x);
-    b += __shfl_xor(b, x);
-  }
-  if (TPR > 64) {
-    const int wave = threadIdx.x >> 6;
+// Sums of two values over the threads of a row: the wave, then (a block per
+// row) the waves' sums through LDS in order. The two halves of `s` alternate
+// between calls, so one barrier a call is enough.
+constexpr int kMaxWaves = 8;
+template <bool WIDE>
+__device__ __forceinline__ void row_sum2(float& a, float& b, bool two, float (*s)[kMaxWaves][2], int& turn) {
+  a = wave_sum(a);
+  if (two) b = wave_sum(b);
+  if (WIDE) {
+    const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) {
-      s[turn][wave][0] = a;
-      s[turn][wave][1] = b;
+      s[turn][threadIdx.x >> 6][0] = a;
+      s[turn][threadIdx.x >> 6][1] = b;
     }
     __syncthreads();
-    a = (s[turn][0][0] + s[turn][1][0]) + (s[turn][2][0] + s[turn][3][0]);
-    b = (s[turn][0][1] + s[turn][1][1]) + (s[turn][2][1] + s[turn][3][1]);
+    a = s[turn][0][0];
+    b = s[turn][0][1];
+    for (int i = 1; i < waves; ++i) {
+      a += s[turn][i][0];
+      b += s[turn][i][1];
+    }
     turn ^= 1;
   }
 }
 
-// Forward: a row's threads walk rows `step` apart, the weights in registers.
-template <bool XF32, bool YF32, int TPR, int NV>
-__global__ __launch_bounds__(kBlock) void norm_fwd_kernel(const NormFwdArgs a) {
-  __shared__ float s[2][4][2];
-  const int t = threadIdx.x % TPR;
-  const int per = kBlock / TPR;
+// Forward: a row's threads (a wave, or with WIDE the block) walk rows `step`
+// apart, the weights in registers, the next row's loads in flight while the
+// present one is worked on.
+template <bool XF32, bool YF32, bool WF32, int NV, bool WIDE>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(const NormFwdArgs a) {
+  constexpr int G = XF32 ? 4 : 8, NG = 8 * NV / G;
+  __shared__ float s[2][kMaxWaves][2];
+  const int threads = WIDE ? blockDim.x : 64;
+  const int t = WIDE ? threadIdx.x : threadIdx.x & 63;
+  const int per = WIDE ? 1 : blockDim.x >> 6;
   const int64_t step = (int64_t)gridDim.x * per;
   const int H = a.H;
   const float inv = 1.0f / (float)H;
   int turn = 0;
-  float w[NV][8], b[NV][8];
-  load_weights<TPR, NV>(a.w, a.w_f32, 1.0f, H, t, w);
-  load_weights<TPR, NV>(a.b, a.w_f32, 0.0f, H, t, b);
-  for (int64_t row = (int64_t)blockIdx.x * per + threadIdx.x / TPR; row < a.N; row += step) {
-    float x[NV][8];
-    load_row<XF32, TPR, NV>(static_cast<const char*>(a.x) + row * H * (XF32 ? 4 : 2), H, t, x);
-    float mu = 0.0f, z = 0.0f;
+  Part<WF32, G, NG> w, b;
+  if (a.w != nullptr) w.load(a.w, 0, H, t, threads); else w.fill(1.0f);
+  if (a.b != nullptr) b.load(a.b, 0, H, t, threads); else b.fill(0.0f);
+  int64_t row = (int64_t)blockIdx.x * per + (WIDE ? 0 : threadIdx.x >> 6);
+  Part<XF32, G, NG> next;
+  if (row < a.N) next.load(a.x, row, H, t, threads);
+  for (; row < a.N; row += step) {
+    float x[NG][G];
+    bool in[NG][G];   // past the row's end nothing counts
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        in[i][k] = G * (i * threads + t) + k < H;
+        x[i][k] = in[i][k] ? next.g[i].at(k) : 0.0f;
+      }
+    if (row + step < a.N) next.load(a.x, row + step, H, t, threads);
+    float mu = 0.0f, none = 0.0f;
     if (!a.rms) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mu += x[v][k];
-      row_sum2<TPR>(mu, z, s, turn);
+        for (int k = 0; k < G; ++k) mu += x[i][k];
+      row_sum2<WIDE>(mu, none, false, s, turn);
       mu *= inv;
     }
     float q = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = x[v][k] - mu;
-        const bool in = 8 * (v * TPR + t) + k < H;   // padding is not part of the variance
-        q = in ? fmaf(d, d, q) : q;
+      for (int k = 0; k < G; ++k) {
+        x[i][k] -= mu;
+        q = in[i][k] ? fmaf(x[i][k], x[i][k], q) : q;
       }
-    row_sum2<TPR>(q, z, s, turn);
+    row_sum2<WIDE>(q, none, false, s, turn);
     const float r = 1.0f / sqrtf(fmaf(q, inv, a.eps));
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[v][k] = fmaf((x[v][k] - mu) * r, w[v][k], b[v][k]);
-    store_row<YF32, TPR, NV>(static_cast<char*>(a.y) + row * H * (YF32 ? 4 : 2), H, t, x);
+      for (int k = 0; k < G; ++k) x[i][k] = fmaf(x[i][k] * r, w.g[i].at(k), b.g[i].at(k));
+    store_part<YF32, G, NG>(a.y, row, H, t, threads, x);
     if (t == 0) {
       if (a.mean != nullptr && !a.rms) a.mean[row] = mu;
       if (a.rstd != nullptr) a.rstd[row] = r;
@@ -221,173 +227,231 @@ __global__ __launch_bounds__(kBlock) void norm_fwd_kernel(const NormFwdArgs a) {
   }
 }
 
-// Backward: a row's threads walk rows step apart and keep their columns' sums
+// Backward: rows are walked likewise and each thread keeps its columns' sums
 // of dw and db in registers; at the end the rows of a block are added through
 // LDS in order and the block writes one partial row of each ([blocks][2][H]),
 // which norm_reduce_kernel sums in block order. A zero in dy contributes a
 // zero whatever x, the statistics and w hold there (mul0), so a masked token,
 // whose dy row is 0, adds nothing and gets dx = 0 even where its x is NaN.
-template <bool XF32, bool YF32, int TPR, int NV>
-__global__ __launch_bounds__(kBlock) void norm_bwd_kernel(const NormBwdArgs a) {
-  extern __shared__ float lds[];   // [2][H]: the block's dw and db (TPR < 256)
-  __shared__ float s[2][4][2];
-  const int t = threadIdx.x % TPR;
-  const int per = kBlock / TPR;
-  const int slot = threadIdx.x / TPR;
+template <bool XF32, bool YF32, bool WF32, int NV, bool WIDE>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int G = XF32 ? 4 : 8, NG = 8 * NV / G;
+  extern __shared__ float lds[];   // [2][H]: the block's dw and db (not WIDE)
+  __shared__ float s[2][kMaxWaves][2];
+  const int threads = WIDE ? blockDim.x : 64;
+  const int t = WIDE ? threadIdx.x : threadIdx.x & 63;
+  const int per = WIDE ? 1 : blockDim.x >> 6;
+  const int slot = WIDE ? 0 : threadIdx.x >> 6;
   const int64_t step = (int64_t)gridDim.x * per;
   const int H = a.H;
   const float inv = 1.0f / (float)H;
   int turn = 0;
-  float dw[NV][8], db[NV][8];
+  constexpr bool ahead = NV <= 2;   // with 32 elements a thread, weights and next row held over would spill
+  Part<WF32, G, NG> w;
+  auto weights = [&] {
+    if (a.w != nullptr) w.load(a.w, 0, H, t, threads); else w.fill(1.0f);
+  };
+  if (ahead) weights();
+  float dw[NG][G], db[NG][G];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int i = 0; i < NG; ++i)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[v][k] = db[v][k] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * per + slot; row < a.N; row += step) {
-    float x[NV][8], g[NV][8], w[NV][8];
-    load_row<XF32, TPR, NV>(static_cast<const char*>(a.x) + row * H * (XF32 ? 4 : 2), H, t, x);
-    load_row<YF32, TPR, NV>(static_cast<const char*>(a.dy) + row * H * (YF32 ? 4 : 2), H, t, g);
-    load_weights<TPR, NV>(a.w, a.w_f32, 1.0f, H, t, w);   // reread: registers are dw's and db's
-    const float mu = a.rms ? 0.0f : a.mean[row];
-    const float r = a.rstd[row];
+    for (int k = 0; k < G; ++k) dw[i][k] = db[i][k] = 0.0f;
+  int64_t row = (int64_t)blockIdx.x * per + slot;
+  Part<XF32, G, NG> nx;
+  Part<YF32, G, NG> ng;
+  float n_mu = 0.0f, n_r = 0.0f;
+  auto fetch = [&](int64_t at) {
+    nx.load(a.x, at, H, t, threads);
+    ng.load(a.dy, at, H, t, threads);
+    if (!a.rms) n_mu = a.mean[at];
+    n_r = a.rstd[at];
+  };
+  if (ahead && row < a.N) fetch(row);
+  for (; row < a.N; row += step) {
+    if (!ahead) {
+      fetch(row);
+      weights();
+    }
+    float x[NG][G], g[NG][G];
+    const float mu = n_mu, r = n_r;
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const bool in = G * (i * threads + t) + k < H;
+        x[i][k] = nx.g[i].at(k);
+        g[i][k] = in ? ng.g[i].at(k) : 0.0f;
+      }
+    if (ahead && row + step < a.N) fetch(row + step);
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float xh = (x[v][k] - mu) * r;
-        dw[v][k] += mul0(g[v][k], xh);
-        db[v][k] += g[v][k];
-        const float gw = mul0(g[v][k], w[v][k]);
+      for (int k = 0; k < G; ++k) {
+        const float xh = (x[i][k] - mu) * r;
+        dw[i][k] += mul0(g[i][k], xh);
+        db[i][k] += g[i][k];
+        const float gw = mul0(g[i][k], w.g[i].at(k));
         c1 += mul0(gw, xh);
         c2 += gw;
-        x[v][k] = xh;
-        g[v][k] = gw;
+        x[i][k] = xh;
+        g[i][k] = gw;
       }
-    row_sum2<TPR>(c1, c2, s, turn);
+    row_sum2<WIDE>(c1, c2, !a.rms, s, turn);
     c1 *= inv;
     c2 = a.rms ? 0.0f : c2 * inv;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[v][k] = mul0(r, (g[v][k] - c2) - mul0(x[v][k], c1));
-    store_row<XF32, TPR, NV>(static_cast<char*>(a.dx) + row * H * (XF32 ? 4 : 2), H, t, x);
+      for (int k = 0; k < G; ++k) x[i][k] = mul0(r, (g[i][k] - c2) - mul0(x[i][k], c1));
+    store_part<XF32, G, NG>(a.dx, row, H, t, threads, x);
   }
   if (a.part == nullptr) return;
   float* out = a.part + (int64_t)blockIdx.x * 2 * H;
-  if (TPR < kBlock) {
-    for (int i = 0; i < per; ++i) {
-      if (slot == i) {
+  if (WIDE) {
+    store_part<true, G, NG>(out, 0, H, t, threads, dw);
+    store_part<true, G, NG>(out + H, 0, H, t, threads, db);
+    return;
+  }
+  for (int i0 = 0; i0 < per; ++i0) {
+    if (slot == i0) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+      for (int i = 0; i < NG; ++i)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int j = 8 * (v * TPR + t) + k;
-            if (j >= H) continue;
-            if (i > 0) {
-              dw[v][k] += lds[j];
-              db[v][k] += lds[H + j];
-            }
-            if (i < per - 1) {
-              lds[j] = dw[v][k];
-              lds[H + j] = db[v][k];
-            } else {
-              out[j] = dw[v][k];
-              out[H + j] = db[v][k];
-            }
+        for (int k = 0; k < G; ++k) {
+          const int j = G * (i * threads + t) + k;
+          if (j >= H) continue;
+          if (i0 > 0) {
+            dw[i][k] += lds[j];
+            db[i][k] += lds[H + j];
           }
-      }
-      __syncthreads();
+          if (i0 < per - 1) {
+            lds[j] = dw[i][k];
+            lds[H + j] = db[i][k];
+          } else {
+            out[j] = dw[i][k];
+            out[H + j] = db[i][k];
+          }
+        }
     }
-  } else {
-    store_row<true, TPR, NV>(out, H, t, dw);
-    store_row<true, TPR, NV>(out + H, H, t, db);
+    __syncthreads();
   }
 }
 
-// Sums the blocks' partial rows, 64 columns per workgroup, 16 waves each a
-// sixteenth of the rows, joined in order.
-constexpr int kRedWaves = 16;
-__global__ __launch_bounds__(64 * kRedWaves) void norm_reduce_kernel(const NormReduceArgs a) {
-  __shared__ float s[kRedWaves][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int H = a.H;
-  const int j = blockIdx.x * 64 + lane;   // column of [dw | db]
-  const int lo = (int)((int64_t)wave * a.blocks / kRedWaves);
-  const int hi = (int)((int64_t)(wave + 1) * a.blocks / kRedWaves);
-  float v = 0.0f;
-  if (j < 2 * H)
-    for (int i = lo; i < hi; ++i) v += a.part[(int64_t)i * 2 * H + j];
-  s[wave][lane] = v;
-  __syncthreads();
-  if (wave != 0 || j >= 2 * H) return;
-  v = s[0][lane];
+// Sums the blocks' partial rows [blocks][2 H]: a workgroup takes 32 columns
+// (128 bytes of each row), its 1024 threads as 128 groups of 8 that sum every
+// 128th row four columns at a time; the groups' sums are then added in order,
+// 8 at a time, and those 16 in order.
+constexpr int kRedThreads = 1024, kRedCols = 32, kRedGroups = kRedThreads / (kRedCols / 4);
+__global__ __launch_bounds__(kRedThreads) void norm_reduce_kernel(const NormReduceArgs a) {
+  __shared__ float s[kRedGroups][kRedCols];
+  __shared__ float s2[kRedGroups / 8][kRedCols];
+  const int n = 2 * a.H;
+  const int group = threadIdx.x / (kRedCols / 4);
+  const int c4 = 4 * (threadIdx.x % (kRedCols / 4));
+  const int j = blockIdx.x * kRedCols + c4;   // column of [dw | db]
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (j + 3 < n) {
+#pragma unroll 4
+    for (int i = group; i < a.blocks; i += kRedGroups) {
+      const Raw<4> p = *reinterpret_cast<const Raw<4>*>(a.part + (int64_t)i * n + j);
 #pragma unroll
-  for (int i = 1; i < kRedWaves; ++i) v += s[i][lane];
-  void* out = j < H ? a.dw : a.db;
-  const int c = j < H ? j : j - H;
+      for (int k = 0; k < 4; ++k) v[k] += __uint_as_float(p.w[k]);
+    }
+  } else {
+    for (int i = group; i < a.blocks; i += kRedGroups)
+      for (int k = 0; k < 4; ++k)
+        if (j + k < n) v[k] += a.part[(int64_t)i * n + j + k];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s[group][c4 + k] = v[k];
+  __syncthreads();
+  const int col = threadIdx.x % kRedCols, part = threadIdx.x / kRedCols;
+  if (part < kRedGroups / 8) {
+    float u = s[8 * part][col];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) u += s[8 * part + i][col];
+    s2[part][col] = u;
+  }
+  __syncthreads();
+  const int at = blockIdx.x * kRedCols + col;
+  if (part != 0 || at >= n) return;
+  float u = s2[0][col];
+#pragma unroll
+  for (int i = 1; i < kRedGroups / 8; ++i) u += s2[i][col];
+  void* out = at < a.H ? a.dw : a.db;
+  const int c = at < a.H ? at : at - a.H;
   if (out == nullptr) return;
   if (a.g_f32) {
     float* o = static_cast<float*>(out) + c;
-    *o = a.accumulate ? *o + v : v;
+    *o = a.accumulate ? *o + u : u;
   } else {
     uint16_t* o = static_cast<uint16_t*>(out) + c;
-    *o = narrow(a.accumulate ? widen(*o) + v : v);
+    *o = narrow(a.accumulate ? widen(*o) + u : u);
   }
 }
 
-// Threads of a row and chunks of each: up to 2560 elements a wave per row
-// (no barrier; up to 5 chunks, so the backward's 32 values per chunk and lane
-// leave two waves per SIMD), above that a block per row.
+// How rows of H are laid over threads: a wave per row up to 1024 elements
+// (no barrier), above that a block per row with as few elements a thread as
+// 512 threads allow.
+struct Shape {
+  int nv;
+  bool wide;
+  int block, per;   // threads per block, rows per block
+};
+Shape shape_of(int64_t H) {
+  if (H <= 1024) return {H <= 512 ? 1 : 2, false, 256, 4};
+  const int nv = H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
+  return {nv, true, (int)((H + 8 * nv * 64 - 1) / (8 * nv * 64)) * 64, 1};
+}
+
 template <class F>
-hipError_t with_shape(int H, F f) {
-#define LMH_NORM_CASE(tpr, nv) \
-  if (H <= 8 * (tpr) * (nv)) return f(std::integral_constant<int, tpr>{}, std::integral_constant<int, nv>{});
-  LMH_NORM_CASE(64, 1)
-  LMH_NORM_CASE(64, 2)
-  LMH_NORM_CASE(64, 3)
-  LMH_NORM_CASE(64, 4)
-  LMH_NORM_CASE(64, 5)
-  LMH_NORM_CASE(256, 2)
-  LMH_NORM_CASE(256, 3)
-  LMH_NORM_CASE(256, 4)
-  LMH_NORM_CASE(256, 6)
-  LMH_NORM_CASE(256, 8)
-#undef LMH_NORM_CASE
-  return hipErrorInvalidValue;
+void with_shape(const Shape& p, F f) {
+  std::true_type yes;
+  std::false_type no;
+  if (!p.wide) {
+    if (p.nv == 1) f(std::integral_constant<int, 1>{}, no);
+    else f(std::integral_constant<int, 2>{}, no);
+  } else if (p.nv == 1) f(std::integral_constant<int, 1>{}, yes);
+  else if (p.nv == 2) f(std::integral_constant<int, 2>{}, yes);
+  else f(std::integral_constant<int, 4>{}, yes);
 }
 
-template <bool XF32, bool YF32>
-hipError_t fwd_typed(const NormFwdArgs& a, hipStream_t stream) {
-  return with_shape(a.H, [&](auto tpr, auto nv) {
-    const int per = kBlock / tpr();
-    const int64_t blocks = std::min<int64_t>((a.N + per - 1) / per, 2048);
-    hipLaunchKernelGGL((norm_fwd_kernel<XF32, YF32, tpr(), nv()>), dim3((unsigned)blocks), dim3(kBlock), 0, stream, a);
-    return hipGetLastError();
-  });
+// The types of x, y and the weights (float32 y comes with float32 x only).
+template <class F>
+void with_types(bool x, bool y, bool w, F f) {
+  std::true_type yes;
+  std::false_type no;
+  if (x && y) w ? f(yes, yes, yes) : f(yes, yes, no);
+  else if (x) w ? f(yes, no, yes) : f(yes, no, no);
+  else w ? f(no, no, yes) : f(no, no, no);
 }
 
-template <bool XF32, bool YF32>
-hipError_t bwd_typed(const NormBwdArgs& a, int blocks, hipStream_t stream) {
-  return with_shape(a.H, [&](auto tpr, auto nv) {
-    const size_t lds = tpr() < kBlock ? (size_t)2 * a.H * 4 : 0;
-    hipLaunchKernelGGL((norm_bwd_kernel<XF32, YF32, tpr(), nv()>), dim3(blocks), dim3(kBlock), lds, stream, a);
-    return hipGetLastError();
-  });
-}
+constexpr int kWavesPerCU = 32;
 
 }  // namespace
 
+// A row per wave or block while that leaves at most a workgroup per CU, then
+// 4 rows each up to 16 waves per CU.
 int norm_bwd_blocks(int64_t N, int64_t H) {
-  const int64_t per = H <= 2560 ? 4 : 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>((N + 4 * per - 1) / (4 * per), 1024));
+  const Shape p = shape_of(H);
+  const int64_t full = kNumCUs * std::max(1, 16 * 64 / p.block);
+  const int64_t rows = (N + p.per - 1) / p.per;
+  return (int)std::max<int64_t>(1, std::min(rows, std::max<int64_t>(kNumCUs, std::min((rows + 3) / 4, full))));
 }
 
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
+  const Shape p = shape_of(a.H);
+  const int64_t blocks = std::min<int64_t>((a.N + p.per - 1) / p.per, kNumCUs * (kWavesPerCU * 64 / p.block));
   trace_begin(stream);
-  const hipError_t e = a.x_f32 ? (a.y_f32 ? fwd_typed<true, true>(a, stream) : fwd_typed<true, false>(a, stream))
-                               : fwd_typed<false, false>(a, stream);
+  with_types(a.x_f32, a.y_f32, a.w_f32, [&](auto x, auto y, auto w) {
+    with_shape(p, [&](auto nv, auto wide) {
+      hipLaunchKernelGGL((norm_fwd_kernel<x(), y(), w(), nv(), wide()>), dim3((unsigned)blocks), dim3(p.block), 0,
+                         stream, a);
+    });
+  });
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const double n = (double)a.N * a.H;
   trace_end(kNormFwd, stream, 8.0 * n, n * ((a.x_f32 ? 4 : 2) + (a.y_f32 ? 4 : 2)) + 8.0 * a.N);
@@ -395,19 +459,25 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int blocks, hipStream_t stream) {
-  const double n = (double)a.N * a.H;
+  const Shape p = shape_of(a.H);
+  const size_t lds = p.wide ? 0 : (size_t)2 * a.H * 4;
   trace_begin(stream);
-  const hipError_t e = a.x_f32 ? (a.y_f32 ? bwd_typed<true, true>(a, blocks, stream)
-                                          : bwd_typed<true, false>(a, blocks, stream))
-                               : bwd_typed<false, false>(a, blocks, stream);
+  with_types(a.x_f32, a.y_f32, a.w_f32, [&](auto x, auto y, auto w) {
+    with_shape(p, [&](auto nv, auto wide) {
+      hipLaunchKernelGGL((norm_bwd_kernel<x(), y(), w(), nv(), wide()>), dim3(blocks), dim3(p.block), lds, stream, a);
+    });
+  });
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const double n = (double)a.N * a.H;
   trace_end(kNormBwd, stream, 14.0 * n, n * (2 * (a.x_f32 ? 4 : 2) + (a.y_f32 ? 4 : 2)) + 8.0 * a.N);
   return hipSuccess;
 }
 
 hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t stream) {
   trace_begin(stream);
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((2 * a.H + 63) / 64)), dim3(64 * kRedWaves), 0, stream, a);
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((2 * a.H + kRedCols - 1) / kRedCols)), dim3(kRedThreads), 0,
+                     stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kNormReduce, stream, 0.0, 8.0 * a.blocks * (double)a.H + 8.0 * a.H);
