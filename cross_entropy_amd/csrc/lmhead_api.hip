@@ -36,12 +36,12 @@ namespace lmh {
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-FwdPlan plan_forward(int64_t N, int64_t H, int64_t V) {
+FwdPlan plan_forward(int64_t N, int64_t H, int64_t V, int most_splits) {
   (void)H;
   FwdPlan p;
   p.n_tt = (int)lmh::ceil_div(N, kTileRows);
   p.n_vt = (int)lmh::ceil_div(V, kTileRows);
-  const int s_max = (int)std::min<int64_t>(p.n_vt, 128);
+  const int s_max = (int)std::min<int64_t>(p.n_vt, most_splits);
   // makespan in tile-steps: rounds of resident workgroups x tiles per split
   auto cost = [&](int S) {
     return ceil_div((int64_t)p.n_tt * S, kNumCUs) * ceil_div(p.n_vt, S);
@@ -391,12 +391,59 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
 namespace {
 
 // The distillation's part of a backward: its per-token preparation, launched
-// before everything else, and the special entries that overwrite each
-// cotangent block once it is formed. `bytes` is the whole workspace it needs.
+// before everything else, the special entries that overwrite each cotangent
+// block once it is formed, and (splits > 1) its launches with split dh tiles.
+// `bytes` is the whole workspace it needs.
 struct DistillHook {
   lmh::DistillPrepArgs prep;
+  int splits, k_split;
+  float* part;
   size_t bytes;
 };
+
+// One launch of the distillation's backward (gradients of one block if `grads`,
+// the next block's cotangent if `forms`) and what follows it.
+hipError_t launch_distill_block(const DistillHook& h, const lmh::BwdStep& st, bool bf16, bool grads, bool forms,
+                                const lmh::BwdPlan& p, hipStream_t s) {
+  lmh::DistillPostArgs a{};
+  if (forms) {
+    a.ent_id = h.prep.ent_id;
+    a.ent_val = h.prep.ent_val;
+    a.K1 = h.prep.K + 1;
+    a.dz = st.z_dz;
+    a.ld_dz = p.ld_dz;
+    a.t0 = st.z_t0;
+    a.Ct = st.z_Ct;
+    a.v0 = st.z_v0;
+    a.Vb = st.z_Vb;
+  }
+  hipError_t e;
+  if (h.splits > 1) {
+    // the block may be shorter than the plan's: as many splits as it fills
+    const int splits = grads ? (int)lmh::ceil_div(lmh::round_up(st.g_Vb, 64), h.k_split) : 1;
+    e = lmh::launch_distill_step({st, splits, h.k_split, h.part}, bf16, s);
+    if (grads) {
+      a.part = h.part;
+      a.splits = splits;
+      a.g_t0 = st.g_t0;
+      a.g_Ct = st.g_Ct;
+      a.H = st.H;
+      a.V = st.Vtot;
+      a.tgt = st.targets;
+      if (bf16) {
+        a.o = st.o_dh;
+        a.dead_zero = st.dh_dead_zero;
+      } else {
+        a.o.src_kind = st.g_acc_dh ? lmh::kSrcF32 : lmh::kSrcNone;
+        a.o.src = a.o.dst = st.dh + (int64_t)st.g_t0 * st.H;
+        a.dead_zero = !st.g_acc_dh;
+      }
+    }
+  } else {
+    e = bf16 ? lmh::launch_bwd_step_bf16(st, s) : lmh::launch_bwd_step(st, s);
+  }
+  return e == hipSuccess ? lmh::launch_distill_post(a, s) : e;
+}
 
 // The backward of W's rows [voff, voff + V) of a vocabulary of Vtot ids.
 // dh / dW are float32 (bf16_out false) or bf16 gradients (bf16_out true).
@@ -548,11 +595,11 @@ int bwd_impl(const char* who, const uint16_t* hidden, const uint16_t* W, const i
       st.z_dz = nullptr;
       st.z_ntt = st.z_nvt = 0;
     }
-    hipError_t e = bf16_out ? lmh::launch_bwd_step_bf16(st, s) : lmh::launch_bwd_step(st, s);
-    if (e == hipSuccess && distill && j < nb) {
-      const lmh::DistillPrepArgs& d = distill->prep;
-      e = lmh::launch_distill_scatter({d.ent_id, d.ent_val, d.K + 1, st.z_dz, p.ld_dz, st.z_t0, st.z_Ct, st.z_v0,
-                                       st.z_Vb}, s);
+    hipError_t e;
+    if (distill == nullptr) {
+      e = bf16_out ? lmh::launch_bwd_step_bf16(st, s) : lmh::launch_bwd_step(st, s);
+    } else {
+      e = launch_distill_block(*distill, st, bf16_out, j >= 1, j < nb, p, s);
     }
     if (e != hipSuccess) return fail(LMH_ERR_HIP, "%s: launch failed: %s", who, hipGetErrorString(e));
   }
@@ -635,16 +682,50 @@ int check_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size
 
 // Where the distillation's arrays lie behind the head's own workspace.
 struct DistillPlan {
-  size_t off_rec = 0, fwd_bytes = 0;                                   // forward: merged records [N][4]
-  size_t off_tgt = 0, off_ga = 0, off_id = 0, off_val = 0, bytes = 0;  // backward
+  size_t fwd_bytes = 0;                                      // the forward: its split records alone
+  size_t off_tgt = 0, off_ga = 0, off_id = 0, off_val = 0;   // the backward
+  size_t off_part = 0, bytes = 0;                            // its dh splits; its total
+  int splits = 1, k_split = 0;
 };
+
+// Splits of the dh tiles over the block's vocabulary. A launch holds the dh
+// tiles (K = Vb), the dW tiles (K = Ct) and the next block's cotangent tiles
+// (K = H); in slices of 64 of K, a CU works off one in about 1 us, so the launch
+// takes all slices over the CUs, but no less than one dh tile's: a small N x H
+// has few dh tiles, each of which walks the whole vocabulary block alone (64
+// tokens, H 2560, V 151936: 10 tiles of 2374 slices, 3.7 ms of 0.3 ms of
+// memory traffic). k splits shorten that walk k times and cost k float32
+// partials of [Ct, H], written and read once at about 4 TB/s.
+int dh_splits(const lmh::BwdPlan& p, int64_t H) {
+  const double T = lmh::kTileRows;
+  const double tt = (double)lmh::ceil_div(p.Ct, lmh::kTileRows), vt = (double)lmh::ceil_div(p.Vb, lmh::kTileRows);
+  const double ht = (double)lmh::ceil_div(H, lmh::kTileRows);
+  const double all = (tt * ht * p.Vb + vt * ht * p.Ct + tt * vt * H) / 64.0 / lmh::kNumCUs;
+  const double chain = p.Vb / 64.0, part = tt * T * H * 8.0 / 4.0e6;   // us
+  int best = 1;
+  double best_t = std::max(all, chain);
+  for (int k = 2; k <= 64 && chain / k >= 8.0; ++k) {
+    const double t = std::max(all, chain / k) + k * part;
+    if (t < best_t) {
+      best_t = t;
+      best = k;
+    }
+  }
+  return best;
+}
+
+// Up to a split per CU, since their records are merged by a wave per token
+// here: with one token tile (N <= 256), 128 splits of 594 vocabulary tiles
+// would take 5 tiles' time on half the CUs, 198 take 3.
+lmh::FwdPlan plan_distill_forward(int64_t N, int64_t H, int64_t V) {
+  return lmh::plan_forward(N, H, V, lmh::kNumCUs);
+}
 
 DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size, int kind) {
   DistillPlan d;
   const int64_t n = std::max<int64_t>(N, 1);
   auto room = [](int64_t bytes) { return (size_t)lmh::round_up(bytes, 256); };
-  d.off_rec = lmh::plan_forward(N, H, V).bytes;
-  d.fwd_bytes = d.off_rec + room(n * 16);
+  d.fwd_bytes = plan_distill_forward(N, H, V).bytes;
   if (kind == LMH_WS_FWD) {
     d.bytes = d.fwd_bytes;
     return d;
@@ -654,7 +735,11 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
   d.off_ga = d.off_tgt + room(n * 4);
   d.off_id = d.off_ga + room(n * 4);
   d.off_val = d.off_id + room(n * (K + 1) * 4);
-  d.bytes = d.off_val + room(n * (K + 1) * 2);
+  d.off_part = d.off_val + room(n * (K + 1) * 2);
+  d.splits = dh_splits(p, H);
+  d.k_split = (int)lmh::round_up(lmh::ceil_div(p.Vb, d.splits), 64);
+  d.splits = (int)lmh::ceil_div(lmh::round_up(p.Vb, 64), d.k_split);
+  d.bytes = d.off_part + (d.splits > 1 ? room((int64_t)d.splits * p.Ct * H * 4) : 0);
   return d;
 }
 
@@ -698,20 +783,19 @@ int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const in
   if (workspace_bytes < d.bytes)
     return fail(LMH_ERR_WORKSPACE, "distill_fwd: workspace of %zu bytes, %zu needed", workspace_bytes, d.bytes);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* rec = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.off_rec);
-  const lmh::FwdPlan p = lmh::plan_forward(N, H, V);
+  const lmh::FwdPlan p = plan_distill_forward(N, H, V);
   const float sc = temper_scale(temperature);
   // without hard targets the tile kernel still reads N ids to pick a logit by:
   // any will do, the pick is not used
   lmh::FwdArgs a{hidden, W, targets != nullptr ? targets : ids, N, H, V, p.S, p.n_tt, p.n_vt, 0, V, sc,
-                 inv_temperature(temperature), workspace, p.part_ld, nullptr, nullptr, nullptr, rec};
-  hipError_t e = lmh::launch_fwd(a, s);
+                 inv_temperature(temperature), workspace, p.part_ld, nullptr, nullptr, nullptr, nullptr};
+  hipError_t e = lmh::launch_fwd_stats(a, s);
   const double back = 1.0 / ((double)sc * (double)temperature);
   const float back_hi = (float)back;
   if (e == hipSuccess)
     e = lmh::launch_distill_top({hidden, W, targets, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
-                                 (int)H, (int)V, (int)K, temperature, back_hi, (float)(back - (double)back_hi), rec,
-                                 kl, logp, lse, logp_top}, s);
+                                 (int)H, (int)V, (int)K, temperature, back_hi, (float)(back - (double)back_hi),
+                                 workspace, p.part_ld, p.S, kl, logp, lse, logp_top}, s);
   if (e != hipSuccess) return fail(LMH_ERR_HIP, "distill_fwd: launch failed: %s", hipGetErrorString(e));
   return ok();
 }
@@ -751,6 +835,9 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
     hook.prep = {g_logp != nullptr ? targets : nullptr, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
                  (int)V, (int)K, temperature, inv_temperature(temperature), logp, logp_top, g_kl, g_logp, w_tgt, w_ga,
                  reinterpret_cast<int32_t*>(ws + d.off_id), reinterpret_cast<uint16_t*>(ws + d.off_val)};
+    hook.splits = d.splits;
+    hook.k_split = d.k_split;
+    hook.part = reinterpret_cast<float*>(ws + d.off_part);
     hook.bytes = d.bytes;
     tgt = w_tgt;
     ga = w_ga;

@@ -23,20 +23,14 @@
 #include <algorithm>
 
 #include "lmhead_internal.h"
+#include "lmhead_tile.h"
 
 namespace lmh {
 namespace {
 
-constexpr float kLn2 = 0.69314718055994531f;
-
-__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-
 __device__ __forceinline__ float teacher_at(const void* t, bool f32, int64_t i) {
-  return f32 ? static_cast<const float*>(t)[i] : widen(static_cast<const uint16_t*>(t)[i]);
+  return f32 ? static_cast<const float*>(t)[i] : widen_bf16(static_cast<const uint16_t*>(t)[i]);
 }
-
-// NaN-propagating max
-__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -127,16 +121,27 @@ __device__ __forceinline__ void distill_dots(const DistillTopArgs& a, int64_t to
   }
 }
 
-// The outputs of one token from its dot products and its log-sum-exp record.
+// The outputs of one token from its dot products and the forward's records.
 __device__ __forceinline__ void distill_token(const DistillTopArgs& a, int64_t tok, int lane, const float* s_z) {
   const int K = a.K, V = a.V;
   const int32_t* ids = a.ids + tok * K;
-  const float4 rec = reinterpret_cast<const float4*>(a.rec)[tok];   // (m2, s1, s2, zt)
-  // The record is in base 2 of logits scaled by the float32 sc ~ log2(e) / T:
+  // the forward's split records: a lane's in split order, then across lanes
+  // by halves (the lower lane's first), so the order is fixed
+  Stats rec{kNegBig, 0.0f, 0.0f, 0.0f};
+  for (int s = lane; s < a.S; s += 64) {
+    const float4 q = reinterpret_cast<const float4*>(a.part)[s * a.part_ld + tok];
+    rec = merge_stats(rec, Stats{q.x, q.y, q.z, q.w});
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const Stats o{__shfl_xor(rec.m2, x), __shfl_xor(rec.s1, x), __shfl_xor(rec.s2, x), __shfl_xor(rec.zt, x)};
+    rec = (lane & x) == 0 ? merge_stats(rec, o) : merge_stats(o, rec);
+  }
+  // The records are in base 2 of logits scaled by the float32 sc ~ log2(e) / T:
   // back = 1 / (sc T) in two words takes the max back to natural units of z / T
   // without sc's rounding, which a loss of the size of the max's last digits
   // would show. A +inf logit (and no NaN) leaves m = +inf and s1 = NaN.
-  const float lse = rec.x == INFINITY ? INFINITY : fmaf(rec.x, a.back_hi, fmaf(rec.x, a.back_lo, kLn2 * log2f(rec.y)));
+  const float lse = rec.m2 == INFINITY ? INFINITY : fmaf(rec.m2, a.back_hi, fmaf(rec.m2, a.back_lo, kLn2 * log2f(rec.s1)));
   auto live_of = [&](int k) { return ids[k] >= 0 && ids[k] < V; };
   auto t_of = [&](int k) { return live_of(k) ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY; };
   const float shift = teacher_shift(a.teacher_lse, tok, K, t_of);
@@ -158,7 +163,7 @@ __device__ __forceinline__ void distill_token(const DistillTopArgs& a, int64_t t
     const bool hard = t >= 0 && t < V;
     a.kl[tok] = kl;
     a.lse[tok] = (hard || some) ? lse : 0.0f;
-    if (a.logp != nullptr) a.logp[tok] = hard ? rec.w / a.T - lse : 0.0f;
+    if (a.logp != nullptr) a.logp[tok] = hard ? rec.zt / a.T - lse : 0.0f;
   }
 }
 
@@ -247,15 +252,107 @@ __global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs
   }
 }
 
-// Overwrites the special entries of tokens [t0, t0 + Ct) and vocabulary rows
-// [v0, v0 + Vb) in their cotangent block, after the launch that formed it.
-__global__ __launch_bounds__(256) void distill_scatter_kernel(const DistillScatterArgs a) {
-  const int64_t n = (int64_t)a.Ct * a.K1;
+// dh tile of one split of the block's vocabulary: the head's dh tile over K =
+// [k0, k0 + k_split) of it, written to its own float32 partial [Ct][H].
+__device__ __forceinline__ void dh_split_tile(const DistillStep& d, int vid, char* lds) {
+  const BwdStep& s = d.step;
+  const int split = vid / s.n_dh;
+  int mt, hb;
+  raster(vid - split * s.n_dh, s.n_dh / s.n_ht, s.n_ht, 4, mt, hb);
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1;
+  const int wn = wave >> 1;
+  const int m0 = mt * kTile;
+  const int h0 = hb * kTile;
+  const int H = s.H;
+  const int k0 = split * d.k_split;
+  const int K = min(d.k_split, (s.g_Vb + kBK - 1) / kBK * kBK - k0);   // > 0: the host counts the splits
+  // negative where the block's last slice lies in another split
+  const int tail_k = s.W_tail != nullptr ? s.v_tail - s.g_v0 - k0 : -1;
+  const Operand oa{s.W + (int64_t)(s.g_v0 + k0) * H + h0, H, min(kTile, H - h0),
+                   s.W_tail != nullptr ? s.W_tail + h0 : nullptr, tail_k};
+  const Operand ob{s.g_dz + (int64_t)m0 * s.ld_dz + k0, s.ld_dz, kTile};
+  f32x4 acc[kNB][kNB];
+  Pipe pipe;
+  mma_tile<true, 64>(oa, ob, K, lds, acc, pipe, oa.base, ob.base, false);
+  write_acc_t(d.part + (int64_t)split * s.g_Ct * H, H, h0 + wm * 128, H, m0 + wn * 128, s.g_Ct, false, s.targets, s.g_t0,
+              s.Vtot, acc);
+}
+
+// One backward launch with the dh tiles split: the head's launch (each XCD an
+// eighth of the dh tiles, of the dW tiles and of the next block's cotangent
+// tiles, in this order, the last off per-XCD counters and then off the others')
+// where a few dh tiles would otherwise run the whole vocabulary in sequence
+// while the chip idles.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillStep d) {
+  __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
+  __shared__ int z_tile;
+  const BwdStep& s = d.step;
+  const int xcd = blockIdx.x & 7;
+  const int loc = blockIdx.x >> 3;
+  const int n_dh = s.n_dh * d.splits;
+  const int dw_lo = xcd * s.n_dw / 8;
+  const int dw_cnt = (xcd + 1) * s.n_dw / 8 - dw_lo;
+  const int dh_lo = xcd * n_dh / 8;
+  const int dh_cnt = (xcd + 1) * n_dh / 8 - dh_lo;
+  if (loc < dh_cnt) {
+    dh_split_tile(d, dh_lo + loc, lds);
+    return;
+  }
+  if (loc < dh_cnt + dw_cnt) {
+    dw_tile<BF16>(s, dw_lo + loc - dh_cnt, lds);
+    return;
+  }
+  const int n_z = s.z_ntt * s.z_nvt;
+  if (n_z == 0) return;
+  if (threadIdx.x == 0) z_tile = take_z_tile(s, xcd, n_z);
+  __syncthreads();
+  if (z_tile >= 0) dz_tile(s, z_tile, lds);
+}
+
+// After each launch, on what it wrote: overwrites the special entries of tokens
+// [t0, t0 + Ct) and vocabulary rows [v0, v0 + Vb) in their cotangent block,
+// and adds up the splits of a block's dh in split order (n4 float4's, o as
+// the bf16-gradient backward's writers take it).
+__global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs a) {
   const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = a.dz != nullptr ? (int64_t)a.Ct * a.K1 : 0;
+  for (int64_t i = i0; i < n; i += step) {
     const int64_t at = (int64_t)a.t0 * a.K1 + i;
-    const int v = a.ent_id[at] - a.v0;   // id -1 falls below every block
-    if (v >= 0 && v < a.Vb && a.ent_id[at] >= 0) a.dz[i / a.K1 * a.ld_dz + v] = a.ent_val[at];
+    const int id = a.ent_id[at];
+    const int v = id - a.v0;
+    if (id >= 0 && v >= 0 && v < a.Vb) a.dz[i / a.K1 * a.ld_dz + v] = a.ent_val[at];
+  }
+  if (a.part == nullptr) return;
+  const int h4 = a.H / 4;
+  const int64_t n4 = (int64_t)a.g_Ct * h4;
+  for (int64_t i = i0; i < n4; i += step) {
+    const int t = a.tgt[a.g_t0 + i / h4];
+    const bool live = t >= 0 && t < a.V;
+    if (!live && !a.dead_zero) continue;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (live) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + i;
+      v = p[0];
+      for (int k = 1; k < a.splits; ++k) v += p[k * n4];
+      if (a.o.src_kind == kSrcF32) {
+        v += static_cast<const f32x4*>(a.o.src)[i];
+      } else if (a.o.src_kind == kSrcBf16) {
+        const uint2 w = static_cast<const uint2*>(a.o.src)[i];
+        v += f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                   __uint_as_float(w.y & 0xFFFF0000u)};
+      }
+    }
+    if (a.o.dst_bf16) {
+      uint2 w;
+      w.x = pack_bf16x2(v[0], v[1]);
+      w.y = pack_bf16x2(v[2], v[3]);
+      static_cast<uint2*>(a.o.dst)[i] = w;
+    } else {
+      static_cast<f32x4*>(a.o.dst)[i] = v;
+    }
   }
 }
 
@@ -282,13 +379,42 @@ hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream) {
   return hipSuccess;
 }
 
-hipError_t launch_distill_scatter(const DistillScatterArgs& a, hipStream_t stream) {
-  const int64_t n = (int64_t)a.Ct * a.K1;
+template <bool BF16>
+static hipError_t launch_step(const DistillStep& d, hipStream_t stream) {
+  const BwdStep& st = d.step;
+  const int n_z = st.z_ntt * st.z_nvt, n_dh = st.n_dh * d.splits;
+  int per = 0;
+  for (int x = 0; x < 8; ++x)
+    per = std::max(per, ((x + 1) * st.n_dw / 8 - x * st.n_dw / 8) + ((x + 1) * n_dh / 8 - x * n_dh / 8) +
+                            ((x + 1) * n_z / 8 - x * n_z / 8) + (n_z > 0 ? kStealSlots : 0));
+  if (per == 0) return hipSuccess;
+  const int n_g = st.n_dw + st.n_dh;
+  const double H = (double)st.H;
+  const double gc = (double)st.g_Ct, gv = (double)st.g_Vb, zc = (double)st.z_Ct, zv = (double)st.z_Vb;
   trace_begin(stream);
-  hipLaunchKernelGGL(distill_scatter_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(distill_step_kernel<BF16>, dim3(8 * per), dim3(kThreads), 0, stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kDistillScatter, stream, 0.0, 4.0 * (double)n);
+  trace_end(kDistillStep, stream, n_g ? 4.0 * gc * gv * H : 0.0,
+            (n_g ? 2.0 * gc * gv + 2.0 * (gc + gv) * H + 4.0 * H * (gc * d.splits + gv) : 0.0) +
+                (n_z ? 2.0 * zc * zv + 2.0 * (zc + zv) * H + 20.0 * zc : 0.0));
+  return hipSuccess;
+}
+
+hipError_t launch_distill_step(const DistillStep& d, bool bf16, hipStream_t stream) {
+  return bf16 ? launch_step<true>(d, stream) : launch_step<false>(d, stream);
+}
+
+hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream) {
+  const int64_t n = a.dz != nullptr ? (int64_t)a.Ct * a.K1 : 0;
+  const int64_t n4 = a.part != nullptr ? (int64_t)a.g_Ct * (a.H / 4) : 0;
+  const int64_t most = std::max(n, n4);
+  if (most == 0) return hipSuccess;
+  trace_begin(stream);
+  hipLaunchKernelGGL(distill_post_kernel, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 4096)), dim3(256), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kDistillPost, stream, 0.0, 4.0 * (double)n + 16.0 * (double)n4 * (a.splits + 1));
   return hipSuccess;
 }
 

@@ -51,7 +51,7 @@ struct BwdPlan {
   size_t bytes_bf16 = 0;       // total with the accumulators
 };
 
-FwdPlan plan_forward(int64_t N, int64_t H, int64_t V);
+FwdPlan plan_forward(int64_t N, int64_t H, int64_t V, int most_splits = 128);
 BwdPlan plan_backward(int64_t N, int64_t H, int64_t V, int64_t chunk_size);
 
 struct FwdArgs {
@@ -136,7 +136,9 @@ struct DistillTopArgs {
   int H, V, K;
   float T;
   float back_hi, back_lo;     // 1 / (sc T) in two words (sc = the base-2 scale of the records)
-  const float* rec;           // merged records [N][4] of the forward
+  const void* part;           // the forward's split records [S][part_ld][4]
+  int64_t part_ld;
+  int S;
   float* kl;
   float* logp;                // or NULL
   float* lse;
@@ -165,13 +167,28 @@ struct DistillPrepArgs {
   uint16_t* ent_val;          // [N][K + 1]
 };
 
-struct DistillScatterArgs {
+// A backward launch whose dh tiles are split over the block's vocabulary.
+struct DistillStep {
+  BwdStep step;
+  int splits;        // splits of the launch's dh tiles
+  int k_split;       // vocabulary rows of each (a multiple of 64)
+  float* part;       // [splits][g_Ct][H] float32
+};
+
+// What follows each launch: the special entries into the cotangent block that
+// it formed (dz, or NULL), and the sum of its dh splits (part, or NULL).
+struct DistillPostArgs {
   const int32_t* ent_id;
   const uint16_t* ent_val;
-  int K1;                     // K + 1
+  int K1;            // K + 1
   uint16_t* dz;
   int64_t ld_dz;
   int t0, Ct, v0, Vb;
+  const float* part;
+  int splits, g_t0, g_Ct, H, V;
+  const int32_t* tgt;
+  GradOut o;
+  int dead_zero;     // masked tokens' rows are written as 0, else left as they are
 };
 
 // The norm in front of the head (lmhead_norm.hip); rows of H elements.
@@ -216,11 +233,12 @@ int norm_bwd_blocks(int64_t N, int64_t H);   // workgroups (partial rows) of the
 // Kernel ids of the tracing facility (lmhead_trace.hip).
 enum KernelId {
   kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
-  kDistillTop, kDistillPrep, kDistillScatter, kNormFwd, kNormBwd, kNormReduce, kNumKernels
+  kDistillTop, kDistillPrep, kDistillStep, kDistillPost, kNormFwd, kNormBwd, kNormReduce, kNumKernels
 };
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);
 
+hipError_t launch_fwd_stats(const FwdArgs& a, hipStream_t stream);   // the split records alone
 hipError_t launch_fwd(const FwdArgs& a, hipStream_t stream);
 // merge of P shard records [P][N] (float4 each) into logp / entropy / lse
 hipError_t launch_merge(const float* partials, int P, int64_t N, const int32_t* targets, int64_t Vtot,
@@ -235,7 +253,8 @@ hipError_t launch_transpose(const uint16_t* in, int64_t ld_in, int64_t R, int64_
                             int64_t ld_out, hipStream_t stream);
 hipError_t launch_distill_top(const DistillTopArgs& a, hipStream_t stream);
 hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream);
-hipError_t launch_distill_scatter(const DistillScatterArgs& a, hipStream_t stream);
+hipError_t launch_distill_step(const DistillStep& d, bool bf16, hipStream_t stream);
+hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int blocks, hipStream_t stream);
 hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t stream);

@@ -438,10 +438,11 @@ const char* lmhead_logps_version(void);
  *   6 bwd_step_bf16_kernel (bwd_step_kernel writing bf16 gradients)
  *   7 distill_top_kernel   (distillation: student's log-probs at the teacher's ids, loss)
  *   8 distill_prep_kernel  (distillation backward: per-token cotangents and special entries)
- *   9 distill_scatter_kernel (distillation backward: special entries into a cotangent block)
- *  10 norm_fwd_kernel
- *  11 norm_bwd_kernel
- *  12 norm_reduce_kernel   (dweight and dbias from their partial sums)
+ *   9 distill_step_kernel  (bwd_step_kernel with its dh tiles split, either gradient type)
+ *  10 distill_post_kernel  (special entries into a cotangent block, sum of dh splits)
+ *  11 norm_fwd_kernel
+ *  12 norm_bwd_kernel
+ *  13 norm_reduce_kernel   (dweight and dbias from their partial sums)
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch

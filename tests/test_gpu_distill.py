@@ -117,6 +117,9 @@ CASES = [
     (513, 256, 4097, 33, 4096, 1.0, "bf16", True, True),
     (700, 320, 3001, 64, 7, 1.0, "f32", True, False),     # several blocks, vocabulary outer for bf16
     (2100, 128, 777, 17, 64, 1.0, "bf16", False, True),   # N > V: token blocks outer
+    (70, 128, 20011, 12, 30, 1.0, "f32", True, True),     # split dh products, several vocabulary blocks, a ragged last
+    (300, 192, 9000, 5, 4096, 2.0, "bf16", False, True),  # split over two token tiles in one block
+    (1, 64, 40000, 1, 1, 1.0, "f32", False, True),
     (130, 64, 70, 100, 32, 1.0, "f32", False, True),      # more entries than the vocabulary has ids
 ]
 
@@ -236,17 +239,18 @@ def test_distill_extreme_teacher_logits():
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-def test_distill_adds_into_gradients(t):
+@pytest.mark.parametrize("V", [900, 12000])      # 12000: split dh products
+def test_distill_adds_into_gradients(t, V):
     import torch
     import cross_entropy_amd as lm
-    args = _case(12, 330, 128, 900, 7, hard=True)
+    args = _case(12, 330, 128, V, 7, hard=True)
     hd, Wd, tg, idd, td, tl = _put(*args)
     ty = torch.float32 if t == "f32" else torch.bfloat16
     g_kl, g_logp = _g(3, 330, True)
     kl, logp, lse, top = lm.distill_forward(hd, Wd, tg, idd, td, 64, tl)
     given = (hd, Wd, tg, idd, td, 64, logp, lse, top, dev(g_kl), dev(g_logp), tl)
     dh0, dW0 = lm.distill_backward(*given)
-    ph, pW = torch.randn(330, 128, device="cuda").to(ty), torch.randn(900, 128, device="cuda").to(ty)
+    ph, pW = torch.randn(330, 128, device="cuda").to(ty), torch.randn(V, 128, device="cuda").to(ty)
     dh, dW = ph.clone(), pW.clone()
     lm.distill_backward(*given, dh=dh, dW=dW, accumulate=True)
     torch.cuda.synchronize()
