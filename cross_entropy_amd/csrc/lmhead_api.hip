@@ -686,7 +686,18 @@ struct DistillPlan {
   size_t off_tgt = 0, off_ga = 0, off_id = 0, off_val = 0;   // the backward
   size_t off_part = 0, bytes = 0;                            // its dh splits; its total
   int splits = 1, k_split = 0;
+  // few tokens: their own kernels
+  bool few = false;
+  size_t off_ht = 0, off_hi = 0, off_lo = 0;
+  int dh_strips = 0, dh_rows = 0;
 };
+
+// The kernels for few tokens take N up to 64 (a vocabulary below the
+// backward's limit), and in the backward hold the cotangent of 32 or 64 tokens
+// as two bf16 words, which chunk_size has to allow.
+bool few_forward(int64_t N, int64_t V) { return N <= lmh::kFewTokens && V < (int64_t(1) << 23); }
+int64_t few_padded(int64_t N) { return N <= 32 ? 32 : 64; }
+bool few_backward(int64_t N, int64_t V, int64_t chunk_size) { return few_forward(N, V) && few_padded(N) <= chunk_size; }
 
 // Splits of the dh tiles over the block's vocabulary. A launch holds the dh
 // tiles (K = Vb), the dW tiles (K = Ct) and the next block's cotangent tiles
@@ -718,7 +729,12 @@ int dh_splits(const lmh::BwdPlan& p, int64_t H) {
 // here: with one token tile (N <= 256), 128 splits of 594 vocabulary tiles
 // would take 5 tiles' time on half the CUs, 198 take 3.
 lmh::FwdPlan plan_distill_forward(int64_t N, int64_t H, int64_t V) {
-  return lmh::plan_forward(N, H, V, lmh::kNumCUs);
+  if (!few_forward(N, V)) return lmh::plan_forward(N, H, V, lmh::kNumCUs);
+  lmh::FwdPlan p;
+  p.S = lmh::few_splits(V);
+  p.part_ld = lmh::kFewTokens;
+  p.bytes = (size_t)p.S * p.part_ld * 16;
+  return p;
 }
 
 DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chunk_size, int kind) {
@@ -730,12 +746,29 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
     d.bytes = d.fwd_bytes;
     return d;
   }
-  const lmh::BwdPlan p = lmh::plan_backward(N, H, V, chunk_size);
-  d.off_tgt = kind == LMH_WS_BWD_BF16 ? p.bytes_bf16 : p.bytes;
+  d.few = few_backward(n, V, chunk_size);
+  lmh::BwdPlan p;
+  if (!d.few) {
+    p = lmh::plan_backward(N, H, V, chunk_size);
+    d.off_tgt = kind == LMH_WS_BWD_BF16 ? p.bytes_bf16 : p.bytes;
+  }
   d.off_ga = d.off_tgt + room(n * 4);
   d.off_id = d.off_ga + room(n * 4);
   d.off_val = d.off_id + room(n * (K + 1) * 4);
-  d.off_part = d.off_val + room(n * (K + 1) * 2);
+  d.off_part = d.off_val + room(n * (K + 1) * 4);
+  if (d.few) {
+    d.off_ht = d.off_part;
+    d.off_hi = d.off_ht + room(H * lmh::kFewTokens * 2);
+    d.off_lo = d.off_hi + room(V * few_padded(n) * 2);
+    d.off_part = d.off_lo + room(V * few_padded(n) * 2);
+    // two workgroups a CU, of at least 128 vocabulary rows each
+    d.dh_strips = (int)lmh::ceil_div(H, 256);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(2 * lmh::kNumCUs / d.dh_strips, lmh::ceil_div(V, 128)));
+    d.dh_rows = (int)lmh::round_up(lmh::ceil_div(V, most), 32);
+    d.splits = (int)lmh::ceil_div(V, d.dh_rows);
+    d.bytes = d.off_part + room(d.splits * n * H * 4);
+    return d;
+  }
   d.splits = dh_splits(p, H);
   d.k_split = (int)lmh::round_up(lmh::ceil_div(p.Vb, d.splits), 64);
   d.splits = (int)lmh::ceil_div(lmh::round_up(p.Vb, 64), d.k_split);
@@ -787,9 +820,24 @@ int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const in
   const float sc = temper_scale(temperature);
   // without hard targets the tile kernel still reads N ids to pick a logit by:
   // any will do, the pick is not used
-  lmh::FwdArgs a{hidden, W, targets != nullptr ? targets : ids, N, H, V, p.S, p.n_tt, p.n_vt, 0, V, sc,
-                 inv_temperature(temperature), workspace, p.part_ld, nullptr, nullptr, nullptr, nullptr};
-  hipError_t e = lmh::launch_fwd_stats(a, s);
+  hipError_t e;
+  if (few_forward(N, V)) {
+    lmh::FewArgs a{};
+    a.hidden = hidden;
+    a.W = W;
+    a.targets = targets;
+    a.N = (int)N;
+    a.H = (int)H;
+    a.V = (int)V;
+    a.sc = sc;
+    a.part = workspace;
+    a.part_ld = p.part_ld;
+    e = lmh::launch_few_stats(a, s);
+  } else {
+    lmh::FwdArgs a{hidden, W, targets != nullptr ? targets : ids, N, H, V, p.S, p.n_tt, p.n_vt, 0, V, sc,
+                   inv_temperature(temperature), workspace, p.part_ld, nullptr, nullptr, nullptr, nullptr};
+    e = lmh::launch_fwd_stats(a, s);
+  }
   const double back = 1.0 / ((double)sc * (double)temperature);
   const float back_hi = (float)back;
   if (e == hipSuccess)
@@ -799,6 +847,63 @@ int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const in
   if (e != hipSuccess) return fail(LMH_ERR_HIP, "distill_fwd: launch failed: %s", hipGetErrorString(e));
   return ok();
 }
+
+}  // extern "C"
+
+namespace {
+
+// The backward of few tokens, after every check.
+hipError_t few_bwd(const DistillPlan& d, const lmh::DistillPrepArgs& prep, const uint16_t* hidden, const uint16_t* W,
+                   int64_t H, float temperature, const float* lse, void* dh, void* dW, bool bf16, unsigned flags,
+                   char* ws, hipStream_t s) {
+  hipError_t e = lmh::launch_distill_prep(prep, s);
+  uint16_t* ht = reinterpret_cast<uint16_t*>(ws + d.off_ht);
+  if (e == hipSuccess)
+    e = lmh::launch_transpose(hidden, H, prep.N, H, lmh::kFewTokens, H, prep.tgt, prep.V, ht, lmh::kFewTokens, s);
+  if (e != hipSuccess) return e;
+  lmh::FewArgs a{};
+  a.hidden = hidden;
+  a.W = W;
+  a.targets = prep.tgt;
+  a.N = (int)prep.N;
+  a.H = (int)H;
+  a.V = prep.V;
+  a.sc = temper_scale(temperature);
+  a.invT = prep.invT;
+  a.lse = lse;
+  a.ga = prep.ga;
+  a.ent_id = prep.ent_id;
+  a.ent_val = prep.ent_val;
+  a.K1 = prep.K + 1;
+  a.dz_hi = reinterpret_cast<uint16_t*>(ws + d.off_hi);
+  a.dz_lo = reinterpret_cast<uint16_t*>(ws + d.off_lo);
+  a.ht = ht;
+  a.dW = dW;
+  a.add_dW = (flags & LMH_BWD_ACCUMULATE_DW) != 0;
+  a.dh_part = reinterpret_cast<float*>(ws + d.off_part);
+  a.dh_strips = d.dh_strips;
+  a.dh_splits = d.splits;
+  a.dh_rows = d.dh_rows;
+  e = lmh::launch_few_bwd(a, bf16, s);
+  if (e != hipSuccess) return e;
+  const bool add = (flags & LMH_BWD_ACCUMULATE_DH) != 0;
+  lmh::DistillPostArgs post{};
+  post.part = a.dh_part;
+  post.splits = d.splits;
+  post.g_Ct = a.N;
+  post.H = a.H;
+  post.V = a.V;
+  post.tgt = prep.tgt;
+  post.o.src_kind = !add ? lmh::kSrcNone : bf16 ? lmh::kSrcBf16 : lmh::kSrcF32;
+  post.o.src = post.o.dst = dh;
+  post.o.dst_bf16 = bf16;
+  post.dead_zero = !add;
+  return lmh::launch_distill_post(post, s);
+}
+
+}  // namespace
+
+extern "C" {
 
 int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const int32_t* targets, const int32_t* ids,
                              const void* teacher, int teacher_type, const float* teacher_lse, int64_t N, int64_t H,
@@ -821,9 +926,12 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
   const int32_t* tgt = nullptr;
   const float* ga = nullptr;
   if (N > 0) {
-    if (!ids || !teacher || !logp_top || !workspace || !dh)
-      return fail(LMH_ERR_NULL, "distill_bwd: ids, teacher, logp_top, dh and workspace must be non-NULL");
-    if (!aligned(targets, 4) || !aligned(ids, 4) || !aligned(teacher, type_size(teacher_type)) ||
+    if (!hidden || !W || !ids || !teacher || !lse || !logp_top || !workspace || !dh || !dW)
+      return fail(LMH_ERR_NULL,
+                  "distill_bwd: hidden, W, ids, teacher, lse, logp_top, dh, dW and workspace must be non-NULL");
+    if (flags & ~(unsigned)(LMH_BWD_ACCUMULATE_DH | LMH_BWD_ACCUMULATE_DW))
+      return fail(LMH_ERR_ARGS, "distill_bwd: unknown flags 0x%x", flags);
+    if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(dh, 16) || !aligned(targets, 4) || !aligned(ids, 4) || !aligned(teacher, type_size(teacher_type)) ||
         !aligned(teacher_lse, 4) || !aligned(logp, 4) || !aligned(lse, 4) || !aligned(logp_top, 4) ||
         !aligned(g_kl, 4) || !aligned(g_logp, 4) || !aligned(workspace, 16) || !aligned(dW, 16))
       return fail(LMH_ERR_UNSUPPORTED, "distill_bwd: a misaligned pointer");
@@ -834,7 +942,15 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
     // a hard target without a cotangent takes no part
     hook.prep = {g_logp != nullptr ? targets : nullptr, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
                  (int)V, (int)K, temperature, inv_temperature(temperature), logp, logp_top, g_kl, g_logp, w_tgt, w_ga,
-                 reinterpret_cast<int32_t*>(ws + d.off_id), reinterpret_cast<uint16_t*>(ws + d.off_val)};
+                 reinterpret_cast<int32_t*>(ws + d.off_id), reinterpret_cast<float*>(ws + d.off_val)};
+    if (d.few) {
+      if (workspace_bytes < d.bytes)
+        return fail(LMH_ERR_WORKSPACE, "distill_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, d.bytes);
+      const hipError_t e = few_bwd(d, hook.prep, hidden, W, H, temperature, lse, dh, dW, bf16, flags, ws,
+                                   static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return fail(LMH_ERR_HIP, "distill_bwd: launch failed: %s", hipGetErrorString(e));
+      return ok();
+    }
     hook.splits = d.splits;
     hook.k_split = d.k_split;
     hook.part = reinterpret_cast<float*>(ws + d.off_part);

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(256) void distill_top_kernel(const DistillTopArgs a
 // Backward, before the tiles. A wave per token forms what the head's tiles
 // read (the combined log-prob cotangent and a target id, one of the special
 // entries or -1 for a token without any) and the token's special entries:
-// (id, cotangent in bf16), K + 1 of them, id -1 where there is none. An id
+// (id, cotangent), K + 1 of them, id -1 where there is none. An id
 // that the teacher lists twice is formed once, at its first place, with the
 // sum of its q in list order.
 __global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs a) {
@@ -223,14 +223,14 @@ __global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs
     float x = 0.0f;
     if (p != 0.0f) x = (kd ? g_kl * fmaf(Q, p, -q) : 0.0f) - g_logp * p;   // an entry of probability 0 has no such term
     else if (kd) x = -g_kl * q;
-    return __builtin_bit_cast(uint16_t, (__bf16)((is_target ? x + g_logp : x) * a.invT));
+    return (is_target ? x + g_logp : x) * a.invT;
   };
   int32_t* e_id = a.ent_id + tok * (K + 1);
-  uint16_t* e_val = a.ent_val + tok * (K + 1);
+  float* e_val = a.ent_val + tok * (K + 1);
   for (int k = lane; k < K; k += 64) {
     const int id = live_of(k) ? ids[k] : -1;
     int out = id;
-    uint16_t val = 0;
+    float val = 0.0f;
     if (id >= 0) {
       float q = 0.0f;
       for (int j = 0; j < K; ++j) {
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs
   if (lane == 0) {
     const bool extra = hard && !listed;
     e_id[K] = extra ? target : -1;
-    e_val[K] = extra ? cotangent(a.logp != nullptr ? a.logp[tok] : 0.0f, 0.0f, true) : (uint16_t)0;
+    e_val[K] = extra ? cotangent(a.logp != nullptr ? a.logp[tok] : 0.0f, 0.0f, true) : 0.0f;
     a.tgt[tok] = hard ? target : (first < K ? ids[first] : -1);
     a.ga[tok] = g_logp - gQ;
   }
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs
     const int64_t at = (int64_t)a.t0 * a.K1 + i;
     const int id = a.ent_id[at];
     const int v = id - a.v0;
-    if (id >= 0 && v >= 0 && v < a.Vb) a.dz[i / a.K1 * a.ld_dz + v] = a.ent_val[at];
+    if (id >= 0 && v >= 0 && v < a.Vb) a.dz[i / a.K1 * a.ld_dz + v] = round_bf16(a.ent_val[at]);
   }
   if (a.part == nullptr) return;
   const int h4 = a.H / 4;

@@ -1,0 +1,485 @@
+// lmhead_few.hip -- the distillation head for few tokens (up to 64), for gfx950.
+//
+// With so few tokens every pass is bound by the vocabulary table: the forward
+// reads W once (2 V H bytes), the backward reads it twice (for the logits and
+// for dh) and writes dW once. The head's 256 x 256 tiles would spend 4 to 256
+// times the products, and leave the chip waiting at their prologues and
+// epilogues. Here waves stream W from memory through registers:
+//
+//   logits   a wave holds 16 MB vocabulary rows x 16 NB tokens and walks H, so a
+//            row of W is loaded by one wave only, and hidden comes from cache
+//   dW       (V x H, K = tokens) a wave keeps its columns of hidden^T in
+//            registers and walks the vocabulary, storing 256 bytes of 16 rows
+//            per step
+//   dh       (tokens x H, K = V) a workgroup stages 32 rows of W and of the
+//            cotangent in LDS and reads both transposed; the vocabulary is
+//            split over workgroups, whose float32 partials are summed in order
+//
+// The cotangent is held as two bf16 words (its rounding and what that left):
+// its products then cost twice the matrix instructions, which are idle here,
+// and carry 16 bits instead of 8.
+//
+// MFMA 16x16x32: lane l supplies row (l % 16) of A and column (l % 16) of B with
+// 8 K values of its quarter l / 16; register r of lane l holds
+// D[4 (l / 16) + r][l % 16]. Which 8 K values a quarter takes is free as long as
+// A and B agree.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "lmhead_internal.h"
+#include "lmhead_tile.h"
+
+namespace lmh {
+namespace {
+
+// acc[i][j] = W rows r0 + 16 i .. times tokens 16 j .., over K = H (a multiple
+// of 64). A unit is 64 of K: quarter q of the lanes takes bytes 32 q .. of the
+// 128 that a row has there, so a wave's two loads use each line whole. D units
+// are in flight; loads past the end reread the last unit.
+template <int MB, int NB, int D>
+__device__ __forceinline__ void few_logits(const uint16_t* W, int V, const uint16_t* hidden, int N, int H, int r0,
+                                           f32x4 (&acc)[MB][NB]) {
+  const int lane = threadIdx.x & 63;
+  const int col = lane & 15, q = lane >> 4;
+  const char* pa[MB];
+  const char* pb[NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    pa[i] = reinterpret_cast<const char*>(W + (int64_t)min(r0 + 16 * i + col, V - 1) * H) + 32 * q;
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+    pb[j] = reinterpret_cast<const char*>(hidden + (int64_t)min(16 * j + col, N - 1) * H) + 32 * q;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  bf16x8 a[D][MB][2], b[D][NB][2];
+  const int units = H / 64;
+  auto load = [&](int d, int u) {
+    const int64_t at = 128 * (int64_t)min(u, units - 1);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const bf16x8* p = reinterpret_cast<const bf16x8*>(pa[i] + at);
+      a[d][i][0] = p[0];
+      a[d][i][1] = p[1];
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const bf16x8* p = reinterpret_cast<const bf16x8*>(pb[j] + at);
+      b[d][j][0] = p[0];
+      b[d][j][1] = p[1];
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  for (int u = 0; u < units; u += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (u + d < units) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d][i][h], b[d][j][h], acc[i][j], 0, 0, 0);
+      }
+      load(d, u + d + D);
+    }
+  }
+}
+
+// Forward: the statistics of the workgroup's 64 MB vocabulary rows per token,
+// as one record of the split (the workgroup).
+template <int MB, int NB>
+__global__ __launch_bounds__(256) void few_stats_kernel(const FewArgs a) {
+  __shared__ float4 xch[4][16 * NB];
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  const int r0 = (blockIdx.x * 4 + wave) * 16 * MB;
+  const int V = a.V;
+  Stats st[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) st[j] = Stats{kNegBig, 0.0f, 0.0f, 0.0f};
+  if (r0 < V) {
+    int tgt[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int tok = 16 * j + (lane & 15);
+      tgt[j] = a.targets != nullptr ? a.targets[min(tok, a.N - 1)] : -1;
+      if (tgt[j] < 0 || tgt[j] >= V) tgt[j] = -1;
+    }
+    f32x4 acc[MB][NB];
+    few_logits<MB, NB, (NB > 2 ? 2 : 3)>(a.W, V, a.hidden, a.N, a.H, r0, acc);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      // rows past V take no part: their logits never win the max, and their
+      // exponentials are selected away
+      float mx = kNegBig;
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = r0 + acc_row(i, r, lane);
+          if (row < V) mx = nan_max(mx, acc[i][j][r]);
+          if (row == tgt[j]) st[j].zt = acc[i][j][r];
+        }
+      const float m = mx * a.sc;   // sc > 0: max commutes with the scaling
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool in = r0 + acc_row(i, r, lane) < V;
+          const float d = in ? fmaf(acc[i][j][r], a.sc, -m) : 0.0f;
+          const float e = in ? fast_exp2(d) : 0.0f;
+          s1 += e;
+          s2 = fmaf(e, d, s2);
+        }
+      st[j].m2 = m;
+      st[j].s1 = s1;
+      st[j].s2 = s2;
+    }
+  }
+#pragma unroll
+  for (int x = 16; x <= 32; x <<= 1)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const Stats o{__shfl_xor(st[j].m2, x), __shfl_xor(st[j].s1, x), __shfl_xor(st[j].s2, x), __shfl_xor(st[j].zt, x)};
+      st[j] = (lane & x) == 0 ? merge_stats(st[j], o) : merge_stats(o, st[j]);
+    }
+  if (lane < 16) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) xch[wave][16 * j + lane] = make_float4(st[j].m2, st[j].s1, st[j].s2, st[j].zt);
+  }
+  __syncthreads();
+  const int tok = threadIdx.x;
+  if (tok < 16 * NB && tok < a.N) {
+    Stats m{kNegBig, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 p = xch[w][tok];
+      m = merge_stats(m, Stats{p.x, p.y, p.z, p.w});
+    }
+    reinterpret_cast<float4*>(a.part)[(int64_t)blockIdx.x * a.part_ld + tok] = make_float4(m.m2, m.s1, m.s2, m.zt);
+  }
+}
+
+// Backward: the cotangent of the workgroup's 64 MB vocabulary rows, formed in
+// LDS as [row][token] pairs of bf16 words, the tokens' special entries
+// overwriting theirs there, and stored as [V][16 NB], high words and low words
+// apart. Masked tokens and tokens past N are 0.
+template <int MB, int NB>
+__global__ __launch_bounds__(256) void few_dz_kernel(const FewArgs a) {
+  constexpr int NP = 16 * NB, rows = 64 * MB;
+  __shared__ __attribute__((aligned(16))) uint16_t t_hi[rows][NP];
+  __shared__ __attribute__((aligned(16))) uint16_t t_lo[rows][NP];
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  const int b0 = blockIdx.x * rows;
+  const int w0 = wave * 16 * MB;
+  const int V = a.V;
+  auto put = [&](int row, int tok, float x) {
+    const uint16_t hi = round_bf16(x);
+    t_hi[row][tok] = hi;
+    // the difference is exact; an infinity leaves nothing
+    t_lo[row][tok] = (hi & 0x7FFF) == 0x7F80 ? (uint16_t)0 : round_bf16(x - widen_bf16(hi));
+  };
+  if (b0 + w0 < V) {
+    f32x4 acc[MB][NB];
+    few_logits<MB, NB, (NB > 2 ? 2 : 3)>(a.W, V, a.hidden, a.N, a.H, b0 + w0, acc);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int tok = 16 * j + (lane & 15);
+      const int at = min(tok, a.N - 1);
+      const int t = a.targets[at];
+      const bool live = tok < a.N && t >= 0 && t < V;
+      const float nlse = live ? -a.lse[at] * kLog2e : 0.0f;
+      const float c0 = live ? -a.ga[at] * a.invT : 0.0f;
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // an entry of probability 0 has no such term, whatever c0 holds
+          const float x = lmh_fmul_legacy(fast_exp2(fmaf(acc[i][j][r], a.sc, nlse)), c0);
+          put(w0 + acc_row(i, r, lane), tok, live ? x : 0.0f);
+        }
+    }
+  }
+  __syncthreads();
+  const int n = a.N * a.K1;
+  for (int e = threadIdx.x; e < n; e += 256) {
+    const int id = a.ent_id[e];
+    if (id >= b0 && id < min(b0 + rows, V)) put(id - b0, e / a.K1, a.ent_val[e]);
+  }
+  __syncthreads();
+  constexpr int per_row = NP / 8;   // 16-byte chunks
+  for (int c = threadIdx.x; c < rows * per_row; c += 256) {
+    if (b0 + c / per_row >= V) break;
+    const int64_t at = (int64_t)b0 * per_row + c;
+    reinterpret_cast<uint4*>(a.dz_hi)[at] = reinterpret_cast<const uint4*>(t_hi)[c];
+    reinterpret_cast<uint4*>(a.dz_lo)[at] = reinterpret_cast<const uint4*>(t_lo)[c];
+  }
+}
+
+// dW[v][h] = sum_tok dz[v][tok] hidden[tok][h]. A wave holds 128 columns of
+// hidden^T as A operands (block pair c: columns 32 c + 8 q + (0..7) fall to
+// quarter q, so a lane ends with 8 consecutive ones) and walks vocabulary
+// groups of 16, the next group's cotangent in flight.
+template <int NB, bool BF16>
+__global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
+  constexpr int NP = 16 * NB, KS = NP / 32;
+  const int lane = threadIdx.x & 63;
+  const int col = lane & 15, q = lane >> 4;
+  const int w = blockIdx.x * 4 + wave_id();
+  const int strip = w % a.strips, split = w / a.strips;
+  if (split >= a.dw_splits) return;
+  const int H = a.H, V = a.V;
+  const int h0 = strip * 128;
+  bf16x8 ht[8][KS];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const int h = min(h0 + 32 * (b >> 1) + 8 * (col >> 2) + 4 * (b & 1) + (col & 3), H - 1);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) ht[b][k] = *reinterpret_cast<const bf16x8*>(a.ht + (int64_t)h * 64 + 32 * k + 8 * q);
+  }
+  const int groups = (V + 15) / 16;
+  const int g_lo = (int)((int64_t)split * groups / a.dw_splits), g_hi = (int)((int64_t)(split + 1) * groups / a.dw_splits);
+  bf16x8 hi[KS], lo[KS];
+  auto load = [&](int g) {
+    const int64_t at = (int64_t)min(16 * g + col, V - 1) * NP + 8 * q;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      hi[k] = *reinterpret_cast<const bf16x8*>(a.dz_hi + at + 32 * k);
+      lo[k] = *reinterpret_cast<const bf16x8*>(a.dz_lo + at + 32 * k);
+    }
+  };
+  if (g_lo < g_hi) load(g_lo);
+  for (int g = g_lo; g < g_hi; ++g) {
+    f32x4 acc[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], lo[k], acc[b], 0, 0, 0);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], hi[k], acc[b], 0, 0, 0);
+    }
+    if (g + 1 < g_hi) load(g + 1);
+    const int row = 16 * g + col;
+    if (row >= V) continue;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (h0 + 32 * c >= H) continue;
+      const int64_t at = (int64_t)row * H + h0 + 32 * c + 8 * q;
+      f32x4 x = acc[2 * c], y = acc[2 * c + 1];
+      if (BF16) {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dW) + at);
+        if (a.add_dW) {
+          const uint4 o = *p;
+          x += f32x4{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u), __uint_as_float(o.y << 16),
+                     __uint_as_float(o.y & 0xFFFF0000u)};
+          y += f32x4{__uint_as_float(o.z << 16), __uint_as_float(o.z & 0xFFFF0000u), __uint_as_float(o.w << 16),
+                     __uint_as_float(o.w & 0xFFFF0000u)};
+        }
+        *p = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      } else {
+        f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(a.dW) + at);
+        if (a.add_dW) {
+          x += p[0];
+          y += p[1];
+        }
+        p[0] = x;
+        p[1] = y;
+      }
+    }
+  }
+}
+
+// dh[tok][h] = sum_v dz[v][tok] W[v][h] over one split of the vocabulary and 256
+// columns (64 a wave), as a float32 partial [split][N][H]. 32 vocabulary rows a
+// step go through registers into LDS (two buffers); W's rows lie there as the
+// tile core's MN-contiguous slices do, the cotangent's with 16 bytes of padding,
+// so that the transposed reads of 16 lanes (4 rows x 32 bytes) meet no bank
+// twice. Rows past the split are 0 in both operands.
+template <int NB>
+__global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
+  constexpr int NP = 16 * NB, pitch = 2 * NP + 16;
+  constexpr int w_bytes = 32 * 512, z_bytes = 32 * pitch, buf = w_bytes + 2 * z_bytes;
+  __shared__ __attribute__((aligned(16))) char lds[2 * buf];
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_id();
+  const int strip = blockIdx.x % a.dh_strips, split = blockIdx.x / a.dh_strips;
+  const int H = a.H;
+  const int h0 = strip * 256;
+  const int v_lo = split * a.dh_rows, v_hi = min(v_lo + a.dh_rows, a.V);
+  const int steps = (v_hi - v_lo + 31) / 32;   // > 0: the host counts the splits
+
+  // staging: W row t / 32 + 8 c, 16-byte chunk t % 32; cotangent row t / (NP / 8)
+  // (of the high words, then of the low ones)
+  const int chunk = threadIdx.x & 31;
+  const int w_col = min(h0 + 8 * chunk, H - 8);
+  constexpr int z_per = NP / 8;                          // chunks of a cotangent row
+  constexpr int z_n = 2 * 32 * z_per;                    // chunks of both words
+  constexpr int z_each = (z_n + 255) / 256;
+  uint4 sw[4], sz[z_each];
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  auto fetch = [&](int step) {
+    const int v0 = v_lo + 32 * step;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int v = v0 + (threadIdx.x >> 5) + 8 * c;
+      sw[c] = *reinterpret_cast<const uint4*>(a.W + (int64_t)min(v, v_hi - 1) * H + w_col);
+      if (v >= v_hi) sw[c] = none;
+    }
+#pragma unroll
+    for (int c = 0; c < z_each; ++c) {
+      const int i = threadIdx.x + 256 * c;
+      const int v = v0 + (i / z_per) % 32;
+      const uint16_t* src = i < 32 * z_per ? a.dz_hi : a.dz_lo;
+      sz[c] = none;
+      if (i < z_n && v < v_hi) sz[c] = *reinterpret_cast<const uint4*>(src + (int64_t)v * NP + 8 * (i % z_per));
+    }
+  };
+  auto stage = [&](char* p) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int r = (threadIdx.x >> 5) + 8 * c;
+      *reinterpret_cast<uint4*>(p + r * 512 + ((chunk ^ swz_mn(r)) << 4)) = sw[c];
+    }
+#pragma unroll
+    for (int c = 0; c < z_each; ++c) {
+      const int i = threadIdx.x + 256 * c;
+      if (i < z_n)
+        *reinterpret_cast<uint4*>(p + w_bytes + (i < 32 * z_per ? 0 : z_bytes) + (i / z_per) % 32 * pitch + 16 * (i % z_per)) = sz[c];
+    }
+  };
+  // transposed reads: lane s of a 16-lane group points at K-row 8 q + s / 4 (+ 4
+  // for the upper half) and 4 columns from 4 (s % 4) on
+  const int s = lane & 15, q = lane >> 4;
+  const int t_row = 8 * q + (s >> 2);
+  const int t_x = swz_mn(t_row);
+  const int t_chunk = wave * 8 + ((s & 3) >> 1);
+  auto read = [&](const char* p0, const char* p1) {
+    short8v v;
+    v.s0123 = ds_read_tr(p0);
+    v.s4567 = ds_read_tr(p1);
+    return __builtin_bit_cast(bf16x8, v);
+  };
+  f32x4 acc[4][NB];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  fetch(0);
+  for (int step = 0; step < steps; ++step) {
+    char* p = lds + (step & 1) * buf;
+    stage(p);
+    __syncthreads();   // one a step: a buffer is refilled two steps on, after every wave is past the step between
+    if (step + 1 < steps) fetch(step + 1);
+    bf16x8 fw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const char* at = p + t_row * 512 + (((t_chunk + 2 * i) ^ t_x) << 4) + 8 * (s & 1);
+      fw[i] = read(at, at + 4 * 512);   // 4 rows on, the swizzle is the same
+    }
+#pragma unroll
+    for (int half = 1; half >= 0; --half)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const char* at = p + w_bytes + half * z_bytes + t_row * pitch + 32 * j + 8 * (s & 3);
+        const bf16x8 fz = read(at, at + 4 * pitch);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fz, acc[i][j], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int tok = 16 * j + s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = h0 + 64 * wave + 16 * i + 4 * q;
+      if (tok < a.N && h < H) *reinterpret_cast<f32x4*>(a.dh_part + ((int64_t)split * a.N + tok) * H + h) = acc[i][j];
+    }
+  }
+}
+
+// Row blocks per wave: as many as leave a workgroup per CU, so that hidden is
+// fetched for as many rows at a time as the vocabulary allows.
+int few_blocks(int64_t V) {
+  for (int mb = 4; mb > 1; mb /= 2)
+    if ((V + 64 * mb - 1) / (64 * mb) >= kNumCUs) return mb;
+  return 1;
+}
+
+template <class F>
+void with_sizes(int mb, int nb, F f) {
+  auto rows = [&](auto n) {
+    if (mb == 4) f(std::integral_constant<int, 4>{}, n);
+    else if (mb == 2) f(std::integral_constant<int, 2>{}, n);
+    else f(std::integral_constant<int, 1>{}, n);
+  };
+  if (nb == 4) rows(std::integral_constant<int, 4>{});
+  else if (nb == 2) rows(std::integral_constant<int, 2>{});
+  else rows(std::integral_constant<int, 1>{});
+}
+
+}  // namespace
+
+int few_splits(int64_t V) {
+  const int rows = 64 * few_blocks(V);
+  return (int)((V + rows - 1) / rows);
+}
+
+hipError_t launch_few_stats(const FewArgs& a, hipStream_t stream) {
+  const double N = a.N, H = a.H, V = a.V;
+  trace_begin(stream);
+  with_sizes(few_blocks(a.V), a.N <= 16 ? 1 : a.N <= 32 ? 2 : 4, [&](auto mb, auto nb) {
+    hipLaunchKernelGGL((few_stats_kernel<mb(), nb()>), dim3(few_splits(a.V)), dim3(256), 0, stream, a);
+  });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kFewStats, stream, 2.0 * N * H * V, 2.0 * (N + V) * H + 4.0 * N + 16.0 * few_splits(a.V) * N);
+  return hipSuccess;
+}
+
+// The cotangent, then dW and the partials of dh.
+hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream) {
+  const double N = a.N, H = a.H, V = a.V;
+  const int nb = a.N <= 32 ? 2 : 4;
+  trace_begin(stream);
+  with_sizes(few_blocks(a.V), nb, [&](auto mb, auto n) {
+    constexpr int NB = n() < 2 ? 2 : n();   // K of the gradient products is at least 32 tokens
+    hipLaunchKernelGGL((few_dz_kernel<mb(), NB>), dim3(few_splits(a.V)), dim3(256), 0, stream, a);
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kFewDz, stream, 0.0, 2.0 * (N + V) * H + 64.0 * nb * V);
+  // waves for dW: 8 a CU, but no less than 4 groups of 16 rows each
+  a.strips = (a.H + 127) / 128;
+  a.dw_splits = std::max(1, std::min((a.V + 63) / 64, 8 * kNumCUs / a.strips));
+  const unsigned blocks = (unsigned)((a.strips * a.dw_splits + 3) / 4);
+  trace_begin(stream);
+  if (nb == 2) {
+    if (bf16) hipLaunchKernelGGL((few_dw_kernel<2, true>), dim3(blocks), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((few_dw_kernel<2, false>), dim3(blocks), dim3(256), 0, stream, a);
+  } else {
+    if (bf16) hipLaunchKernelGGL((few_dw_kernel<4, true>), dim3(blocks), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((few_dw_kernel<4, false>), dim3(blocks), dim3(256), 0, stream, a);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kFewDw, stream, 2.0 * N * H * V, (bf16 ? 2.0 : 4.0) * V * H + 64.0 * nb * V);
+  trace_begin(stream);
+  if (nb == 2) hipLaunchKernelGGL((few_dh_kernel<2>), dim3(a.dh_strips * a.dh_splits), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((few_dh_kernel<4>), dim3(a.dh_strips * a.dh_splits), dim3(256), 0, stream, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kFewDh, stream, 2.0 * N * H * V, 2.0 * V * H + 64.0 * nb * V + 4.0 * a.dh_splits * N * H);
+  return hipSuccess;
+}
+
+}  // namespace lmh

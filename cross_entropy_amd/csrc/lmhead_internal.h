@@ -147,7 +147,7 @@ struct DistillTopArgs {
 
 // What the backward forms per token before the tiles run: the combined
 // log-prob cotangent ga and target id tgt that the tiles read, and K + 1
-// special entries (id or -1, cotangent in bf16) that overwrite the tiles'.
+// special entries (id or -1, cotangent) that overwrite the tiles'.
 struct DistillPrepArgs {
   const int32_t* targets;     // or NULL
   const int32_t* ids;
@@ -164,7 +164,7 @@ struct DistillPrepArgs {
   int32_t* tgt;               // [N]
   float* ga;                  // [N]
   int32_t* ent_id;            // [N][K + 1]
-  uint16_t* ent_val;          // [N][K + 1]
+  float* ent_val;             // [N][K + 1]
 };
 
 // A backward launch whose dh tiles are split over the block's vocabulary.
@@ -179,7 +179,7 @@ struct DistillStep {
 // it formed (dz, or NULL), and the sum of its dh splits (part, or NULL).
 struct DistillPostArgs {
   const int32_t* ent_id;
-  const uint16_t* ent_val;
+  const float* ent_val;
   int K1;            // K + 1
   uint16_t* dz;
   int64_t ld_dz;
@@ -190,6 +190,37 @@ struct DistillPostArgs {
   GradOut o;
   int dead_zero;     // masked tokens' rows are written as 0, else left as they are
 };
+
+// The distillation for few tokens (lmhead_few.hip).
+constexpr int kFewTokens = 64;
+
+struct FewArgs {
+  const uint16_t* hidden;
+  const uint16_t* W;
+  const int32_t* targets;   // forward: the hard targets or NULL; backward: what the preparation wrote
+  int N, H, V;
+  float sc, invT;           // log2(e) / T, 1 / T
+  void* part;               // forward: split records [few_splits(V)][part_ld][4]
+  int64_t part_ld;
+  // backward
+  const float* lse;
+  const float* ga;
+  const int32_t* ent_id;
+  const float* ent_val;
+  int K1;
+  uint16_t* dz_hi;          // [V][32 or 64] each
+  uint16_t* dz_lo;
+  const uint16_t* ht;       // hidden^T [H][64], masked tokens and those past N zeroed
+  void* dW;
+  bool add_dW;
+  int strips, dw_splits;    // set by launch_few_bwd
+  float* dh_part;           // [dh_splits][N][H]
+  int dh_strips, dh_splits, dh_rows;
+};
+
+int few_splits(int64_t V);   // records per token of the forward
+hipError_t launch_few_stats(const FewArgs& a, hipStream_t stream);
+hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream);   // the cotangent, dW and the partials of dh
 
 // The norm in front of the head (lmhead_norm.hip); rows of H elements.
 constexpr int kNormMaxH = 16384;
@@ -233,7 +264,8 @@ int norm_bwd_blocks(int64_t N, int64_t H);   // workgroups (partial rows) of the
 // Kernel ids of the tracing facility (lmhead_trace.hip).
 enum KernelId {
   kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
-  kDistillTop, kDistillPrep, kDistillStep, kDistillPost, kNormFwd, kNormBwd, kNormReduce, kNumKernels
+  kDistillTop, kDistillPrep, kDistillStep, kDistillPost,
+  kFewStats, kFewDz, kFewDw, kFewDh, kNormFwd, kNormBwd, kNormReduce, kNumKernels
 };
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);

@@ -349,8 +349,11 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  *   flags        LMH_BWD_ACCUMULATE_DH / _DW, as for lmhead_logps_bwd_ex and
  *                lmhead_logps_bwd_bf16
  * The workspace holds the head's backward workspace (chunk_size bounds the
- * cotangent block as there) and 8 N + 6 N (K + 1) bytes of the tokens' special
- * entries. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
+ * cotangent block as there), 8 N + 8 N (K + 1) bytes of the tokens' special
+ * entries and, where a block's dh is summed in splits, at most 64 float32
+ * partials of it. Up to 64 tokens (32 or 64, whichever N fits, at most
+ * chunk_size) hold their whole cotangent instead, as two bf16 words, and up to
+ * 512 float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
  * LMH_WS_FWD, LMH_WS_BWD or LMH_WS_BWD_BF16. A smaller size than the query
  * gives is refused. Results do not depend on anything but the arguments:
  * no atomics take part in sums.
@@ -440,9 +443,11 @@ const char* lmhead_logps_version(void);
  *   8 distill_prep_kernel  (distillation backward: per-token cotangents and special entries)
  *   9 distill_step_kernel  (bwd_step_kernel with its dh tiles split, either gradient type)
  *  10 distill_post_kernel  (special entries into a cotangent block, sum of dh splits)
- *  11 norm_fwd_kernel
- *  12 norm_bwd_kernel
- *  13 norm_reduce_kernel   (dweight and dbias from their partial sums)
+ *  11 few_stats_kernel     (distillation of up to 64 tokens: forward statistics)
+ *  12 few_dz_kernel        (its cotangent), 13 few_dw_kernel, 14 few_dh_kernel (its products)
+ *  15 norm_fwd_kernel
+ *  16 norm_bwd_kernel
+ *  17 norm_reduce_kernel   (dweight and dbias from their partial sums)
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch

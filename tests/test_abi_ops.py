@@ -83,19 +83,20 @@ def test_distill_workspace():
     assert _fwd(workspace_bytes=need[0] - 1) == -4
     assert _bwd(workspace_bytes=need[1] - 1, grad_type=1) == -4
     assert _bwd(workspace_bytes=need[2] - 1, grad_type=0) == -4
-    head = [nat.raw_workspace_bytes(64, 128, 300, 16, kind) for kind in (0, 1, 2)]
-    # the forward: 16-byte records of every token, for at most a split per vocabulary tile of 256
-    assert need[0] in (64 * 16, 2 * 64 * 16)
+    # the forward: 16-byte records of every token, for at most a split per 64 vocabulary rows
+    assert 0 < need[0] <= 64 * 16 * -(-300 // 64)
     assert q(256, 128, 151936, 5, 16, 0) <= 256 * 256 * 16
     up = lambda n: -(-n // 256) * 256  # noqa: E731
-    for kind in (1, 2):
-        assert need[kind] >= head[kind]
-        assert need[kind] <= head[kind] + 2 * up(64 * 4) + up(64 * 6 * 4) + up(64 * 6 * 2)
-    # few tokens over a large vocabulary split their dh products: at most 64 float32 partials of a block's dh
-    for N, H, V in ((1, 2560, 151936), (300, 1024, 151936), (256, 256, 4096)):
+    # the backward: the head's, the special entries, and at most 64 partials of a block's dh
+    for N, H, V, chunk in ((64, 128, 300, 16), (300, 1024, 151936, 512), (256, 256, 4096, 512), (5000, 2560, 9000, 64)):
         for kind in (1, 2):
-            more = q(N, H, V, 5, 512, kind) - nat.raw_workspace_bytes(N, H, V, 512, kind)
-            assert 0 < more <= 64 * (-(-N // 256) * 256) * H * 4 + 8 * N + 36 * N + 4096
+            more = q(N, H, V, 5, chunk, kind) - nat.raw_workspace_bytes(N, H, V, chunk, kind)
+            ct = up(min(N, 1 << 14))
+            assert 0 <= more <= 64 * ct * H * 4 + 8 * N + 48 * N + 4096
+    # few tokens within a chunk: two words of their cotangent, within a float32 [chunk, V]
+    for N, pad in ((1, 32), (32, 32), (33, 64), (64, 64)):
+        b = q(N, 2560, 151936, 5, 64, 1)
+        assert b <= 4 * 151936 * pad + 2 * 2560 * 64 + 512 * N * 2560 * 4 + 8 * N + 48 * N + 4096
     # beyond 2^31 entries the sizes are still whole
     N, K = 1 << 22, 1024
     assert q(N, 64, 1000, K, 16, 1) > N * (K + 1) * 6
