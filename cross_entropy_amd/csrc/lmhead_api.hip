@@ -763,7 +763,7 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
     d.off_part = d.off_lo + room(V * few_padded(n) * 2);
     // two workgroups a CU, of at least 128 vocabulary rows each
     d.dh_strips = (int)lmh::ceil_div(H, 256);
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(2 * lmh::kNumCUs / d.dh_strips, lmh::ceil_div(V, 128)));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>((few_padded(n) == 32 ? 3 : 2) * lmh::kNumCUs / d.dh_strips, lmh::ceil_div(V, 128)));
     d.dh_rows = (int)lmh::round_up(lmh::ceil_div(V, most), 32);
     d.splits = (int)lmh::ceil_div(V, d.dh_rows);
     d.bytes = d.off_part + room(d.splits * n * H * 4);

@@ -188,36 +188,47 @@ __global__ __launch_bounds__(256) void distill_top_kernel(const DistillTopArgs a
 // (id, cotangent), K + 1 of them, id -1 where there is none. An id
 // that the teacher lists twice is formed once, at its first place, with the
 // sum of its q in list order.
-__global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs a) {
+constexpr int kPrepWaves = 4;
+__global__ __launch_bounds__(64 * kPrepWaves) void distill_prep_kernel(const DistillPrepArgs a) {
+  extern __shared__ int lds[];   // per wave: the token's K ids (-1 for a missing entry), then its K q
   const int lane = threadIdx.x & 63;
-  const int64_t tok = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (tok >= a.N) return;
+  const int wave = threadIdx.x >> 6;
   const int K = a.K, V = a.V;
+  int* s_id = lds + wave * 2 * K;
+  float* s_q = reinterpret_cast<float*>(s_id + K);
+  const int64_t tok = min((int64_t)blockIdx.x * kPrepWaves + wave, a.N - 1);   // a wave too many repeats the last token
   const int32_t* ids = a.ids + tok * K;
   const int target = a.targets != nullptr ? a.targets[tok] : -1;
   const bool hard = target >= 0 && target < V;
   const float g_kl = a.g_kl != nullptr ? a.g_kl[tok] : 0.0f;
   const float g_logp = (hard && a.g_logp != nullptr) ? a.g_logp[tok] : 0.0f;
-  auto live_of = [&](int k) { return ids[k] >= 0 && ids[k] < V; };
-  auto t_of = [&](int k) { return live_of(k) ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY; };
   // a token whose loss term has no cotangent forms none of it (selected, so a
   // NaN in the teacher's row under g_kl = 0 stays out)
   const bool kd = g_kl != 0.0f;
-  const float shift = kd ? teacher_shift(a.teacher_lse, tok, K, t_of) : 0.0f;
-  float Q = 0.0f;
   int first = K;   // the first live entry
   bool listed = false;
   for (int k = lane; k < K; k += 64) {
-    if (!live_of(k)) continue;
-    first = min(first, k);
-    listed |= hard && ids[k] == target;
-    if (kd) Q += teacher_q(t_of(k), shift);
+    const int id = ids[k];
+    const bool live = id >= 0 && id < V;
+    s_id[k] = live ? id : -1;
+    s_q[k] = live && kd ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY;
+    if (live) first = min(first, k);
+    listed |= hard && id == target;
   }
-  Q = wave_sum(Q);
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) first = min(first, __shfl_xor(first, x));
   listed = __any(listed);
+  auto t_of = [&](int k) { return s_q[k]; };   // a lane's own entries: no wait between lanes is needed
+  const float shift = kd ? teacher_shift(a.teacher_lse, tok, K, t_of) : 0.0f;
+  float Q = 0.0f;
+  for (int k = lane; k < K; k += 64) {
+    const float q = teacher_q(s_q[k], shift);
+    s_q[k] = q;
+    Q += q;
+  }
+  Q = wave_sum(Q);
   const float gQ = kd ? g_kl * Q : 0.0f;
+  __syncthreads();   // every lane's ids and q are read below
   auto cotangent = [&](float s, float q, bool is_target) {
     const float p = expf(s);
     float x = 0.0f;
@@ -228,26 +239,24 @@ __global__ __launch_bounds__(256) void distill_prep_kernel(const DistillPrepArgs
   int32_t* e_id = a.ent_id + tok * (K + 1);
   float* e_val = a.ent_val + tok * (K + 1);
   for (int k = lane; k < K; k += 64) {
-    const int id = live_of(k) ? ids[k] : -1;
+    const int id = s_id[k];
     int out = id;
-    float val = 0.0f;
-    if (id >= 0) {
-      float q = 0.0f;
-      for (int j = 0; j < K; ++j) {
-        if (ids[j] != id) continue;
+    float q = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < K; ++j) {
+      if (s_id[j] == id) {
         if (j < k) out = -1;
-        if (kd) q += teacher_q(t_of(j), shift);
+        q += s_q[j];
       }
-      val = cotangent(a.logp_top[tok * K + k], q, hard && id == target);
     }
     e_id[k] = out;
-    e_val[k] = val;
+    e_val[k] = out >= 0 ? cotangent(a.logp_top[tok * K + k], q, hard && id == target) : 0.0f;
   }
   if (lane == 0) {
     const bool extra = hard && !listed;
     e_id[K] = extra ? target : -1;
     e_val[K] = extra ? cotangent(a.logp != nullptr ? a.logp[tok] : 0.0f, 0.0f, true) : 0.0f;
-    a.tgt[tok] = hard ? target : (first < K ? ids[first] : -1);
+    a.tgt[tok] = hard ? target : (first < K ? s_id[first] : -1);
     a.ga[tok] = g_logp - gQ;
   }
 }
@@ -336,6 +345,7 @@ __global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs
     if (live) {
       const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + i;
       v = p[0];
+#pragma unroll 8
       for (int k = 1; k < a.splits; ++k) v += p[k * n4];
       if (a.o.src_kind == kSrcF32) {
         v += static_cast<const f32x4*>(a.o.src)[i];
@@ -372,7 +382,8 @@ hipError_t launch_distill_top(const DistillTopArgs& a, hipStream_t stream) {
 hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream) {
   const double N = (double)a.N, K = (double)a.K;
   trace_begin(stream);
-  hipLaunchKernelGGL(distill_prep_kernel, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(distill_prep_kernel, dim3((unsigned)((a.N + kPrepWaves - 1) / kPrepWaves)), dim3(64 * kPrepWaves),
+                     (size_t)kPrepWaves * 2 * a.K * 4, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kDistillPrep, stream, 0.0, N * K * (14 + (a.t_f32 ? 4 : 2)) + 24.0 * N);

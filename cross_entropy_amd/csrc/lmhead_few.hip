@@ -34,6 +34,8 @@
 namespace lmh {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 // acc[i][j] = W rows r0 + 16 i .. times tokens 16 j .., over K = H (a multiple
 // of 64). A unit is 64 of K: quarter q of the lanes takes bytes 32 q .. of the
 // 128 that a row has there, so a wave's two loads use each line whole. D units
@@ -91,10 +93,95 @@ __device__ __forceinline__ void few_logits(const uint16_t* W, int V, const uint1
   }
 }
 
+// The same for 64 tokens, hidden through LDS: from cache, four waves' fetches of
+// 64 tokens' rows come to 0.8 of W's bytes again each and bound the pass (240 us
+// where memory takes 145). The workgroup stages kFewK of K of every token, the
+// next chunk in registers meanwhile; rows are padded by 16 bytes, so the 16
+// tokens of a fragment read fall on 16 different bank groups. `lds` holds two
+// chunks; every wave of the workgroup has to call, also one without rows.
+constexpr int kFewK = 256, kFewPitch = 2 * kFewK + 16, kFewLds = 2 * 64 * kFewPitch;
+template <int MB, int D>
+__device__ __forceinline__ void few_logits_lds(const uint16_t* W, int V, const uint16_t* hidden, int N, int H, int r0,
+                                               char* lds, f32x4 (&acc)[MB][4]) {
+  constexpr int NB = 4, UC = kFewK / 64, pieces = 64 * kFewK / 8 / 256;
+  const int lane = threadIdx.x & 63;
+  const int col = lane & 15, q = lane >> 4;
+  const char* pa[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    pa[i] = reinterpret_cast<const char*>(W + (int64_t)min(r0 + 16 * i + col, V - 1) * H) + 32 * q;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int units = H / 64, chunks = (units + UC - 1) / UC;
+  bf16x8 a[D][MB][2];
+  auto load = [&](int d, int u) {
+    const int64_t at = 128 * (int64_t)min(u, units - 1);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const bf16x8* p = reinterpret_cast<const bf16x8*>(pa[i] + at);
+      a[d][i][0] = p[0];
+      a[d][i][1] = p[1];
+    }
+  };
+  // staging: thread t takes 16 bytes at 8 (t % 32) of tokens t / 32 + 8 c
+  u32x4 next[pieces];
+  const int t_tok = threadIdx.x >> 5, t_k = 8 * (threadIdx.x & 31);
+  auto fetch = [&](int chunk) {
+#pragma unroll
+    for (int c = 0; c < pieces; ++c)
+      next[c] = *reinterpret_cast<const u32x4*>(hidden + (int64_t)min(t_tok + 8 * c, N - 1) * H +
+                                                min(chunk * kFewK + t_k, H - 8));
+  };
+  auto stage = [&](int chunk) {
+#pragma unroll
+    for (int c = 0; c < pieces; ++c)
+      *reinterpret_cast<u32x4*>(lds + (chunk & 1) * 64 * kFewPitch + (t_tok + 8 * c) * kFewPitch + 2 * t_k) = next[c];
+  };
+  fetch(0);
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  stage(0);
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    fetch(min(chunk + 1, chunks - 1));
+    __syncthreads();   // chunk is staged; chunk - 1, whose buffer is filled below, has been read
+    const char* p = lds + (chunk & 1) * 64 * kFewPitch + col * kFewPitch + 32 * q;
+#pragma unroll
+    for (int uc = 0; uc < UC; ++uc) {
+      const int u = chunk * UC + uc;
+      if (u < units) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bf16x8 b[NB];
+#pragma unroll
+          for (int j = 0; j < NB; ++j) b[j] = *reinterpret_cast<const bf16x8*>(p + 16 * j * kFewPitch + 128 * uc + 16 * h);
+#pragma unroll
+          for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[uc % D][i][h], b[j], acc[i][j], 0, 0, 0);
+        }
+      }
+      load(uc % D, u + D);
+    }
+    stage(chunk + 1);   // after the last, a copy of it that nobody reads
+  }
+}
+
+template <int MB, int NB>
+__device__ __forceinline__ void few_logits_of(const FewArgs& a, int r0, char* lds, f32x4 (&acc)[MB][NB]) {
+  if constexpr (NB == 4) few_logits_lds<MB, 2>(a.W, a.V, a.hidden, a.N, a.H, r0, lds, acc);
+  else few_logits<MB, NB, 3>(a.W, a.V, a.hidden, a.N, a.H, r0, acc);
+}
+template <int NB>
+constexpr int few_lds() { return NB == 4 ? kFewLds : 16; }
+
 // Forward: the statistics of the workgroup's 64 MB vocabulary rows per token,
 // as one record of the split (the workgroup).
 template <int MB, int NB>
-__global__ __launch_bounds__(256) void few_stats_kernel(const FewArgs a) {
+__global__ __launch_bounds__(256, 2) void few_stats_kernel(const FewArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[few_lds<NB>()];
   __shared__ float4 xch[4][16 * NB];
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
@@ -103,7 +190,7 @@ __global__ __launch_bounds__(256) void few_stats_kernel(const FewArgs a) {
   Stats st[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) st[j] = Stats{kNegBig, 0.0f, 0.0f, 0.0f};
-  if (r0 < V) {
+  {
     int tgt[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -112,7 +199,7 @@ __global__ __launch_bounds__(256) void few_stats_kernel(const FewArgs a) {
       if (tgt[j] < 0 || tgt[j] >= V) tgt[j] = -1;
     }
     f32x4 acc[MB][NB];
-    few_logits<MB, NB, (NB > 2 ? 2 : 3)>(a.W, V, a.hidden, a.N, a.H, r0, acc);
+    few_logits_of<MB, NB>(a, r0, lds, acc);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       // rows past V take no part: their logits never win the max, and their
@@ -172,10 +259,12 @@ __global__ __launch_bounds__(256) void few_stats_kernel(const FewArgs a) {
 // overwriting theirs there, and stored as [V][16 NB], high words and low words
 // apart. Masked tokens and tokens past N are 0.
 template <int MB, int NB>
-__global__ __launch_bounds__(256) void few_dz_kernel(const FewArgs a) {
-  constexpr int NP = 16 * NB, rows = 64 * MB;
-  __shared__ __attribute__((aligned(16))) uint16_t t_hi[rows][NP];
-  __shared__ __attribute__((aligned(16))) uint16_t t_lo[rows][NP];
+__global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
+  constexpr int NP = 16 * NB, rows = 64 * MB, tile = rows * NP * 2;
+  // the logits' staging, then the two words' tiles in its place
+  __shared__ __attribute__((aligned(16))) char lds[few_lds<NB>() > 2 * tile ? few_lds<NB>() : 2 * tile];
+  uint16_t (*t_hi)[NP] = reinterpret_cast<uint16_t (*)[NP]>(lds);
+  uint16_t (*t_lo)[NP] = reinterpret_cast<uint16_t (*)[NP]>(lds + tile);
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
   const int b0 = blockIdx.x * rows;
@@ -187,9 +276,10 @@ __global__ __launch_bounds__(256) void few_dz_kernel(const FewArgs a) {
     // the difference is exact; an infinity leaves nothing
     t_lo[row][tok] = (hi & 0x7FFF) == 0x7F80 ? (uint16_t)0 : round_bf16(x - widen_bf16(hi));
   };
-  if (b0 + w0 < V) {
+  {
     f32x4 acc[MB][NB];
-    few_logits<MB, NB, (NB > 2 ? 2 : 3)>(a.W, V, a.hidden, a.N, a.H, b0 + w0, acc);
+    few_logits_of<MB, NB>(a, b0 + w0, lds, acc);
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int tok = 16 * j + (lane & 15);
@@ -227,13 +317,19 @@ __global__ __launch_bounds__(256) void few_dz_kernel(const FewArgs a) {
 // dW[v][h] = sum_tok dz[v][tok] hidden[tok][h]. A wave holds 128 columns of
 // hidden^T as A operands (block pair c: columns 32 c + 8 q + (0..7) fall to
 // quarter q, so a lane ends with 8 consecutive ones) and walks vocabulary
-// groups of 16, the next group's cotangent in flight.
-template <int NB, bool BF16>
+// groups of 16, the next group's cotangent in flight. Bound by the stores: the
+// group's 16 x 128 results turn in the wave's LDS, so that a store covers whole
+// lines (4 rows x 256 bytes of bf16, 2 x 512 of float32) and not 16 pieces of 64.
+template <int NB, bool BF16, bool ADD>
 __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
   constexpr int NP = 16 * NB, KS = NP / 32;
+  constexpr int bytes = BF16 ? 2 : 4, pitch = 128 * bytes + 16;
+  constexpr int per_row = 128 * bytes / 16, stores = 16 * per_row / 64;   // 16-byte pieces of a row; stores of a group
+  __shared__ __attribute__((aligned(16))) char turn[4][16 * pitch];
   const int lane = threadIdx.x & 63;
   const int col = lane & 15, q = lane >> 4;
-  const int w = blockIdx.x * 4 + wave_id();
+  const int wave = wave_id();
+  const int w = xcd_remap(blockIdx.x, gridDim.x) * 4 + wave;   // a split's strips share an XCD's L2
   const int strip = w % a.strips, split = w / a.strips;
   if (split >= a.dw_splits) return;
   const int H = a.H, V = a.V;
@@ -256,8 +352,8 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
       lo[k] = *reinterpret_cast<const bf16x8*>(a.dz_lo + at + 32 * k);
     }
   };
-  if (g_lo < g_hi) load(g_lo);
-  for (int g = g_lo; g < g_hi; ++g) {
+  char* mine = turn[wave];
+  auto group = [&](int g, bool checked) {
     f32x4 acc[8];
 #pragma unroll
     for (int b = 0; b < 8; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -268,35 +364,52 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
 #pragma unroll
       for (int b = 0; b < 8; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], hi[k], acc[b], 0, 0, 0);
     }
-    if (g + 1 < g_hi) load(g + 1);
-    const int row = 16 * g + col;
-    if (row >= V) continue;
+    load(g + 1);
+    if (ADD) {   // the sum is rounded once: the old values join in float32, where they lie
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (h0 + 32 * c >= H) continue;
-      const int64_t at = (int64_t)row * H + h0 + 32 * c + 8 * q;
-      f32x4 x = acc[2 * c], y = acc[2 * c + 1];
-      if (BF16) {
-        uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dW) + at);
-        if (a.add_dW) {
-          const uint4 o = *p;
-          x += f32x4{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u), __uint_as_float(o.y << 16),
-                     __uint_as_float(o.y & 0xFFFF0000u)};
-          y += f32x4{__uint_as_float(o.z << 16), __uint_as_float(o.z & 0xFFFF0000u), __uint_as_float(o.w << 16),
-                     __uint_as_float(o.w & 0xFFFF0000u)};
+      for (int c = 0; c < 4; ++c) {
+        const int row = 16 * g + col;
+        if (row >= V || h0 + 32 * c >= H) continue;
+        const int64_t at = (int64_t)row * H + h0 + 32 * c + 8 * q;
+        if (BF16) {
+          const u32x4 o = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dW) + at);
+          acc[2 * c] += f32x4{__uint_as_float(o[0] << 16), __uint_as_float(o[0] & 0xFFFF0000u),
+                              __uint_as_float(o[1] << 16), __uint_as_float(o[1] & 0xFFFF0000u)};
+          acc[2 * c + 1] += f32x4{__uint_as_float(o[2] << 16), __uint_as_float(o[2] & 0xFFFF0000u),
+                                  __uint_as_float(o[3] << 16), __uint_as_float(o[3] & 0xFFFF0000u)};
+        } else {
+          const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dW) + at);
+          acc[2 * c] += p[0];
+          acc[2 * c + 1] += p[1];
         }
-        *p = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-      } else {
-        f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(a.dW) + at);
-        if (a.add_dW) {
-          x += p[0];
-          y += p[1];
-        }
-        p[0] = x;
-        p[1] = y;
       }
     }
-  }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const f32x4 x = acc[2 * c], y = acc[2 * c + 1];
+      char* p = mine + col * pitch + (32 * c + 8 * q) * bytes;
+      if (BF16) {
+        *reinterpret_cast<u32x4*>(p) =
+            u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+      } else {
+        reinterpret_cast<f32x4*>(p)[0] = x;
+        reinterpret_cast<f32x4*>(p)[1] = y;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+#pragma unroll
+    for (int i = 0; i < stores; ++i) {
+      const int r = (64 * i + lane) / per_row, piece = lane % per_row;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * pitch + 16 * piece);
+      if (checked && (16 * g + r >= V || h0 + 16 / bytes * piece >= H)) continue;
+      *reinterpret_cast<u32x4*>(static_cast<char*>(a.dW) + ((int64_t)(16 * g + r) * H + h0) * bytes + 16 * piece) = v;
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  load(g_lo);
+  const int whole = h0 + 128 <= H ? min(g_hi, V / 16) : g_lo;   // groups whose every store lies inside
+  for (int g = g_lo; g < whole; ++g) group(g, false);
+  for (int g = max(g_lo, whole); g < g_hi; ++g) group(g, true);
 }
 
 // dh[tok][h] = sum_v dz[v][tok] W[v][h] over one split of the vocabulary and 256
@@ -306,13 +419,15 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
 // so that the transposed reads of 16 lanes (4 rows x 32 bytes) meet no bank
 // twice. Rows past the split are 0 in both operands.
 template <int NB>
-__global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
+__global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
   constexpr int NP = 16 * NB, pitch = 2 * NP + 16;
   constexpr int w_bytes = 32 * 512, z_bytes = 32 * pitch, buf = w_bytes + 2 * z_bytes;
   __shared__ __attribute__((aligned(16))) char lds[2 * buf];
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const int strip = blockIdx.x % a.dh_strips, split = blockIdx.x / a.dh_strips;
+  const int vid = xcd_remap(blockIdx.x, gridDim.x);   // a split's strips share an XCD's L2
+  const int strip = vid % a.dh_strips, split = vid / a.dh_strips;
+  if (split >= a.dh_splits) return;
   const int H = a.H;
   const int h0 = strip * 256;
   const int v_lo = split * a.dh_rows, v_hi = min(v_lo + a.dh_rows, a.V);
@@ -325,14 +440,14 @@ __global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
   constexpr int z_per = NP / 8;                          // chunks of a cotangent row
   constexpr int z_n = 2 * 32 * z_per;                    // chunks of both words
   constexpr int z_each = (z_n + 255) / 256;
-  uint4 sw[4], sz[z_each];
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  auto fetch = [&](int step) {
+  u32x4 sw2[2][4], sz2[2][z_each];   // two steps in flight
+  const u32x4 none = {0u, 0u, 0u, 0u};
+  auto fetch = [&](int step, u32x4 (&sw)[4], u32x4 (&sz)[z_each]) {
     const int v0 = v_lo + 32 * step;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int v = v0 + (threadIdx.x >> 5) + 8 * c;
-      sw[c] = *reinterpret_cast<const uint4*>(a.W + (int64_t)min(v, v_hi - 1) * H + w_col);
+      sw[c] = *reinterpret_cast<const u32x4*>(a.W + (int64_t)min(v, v_hi - 1) * H + w_col);
       if (v >= v_hi) sw[c] = none;
     }
 #pragma unroll
@@ -341,20 +456,20 @@ __global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
       const int v = v0 + (i / z_per) % 32;
       const uint16_t* src = i < 32 * z_per ? a.dz_hi : a.dz_lo;
       sz[c] = none;
-      if (i < z_n && v < v_hi) sz[c] = *reinterpret_cast<const uint4*>(src + (int64_t)v * NP + 8 * (i % z_per));
+      if (i < z_n && v < v_hi) sz[c] = *reinterpret_cast<const u32x4*>(src + (int64_t)v * NP + 8 * (i % z_per));
     }
   };
-  auto stage = [&](char* p) {
+  auto stage = [&](char* p, const u32x4 (&sw)[4], const u32x4 (&sz)[z_each]) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int r = (threadIdx.x >> 5) + 8 * c;
-      *reinterpret_cast<uint4*>(p + r * 512 + ((chunk ^ swz_mn(r)) << 4)) = sw[c];
+      *reinterpret_cast<u32x4*>(p + r * 512 + ((chunk ^ swz_mn(r)) << 4)) = sw[c];
     }
 #pragma unroll
     for (int c = 0; c < z_each; ++c) {
       const int i = threadIdx.x + 256 * c;
       if (i < z_n)
-        *reinterpret_cast<uint4*>(p + w_bytes + (i < 32 * z_per ? 0 : z_bytes) + (i / z_per) % 32 * pitch + 16 * (i % z_per)) = sz[c];
+        *reinterpret_cast<u32x4*>(p + w_bytes + (i < 32 * z_per ? 0 : z_bytes) + (i / z_per) % 32 * pitch + 16 * (i % z_per)) = sz[c];
     }
   };
   // transposed reads: lane s of a 16-lane group points at K-row 8 q + s / 4 (+ 4
@@ -374,12 +489,11 @@ __global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  fetch(0);
-  for (int step = 0; step < steps; ++step) {
+  auto turn = [&](int step, u32x4 (&sw)[4], u32x4 (&sz)[z_each]) {
     char* p = lds + (step & 1) * buf;
-    stage(p);
+    stage(p, sw, sz);
     __syncthreads();   // one a step: a buffer is refilled two steps on, after every wave is past the step between
-    if (step + 1 < steps) fetch(step + 1);
+    if (step + 2 < steps) fetch(step + 2, sw, sz);
     bf16x8 fw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -395,6 +509,12 @@ __global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fz, acc[i][j], 0, 0, 0);
       }
+  };
+  fetch(0, sw2[0], sz2[0]);
+  if (steps > 1) fetch(1, sw2[1], sz2[1]);
+  for (int step = 0; step < steps; step += 2) {
+    turn(step, sw2[0], sz2[0]);
+    if (step + 1 < steps) turn(step + 1, sw2[1], sz2[1]);
   }
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
@@ -407,18 +527,20 @@ __global__ __launch_bounds__(256) void few_dh_kernel(const FewArgs a) {
   }
 }
 
-// Row blocks per wave: as many as leave a workgroup per CU, so that hidden is
-// fetched for as many rows at a time as the vocabulary allows.
+// Row blocks (of 16) per wave: as few as let two workgroups a CU cover the
+// vocabulary at once, so that no CU is left a second round (V = 151936: 475
+// workgroups of 5 blocks a wave take 201 us for 64 tokens, 594 of 4 take 311).
+constexpr int kMostBlocks = 5;
 int few_blocks(int64_t V) {
-  for (int mb = 4; mb > 1; mb /= 2)
-    if ((V + 64 * mb - 1) / (64 * mb) >= kNumCUs) return mb;
-  return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kMostBlocks, (V + 128 * kNumCUs - 1) / (128 * kNumCUs)));
 }
 
 template <class F>
 void with_sizes(int mb, int nb, F f) {
   auto rows = [&](auto n) {
-    if (mb == 4) f(std::integral_constant<int, 4>{}, n);
+    if (mb == 5) f(std::integral_constant<int, 5>{}, n);
+    else if (mb == 4) f(std::integral_constant<int, 4>{}, n);
+    else if (mb == 3) f(std::integral_constant<int, 3>{}, n);
     else if (mb == 2) f(std::integral_constant<int, 2>{}, n);
     else f(std::integral_constant<int, 1>{}, n);
   };
@@ -458,27 +580,32 @@ hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kFewDz, stream, 0.0, 2.0 * (N + V) * H + 64.0 * nb * V);
-  // waves for dW: 8 a CU, but no less than 4 groups of 16 rows each
-  a.strips = (a.H + 127) / 128;
-  a.dw_splits = std::max(1, std::min((a.V + 63) / 64, 8 * kNumCUs / a.strips));
-  const unsigned blocks = (unsigned)((a.strips * a.dw_splits + 3) / 4);
+  const unsigned dh_blocks = (unsigned)((a.dh_strips * a.dh_splits + 7) / 8 * 8);
   trace_begin(stream);
-  if (nb == 2) {
-    if (bf16) hipLaunchKernelGGL((few_dw_kernel<2, true>), dim3(blocks), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((few_dw_kernel<2, false>), dim3(blocks), dim3(256), 0, stream, a);
-  } else {
-    if (bf16) hipLaunchKernelGGL((few_dw_kernel<4, true>), dim3(blocks), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((few_dw_kernel<4, false>), dim3(blocks), dim3(256), 0, stream, a);
-  }
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  trace_end(kFewDw, stream, 2.0 * N * H * V, (bf16 ? 2.0 : 4.0) * V * H + 64.0 * nb * V);
-  trace_begin(stream);
-  if (nb == 2) hipLaunchKernelGGL((few_dh_kernel<2>), dim3(a.dh_strips * a.dh_splits), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((few_dh_kernel<4>), dim3(a.dh_strips * a.dh_splits), dim3(256), 0, stream, a);
+  if (nb == 2) hipLaunchKernelGGL((few_dh_kernel<2>), dim3(dh_blocks), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((few_dh_kernel<4>), dim3(dh_blocks), dim3(256), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kFewDh, stream, 2.0 * N * H * V, 2.0 * V * H + 64.0 * nb * V + 4.0 * a.dh_splits * N * H);
+  // waves for dW: 8 a CU, but no less than 4 groups of 16 rows each
+  a.strips = (a.H + 127) / 128;
+  a.dw_splits = std::max(1, std::min((a.V + 63) / 64, 8 * kNumCUs / a.strips));
+  const unsigned blocks = (unsigned)((a.strips * a.dw_splits + 31) / 32 * 8);
+  trace_begin(stream);
+  auto dw = [&](auto n, auto half, auto add) {
+    hipLaunchKernelGGL((few_dw_kernel<n(), half(), add()>), dim3(blocks), dim3(256), 0, stream, a);
+  };
+  auto dw_types = [&](auto n) {
+    std::true_type yes;
+    std::false_type no;
+    if (bf16) a.add_dW ? dw(n, yes, yes) : dw(n, yes, no);
+    else a.add_dW ? dw(n, no, yes) : dw(n, no, no);
+  };
+  if (nb == 2) dw_types(std::integral_constant<int, 2>{});
+  else dw_types(std::integral_constant<int, 4>{});
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kFewDw, stream, 2.0 * N * H * V, (bf16 ? 2.0 : 4.0) * V * H + 64.0 * nb * V);
   return hipSuccess;
 }
 
