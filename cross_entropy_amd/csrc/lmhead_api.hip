@@ -692,12 +692,24 @@ struct DistillPlan {
   int dh_strips = 0, dh_rows = 0;
 };
 
-// The kernels for few tokens take N up to 64 (a vocabulary below the
-// backward's limit), and in the backward hold the cotangent of 32 or 64 tokens
-// as two bf16 words, which chunk_size has to allow.
-bool few_forward(int64_t N, int64_t V) { return N <= lmh::kFewTokens && V < (int64_t(1) << 23); }
-int64_t few_padded(int64_t N) { return N <= 32 ? 32 : 64; }
-bool few_backward(int64_t N, int64_t V, int64_t chunk_size) { return few_forward(N, V) && few_padded(N) <= chunk_size; }
+// When the kernels for few tokens (lmhead_few.hip) run: they fetch W once per
+// 64 tokens, where the 256 x 256 tiles fetch it once per 256 but spend a whole
+// tile's time on what little there is. Measured (us, few / tiles): forward, H
+// 2560, V 151936: 64 tokens 170 / 234, 128: 251 / 227; 256 tokens: V 8000 41 /
+// 65, V 32000 118 / 68. Backward, V 151936: 128 tokens 834 / 958, 256: 1332 /
+// 1035; 256 tokens: V 8000 109 / 139, V 32000 311 / 265, and 256 x 256 x 4096
+// 41 / 135.
+constexpr int64_t kFewVocabulary = 16384;
+bool few_sizes(int64_t N, int64_t V, int64_t any_vocabulary) {
+  return N <= any_vocabulary ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && V <= kFewVocabulary;
+}
+bool few_forward(int64_t N, int64_t V) { return few_sizes(N, V, 64); }
+// The backward holds the tokens' whole cotangent, as two bf16 words up to 64
+// tokens and one above, which chunk_size has to allow.
+int64_t few_padded(int64_t N) { return N <= 32 ? 32 : lmh::round_up(N, 64); }
+bool few_backward(int64_t N, int64_t V, int64_t chunk_size) {
+  return few_sizes(N, V, 128) && few_padded(N) * (N <= 64 ? 2 : 1) <= 2 * chunk_size;
+}
 
 // Splits of the dh tiles over the block's vocabulary. A launch holds the dh
 // tiles (K = Vb), the dW tiles (K = Ct) and the next block's cotangent tiles
@@ -732,7 +744,7 @@ lmh::FwdPlan plan_distill_forward(int64_t N, int64_t H, int64_t V) {
   if (!few_forward(N, V)) return lmh::plan_forward(N, H, V, lmh::kNumCUs);
   lmh::FwdPlan p;
   p.S = lmh::few_splits(V);
-  p.part_ld = lmh::kFewTokens;
+  p.part_ld = lmh::round_up(std::max<int64_t>(N, 1), 64);
   p.bytes = (size_t)p.S * p.part_ld * 16;
   return p;
 }
@@ -758,12 +770,13 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
   d.off_part = d.off_val + room(n * (K + 1) * 4);
   if (d.few) {
     d.off_ht = d.off_part;
-    d.off_hi = d.off_ht + room(H * lmh::kFewTokens * 2);
+    d.off_hi = d.off_ht + room(H * lmh::round_up(n, 64) * 2);
     d.off_lo = d.off_hi + room(V * few_padded(n) * 2);
-    d.off_part = d.off_lo + room(V * few_padded(n) * 2);
+    d.off_part = d.off_lo + (n <= 64 ? room(V * few_padded(n) * 2) : 0);
     // two workgroups a CU, of at least 128 vocabulary rows each
     d.dh_strips = (int)lmh::ceil_div(H, 256);
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>((few_padded(n) == 32 ? 3 : 2) * lmh::kNumCUs / d.dh_strips, lmh::ceil_div(V, 128)));
+    const int64_t wgs = (n <= 32 ? 3 : 2) * lmh::kNumCUs / (d.dh_strips * lmh::ceil_div(n, 64));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(wgs, lmh::ceil_div(V, 128)));
     d.dh_rows = (int)lmh::round_up(lmh::ceil_div(V, most), 32);
     d.splits = (int)lmh::ceil_div(V, d.dh_rows);
     d.bytes = d.off_part + room(d.splits * n * H * 4);
@@ -859,7 +872,8 @@ hipError_t few_bwd(const DistillPlan& d, const lmh::DistillPrepArgs& prep, const
   hipError_t e = lmh::launch_distill_prep(prep, s);
   uint16_t* ht = reinterpret_cast<uint16_t*>(ws + d.off_ht);
   if (e == hipSuccess)
-    e = lmh::launch_transpose(hidden, H, prep.N, H, lmh::kFewTokens, H, prep.tgt, prep.V, ht, lmh::kFewTokens, s);
+    e = lmh::launch_transpose(hidden, H, prep.N, H, lmh::round_up(prep.N, 64), H, prep.tgt, prep.V, ht,
+                              lmh::round_up(prep.N, 64), s);
   if (e != hipSuccess) return e;
   lmh::FewArgs a{};
   a.hidden = hidden;
@@ -876,7 +890,8 @@ hipError_t few_bwd(const DistillPlan& d, const lmh::DistillPrepArgs& prep, const
   a.ent_val = prep.ent_val;
   a.K1 = prep.K + 1;
   a.dz_hi = reinterpret_cast<uint16_t*>(ws + d.off_hi);
-  a.dz_lo = reinterpret_cast<uint16_t*>(ws + d.off_lo);
+  a.dz_lo = prep.N <= 64 ? reinterpret_cast<uint16_t*>(ws + d.off_lo) : nullptr;
+  a.padded = (int)few_padded(prep.N);
   a.ht = ht;
   a.dW = dW;
   a.add_dW = (flags & LMH_BWD_ACCUMULATE_DW) != 0;

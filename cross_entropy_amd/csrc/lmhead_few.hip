@@ -1,23 +1,28 @@
-// lmhead_few.hip -- the distillation head for few tokens (up to 64), for gfx950.
+// lmhead_few.hip -- the distillation head for few tokens, for gfx950.
 //
-// With so few tokens every pass is bound by the vocabulary table: the forward
+// With few tokens every pass is bound by the vocabulary table: the forward
 // reads W once (2 V H bytes), the backward reads it twice (for the logits and
 // for dh) and writes dW once. The head's 256 x 256 tiles would spend 4 to 256
 // times the products, and leave the chip waiting at their prologues and
-// epilogues. Here waves stream W from memory through registers:
+// epilogues. Here waves stream W from memory through registers, for tiles of
+// up to 64 tokens:
 //
 //   logits   a wave holds 16 MB vocabulary rows x 16 NB tokens and walks H, so a
-//            row of W is loaded by one wave only, and hidden comes from cache
+//            row of W is loaded by one wave only
 //   dW       (V x H, K = tokens) a wave keeps its columns of hidden^T in
-//            registers and walks the vocabulary, storing 256 bytes of 16 rows
-//            per step
+//            registers and walks the vocabulary
 //   dh       (tokens x H, K = V) a workgroup stages 32 rows of W and of the
 //            cotangent in LDS and reads both transposed; the vocabulary is
 //            split over workgroups, whose float32 partials are summed in order
 //
-// The cotangent is held as two bf16 words (its rounding and what that left):
-// its products then cost twice the matrix instructions, which are idle here,
-// and carry 16 bits instead of 8.
+// Up to 64 tokens the cotangent is held as two bf16 words (its rounding and
+// what that left): its products then cost twice the matrix instructions, which
+// are idle there, and carry 16 bits instead of 8.
+//
+// Measured with H = 2560, V = 151936 (778 MB of W; a copy reaches 5.0 TB/s): the
+// forward's pass 143 us for one token and 147 us for 64 (5.4 TB/s); in the backward
+// the cotangent 150-170 us, dh 135-190 us and dW 200-240 us, each paying for the
+// write-back of the last one's stores: 2.33 GB in 0.55-0.6 ms, 4.1 TB/s.
 //
 // MFMA 16x16x32: lane l supplies row (l % 16) of A and column (l % 16) of B with
 // 8 K values of its quarter l / 16; register r of lane l holds
@@ -93,9 +98,9 @@ __device__ __forceinline__ void few_logits(const uint16_t* W, int V, const uint1
   }
 }
 
-// The same for 64 tokens, hidden through LDS: from cache, four waves' fetches of
-// 64 tokens' rows come to 0.8 of W's bytes again each and bound the pass (240 us
-// where memory takes 145). The workgroup stages kFewK of K of every token, the
+// The same for 64 tokens, hidden through LDS: from cache, each wave fetches
+// 0.8 of W's bytes of hidden again, which bounds the pass (240 us against 147 at
+// H = 2560, V = 151936). The workgroup stages kFewK of K of every token, the
 // next chunk in registers meanwhile; rows are padded by 16 bytes, so the 16
 // tokens of a fragment read fall on 16 different bank groups. `lds` holds two
 // chunks; every wave of the workgroup has to call, also one without rows.
@@ -169,10 +174,24 @@ __device__ __forceinline__ void few_logits_lds(const uint16_t* W, int V, const u
   }
 }
 
+// The token tile (up to 64 tokens) and the split of a workgroup: the tiles of a
+// split are neighbours on one XCD, whose L2 then serves all but the first
+// with the split's rows of W. split -1: a workgroup too many.
+struct FewTile {
+  int tok0, n, split;
+};
+__device__ __forceinline__ FewTile few_tile(const FewArgs& a, int splits) {
+  const int vid = xcd_remap(blockIdx.x, gridDim.x);
+  const int tok0 = vid % a.tiles * 64;
+  const int split = vid / a.tiles;
+  return {tok0, min(64, a.N - tok0), split < splits ? split : -1};
+}
+
 template <int MB, int NB>
-__device__ __forceinline__ void few_logits_of(const FewArgs& a, int r0, char* lds, f32x4 (&acc)[MB][NB]) {
-  if constexpr (NB == 4) few_logits_lds<MB, 2>(a.W, a.V, a.hidden, a.N, a.H, r0, lds, acc);
-  else few_logits<MB, NB, 3>(a.W, a.V, a.hidden, a.N, a.H, r0, acc);
+__device__ __forceinline__ void few_logits_of(const FewArgs& a, const FewTile& t, int r0, char* lds, f32x4 (&acc)[MB][NB]) {
+  const uint16_t* hidden = a.hidden + (int64_t)t.tok0 * a.H;
+  if constexpr (NB == 4) few_logits_lds<MB, 2>(a.W, a.V, hidden, t.n, a.H, r0, lds, acc);
+  else few_logits<MB, NB, 3>(a.W, a.V, hidden, t.n, a.H, r0, acc);
 }
 template <int NB>
 constexpr int few_lds() { return NB == 4 ? kFewLds : 16; }
@@ -185,7 +204,9 @@ __global__ __launch_bounds__(256, 2) void few_stats_kernel(const FewArgs a) {
   __shared__ float4 xch[4][16 * NB];
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const int r0 = (blockIdx.x * 4 + wave) * 16 * MB;
+  const FewTile t = few_tile(a, a.splits);
+  if (t.split < 0) return;
+  const int r0 = (t.split * 4 + wave) * 16 * MB;
   const int V = a.V;
   Stats st[NB];
 #pragma unroll
@@ -195,11 +216,11 @@ __global__ __launch_bounds__(256, 2) void few_stats_kernel(const FewArgs a) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int tok = 16 * j + (lane & 15);
-      tgt[j] = a.targets != nullptr ? a.targets[min(tok, a.N - 1)] : -1;
+      tgt[j] = a.targets != nullptr ? a.targets[t.tok0 + min(tok, t.n - 1)] : -1;
       if (tgt[j] < 0 || tgt[j] >= V) tgt[j] = -1;
     }
     f32x4 acc[MB][NB];
-    few_logits_of<MB, NB>(a, r0, lds, acc);
+    few_logits_of<MB, NB>(a, t, r0, lds, acc);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       // rows past V take no part: their logits never win the max, and their
@@ -243,21 +264,21 @@ __global__ __launch_bounds__(256, 2) void few_stats_kernel(const FewArgs a) {
   }
   __syncthreads();
   const int tok = threadIdx.x;
-  if (tok < 16 * NB && tok < a.N) {
+  if (tok < 16 * NB && tok < t.n) {
     Stats m{kNegBig, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const float4 p = xch[w][tok];
       m = merge_stats(m, Stats{p.x, p.y, p.z, p.w});
     }
-    reinterpret_cast<float4*>(a.part)[(int64_t)blockIdx.x * a.part_ld + tok] = make_float4(m.m2, m.s1, m.s2, m.zt);
+    reinterpret_cast<float4*>(a.part)[t.split * a.part_ld + t.tok0 + tok] = make_float4(m.m2, m.s1, m.s2, m.zt);
   }
 }
 
 // Backward: the cotangent of the workgroup's 64 MB vocabulary rows, formed in
 // LDS as [row][token] pairs of bf16 words, the tokens' special entries
-// overwriting theirs there, and stored as [V][16 NB], high words and low words
-// apart. Masked tokens and tokens past N are 0.
+// overwriting theirs there, and stored as [V][padded tokens], high words and (up
+// to 64 tokens) low words apart. Masked tokens and tokens past N are 0.
 template <int MB, int NB>
 __global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
   constexpr int NP = 16 * NB, rows = 64 * MB, tile = rows * NP * 2;
@@ -267,7 +288,9 @@ __global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
   uint16_t (*t_lo)[NP] = reinterpret_cast<uint16_t (*)[NP]>(lds + tile);
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const int b0 = blockIdx.x * rows;
+  const FewTile t = few_tile(a, a.splits);
+  if (t.split < 0) return;
+  const int b0 = t.split * rows;
   const int w0 = wave * 16 * MB;
   const int V = a.V;
   auto put = [&](int row, int tok, float x) {
@@ -278,14 +301,14 @@ __global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
   };
   {
     f32x4 acc[MB][NB];
-    few_logits_of<MB, NB>(a, b0 + w0, lds, acc);
+    few_logits_of<MB, NB>(a, t, b0 + w0, lds, acc);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int tok = 16 * j + (lane & 15);
-      const int at = min(tok, a.N - 1);
-      const int t = a.targets[at];
-      const bool live = tok < a.N && t >= 0 && t < V;
+      const int at = t.tok0 + min(tok, t.n - 1);
+      const int id = a.targets[at];
+      const bool live = tok < t.n && id >= 0 && id < V;
       const float nlse = live ? -a.lse[at] * kLog2e : 0.0f;
       const float c0 = live ? -a.ga[at] * a.invT : 0.0f;
 #pragma unroll
@@ -299,32 +322,33 @@ __global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
     }
   }
   __syncthreads();
-  const int n = a.N * a.K1;
+  const int n = t.n * a.K1;
+  const int32_t* ent_id = a.ent_id + (int64_t)t.tok0 * a.K1;
   for (int e = threadIdx.x; e < n; e += 256) {
-    const int id = a.ent_id[e];
-    if (id >= b0 && id < min(b0 + rows, V)) put(id - b0, e / a.K1, a.ent_val[e]);
+    const int id = ent_id[e];
+    if (id >= b0 && id < min(b0 + rows, V)) put(id - b0, e / a.K1, a.ent_val[(int64_t)t.tok0 * a.K1 + e]);
   }
   __syncthreads();
   constexpr int per_row = NP / 8;   // 16-byte chunks
   for (int c = threadIdx.x; c < rows * per_row; c += 256) {
     if (b0 + c / per_row >= V) break;
-    const int64_t at = (int64_t)b0 * per_row + c;
-    reinterpret_cast<uint4*>(a.dz_hi)[at] = reinterpret_cast<const uint4*>(t_hi)[c];
-    reinterpret_cast<uint4*>(a.dz_lo)[at] = reinterpret_cast<const uint4*>(t_lo)[c];
+    const int64_t at = (int64_t)(b0 + c / per_row) * (a.padded / 8) + t.tok0 / 8 + c % per_row;
+    reinterpret_cast<u32x4*>(a.dz_hi)[at] = reinterpret_cast<const u32x4*>(t_hi)[c];
+    if (a.dz_lo != nullptr) reinterpret_cast<u32x4*>(a.dz_lo)[at] = reinterpret_cast<const u32x4*>(t_lo)[c];
   }
 }
 
-// dW[v][h] = sum_tok dz[v][tok] hidden[tok][h]. A wave holds 128 columns of
-// hidden^T as A operands (block pair c: columns 32 c + 8 q + (0..7) fall to
+// dW[v][h] = sum_tok dz[v][tok] hidden[tok][h]. A wave holds 128 columns
+// (64 above 64 tokens) of hidden^T as A operands (block pair c: columns 32 c + 8 q + (0..7) fall to
 // quarter q, so a lane ends with 8 consecutive ones) and walks vocabulary
 // groups of 16, the next group's cotangent in flight. Bound by the stores: the
-// group's 16 x 128 results turn in the wave's LDS, so that a store covers whole
+// group's results turn in the wave's LDS, so that a store covers whole
 // lines (4 rows x 256 bytes of bf16, 2 x 512 of float32) and not 16 pieces of 64.
-template <int NB, bool BF16, bool ADD>
+template <int KS, int BL, bool LO, bool BF16, bool ADD>
 __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
-  constexpr int NP = 16 * NB, KS = NP / 32;
-  constexpr int bytes = BF16 ? 2 : 4, pitch = 128 * bytes + 16;
-  constexpr int per_row = 128 * bytes / 16, stores = 16 * per_row / 64;   // 16-byte pieces of a row; stores of a group
+  constexpr int NP = 32 * KS, ht_ld = NP < 64 ? 64 : NP, cols = 16 * BL;
+  constexpr int bytes = BF16 ? 2 : 4, pitch = cols * bytes + 16;
+  constexpr int per_row = cols * bytes / 16, stores = 16 * per_row / 64;   // 16-byte pieces of a row; stores of a group
   __shared__ __attribute__((aligned(16))) char turn[4][16 * pitch];
   const int lane = threadIdx.x & 63;
   const int col = lane & 15, q = lane >> 4;
@@ -333,41 +357,43 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
   const int strip = w % a.strips, split = w / a.strips;
   if (split >= a.dw_splits) return;
   const int H = a.H, V = a.V;
-  const int h0 = strip * 128;
-  bf16x8 ht[8][KS];
+  const int h0 = strip * cols;
+  bf16x8 ht[BL][KS];
 #pragma unroll
-  for (int b = 0; b < 8; ++b) {
+  for (int b = 0; b < BL; ++b) {
     const int h = min(h0 + 32 * (b >> 1) + 8 * (col >> 2) + 4 * (b & 1) + (col & 3), H - 1);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) ht[b][k] = *reinterpret_cast<const bf16x8*>(a.ht + (int64_t)h * 64 + 32 * k + 8 * q);
+    for (int k = 0; k < KS; ++k) ht[b][k] = *reinterpret_cast<const bf16x8*>(a.ht + (int64_t)h * ht_ld + 32 * k + 8 * q);
   }
   const int groups = (V + 15) / 16;
   const int g_lo = (int)((int64_t)split * groups / a.dw_splits), g_hi = (int)((int64_t)(split + 1) * groups / a.dw_splits);
-  bf16x8 hi[KS], lo[KS];
+  bf16x8 hi[KS], lo[LO ? KS : 1];
   auto load = [&](int g) {
     const int64_t at = (int64_t)min(16 * g + col, V - 1) * NP + 8 * q;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       hi[k] = *reinterpret_cast<const bf16x8*>(a.dz_hi + at + 32 * k);
-      lo[k] = *reinterpret_cast<const bf16x8*>(a.dz_lo + at + 32 * k);
+      if (LO) lo[k] = *reinterpret_cast<const bf16x8*>(a.dz_lo + at + 32 * k);
     }
   };
   char* mine = turn[wave];
   auto group = [&](int g, bool checked) {
-    f32x4 acc[8];
+    f32x4 acc[BL];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < BL; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
+      if (LO) {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], lo[k], acc[b], 0, 0, 0);
+        for (int b = 0; b < BL; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], lo[LO ? k : 0], acc[b], 0, 0, 0);
+      }
 #pragma unroll
-      for (int b = 0; b < 8; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], hi[k], acc[b], 0, 0, 0);
+      for (int b = 0; b < BL; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ht[b][k], hi[k], acc[b], 0, 0, 0);
     }
     load(g + 1);
     if (ADD) {   // the sum is rounded once: the old values join in float32, where they lie
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < BL / 2; ++c) {
         const int row = 16 * g + col;
         if (row >= V || h0 + 32 * c >= H) continue;
         const int64_t at = (int64_t)row * H + h0 + 32 * c + 8 * q;
@@ -385,7 +411,7 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
       }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < BL / 2; ++c) {
       const f32x4 x = acc[2 * c], y = acc[2 * c + 1];
       char* p = mine + col * pitch + (32 * c + 8 * q) * bytes;
       if (BF16) {
@@ -407,7 +433,7 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
     __builtin_amdgcn_wave_barrier();
   };
   load(g_lo);
-  const int whole = h0 + 128 <= H ? min(g_hi, V / 16) : g_lo;   // groups whose every store lies inside
+  const int whole = h0 + cols <= H ? min(g_hi, V / 16) : g_lo;   // groups whose every store lies inside
   for (int g = g_lo; g < whole; ++g) group(g, false);
   for (int g = max(g_lo, whole); g < g_hi; ++g) group(g, true);
 }
@@ -418,16 +444,16 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
 // tile core's MN-contiguous slices do, the cotangent's with 16 bytes of padding,
 // so that the transposed reads of 16 lanes (4 rows x 32 bytes) meet no bank
 // twice. Rows past the split are 0 in both operands.
-template <int NB>
+template <int NB, bool LO>
 __global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
-  constexpr int NP = 16 * NB, pitch = 2 * NP + 16;
-  constexpr int w_bytes = 32 * 512, z_bytes = 32 * pitch, buf = w_bytes + 2 * z_bytes;
+  constexpr int NP = 16 * NB, pitch = 2 * NP + 16, words = LO ? 2 : 1;
+  constexpr int w_bytes = 32 * 512, z_bytes = 32 * pitch, buf = w_bytes + words * z_bytes;
   __shared__ __attribute__((aligned(16))) char lds[2 * buf];
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const int vid = xcd_remap(blockIdx.x, gridDim.x);   // a split's strips share an XCD's L2
-  const int strip = vid % a.dh_strips, split = vid / a.dh_strips;
-  if (split >= a.dh_splits) return;
+  const FewTile t = few_tile(a, a.dh_strips * a.dh_splits);   // a split's strips, and a strip's tiles, share an XCD's L2
+  if (t.split < 0) return;
+  const int strip = t.split % a.dh_strips, split = t.split / a.dh_strips;
   const int H = a.H;
   const int h0 = strip * 256;
   const int v_lo = split * a.dh_rows, v_hi = min(v_lo + a.dh_rows, a.V);
@@ -438,7 +464,7 @@ __global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
   const int chunk = threadIdx.x & 31;
   const int w_col = min(h0 + 8 * chunk, H - 8);
   constexpr int z_per = NP / 8;                          // chunks of a cotangent row
-  constexpr int z_n = 2 * 32 * z_per;                    // chunks of both words
+  constexpr int z_n = words * 32 * z_per;                // chunks of the words
   constexpr int z_each = (z_n + 255) / 256;
   u32x4 sw2[2][4], sz2[2][z_each];   // two steps in flight
   const u32x4 none = {0u, 0u, 0u, 0u};
@@ -456,7 +482,7 @@ __global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
       const int v = v0 + (i / z_per) % 32;
       const uint16_t* src = i < 32 * z_per ? a.dz_hi : a.dz_lo;
       sz[c] = none;
-      if (i < z_n && v < v_hi) sz[c] = *reinterpret_cast<const u32x4*>(src + (int64_t)v * NP + 8 * (i % z_per));
+      if (i < z_n && v < v_hi) sz[c] = *reinterpret_cast<const u32x4*>(src + (int64_t)v * a.padded + t.tok0 + 8 * (i % z_per));
     }
   };
   auto stage = [&](char* p, const u32x4 (&sw)[4], const u32x4 (&sz)[z_each]) {
@@ -501,7 +527,7 @@ __global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
       fw[i] = read(at, at + 4 * 512);   // 4 rows on, the swizzle is the same
     }
 #pragma unroll
-    for (int half = 1; half >= 0; --half)
+    for (int half = words - 1; half >= 0; --half)
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const char* at = p + w_bytes + half * z_bytes + t_row * pitch + 32 * j + 8 * (s & 3);
@@ -522,14 +548,15 @@ __global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int h = h0 + 64 * wave + 16 * i + 4 * q;
-      if (tok < a.N && h < H) *reinterpret_cast<f32x4*>(a.dh_part + ((int64_t)split * a.N + tok) * H + h) = acc[i][j];
+      if (tok < t.n && h < H)
+        *reinterpret_cast<f32x4*>(a.dh_part + ((int64_t)split * a.N + t.tok0 + tok) * H + h) = acc[i][j];
     }
   }
 }
 
 // Row blocks (of 16) per wave: as few as let two workgroups a CU cover the
 // vocabulary at once, so that no CU is left a second round (V = 151936: 475
-// workgroups of 5 blocks a wave take 201 us for 64 tokens, 594 of 4 take 311).
+// workgroups of 5 blocks a wave take 143 us for one token, 594 of 4 take 162).
 constexpr int kMostBlocks = 5;
 int few_blocks(int64_t V) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kMostBlocks, (V + 128 * kNumCUs - 1) / (128 * kNumCUs)));
@@ -556,56 +583,72 @@ int few_splits(int64_t V) {
   return (int)((V + rows - 1) / rows);
 }
 
-hipError_t launch_few_stats(const FewArgs& a, hipStream_t stream) {
+static unsigned few_grid(int64_t n) { return (unsigned)((n + 7) / 8 * 8); }
+
+hipError_t launch_few_stats(FewArgs a, hipStream_t stream) {
   const double N = a.N, H = a.H, V = a.V;
+  a.tiles = (a.N + 63) / 64;
+  a.splits = few_splits(a.V);
   trace_begin(stream);
   with_sizes(few_blocks(a.V), a.N <= 16 ? 1 : a.N <= 32 ? 2 : 4, [&](auto mb, auto nb) {
-    hipLaunchKernelGGL((few_stats_kernel<mb(), nb()>), dim3(few_splits(a.V)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((few_stats_kernel<mb(), nb()>), dim3(few_grid((int64_t)a.tiles * a.splits)), dim3(256), 0, stream, a);
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kFewStats, stream, 2.0 * N * H * V, 2.0 * (N + V) * H + 4.0 * N + 16.0 * few_splits(a.V) * N);
+  trace_end(kFewStats, stream, 2.0 * N * H * V, 2.0 * (N + V) * H + 4.0 * N + 16.0 * a.splits * N);
   return hipSuccess;
 }
 
-// The cotangent, then dW and the partials of dh.
+// The cotangent, then the partials of dh and dW (dh first: the end of the table
+// is still in the memory-side cache).
 hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream) {
   const double N = a.N, H = a.H, V = a.V;
+  const bool two = a.dz_lo != nullptr;
   const int nb = a.N <= 32 ? 2 : 4;
+  a.tiles = (a.N + 63) / 64;
+  a.splits = few_splits(a.V);
   trace_begin(stream);
   with_sizes(few_blocks(a.V), nb, [&](auto mb, auto n) {
     constexpr int NB = n() < 2 ? 2 : n();   // K of the gradient products is at least 32 tokens
-    hipLaunchKernelGGL((few_dz_kernel<mb(), NB>), dim3(few_splits(a.V)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((few_dz_kernel<mb(), NB>), dim3(few_grid((int64_t)a.tiles * a.splits)), dim3(256), 0, stream, a);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kFewDz, stream, 0.0, 2.0 * (N + V) * H + 64.0 * nb * V);
-  const unsigned dh_blocks = (unsigned)((a.dh_strips * a.dh_splits + 7) / 8 * 8);
+  const double dz = (two ? 4.0 : 2.0) * a.padded * V;
+  trace_end(kFewDz, stream, 0.0, 2.0 * (N + V) * H + dz);
+  const unsigned dh_blocks = few_grid((int64_t)a.tiles * a.dh_strips * a.dh_splits);
   trace_begin(stream);
-  if (nb == 2) hipLaunchKernelGGL((few_dh_kernel<2>), dim3(dh_blocks), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((few_dh_kernel<4>), dim3(dh_blocks), dim3(256), 0, stream, a);
+  if (nb == 2) hipLaunchKernelGGL((few_dh_kernel<2, true>), dim3(dh_blocks), dim3(256), 0, stream, a);
+  else if (two) hipLaunchKernelGGL((few_dh_kernel<4, true>), dim3(dh_blocks), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((few_dh_kernel<4, false>), dim3(dh_blocks), dim3(256), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kFewDh, stream, 2.0 * N * H * V, 2.0 * V * H + 64.0 * nb * V + 4.0 * a.dh_splits * N * H);
+  trace_end(kFewDh, stream, 2.0 * N * H * V, 2.0 * V * H + dz + 4.0 * a.dh_splits * N * H);
   // waves for dW: 8 a CU, but no less than 4 groups of 16 rows each
-  a.strips = (a.H + 127) / 128;
+  const int cols = two ? 128 : 64;
+  a.strips = (a.H + cols - 1) / cols;
   a.dw_splits = std::max(1, std::min((a.V + 63) / 64, 8 * kNumCUs / a.strips));
-  const unsigned blocks = (unsigned)((a.strips * a.dw_splits + 31) / 32 * 8);
-  trace_begin(stream);
-  auto dw = [&](auto n, auto half, auto add) {
-    hipLaunchKernelGGL((few_dw_kernel<n(), half(), add()>), dim3(blocks), dim3(256), 0, stream, a);
-  };
-  auto dw_types = [&](auto n) {
+  const unsigned blocks = few_grid(((int64_t)a.strips * a.dw_splits + 3) / 4);
+  auto dw = [&](auto ks, auto bl, auto lo) {
     std::true_type yes;
     std::false_type no;
-    if (bf16) a.add_dW ? dw(n, yes, yes) : dw(n, yes, no);
-    else a.add_dW ? dw(n, no, yes) : dw(n, no, no);
+    auto typed = [&](auto half, auto add) {
+      hipLaunchKernelGGL((few_dw_kernel<ks(), bl(), lo(), half(), add()>), dim3(blocks), dim3(256), 0, stream, a);
+    };
+    if (bf16) a.add_dW ? typed(yes, yes) : typed(yes, no);
+    else a.add_dW ? typed(no, yes) : typed(no, no);
   };
-  if (nb == 2) dw_types(std::integral_constant<int, 2>{});
-  else dw_types(std::integral_constant<int, 4>{});
+  trace_begin(stream);
+  constexpr std::integral_constant<int, 4> four{};
+  constexpr std::integral_constant<int, 8> eight{};
+  if (two && a.padded == 32) dw(std::integral_constant<int, 1>{}, eight, std::true_type{});
+  else if (two) dw(std::integral_constant<int, 2>{}, eight, std::true_type{});
+  else if (a.padded == 128) dw(four, four, std::false_type{});
+  else if (a.padded == 192) dw(std::integral_constant<int, 6>{}, four, std::false_type{});
+  else dw(eight, four, std::false_type{});
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kFewDw, stream, 2.0 * N * H * V, (bf16 ? 2.0 : 4.0) * V * H + 64.0 * nb * V);
+  trace_end(kFewDw, stream, 2.0 * N * H * V, (bf16 ? 2.0 : 4.0) * V * H + dz);
   return hipSuccess;
 }
 

@@ -192,7 +192,7 @@ struct DistillPostArgs {
 };
 
 // The distillation for few tokens (lmhead_few.hip).
-constexpr int kFewTokens = 64;
+constexpr int kFewTokens = 256;
 
 struct FewArgs {
   const uint16_t* hidden;
@@ -208,18 +208,19 @@ struct FewArgs {
   const int32_t* ent_id;
   const float* ent_val;
   int K1;
-  uint16_t* dz_hi;          // [V][32 or 64] each
-  uint16_t* dz_lo;
-  const uint16_t* ht;       // hidden^T [H][64], masked tokens and those past N zeroed
+  int padded;               // tokens rounded up to 32 or a multiple of 64
+  uint16_t* dz_hi;          // [V][padded] each
+  uint16_t* dz_lo;          // NULL above 64 tokens
+  const uint16_t* ht;       // hidden^T [H][tokens up to a multiple of 64], masked tokens and those past N zeroed
   void* dW;
   bool add_dW;
-  int strips, dw_splits;    // set by launch_few_bwd
+  int tiles, splits, strips, dw_splits;   // set by the launchers
   float* dh_part;           // [dh_splits][N][H]
   int dh_strips, dh_splits, dh_rows;
 };
 
 int few_splits(int64_t V);   // records per token of the forward
-hipError_t launch_few_stats(const FewArgs& a, hipStream_t stream);
+hipError_t launch_few_stats(FewArgs a, hipStream_t stream);
 hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream);   // the cotangent, dW and the partials of dh
 
 // The norm in front of the head (lmhead_norm.hip); rows of H elements.

@@ -351,9 +351,9 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  * The workspace holds the head's backward workspace (chunk_size bounds the
  * cotangent block as there), 8 N + 8 N (K + 1) bytes of the tokens' special
  * entries and, where a block's dh is summed in splits, at most 64 float32
- * partials of it. Up to 64 tokens (32 or 64, whichever N fits, at most
- * chunk_size) hold their whole cotangent instead, as two bf16 words, and up to
- * 512 float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
+ * partials of it. A call of few tokens (at most 256) whose whole cotangent
+ * chunk_size allows holds that instead, as two bf16 words up to 64 tokens,
+ * and at most 50 MB of float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
  * LMH_WS_FWD, LMH_WS_BWD or LMH_WS_BWD_BF16. A smaller size than the query
  * gives is refused. Results do not depend on anything but the arguments:
  * no atomics take part in sums.
@@ -443,7 +443,7 @@ const char* lmhead_logps_version(void);
  *   8 distill_prep_kernel  (distillation backward: per-token cotangents and special entries)
  *   9 distill_step_kernel  (bwd_step_kernel with its dh tiles split, either gradient type)
  *  10 distill_post_kernel  (special entries into a cotangent block, sum of dh splits)
- *  11 few_stats_kernel     (distillation of up to 64 tokens: forward statistics)
+ *  11 few_stats_kernel     (distillation of few tokens: forward statistics)
  *  12 few_dz_kernel        (its cotangent), 13 few_dw_kernel, 14 few_dh_kernel (its products)
  *  15 norm_fwd_kernel
  *  16 norm_bwd_kernel

@@ -93,10 +93,11 @@ def test_distill_workspace():
             more = q(N, H, V, 5, chunk, kind) - nat.raw_workspace_bytes(N, H, V, chunk, kind)
             ct = up(min(N, 1 << 14))
             assert 0 <= more <= 64 * ct * H * 4 + 8 * N + 48 * N + 4096
-    # few tokens within a chunk: two words of their cotangent, within a float32 [chunk, V]
-    for N, pad in ((1, 32), (32, 32), (33, 64), (64, 64)):
-        b = q(N, 2560, 151936, 5, 64, 1)
-        assert b <= 4 * 151936 * pad + 2 * 2560 * 64 + 512 * N * 2560 * 4 + 8 * N + 48 * N + 4096
+    # few tokens within a chunk: their whole cotangent (within a float32 [chunk, V]) and 50 MB of partials
+    for N, H, V, chunk in ((1, 2560, 151936, 64), (33, 2560, 151936, 64), (64, 128, 9000, 64), (128, 512, 151936, 64),
+                           (256, 16384, 16384, 128)):
+        b = q(N, H, V, 5, chunk, 1)
+        assert b <= max(4 * V * chunk, 4 * V * 64) + 2 * H * 256 + (50 << 20) + 8 * N + 48 * N + 4096
     # beyond 2^31 entries the sizes are still whole
     N, K = 1 << 22, 1024
     assert q(N, 64, 1000, K, 16, 1) > N * (K + 1) * 6

@@ -120,6 +120,15 @@ CASES = [
     (70, 128, 20011, 12, 30, 1.0, "f32", True, True),     # split dh products, several vocabulary blocks, a ragged last
     (300, 192, 9000, 5, 4096, 2.0, "bf16", False, True),  # split over two token tiles in one block
     (1, 64, 40000, 1, 1, 1.0, "f32", False, True),
+    (33, 320, 2000, 7, 64, 1.0, "bf16", False, True),     # few tokens at each count of their tiles
+    (64, 64, 17, 5, 4096, 0.7, "f32", True, True),
+    (65, 192, 5003, 9, 64, 1.0, "f32", False, True),
+    (128, 448, 3000, 20, 64, 1.0, "bf16", True, False),
+    (129, 128, 12345, 6, 4096, 2.0, "f32", False, True),
+    (200, 512, 8000, 32, 128, 1.0, "f32", True, True),
+    (256, 64, 1025, 3, 128, 1.0, "bf16", False, True),
+    (257, 64, 1025, 3, 512, 1.0, "bf16", False, True),
+    (40, 128, 3000, 6, 31, 1.0, "f32", False, True),      # few tokens, beyond what chunk_size allows of their own
     (130, 64, 70, 100, 32, 1.0, "f32", False, True),      # more entries than the vocabulary has ids
 ]
 
