@@ -440,7 +440,7 @@ hipError_t launch_distill_block(const DistillHook& h, const lmh::BwdStep& st, bo
       }
     }
   } else {
-    e = bf16 ? lmh::launch_bwd_step_bf16(st, s) : lmh::launch_bwd_step(st, s);
+    e = lmh::launch_distill_step({st, 1, 0, nullptr}, bf16, s);
   }
   return e == hipSuccess ? lmh::launch_distill_post(a, s) : e;
 }

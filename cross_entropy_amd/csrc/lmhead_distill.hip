@@ -288,12 +288,69 @@ __device__ __forceinline__ void dh_split_tile(const DistillStep& d, int vid, cha
               s.Vtot, acc);
 }
 
-// One backward launch with the dh tiles split: the head's launch (each XCD an
-// eighth of the dh tiles, of the dW tiles and of the next block's cotangent
-// tiles, in this order, the last off per-XCD counters and then off the others')
-// where a few dh tiles would otherwise run the whole vocabulary in sequence
-// while the chip idles.
+// Write one wave's 128 x 128 block of a dW tile as bf16 rows of H, through the
+// (by then idle) slice ring, 64 rows at a time: a lane holds 4 rows of 16
+// columns each, which as they lie take 256 stores of 2 bytes; turned they take
+// 32 of 16 bytes, each covering 4 rows x 256 bytes.
+constexpr int kTurnPitch = 256 + 16;
+static_assert(4 * 64 * kTurnPitch <= kRingBytes, "staging fits in the slice ring");
+__device__ __forceinline__ void write_acc_turned(uint16_t* __restrict__ out, int64_t ld, int r_base, int rows, int c_base,
+                                                 int cols, char* lds, f32x4 (&acc)[kNB][kNB]) {
+  const int lane = threadIdx.x & 63;
+  char* mine = lds + wave_id() * 64 * kTurnPitch;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        pin_acc(acc[4 * half + i][j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<uint16_t*>(mine + acc_row(i, r, lane) * kTurnPitch + 2 * (16 * j + (lane & 15))) =
+              round_bf16(acc[4 * half + i][j][r]);
+      }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int r = 4 * q + (lane >> 4);
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + r * kTurnPitch + 16 * (lane & 15));
+      const int row = r_base + 64 * half + r, col = c_base + 8 * (lane & 15);
+      if (row < rows && col < cols) *reinterpret_cast<uint4*>(out + (int64_t)row * ld + col) = v;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// dW tile: the head's, with the writer above where a gradient's only block is
+// written as bf16.
 template <bool BF16>
+__device__ __forceinline__ void dw_tile_turned(const BwdStep& s, int vid, char* lds) {
+  int mt, hb;
+  raster(vid, s.n_dw / s.n_ht, s.n_ht, 4, mt, hb);
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1;
+  const int wn = wave >> 1;
+  const int m0 = mt * kTile;
+  const int h0 = hb * kTile;
+  const int H = s.H;
+  const Operand oa{s.g_dz + m0, s.ld_dz, kTile};
+  const Operand ob{s.ht + (int64_t)h0 * s.ld_ht + s.g_t0, s.ld_ht, kTile};
+  f32x4 acc[kNB][kNB];
+  Pipe pipe;
+  mma_tile<true, 64>(oa, ob, (s.g_Ct + kBK - 1) / kBK * kBK, lds, acc, pipe, oa.base, ob.base, false);
+  if (s.o_dW.src_kind == kSrcNone && s.o_dW.dst_bf16) {
+    write_acc_turned(static_cast<uint16_t*>(s.o_dW.dst), H, m0 + wm * 128, s.g_Vb, h0 + wn * 128, H, lds, acc);
+  } else {
+    write_acc_g(s.o_dW, H, m0 + wm * 128, s.g_Vb, h0 + wn * 128, H, acc);
+  }
+}
+
+// One backward launch: the head's (each XCD an eighth of the gradient tiles,
+// the kind with the longer K first, then of the next block's cotangent tiles,
+// the last off per-XCD counters and then off the others'), with the dW writer
+// above, and with SPLIT the dh tiles split: where a few dh tiles would
+// otherwise run the whole vocabulary in sequence while the chip idles.
+template <bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillStep d) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   __shared__ int z_tile;
@@ -305,19 +362,26 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillSte
   const int dw_cnt = (xcd + 1) * s.n_dw / 8 - dw_lo;
   const int dh_lo = xcd * n_dh / 8;
   const int dh_cnt = (xcd + 1) * n_dh / 8 - dh_lo;
-  if (loc < dh_cnt) {
-    dh_split_tile(d, dh_lo + loc, lds);
-    return;
-  }
+  const bool dh_first = SPLIT || s.g_Vb > s.g_Ct;   // dh tiles run K = Vb, dW tiles K = Ct
+  const int first_cnt = dh_first ? dh_cnt : dw_cnt;
   if (loc < dh_cnt + dw_cnt) {
-    dw_tile<BF16>(s, dw_lo + loc - dh_cnt, lds);
+    if ((loc < first_cnt) == dh_first) {
+      const int vid = dh_lo + (dh_first ? loc : loc - dw_cnt);
+      if constexpr (SPLIT) dh_split_tile(d, vid, lds);
+      else dh_tile<BF16>(s, vid, lds);
+    } else {
+      const int vid = dw_lo + (dh_first ? loc - dh_cnt : loc);
+      if constexpr (BF16) dw_tile_turned<BF16>(s, vid, lds);
+      else dw_tile<BF16>(s, vid, lds);
+    }
     return;
   }
   const int n_z = s.z_ntt * s.z_nvt;
   if (n_z == 0) return;
   if (threadIdx.x == 0) z_tile = take_z_tile(s, xcd, n_z);
   __syncthreads();
-  if (z_tile >= 0) dz_tile(s, z_tile, lds);
+  const int tile = z_tile;
+  if (tile >= 0) dz_tile(s, tile, lds);
 }
 
 // After each launch, on what it wrote: overwrites the special entries of tokens
@@ -390,7 +454,7 @@ hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream) {
   return hipSuccess;
 }
 
-template <bool BF16>
+template <bool BF16, bool SPLIT>
 static hipError_t launch_step(const DistillStep& d, hipStream_t stream) {
   const BwdStep& st = d.step;
   const int n_z = st.z_ntt * st.z_nvt, n_dh = st.n_dh * d.splits;
@@ -403,7 +467,7 @@ static hipError_t launch_step(const DistillStep& d, hipStream_t stream) {
   const double H = (double)st.H;
   const double gc = (double)st.g_Ct, gv = (double)st.g_Vb, zc = (double)st.z_Ct, zv = (double)st.z_Vb;
   trace_begin(stream);
-  hipLaunchKernelGGL(distill_step_kernel<BF16>, dim3(8 * per), dim3(kThreads), 0, stream, d);
+  hipLaunchKernelGGL((distill_step_kernel<BF16, SPLIT>), dim3(8 * per), dim3(kThreads), 0, stream, d);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kDistillStep, stream, n_g ? 4.0 * gc * gv * H : 0.0,
@@ -413,7 +477,8 @@ static hipError_t launch_step(const DistillStep& d, hipStream_t stream) {
 }
 
 hipError_t launch_distill_step(const DistillStep& d, bool bf16, hipStream_t stream) {
-  return bf16 ? launch_step<true>(d, stream) : launch_step<false>(d, stream);
+  if (d.part == nullptr) return bf16 ? launch_step<true, false>(d, stream) : launch_bwd_step(d.step, stream);
+  return bf16 ? launch_step<true, true>(d, stream) : launch_step<false, true>(d, stream);
 }
 
 hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream) {

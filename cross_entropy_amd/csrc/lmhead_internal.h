@@ -167,7 +167,8 @@ struct DistillPrepArgs {
   float* ent_val;             // [N][K + 1]
 };
 
-// A backward launch whose dh tiles are split over the block's vocabulary.
+// A backward launch, its dh tiles split over the block's vocabulary or (part
+// NULL, splits 1) not.
 struct DistillStep {
   BwdStep step;
   int splits;        // splits of the launch's dh tiles
