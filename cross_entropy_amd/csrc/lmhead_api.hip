@@ -694,21 +694,21 @@ struct DistillPlan {
 
 // When the kernels for few tokens (lmhead_few.hip) run: they fetch W once per
 // 64 tokens, where the 256 x 256 tiles fetch it once per 256 but spend a whole
-// tile's time on what little there is. Measured (us, few / tiles): forward, H
-// 2560, V 151936: 64 tokens 170 / 234, 128: 251 / 227; 256 tokens: V 8000 41 /
-// 65, V 32000 118 / 68. Backward, V 151936: 128 tokens 834 / 958, 256: 1332 /
-// 1035; 256 tokens: V 8000 109 / 139, V 32000 311 / 265, and 256 x 256 x 4096
-// 41 / 135.
-constexpr int64_t kFewVocabulary = 16384;
-bool few_sizes(int64_t N, int64_t V, int64_t any_vocabulary) {
-  return N <= any_vocabulary ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && V <= kFewVocabulary;
+// tile's time on what little there is. Up to 64 tokens always, up to 256 for a
+// small vocabulary. Measured (us, few / tiles), forward: H 2560, V 151936: 64
+// tokens 170 / 234, 128 tokens 251 / 227; 256 tokens, H 2560: V 8000 41 / 65, V
+// 32000 118 / 68. Backward: 64 tokens, H 2560, V 151936 632 / 809; 128 tokens
+// 839 / 813, and 46 / 69 at H 512, V 8000; 256 tokens: 44 / 64 at H 256, V 4096,
+// 107 / 120 at H 2560, V 8000, 240 / 194 at H 4096, V 16000.
+constexpr int64_t kFewVocabulary = 8192;
+bool few_tokens(int64_t N, int64_t V) {
+  return N <= 64 ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && V <= kFewVocabulary;
 }
-bool few_forward(int64_t N, int64_t V) { return few_sizes(N, V, 64); }
 // The backward holds the tokens' whole cotangent, as two bf16 words up to 64
 // tokens and one above, which chunk_size has to allow.
 int64_t few_padded(int64_t N) { return N <= 32 ? 32 : lmh::round_up(N, 64); }
 bool few_backward(int64_t N, int64_t V, int64_t chunk_size) {
-  return few_sizes(N, V, 128) && few_padded(N) * (N <= 64 ? 2 : 1) <= 2 * chunk_size;
+  return few_tokens(N, V) && few_padded(N) * (N <= 64 ? 2 : 1) <= 2 * chunk_size;
 }
 
 // Splits of the dh tiles over the block's vocabulary. A launch holds the dh
@@ -741,7 +741,7 @@ int dh_splits(const lmh::BwdPlan& p, int64_t H) {
 // here: with one token tile (N <= 256), 128 splits of 594 vocabulary tiles
 // would take 5 tiles' time on half the CUs, 198 take 3.
 lmh::FwdPlan plan_distill_forward(int64_t N, int64_t H, int64_t V) {
-  if (!few_forward(N, V)) return lmh::plan_forward(N, H, V, lmh::kNumCUs);
+  if (!few_tokens(N, V)) return lmh::plan_forward(N, H, V, lmh::kNumCUs);
   lmh::FwdPlan p;
   p.S = lmh::few_splits(V);
   p.part_ld = lmh::round_up(std::max<int64_t>(N, 1), 64);
@@ -834,7 +834,7 @@ int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const in
   // without hard targets the tile kernel still reads N ids to pick a logit by:
   // any will do, the pick is not used
   hipError_t e;
-  if (few_forward(N, V)) {
+  if (few_tokens(N, V)) {
     lmh::FewArgs a{};
     a.hidden = hidden;
     a.W = W;
