@@ -316,8 +316,7 @@ def raw_norm_bwd(x, x_type, weight, w_type, N, H, kind, mean, rstd, dy, y_type, 
 TRACE_KERNELS = ("fwd_stats_kernel", "fwd_merge_kernel", "bwd_step_kernel", "transpose_kernel",
                  "fill_zero_kernel", "pad_rows_kernel", "bwd_step_bf16_kernel", "distill_top_kernel",
                  "distill_prep_kernel", "distill_step_kernel", "distill_post_kernel", "few_stats_kernel",
-                 "few_dz_kernel", "few_dw_kernel", "few_dh_kernel", "norm_fwd_kernel", "norm_bwd_kernel",
-                 "norm_reduce_kernel")
+                 "few_dz_kernel", "few_grads_kernel", "norm_fwd_kernel", "norm_bwd_kernel", "norm_reduce_kernel")
 
 
 def trace_enable(on: bool) -> None:

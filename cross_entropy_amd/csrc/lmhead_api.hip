@@ -688,7 +688,7 @@ struct DistillPlan {
   int splits = 1, k_split = 0;
   // few tokens: their own kernels
   bool few = false;
-  size_t off_ht = 0, off_hi = 0, off_lo = 0;
+  size_t off_hi = 0, off_lo = 0;
   int dh_strips = 0, dh_rows = 0;
 };
 
@@ -769,8 +769,7 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
   d.off_val = d.off_id + room(n * (K + 1) * 4);
   d.off_part = d.off_val + room(n * (K + 1) * 4);
   if (d.few) {
-    d.off_ht = d.off_part;
-    d.off_hi = d.off_ht + room(H * lmh::round_up(n, 64) * 2);
+    d.off_hi = d.off_part;
     d.off_lo = d.off_hi + room(V * few_padded(n) * 2);
     d.off_part = d.off_lo + (n <= 64 ? room(V * few_padded(n) * 2) : 0);
     // two workgroups a CU, of at least 128 vocabulary rows each
@@ -870,10 +869,6 @@ hipError_t few_bwd(const DistillPlan& d, const lmh::DistillPrepArgs& prep, const
                    int64_t H, float temperature, const float* lse, void* dh, void* dW, bool bf16, unsigned flags,
                    char* ws, hipStream_t s) {
   hipError_t e = lmh::launch_distill_prep(prep, s);
-  uint16_t* ht = reinterpret_cast<uint16_t*>(ws + d.off_ht);
-  if (e == hipSuccess)
-    e = lmh::launch_transpose(hidden, H, prep.N, H, lmh::round_up(prep.N, 64), H, prep.tgt, prep.V, ht,
-                              lmh::round_up(prep.N, 64), s);
   if (e != hipSuccess) return e;
   lmh::FewArgs a{};
   a.hidden = hidden;
@@ -892,7 +887,6 @@ hipError_t few_bwd(const DistillPlan& d, const lmh::DistillPrepArgs& prep, const
   a.dz_hi = reinterpret_cast<uint16_t*>(ws + d.off_hi);
   a.dz_lo = prep.N <= 64 ? reinterpret_cast<uint16_t*>(ws + d.off_lo) : nullptr;
   a.padded = (int)few_padded(prep.N);
-  a.ht = ht;
   a.dW = dW;
   a.add_dW = (flags & LMH_BWD_ACCUMULATE_DW) != 0;
   a.dh_part = reinterpret_cast<float*>(ws + d.off_part);

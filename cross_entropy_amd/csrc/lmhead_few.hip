@@ -98,17 +98,22 @@ __device__ __forceinline__ void few_logits(const uint16_t* W, int V, const uint1
   }
 }
 
-// The same for 64 tokens, hidden through LDS: from cache, each wave fetches
-// 0.8 of W's bytes of hidden again, which bounds the pass (240 us against 147 at
-// H = 2560, V = 151936). The workgroup stages kFewK of K of every token, the
-// next chunk in registers meanwhile; rows are padded by 16 bytes, so the 16
-// tokens of a fragment read fall on 16 different bank groups. `lds` holds two
-// chunks; every wave of the workgroup has to call, also one without rows.
-constexpr int kFewK = 256, kFewPitch = 2 * kFewK + 16, kFewLds = 2 * 64 * kFewPitch;
-template <int MB, int D>
+// The same for 32 and 64 tokens, hidden through LDS: from cache, each wave
+// fetches up to 0.8 of W's bytes of hidden again, which bounds the pass (64
+// tokens, H = 2560, V = 151936: 240 us against 147). The workgroup stages few_k
+// of K of every token, the next chunk in registers meanwhile; rows are padded by
+// 16 bytes, so the 16 tokens of a fragment read fall on 16 different bank
+// groups. `lds` holds two chunks; every wave of the workgroup has to call, also
+// one without rows.
+template <int NB>
+constexpr int few_k() { return 1024 / NB; }
+template <int NB>
+constexpr int few_pitch() { return 2 * few_k<NB>() + 16; }
+template <int MB, int NB, int D>
 __device__ __forceinline__ void few_logits_lds(const uint16_t* W, int V, const uint16_t* hidden, int N, int H, int r0,
-                                               char* lds, f32x4 (&acc)[MB][4]) {
-  constexpr int NB = 4, UC = kFewK / 64, pieces = 64 * kFewK / 8 / 256;
+                                               char* lds, f32x4 (&acc)[MB][NB]) {
+  constexpr int kFewK = few_k<NB>(), kFewPitch = few_pitch<NB>(), UC = kFewK / 64, pieces = 8;
+  constexpr int buffer = 16 * NB * kFewPitch, per = kFewK / 8, step = 256 / per;   // threads of a token's row; tokens at once
   const int lane = threadIdx.x & 63;
   const int col = lane & 15, q = lane >> 4;
   const char* pa[MB];
@@ -130,19 +135,19 @@ __device__ __forceinline__ void few_logits_lds(const uint16_t* W, int V, const u
       a[d][i][1] = p[1];
     }
   };
-  // staging: thread t takes 16 bytes at 8 (t % 32) of tokens t / 32 + 8 c
+  // staging: thread t takes 16 bytes at 8 (t % per) of tokens t / per + step c
   u32x4 next[pieces];
-  const int t_tok = threadIdx.x >> 5, t_k = 8 * (threadIdx.x & 31);
+  const int t_tok = threadIdx.x / per, t_k = 8 * (threadIdx.x % per);
   auto fetch = [&](int chunk) {
 #pragma unroll
     for (int c = 0; c < pieces; ++c)
-      next[c] = *reinterpret_cast<const u32x4*>(hidden + (int64_t)min(t_tok + 8 * c, N - 1) * H +
+      next[c] = *reinterpret_cast<const u32x4*>(hidden + (int64_t)min(t_tok + step * c, N - 1) * H +
                                                 min(chunk * kFewK + t_k, H - 8));
   };
   auto stage = [&](int chunk) {
 #pragma unroll
     for (int c = 0; c < pieces; ++c)
-      *reinterpret_cast<u32x4*>(lds + (chunk & 1) * 64 * kFewPitch + (t_tok + 8 * c) * kFewPitch + 2 * t_k) = next[c];
+      *reinterpret_cast<u32x4*>(lds + (chunk & 1) * buffer + (t_tok + step * c) * kFewPitch + 2 * t_k) = next[c];
   };
   fetch(0);
 #pragma unroll
@@ -151,7 +156,7 @@ __device__ __forceinline__ void few_logits_lds(const uint16_t* W, int V, const u
   for (int chunk = 0; chunk < chunks; ++chunk) {
     fetch(min(chunk + 1, chunks - 1));
     __syncthreads();   // chunk is staged; chunk - 1, whose buffer is filled below, has been read
-    const char* p = lds + (chunk & 1) * 64 * kFewPitch + col * kFewPitch + 32 * q;
+    const char* p = lds + (chunk & 1) * buffer + col * kFewPitch + 32 * q;
 #pragma unroll
     for (int uc = 0; uc < UC; ++uc) {
       const int u = chunk * UC + uc;
@@ -180,8 +185,7 @@ __device__ __forceinline__ void few_logits_lds(const uint16_t* W, int V, const u
 struct FewTile {
   int tok0, n, split;
 };
-__device__ __forceinline__ FewTile few_tile(const FewArgs& a, int splits) {
-  const int vid = xcd_remap(blockIdx.x, gridDim.x);
+__device__ __forceinline__ FewTile few_tile(const FewArgs& a, int vid, int splits) {
   const int tok0 = vid % a.tiles * 64;
   const int split = vid / a.tiles;
   return {tok0, min(64, a.N - tok0), split < splits ? split : -1};
@@ -190,11 +194,11 @@ __device__ __forceinline__ FewTile few_tile(const FewArgs& a, int splits) {
 template <int MB, int NB>
 __device__ __forceinline__ void few_logits_of(const FewArgs& a, const FewTile& t, int r0, char* lds, f32x4 (&acc)[MB][NB]) {
   const uint16_t* hidden = a.hidden + (int64_t)t.tok0 * a.H;
-  if constexpr (NB == 4) few_logits_lds<MB, 2>(a.W, a.V, hidden, t.n, a.H, r0, lds, acc);
+  if constexpr (NB > 1) few_logits_lds<MB, NB, 2>(a.W, a.V, hidden, t.n, a.H, r0, lds, acc);
   else few_logits<MB, NB, 3>(a.W, a.V, hidden, t.n, a.H, r0, acc);
 }
 template <int NB>
-constexpr int few_lds() { return NB == 4 ? kFewLds : 16; }
+constexpr int few_lds() { return NB > 1 ? 2 * 16 * NB * few_pitch<NB>() : 16; }
 
 // Forward: the statistics of the workgroup's 64 MB vocabulary rows per token,
 // as one record of the split (the workgroup).
@@ -204,7 +208,7 @@ __global__ __launch_bounds__(256, 2) void few_stats_kernel(const FewArgs a) {
   __shared__ float4 xch[4][16 * NB];
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const FewTile t = few_tile(a, a.splits);
+  const FewTile t = few_tile(a, xcd_remap(blockIdx.x, gridDim.x), a.splits);
   if (t.split < 0) return;
   const int r0 = (t.split * 4 + wave) * 16 * MB;
   const int V = a.V;
@@ -288,7 +292,7 @@ __global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
   uint16_t (*t_lo)[NP] = reinterpret_cast<uint16_t (*)[NP]>(lds + tile);
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const FewTile t = few_tile(a, a.splits);
+  const FewTile t = few_tile(a, xcd_remap(blockIdx.x, gridDim.x), a.splits);
   if (t.split < 0) return;
   const int b0 = t.split * rows;
   const int w0 = wave * 16 * MB;
@@ -344,26 +348,54 @@ __global__ __launch_bounds__(256, 2) void few_dz_kernel(const FewArgs a) {
 // groups of 16, the next group's cotangent in flight. Bound by the stores: the
 // group's results turn in the wave's LDS, so that a store covers whole
 // lines (4 rows x 256 bytes of bf16, 2 x 512 of float32) and not 16 pieces of 64.
+template <int BL>
+constexpr int few_ht_lds() { return 4 * 32 * (32 * BL + 16); }
+template <int BL, bool BF16>
+constexpr int few_dw_lds() { return std::max(4 * 16 * (16 * BL * (BF16 ? 2 : 4) + 16), few_ht_lds<BL>()); }
 template <int KS, int BL, bool LO, bool BF16, bool ADD>
-__global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
-  constexpr int NP = 32 * KS, ht_ld = NP < 64 ? 64 : NP, cols = 16 * BL;
+__device__ __forceinline__ void few_dw(const FewArgs& a, int vid, char* lds) {
+  constexpr int NP = 32 * KS, cols = 16 * BL;
   constexpr int bytes = BF16 ? 2 : 4, pitch = cols * bytes + 16;
   constexpr int per_row = cols * bytes / 16, stores = 16 * per_row / 64;   // 16-byte pieces of a row; stores of a group
-  __shared__ __attribute__((aligned(16))) char turn[4][16 * pitch];
   const int lane = threadIdx.x & 63;
   const int col = lane & 15, q = lane >> 4;
   const int wave = wave_id();
-  const int w = xcd_remap(blockIdx.x, gridDim.x) * 4 + wave;   // a split's strips share an XCD's L2
+  const int w = vid * 4 + wave;
   const int strip = w % a.strips, split = w / a.strips;
   if (split >= a.dw_splits) return;
   const int H = a.H, V = a.V;
   const int h0 = strip * cols;
+  // hidden^T: 32 tokens at a time turn in the wave's LDS (masked tokens are 0,
+  // whatever their rows hold)
   bf16x8 ht[BL][KS];
+  constexpr int h_pitch = 2 * cols + 16, h_per = cols / 8, h_each = 32 * h_per / 64;
+  static_assert(4 * 32 * h_pitch <= few_dw_lds<BL, BF16>(), "a wave's quarter holds 32 tokens");
+  char* turn = lds + wave * (few_dw_lds<BL, BF16>() / 4);
 #pragma unroll
-  for (int b = 0; b < BL; ++b) {
-    const int h = min(h0 + 32 * (b >> 1) + 8 * (col >> 2) + 4 * (b & 1) + (col & 3), H - 1);
+  for (int k = 0; k < KS; ++k) {
+    u32x4 x[h_each];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) ht[b][k] = *reinterpret_cast<const bf16x8*>(a.ht + (int64_t)h * ht_ld + 32 * k + 8 * q);
+    for (int c = 0; c < h_each; ++c) {
+      const int tok = 32 * k + (64 * c + lane) / h_per;
+      const int at = min(tok, a.N - 1);
+      const int id = a.targets[at];
+      x[c] = *reinterpret_cast<const u32x4*>(a.hidden + (int64_t)at * H + min(h0 + 8 * (lane % h_per), H - 8));
+      if (tok >= a.N || id < 0 || id >= V) x[c] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int c = 0; c < h_each; ++c)
+      *reinterpret_cast<u32x4*>(turn + (64 * c + lane) / h_per * h_pitch + 16 * (lane % h_per)) = x[c];
+    __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+    // a transposed read hands lane j the columns that lane j / 4 points at, element j % 4
+#pragma unroll
+    for (int b = 0; b < BL; ++b) {
+      const char* p = turn + (8 * q + (col >> 2)) * h_pitch + 2 * (32 * (b >> 1) + 8 * (col & 3) + 4 * (b & 1));
+      short8v v;
+      v.s0123 = ds_read_tr(p);
+      v.s4567 = ds_read_tr(p + 4 * h_pitch);
+      ht[b][k] = __builtin_bit_cast(bf16x8, v);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
   const int groups = (V + 15) / 16;
   const int g_lo = (int)((int64_t)split * groups / a.dw_splits), g_hi = (int)((int64_t)(split + 1) * groups / a.dw_splits);
@@ -376,7 +408,7 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
       if (LO) lo[k] = *reinterpret_cast<const bf16x8*>(a.dz_lo + at + 32 * k);
     }
   };
-  char* mine = turn[wave];
+  char* mine = lds + wave * (few_dw_lds<BL, BF16>() / 4);
   auto group = [&](int g, bool checked) {
     f32x4 acc[BL];
 #pragma unroll
@@ -445,13 +477,15 @@ __global__ __launch_bounds__(256) void few_dw_kernel(const FewArgs a) {
 // so that the transposed reads of 16 lanes (4 rows x 32 bytes) meet no bank
 // twice. Rows past the split are 0 in both operands.
 template <int NB, bool LO>
-__global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
+constexpr int few_dh_lds() { return 2 * (32 * 512 + (LO ? 2 : 1) * 32 * (32 * NB + 16)); }
+template <int NB, bool LO>
+__device__ __forceinline__ void few_dh(const FewArgs& a, int vid, char* lds) {
   constexpr int NP = 16 * NB, pitch = 2 * NP + 16, words = LO ? 2 : 1;
   constexpr int w_bytes = 32 * 512, z_bytes = 32 * pitch, buf = w_bytes + words * z_bytes;
-  __shared__ __attribute__((aligned(16))) char lds[2 * buf];
+  static_assert(2 * buf == few_dh_lds<NB, LO>(), "two buffers");
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const FewTile t = few_tile(a, a.dh_strips * a.dh_splits);   // a split's strips, and a strip's tiles, share an XCD's L2
+  const FewTile t = few_tile(a, vid, a.dh_strips * a.dh_splits);
   if (t.split < 0) return;
   const int strip = t.split % a.dh_strips, split = t.split / a.dh_strips;
   const int H = a.H;
@@ -554,6 +588,20 @@ __global__ __launch_bounds__(256, 2) void few_dh_kernel(const FewArgs a) {
   }
 }
 
+// Both products in one launch, dh's workgroups first (they read the end of W
+// that the memory-side cache still holds); neither waits for the other, so
+// each fills the other's tail. Ids are remapped within each part: a split's
+// strips, and a strip's token tiles, share an XCD's L2.
+template <int KS, int BL, bool LO, bool BF16, bool ADD>
+__global__ __launch_bounds__(256, 2) void few_grads_kernel(const FewArgs a) {
+  constexpr int NB = KS == 1 ? 2 : 4;
+  constexpr int n_dw = few_dw_lds<BL, BF16>(), n_dh = few_dh_lds<NB, LO>();
+  __shared__ __attribute__((aligned(16))) char lds[n_dw > n_dh ? n_dw : n_dh];
+  const int bid = blockIdx.x;
+  if (bid < a.dh_blocks) few_dh<NB, LO>(a, xcd_remap(bid, a.dh_blocks), lds);
+  else few_dw<KS, BL, LO, BF16, ADD>(a, xcd_remap(bid - a.dh_blocks, gridDim.x - a.dh_blocks), lds);
+}
+
 // Row blocks (of 16) per wave: as few as let two workgroups a CU cover the
 // vocabulary at once, so that no CU is left a second round (V = 151936: 475
 // workgroups of 5 blocks a wave take 143 us for one token, 594 of 4 take 162).
@@ -599,16 +647,14 @@ hipError_t launch_few_stats(FewArgs a, hipStream_t stream) {
   return hipSuccess;
 }
 
-// The cotangent, then the partials of dh and dW (dh first: the end of the table
-// is still in the memory-side cache).
+// The cotangent, then dW and the partials of dh.
 hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream) {
   const double N = a.N, H = a.H, V = a.V;
   const bool two = a.dz_lo != nullptr;
-  const int nb = a.N <= 32 ? 2 : 4;
   a.tiles = (a.N + 63) / 64;
   a.splits = few_splits(a.V);
   trace_begin(stream);
-  with_sizes(few_blocks(a.V), nb, [&](auto mb, auto n) {
+  with_sizes(few_blocks(a.V), a.N <= 32 ? 2 : 4, [&](auto mb, auto n) {
     constexpr int NB = n() < 2 ? 2 : n();   // K of the gradient products is at least 32 tokens
     hipLaunchKernelGGL((few_dz_kernel<mb(), NB>), dim3(few_grid((int64_t)a.tiles * a.splits)), dim3(256), 0, stream, a);
   });
@@ -616,39 +662,32 @@ hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const double dz = (two ? 4.0 : 2.0) * a.padded * V;
   trace_end(kFewDz, stream, 0.0, 2.0 * (N + V) * H + dz);
-  const unsigned dh_blocks = few_grid((int64_t)a.tiles * a.dh_strips * a.dh_splits);
-  trace_begin(stream);
-  if (nb == 2) hipLaunchKernelGGL((few_dh_kernel<2, true>), dim3(dh_blocks), dim3(256), 0, stream, a);
-  else if (two) hipLaunchKernelGGL((few_dh_kernel<4, true>), dim3(dh_blocks), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((few_dh_kernel<4, false>), dim3(dh_blocks), dim3(256), 0, stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  trace_end(kFewDh, stream, 2.0 * N * H * V, 2.0 * V * H + dz + 4.0 * a.dh_splits * N * H);
+  a.dh_blocks = few_grid((int64_t)a.tiles * a.dh_strips * a.dh_splits);
   // waves for dW: 8 a CU, but no less than 4 groups of 16 rows each
   const int cols = two ? 128 : 64;
   a.strips = (a.H + cols - 1) / cols;
   a.dw_splits = std::max(1, std::min((a.V + 63) / 64, 8 * kNumCUs / a.strips));
-  const unsigned blocks = few_grid(((int64_t)a.strips * a.dw_splits + 3) / 4);
-  auto dw = [&](auto ks, auto bl, auto lo) {
+  const unsigned blocks = a.dh_blocks + few_grid(((int64_t)a.strips * a.dw_splits + 3) / 4);
+  auto launch = [&](auto ks, auto bl, auto lo) {
     std::true_type yes;
     std::false_type no;
     auto typed = [&](auto half, auto add) {
-      hipLaunchKernelGGL((few_dw_kernel<ks(), bl(), lo(), half(), add()>), dim3(blocks), dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((few_grads_kernel<ks(), bl(), lo(), half(), add()>), dim3(blocks), dim3(256), 0, stream, a);
     };
     if (bf16) a.add_dW ? typed(yes, yes) : typed(yes, no);
     else a.add_dW ? typed(no, yes) : typed(no, no);
   };
-  trace_begin(stream);
   constexpr std::integral_constant<int, 4> four{};
   constexpr std::integral_constant<int, 8> eight{};
-  if (two && a.padded == 32) dw(std::integral_constant<int, 1>{}, eight, std::true_type{});
-  else if (two) dw(std::integral_constant<int, 2>{}, eight, std::true_type{});
-  else if (a.padded == 128) dw(four, four, std::false_type{});
-  else if (a.padded == 192) dw(std::integral_constant<int, 6>{}, four, std::false_type{});
-  else dw(eight, four, std::false_type{});
+  trace_begin(stream);
+  if (two && a.padded == 32) launch(std::integral_constant<int, 1>{}, eight, std::true_type{});
+  else if (two) launch(std::integral_constant<int, 2>{}, eight, std::true_type{});
+  else if (a.padded == 128) launch(four, four, std::false_type{});
+  else if (a.padded == 192) launch(std::integral_constant<int, 6>{}, four, std::false_type{});
+  else launch(eight, four, std::false_type{});
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kFewDw, stream, 2.0 * N * H * V, (bf16 ? 2.0 : 4.0) * V * H + dz);
+  trace_end(kFewGrads, stream, 4.0 * N * H * V, (bf16 ? 4.0 : 6.0) * V * H + 2.0 * dz + 4.0 * a.dh_splits * N * H);
   return hipSuccess;
 }
 

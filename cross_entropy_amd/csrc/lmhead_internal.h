@@ -212,10 +212,9 @@ struct FewArgs {
   int padded;               // tokens rounded up to 32 or a multiple of 64
   uint16_t* dz_hi;          // [V][padded] each
   uint16_t* dz_lo;          // NULL above 64 tokens
-  const uint16_t* ht;       // hidden^T [H][tokens up to a multiple of 64], masked tokens and those past N zeroed
   void* dW;
   bool add_dW;
-  int tiles, splits, strips, dw_splits;   // set by the launchers
+  int tiles, splits, strips, dw_splits, dh_blocks;   // set by the launchers
   float* dh_part;           // [dh_splits][N][H]
   int dh_strips, dh_splits, dh_rows;
 };
@@ -267,7 +266,7 @@ int norm_bwd_blocks(int64_t N, int64_t H);   // workgroups (partial rows) of the
 enum KernelId {
   kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
   kDistillTop, kDistillPrep, kDistillStep, kDistillPost,
-  kFewStats, kFewDz, kFewDw, kFewDh, kNormFwd, kNormBwd, kNormReduce, kNumKernels
+  kFewStats, kFewDz, kFewGrads, kNormFwd, kNormBwd, kNormReduce, kNumKernels
 };
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);

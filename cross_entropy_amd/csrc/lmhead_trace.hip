@@ -41,7 +41,7 @@ const char* const kNames[kNumKernels] = {
     "fwd_stats_kernel", "fwd_merge_kernel", "bwd_step_kernel", "transpose_kernel", "fill_zero_kernel",
     "pad_rows_kernel", "bwd_step_bf16_kernel", "distill_top_kernel", "distill_prep_kernel",
     "distill_step_kernel", "distill_post_kernel", "few_stats_kernel", "few_dz_kernel",
-    "few_dw_kernel", "few_dh_kernel", "norm_fwd_kernel", "norm_bwd_kernel", "norm_reduce_kernel",
+    "few_grads_kernel", "norm_fwd_kernel", "norm_bwd_kernel", "norm_reduce_kernel",
 };
 
 hipEvent_t take_event() {

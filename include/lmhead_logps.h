@@ -444,10 +444,11 @@ const char* lmhead_logps_version(void);
  *   9 distill_step_kernel  (bwd_step_kernel with its dh tiles split, either gradient type)
  *  10 distill_post_kernel  (special entries into a cotangent block, sum of dh splits)
  *  11 few_stats_kernel     (distillation of few tokens: forward statistics)
- *  12 few_dz_kernel        (its cotangent), 13 few_dw_kernel, 14 few_dh_kernel (its products)
- *  15 norm_fwd_kernel
- *  16 norm_bwd_kernel
- *  17 norm_reduce_kernel   (dweight and dbias from their partial sums)
+ *  12 few_dz_kernel        (its cotangent)
+ *  13 few_grads_kernel     (its gradient products)
+ *  14 norm_fwd_kernel
+ *  15 norm_bwd_kernel
+ *  16 norm_reduce_kernel   (dweight and dbias from their partial sums)
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch
