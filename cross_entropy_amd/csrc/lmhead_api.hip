@@ -855,7 +855,7 @@ int lmhead_logps_distill_fwd(const uint16_t* hidden, const uint16_t* W, const in
   if (e == hipSuccess)
     e = lmh::launch_distill_top({hidden, W, targets, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
                                  (int)H, (int)V, (int)K, temperature, back_hi, (float)(back - (double)back_hi),
-                                 workspace, p.part_ld, p.S, kl, logp, lse, logp_top}, s);
+                                 workspace, p.part_ld, p.S, kl, logp, lse, logp_top, 0}, s);
   if (e != hipSuccess) return fail(LMH_ERR_HIP, "distill_fwd: launch failed: %s", hipGetErrorString(e));
   return ok();
 }

@@ -121,63 +121,71 @@ __device__ __forceinline__ void distill_dots(const DistillTopArgs& a, int64_t to
   }
 }
 
-// The outputs of one token from its dot products and the forward's records.
-__device__ __forceinline__ void distill_token(const DistillTopArgs& a, int64_t tok, int lane, const float* s_z) {
-  const int K = a.K, V = a.V;
-  const int32_t* ids = a.ids + tok * K;
-  // the forward's split records: a lane's in split order, then across lanes
-  // by halves (the lower lane's first), so the order is fixed
-  Stats rec{kNegBig, 0.0f, 0.0f, 0.0f};
-  for (int s = lane; s < a.S; s += 64) {
-    const float4 q = reinterpret_cast<const float4*>(a.part)[s * a.part_ld + tok];
-    rec = merge_stats(rec, Stats{q.x, q.y, q.z, q.w});
-  }
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) {
-    const Stats o{__shfl_xor(rec.m2, x), __shfl_xor(rec.s1, x), __shfl_xor(rec.s2, x), __shfl_xor(rec.zt, x)};
-    rec = (lane & x) == 0 ? merge_stats(rec, o) : merge_stats(o, rec);
-  }
-  // The records are in base 2 of logits scaled by the float32 sc ~ log2(e) / T:
-  // back = 1 / (sc T) in two words takes the max back to natural units of z / T
-  // without sc's rounding, which a loss of the size of the max's last digits
-  // would show. A +inf logit (and no NaN) leaves m = +inf and s1 = NaN.
-  const float lse = rec.m2 == INFINITY ? INFINITY : fmaf(rec.m2, a.back_hi, fmaf(rec.m2, a.back_lo, kLn2 * log2f(rec.s1)));
-  auto live_of = [&](int k) { return ids[k] >= 0 && ids[k] < V; };
-  auto t_of = [&](int k) { return live_of(k) ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY; };
-  const float shift = teacher_shift(a.teacher_lse, tok, K, t_of);
-  float kl = 0.0f;
-  bool any = false;
-  for (int k = lane; k < K; k += 64) {
-    const bool live = live_of(k);
-    any |= live;
-    const float top = live ? s_z[k] / a.T - lse : 0.0f;
-    const float t = t_of(k);
-    const float q = teacher_q(t, shift);
-    if (q != 0.0f) kl += q * ((t - shift) - top);
-    a.logp_top[tok * K + k] = top;
-  }
-  kl = wave_sum(kl);
-  const bool some = __any(any);
-  if (lane == 0) {
-    const int t = a.targets != nullptr ? a.targets[tok] : -1;
-    const bool hard = t >= 0 && t < V;
-    a.kl[tok] = kl;
-    a.lse[tok] = (hard || some) ? lse : 0.0f;
-    if (a.logp != nullptr) a.logp[tok] = hard ? rec.zt / a.T - lse : 0.0f;
-  }
-}
-
-// Forward tail, a workgroup per token. Bound by the fetch of the K rows of W (2 H bytes each),
-// from the last-level cache where teachers agree on frequent ids.
-__global__ __launch_bounds__(256) void distill_top_kernel(const DistillTopArgs a) {
+// Forward tail, a workgroup per token: the first n_dot waves take the dot
+// products, and the last merges the forward's split records and takes the
+// teacher's shift, then forms the outputs. Bound by the fetch of the K rows
+// of W (2 H bytes each), from the caches where teachers agree on frequent ids:
+// 4096 tokens x 64 rows of 5 KB in 120 us (11 TB/s).
+__global__ __launch_bounds__(320) void distill_top_kernel(const DistillTopArgs a) {
   __shared__ float s_z[kDistillMaxK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n_waves = blockDim.x >> 6;
+  const int last = (blockDim.x >> 6) - 1;
+  const int n_dot = a.n_dot;
+  const int K = a.K, V = a.V;
   for (int64_t tok = blockIdx.x; tok < a.N; tok += gridDim.x) {
-    distill_dots(a, tok, lane, wave, n_waves, s_z);
+    const int32_t* ids = a.ids + tok * K;
+    auto live_of = [&](int k) { return ids[k] >= 0 && ids[k] < V; };
+    auto t_of = [&](int k) { return live_of(k) ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY; };
+    float lse = 0.0f, shift = 0.0f, zt = 0.0f;
+    if (wave < n_dot) {
+      distill_dots(a, tok, lane, wave, n_dot, s_z);
+    }
+    if (wave == last) {
+      // a lane's records in split order, then across lanes by halves (the lower
+      // lane's first), so the order is fixed
+      Stats rec{kNegBig, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int s = lane; s < a.S; s += 64) {
+        const float4 q = reinterpret_cast<const float4*>(a.part)[s * a.part_ld + tok];
+        rec = merge_stats(rec, Stats{q.x, q.y, q.z, q.w});
+      }
+#pragma unroll
+      for (int x = 1; x < 64; x <<= 1) {
+        const Stats o{__shfl_xor(rec.m2, x), __shfl_xor(rec.s1, x), __shfl_xor(rec.s2, x), __shfl_xor(rec.zt, x)};
+        rec = (lane & x) == 0 ? merge_stats(rec, o) : merge_stats(o, rec);
+      }
+      // The records are in base 2 of logits scaled by the float32 sc ~ log2(e) / T:
+      // back = 1 / (sc T) in two words takes the max back to natural units of z / T
+      // without sc's rounding, which a loss of the size of the max's last digits
+      // would show. A +inf logit (and no NaN) leaves m = +inf and s1 = NaN.
+      lse = rec.m2 == INFINITY ? INFINITY : fmaf(rec.m2, a.back_hi, fmaf(rec.m2, a.back_lo, kLn2 * log2f(rec.s1)));
+      zt = rec.zt;
+      shift = teacher_shift(a.teacher_lse, tok, K, t_of);
+    }
     __syncthreads();
-    if (wave == 0) distill_token(a, tok, lane, s_z);
+    if (wave == last) {
+      float kl = 0.0f;
+      bool any = false;
+      for (int k = lane; k < K; k += 64) {
+        const bool live = live_of(k);
+        any |= live;
+        const float top = live ? s_z[k] / a.T - lse : 0.0f;
+        const float t = t_of(k);
+        const float q = teacher_q(t, shift);
+        if (q != 0.0f) kl += q * ((t - shift) - top);
+        a.logp_top[tok * K + k] = top;
+      }
+      kl = wave_sum(kl);
+      const bool some = __any(any);
+      if (lane == 0) {
+        const int t = a.targets != nullptr ? a.targets[tok] : -1;
+        const bool hard = t >= 0 && t < V;
+        a.kl[tok] = kl;
+        a.lse[tok] = (hard || some) ? lse : 0.0f;
+        if (a.logp != nullptr) a.logp[tok] = hard ? zt / a.T - lse : 0.0f;
+      }
+    }
     __syncthreads();   // s_z is read before the next token's dot products
   }
 }
@@ -432,8 +440,12 @@ __global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs
 
 }  // namespace
 
-hipError_t launch_distill_top(const DistillTopArgs& a, hipStream_t stream) {
-  const int waves = std::max(1, std::min(4, (a.K + kDotRows - 1) / kDotRows));
+hipError_t launch_distill_top(DistillTopArgs a, hipStream_t stream) {
+  a.n_dot = std::max(1, std::min(4, (a.K + kDotRows - 1) / kDotRows));
+  // a wave of its own for the last wave's part while every workgroup is
+  // resident at once and latency counts (1 token: 9.8 us instead of 14.4);
+  // beyond, the waves are better spent on more tokens (4096: 200 us instead of 120)
+  const int waves = a.n_dot + (a.N <= 2 * kNumCUs ? 1 : 0);
   const double N = (double)a.N, K = (double)a.K, H = (double)a.H;
   trace_begin(stream);
   hipLaunchKernelGGL(distill_top_kernel, dim3((unsigned)std::min<int64_t>(a.N, 1 << 20)), dim3(64 * waves), 0, stream, a);

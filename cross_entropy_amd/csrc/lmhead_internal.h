@@ -143,6 +143,7 @@ struct DistillTopArgs {
   float* logp;                // or NULL
   float* lse;
   float* logp_top;            // [N][K]
+  int n_dot;                  // waves that take dot products (set by the launcher)
 };
 
 // What the backward forms per token before the tiles run: the combined
@@ -284,7 +285,7 @@ hipError_t launch_pad_rows(const uint16_t* in, int64_t R, int64_t C, int64_t R_p
 hipError_t launch_transpose(const uint16_t* in, int64_t ld_in, int64_t R, int64_t C, int64_t R_pad,
                             int64_t C_pad, const int32_t* tgt, int64_t V, uint16_t* out,
                             int64_t ld_out, hipStream_t stream);
-hipError_t launch_distill_top(const DistillTopArgs& a, hipStream_t stream);
+hipError_t launch_distill_top(DistillTopArgs a, hipStream_t stream);
 hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream);
 hipError_t launch_distill_step(const DistillStep& d, bool bf16, hipStream_t stream);
 hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream);
