@@ -36,6 +36,7 @@ norm too (``norm=Norm(...)``: hidden is then the stream in front of it).
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Any, NamedTuple, Optional, Tuple
 
 from . import _native
@@ -394,6 +395,18 @@ def _enqueue(dev, raw, *args):
             _native.check(raw(*args))
 
 
+def _allocating(device, stream):
+    """Context in which tensors are allocated for work on ``stream`` (None: the
+    current one): from that stream's own pool, so that neither their earlier
+    nor their later use elsewhere overlaps it."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def lmhead_logps_distill_workspace_bytes(N: int, H: int, V: int, K: int, chunk_size: int, with_backward=True) -> int:
     """Workspace bytes of the distillation calls; with_backward as for
     ``lmhead_logps_workspace_bytes``."""
@@ -484,11 +497,12 @@ def distill_forward(hidden, W, targets, ids, teacher, chunk_size: int, teacher_l
     torch = _torch()
     N, K = ids.shape
     dev = hidden.device
-    kl, lse = (torch.empty(N, dtype=torch.float32, device=dev) for _ in range(2))
-    logp = None if targets is None else torch.empty(N, dtype=torch.float32, device=dev)
-    logp_top = torch.empty((N, K), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = distill_workspace_for(hidden, W, ids, chunk_size, with_backward=False)
+    with _allocating(dev, stream):
+        kl, lse = (torch.empty(N, dtype=torch.float32, device=dev) for _ in range(2))
+        logp = None if targets is None else torch.empty(N, dtype=torch.float32, device=dev)
+        logp_top = torch.empty((N, K), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = distill_workspace_for(hidden, W, ids, chunk_size, with_backward=False)
     lmhead_logps_distill_fwd(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature, kl, logp, lse,
                              logp_top, workspace, stream)
     return kl, logp, lse, logp_top
@@ -506,13 +520,14 @@ def distill_backward(hidden, W, targets, ids, teacher, chunk_size: int, logp, ls
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
     if accumulate and (dh is None or dW is None):
         raise ValueError("accumulate needs both dh and dW buffers")
-    if dh is None:
-        dh = torch.empty(hidden.shape, dtype=grad_dtype, device=hidden.device)
-    if dW is None:
-        dW = torch.empty(W.shape, dtype=grad_dtype, device=hidden.device)
-    if workspace is None:
-        workspace = distill_workspace_for(hidden, W, ids, chunk_size,
-                                          with_backward="bf16" if grad_dtype == torch.bfloat16 else True)
+    with _allocating(hidden.device, stream):
+        if dh is None:
+            dh = torch.empty(hidden.shape, dtype=grad_dtype, device=hidden.device)
+        if dW is None:
+            dW = torch.empty(W.shape, dtype=grad_dtype, device=hidden.device)
+        if workspace is None:
+            workspace = distill_workspace_for(hidden, W, ids, chunk_size,
+                                              with_backward="bf16" if grad_dtype == torch.bfloat16 else True)
     flags = (_native.BWD_ACCUMULATE_DH | _native.BWD_ACCUMULATE_DW) if accumulate else 0
     lmhead_logps_distill_bwd(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature, logp, lse,
                              logp_top, g_kl, g_logp, dh, dW, flags, workspace, stream)
@@ -614,9 +629,10 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "laye
     (default: x's) may be bfloat16 for a float32 x."""
     torch = _torch()
     N, _ = _norm_shape(x)
-    y = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
-    mean = torch.empty_like(rstd) if kind == "layer" else None
+    with _allocating(x.device, stream):
+        y = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        rstd = torch.empty(N, dtype=torch.float32, device=x.device)
+        mean = torch.empty_like(rstd) if kind == "layer" else None
     lmhead_logps_norm_fwd(x, weight, bias, eps, kind, y, mean, rstd, stream)
     return y, mean, rstd
 
@@ -630,18 +646,19 @@ def norm_backward(x, weight, mean, rstd, dy, kind: str = "layer", with_weight: b
     ``accumulate`` the given buffers are added into."""
     torch = _torch()
     _, H = _norm_shape(x)
-    dx = torch.empty_like(x)
     if accumulate and ((with_weight and dweight is None) or (with_bias and dbias is None)):
         raise ValueError("accumulate needs the gradient buffers that are wanted")
     if grad_dtype is None:
         given = dweight if dweight is not None else dbias if dbias is not None else weight
         grad_dtype = torch.float32 if given is None else given.dtype
-    if dweight is None and with_weight:
-        dweight = torch.empty(H, dtype=grad_dtype, device=x.device)
-    if dbias is None and with_bias:
-        dbias = torch.empty(H, dtype=grad_dtype, device=x.device)
-    if workspace is None and (dweight is not None or dbias is not None):
-        workspace = norm_workspace_for(x)
+    with _allocating(x.device, stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if dweight is None and with_weight:
+            dweight = torch.empty(H, dtype=grad_dtype, device=x.device)
+        if dbias is None and with_bias:
+            dbias = torch.empty(H, dtype=grad_dtype, device=x.device)
+        if workspace is None and (dweight is not None or dbias is not None):
+            workspace = norm_workspace_for(x)
     flags = _native.BWD_ACCUMULATE_DW if accumulate else 0
     lmhead_logps_norm_bwd(x, weight, kind, mean, rstd, dy, dx, dweight, dbias, flags, workspace, stream)
     return dx, dweight, dbias

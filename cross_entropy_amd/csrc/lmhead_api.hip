@@ -708,7 +708,7 @@ bool few_tokens(int64_t N, int64_t V) {
 // tokens and one above, which chunk_size has to allow.
 int64_t few_padded(int64_t N) { return N <= 32 ? 32 : lmh::round_up(N, 64); }
 bool few_backward(int64_t N, int64_t V, int64_t chunk_size) {
-  return few_tokens(N, V) && few_padded(N) * (N <= 64 ? 2 : 1) <= 2 * chunk_size;
+  return few_tokens(N, V) && few_padded(N) / (N <= 64 ? 1 : 2) <= chunk_size;
 }
 
 // Splits of the dh tiles over the block's vocabulary. A launch holds the dh

@@ -210,22 +210,24 @@ __global__ __launch_bounds__(64 * kPrepWaves) void distill_prep_kernel(const Dis
   const bool hard = target >= 0 && target < V;
   const float g_kl = a.g_kl != nullptr ? a.g_kl[tok] : 0.0f;
   const float g_logp = (hard && a.g_logp != nullptr) ? a.g_logp[tok] : 0.0f;
-  // a token whose loss term has no cotangent forms none of it (selected, so a
-  // NaN in the teacher's row under g_kl = 0 stays out)
-  const bool kd = g_kl != 0.0f;
   int first = K;   // the first live entry
   bool listed = false;
   for (int k = lane; k < K; k += 64) {
     const int id = ids[k];
     const bool live = id >= 0 && id < V;
     s_id[k] = live ? id : -1;
-    s_q[k] = live && kd ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY;
     if (live) first = min(first, k);
     listed |= hard && id == target;
   }
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) first = min(first, __shfl_xor(first, x));
   listed = __any(listed);
+  // a token without a cotangent of its loss term, or without an entry, forms
+  // none of the term (selected, so a NaN in the teacher's row under g_kl = 0, or
+  // in g_kl under an empty row, stays out)
+  const bool kd = g_kl != 0.0f && first < K;
+  for (int k = lane; k < K; k += 64)
+    s_q[k] = s_id[k] >= 0 && kd ? teacher_at(a.teacher, a.t_f32, tok * K + k) / a.T : -INFINITY;
   auto t_of = [&](int k) { return s_q[k]; };   // a lane's own entries: no wait between lanes is needed
   const float shift = kd ? teacher_shift(a.teacher_lse, tok, K, t_of) : 0.0f;
   float Q = 0.0f;

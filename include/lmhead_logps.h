@@ -341,8 +341,9 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  * lmhead_logps_distill_bwd: dh and dW of L = sum_i g_kl_i kl_i + g_logp_i
  * logp_i (the teacher's logits get no gradient), through
  *   dz_v = [g_kl (Q p_v - sum_{id_k = v} q_k) + g_logp (1[v = target] - p_v)] / T.
- *   g_kl         f32 [N] or NULL (zeros); a token with g_kl = 0 does not form
- *                        the term, whatever its teacher row holds
+ *   g_kl         f32 [N] or NULL (zeros); a token with g_kl = 0, or without
+ *                        an entry, does not form the term, whatever its
+ *                        teacher row, or its g_kl, holds
  *   g_logp       f32 [N] or NULL (zeros); needs targets and the forward's logp
  *   dh, dW       [N,H] and [V,H], 16-byte aligned, of type grad_type
  *                (LMH_TYPE_F32, or LMH_TYPE_BF16 through float32 sums)

@@ -98,6 +98,14 @@ def test_distill_workspace():
                            (256, 16384, 16384, 128)):
         b = q(N, H, V, 5, chunk, 1)
         assert b <= max(4 * V * chunk, 4 * V * 64) + 2 * H * 256 + (50 << 20) + 8 * N + 48 * N + 4096
+    # a huge chunk_size is a chunk past N
+    assert q(40, 64, 1000, 5, (1 << 63) - 1, 2) == q(40, 64, 1000, 5, 1 << 40, 2)
+    # every size on the way between the kernels' limits
+    for N in (0, 1, 16, 17, 32, 33, 64, 65, 128, 129, 192, 193, 256, 257, 5000):
+        for V in (1, 63, 8191, 8192, 8193, 151936, (1 << 23) - 256):
+            for chunk in (1, 31, 32, 64, 4096):
+                sizes = [q(N, 64, V, 3, chunk, kind) for kind in (0, 1, 2)]
+                assert 0 < sizes[0] <= sizes[1] <= sizes[2]
     # beyond 2^31 entries the sizes are still whole
     N, K = 1 << 22, 1024
     assert q(N, 64, 1000, K, 16, 1) > N * (K + 1) * 6

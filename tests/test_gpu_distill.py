@@ -222,6 +222,107 @@ def test_distill_masked_places_hold_anything():
     assert (good[0][108:] == 0).all() and (good[2][108:] == 0).all() and (good[4][108:] == 0).all()
 
 
+def test_distill_empty_rows_with_any_cotangent():
+    """A token without a teacher entry but with a hard target: its kl cotangent
+    is not looked at. One with entries of no mass: kl 0, no gradient of it."""
+    import torch
+    import cross_entropy_amd as lm
+    for N, V in ((20, 300), (300, 2000)):
+        args = _case(30, N, 128, V, 6, hard=True, pad=0.0)
+        h, W, targets, ids, t, tlse = args
+        ids[:10] = -1
+        targets[:10] = np.arange(10)
+        t[10:15] = -np.inf
+        hd, Wd, tg, idd, td, tl = _put(*args)
+        g_kl, g_logp = _g(31, N, True)
+        kl, logp, lse, top = lm.distill_forward(hd, Wd, tg, idd, td, 64, tl)
+        good = lm.distill_backward(hd, Wd, tg, idd, td, 64, logp, lse, top, dev(g_kl), dev(g_logp), tl)
+        g_kl[:5], g_kl[5:10] = np.nan, np.inf
+        bad = lm.distill_backward(hd, Wd, tg, idd, td, 64, logp, lse, top, dev(g_kl), dev(g_logp), tl)
+        torch.cuda.synchronize()
+        assert (kl[:15] == 0).all() and all(torch.equal(a, b) for a, b in zip(good, bad))
+        ref = R.Distill(bf16_bits_to_f32(h), bf16_bits_to_f32(W), targets, ids, t, tlse, 1.0)
+        g_kl[:10] = 0.0
+        rh, rW, eh, eW = ref.backward(g_kl, g_logp, "f32")
+        R.check(_np(good[0]), rh, eh, "dh")
+        R.check(_np(good[1]), rW, eW, "dW")
+
+
+def test_calls_on_a_stream_of_their_own():
+    """The allocating helpers given a stream: results, workspaces and outputs
+    belong to it, with work of the current stream around the call."""
+    import torch
+    import cross_entropy_amd as lm
+    hd, Wd, tg, idd, td, tl = _put(*_case(32, 300, 128, 1300, 8, hard=True))
+    gk, gl = (dev(a) for a in _g(8, 300, True))
+    x = torch.randn(400, 640, device="cuda")
+
+    def run(stream):
+        kl, logp, lse, top = lm.distill_forward(hd, Wd, tg, idd, td, 64, tl, stream=stream)
+        out = (kl, logp, lse, top) + lm.distill_backward(hd, Wd, tg, idd, td, 64, logp, lse, top, gk, gl, tl,
+                                                         stream=stream)
+        y, mean, rstd = lm.norm_forward(x, stream=stream)
+        return out + (y, mean, rstd) + lm.norm_backward(x, None, mean, rstd, y, with_bias=True, stream=stream)
+
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        junk = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(8)]
+        del junk
+        got = run(stream)
+        junk = [torch.full((1 << 20,), 9.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_distill_table_beyond_32_bit_offsets():
+    """W and dW of 5.2 GB, ids at their end, for few tokens and for the tiles:
+    against float32 on the rows that matter."""
+    import torch
+    import cross_entropy_amd as lm
+    H, V, K = 4096, 640000, 4
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    W = torch.empty(V, H, device="cuda", dtype=torch.bfloat16)
+    for r in range(0, V, 80000):
+        W[r:r + 80000] = 0.02 * torch.randn(80000, H, device="cuda", generator=gen)
+    for N in (5, 300):
+        log(f"[distill] beyond 32-bit offsets N={N}")
+        h = torch.randn(N, H, device="cuda", generator=gen).bfloat16()
+        ids = (V - 1 - torch.arange(N * K, device="cuda", dtype=torch.int32) * 7).view(N, K)
+        t = torch.randn(N, K, device="cuda", generator=gen)
+        tg = ids[:, 1].contiguous()
+        kl, logp, lse, top = lm.distill_forward(h, W, tg, ids, t, 64)
+        one = torch.ones(N, device="cuda")
+        dh, dW = lm.distill_backward(h, W, tg, ids, t, 64, logp, lse, top, one, one, grad_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        z = torch.cat([h.float() @ W[r:r + 80000].float().t() for r in range(0, V, 80000)], 1)
+        want = torch.logsumexp(z, 1)
+        # either side's logits are 2^-24 (4096 + 8) sum |h w| off at most, sum |h w| = 4096 * 0.8 * 0.016 = 52 on average
+        # and below 70; their log-sum-exps 2^-10 more (2^10 additions, logarithm, size 13)
+        tol = 2 * 2.0 ** -24 * 4104 * 70 + 2 * 2.0 ** -10
+        assert (lse - want).abs().max() <= tol
+        assert (top - (z.gather(1, ids.long()) - want[:, None])).abs().max() <= 2 * tol
+        q = torch.softmax(t, 1)
+        p = torch.exp(z - want[:, None])
+        dz = p * 0.0                             # Q = 1: g_kl Q - g_logp = 0 away from the special entries
+        dz.scatter_add_(1, ids.long(), -q)
+        dz.scatter_add_(1, tg.long()[:, None], one[:, None])
+        last = slice(V - 8 * N * K, V)
+        ref = dz[:, last].t() @ h.float()
+        # each entry: q off by 2^-20, one rounding of the cotangent, float32 sums, the stored rounding
+        lim = (2 * 2.0 ** -8 + 2.0 ** -12) * (dz[:, last].abs().t() @ h.float().abs()) + 1e-6
+        assert ((dW[last].float() - ref).abs() <= lim).all()
+        assert (dW[:V // 2].float().abs() <= 1e-5).all()
+        rows = W[ids.long()].float()                                # [N, K, H]
+        coef = dz.gather(1, ids.long())
+        ref = (coef[:, :, None] * rows).sum(1)
+        lim = (2 * 2.0 ** -8 + 2.0 ** -12) * (coef.abs()[:, :, None] * rows.abs()).sum(1) + 1e-5
+        assert ((dh.float() - ref).abs() <= lim).all()
+        del z, p, dz, dW
+
+
 def test_distill_extreme_teacher_logits():
     """Lowest values, -inf rows, huge spreads; NaN and +inf stay in their row."""
     args = _case(11, 64, 64, 300, 6, hard=True, pad=0.0)

@@ -153,6 +153,25 @@ def test_norm_writes_only_its_rows():
         assert not (big[1:N + 1] == 3).all()
 
 
+def test_norm_beyond_32_bit_offsets():
+    """5.2 GB of rows: the last ones give the bits of a call of their own."""
+    import torch
+    import cross_entropy_amd as lm
+    N, H = 640000, 4096
+    x = torch.empty(N, H, device="cuda", dtype=torch.bfloat16)
+    for r in range(0, N, 80000):
+        x[r:r + 80000] = torch.randn(80000, H, device="cuda")
+    y, mean, rstd = lm.norm_forward(x)
+    dx, _, _ = lm.norm_backward(x, None, mean, rstd, y, with_weight=False)
+    for rows in (slice(0, 50), slice(N - 50, N)):
+        part = x[rows].contiguous()
+        y2, m2, r2 = lm.norm_forward(part)
+        d2, _, _ = lm.norm_backward(part, None, m2, r2, y2, with_weight=False)
+        torch.cuda.synchronize()
+        for a, b in ((y[rows], y2), (mean[rows], m2), (rstd[rows], r2), (dx[rows], d2)):
+            assert torch.equal(a, b)
+
+
 def test_norm_adds_into_gradients():
     import torch
     import cross_entropy_amd as lm
