@@ -123,32 +123,39 @@ __device__ __forceinline__ void store_part(void* base, int64_t row, int H, int t
   }
 }
 
-// Sum over a wave in a fixed order, on the vector unit alone (data-parallel
-// moves within rows of 16 lanes, then across rows; lane 63 holds the total).
+// Sum over LANES lanes (16, 32 or 64) in a fixed order, on the vector unit alone
+// up to 16 (data-parallel moves within rows of 16 lanes; then across rows).
+// Every one of them gets the sum.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_add(float v) {
   const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false);
   return v + __int_as_float(o);
 }
-__device__ __forceinline__ float wave_sum(float v) {
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float v) {
   v = dpp_add<0xB1, 0xF>(v);    // lanes ^ 1
   v = dpp_add<0x4E, 0xF>(v);    // lanes ^ 2
   v = dpp_add<0x141, 0xF>(v);   // the other four of eight
   v = dpp_add<0x140, 0xF>(v);   // the other eight of the row
-  v = dpp_add<0x142, 0xA>(v);   // rows 1 and 3 add rows 0 and 2
-  v = dpp_add<0x143, 0xC>(v);   // rows 2 and 3 add row 1's
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+  if (LANES == 32) v += __shfl_xor(v, 16);
+  if (LANES == 64) {
+    v = dpp_add<0x142, 0xA>(v);   // rows 1 and 3 add rows 0 and 2
+    v = dpp_add<0x143, 0xC>(v);   // rows 2 and 3 add row 1's
+    v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+  }
+  return v;
 }
 
-// Sums of two values over the threads of a row: the wave, then (a block per
-// row) the waves' sums through LDS in order. The two halves of `s` alternate
-// between calls, so one barrier a call is enough.
-constexpr int kMaxWaves = 8;
-template <bool WIDE>
+// Sums of two values over the threads of a row: LANES lanes, or (WIDE, a block
+// per row) the wave, then the waves' sums through LDS in order. The two halves
+// of `s` alternate between calls, so one barrier a call is enough.
+constexpr int kMaxWaves = 16;
+constexpr int kWide = 0, kHuge = -1;   // LANES of a block per row: up to 512 threads, up to 1024
+template <int LANES>
 __device__ __forceinline__ void row_sum2(float& a, float& b, bool two, float (*s)[kMaxWaves][2], int& turn) {
-  a = wave_sum(a);
-  if (two) b = wave_sum(b);
-  if (WIDE) {
+  a = lane_sum<LANES <= 0 ? 64 : LANES>(a);
+  if (two) b = lane_sum<LANES <= 0 ? 64 : LANES>(b);
+  if (LANES <= 0) {
     const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) {
       s[turn][threadIdx.x >> 6][0] = a;
@@ -165,16 +172,17 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, bool two, float (*s
   }
 }
 
-// Forward: a row's threads (a wave, or with WIDE the block) walk rows `step`
+// Forward: a row's threads (LANES lanes, or kWide the block) walk rows `step`
 // apart, the weights in registers, the next row's loads in flight while the
 // present one is worked on.
-template <bool XF32, bool YF32, bool WF32, int NV, bool WIDE>
-__global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(const NormFwdArgs a) {
+template <bool XF32, bool YF32, bool WF32, int NV, int LANES>
+__global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_fwd_kernel(const NormFwdArgs a) {
   constexpr int G = XF32 ? 4 : 8, NG = 8 * NV / G;
   __shared__ float s[2][kMaxWaves][2];
-  const int threads = WIDE ? blockDim.x : 64;
-  const int t = WIDE ? threadIdx.x : threadIdx.x & 63;
-  const int per = WIDE ? 1 : blockDim.x >> 6;
+  constexpr bool WIDE = LANES <= 0;
+  const int threads = WIDE ? blockDim.x : LANES;
+  const int t = WIDE ? threadIdx.x : threadIdx.x % (WIDE ? 1 : LANES);
+  const int per = WIDE ? 1 : blockDim.x / threads;
   const int64_t step = (int64_t)gridDim.x * per;
   const int H = a.H;
   const float inv = 1.0f / (float)H;
@@ -182,7 +190,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(const NormFwdA
   Part<WF32, G, NG> w, b;
   if (a.w != nullptr) w.load(a.w, 0, H, t, threads); else w.fill(1.0f);
   if (a.b != nullptr) b.load(a.b, 0, H, t, threads); else b.fill(0.0f);
-  int64_t row = (int64_t)blockIdx.x * per + (WIDE ? 0 : threadIdx.x >> 6);
+  int64_t row = (int64_t)blockIdx.x * per + (WIDE ? 0 : threadIdx.x / threads);
   Part<XF32, G, NG> next;
   if (row < a.N) next.load(a.x, row, H, t, threads);
   for (; row < a.N; row += step) {
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(const NormFwdA
       for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int k = 0; k < G; ++k) mu += x[i][k];
-      row_sum2<WIDE>(mu, none, false, s, turn);
+      row_sum2<LANES>(mu, none, false, s, turn);
       mu *= inv;
     }
     float q = 0.0f;
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(const NormFwdA
         x[i][k] -= mu;
         q = in[i][k] ? fmaf(x[i][k], x[i][k], q) : q;
       }
-    row_sum2<WIDE>(q, none, false, s, turn);
+    row_sum2<LANES>(q, none, false, s, turn);
     const float r = 1.0f / sqrtf(fmaf(q, inv, a.eps));
 #pragma unroll
     for (int i = 0; i < NG; ++i)
@@ -233,30 +241,34 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_fwd_kernel(const NormFwdA
 // which norm_reduce_kernel sums in block order. A zero in dy contributes a
 // zero whatever x, the statistics and w hold there (mul0), so a masked token,
 // whose dy row is 0, adds nothing and gets dx = 0 even where its x is NaN.
-template <bool XF32, bool YF32, bool WF32, int NV, bool WIDE>
-__global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_kernel(const NormBwdArgs a) {
+template <bool XF32, bool YF32, bool WF32, int NV, int LANES>
+__global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int G = XF32 ? 4 : 8, NG = 8 * NV / G;
-  extern __shared__ float lds[];   // [2][H]: the block's dw and db (not WIDE)
+  extern __shared__ float lds[];   // [2][H]: the block's dw and db (LANES > 0)
+  // 1024 threads have 128 registers each, which the sums would overflow: there
+  // they live in LDS, each thread's at its own columns
+  constexpr bool kept = LANES == kHuge;
+  __shared__ __attribute__((aligned(16))) float sums[2][kept ? kNormMaxH : 4];
   __shared__ float s[2][kMaxWaves][2];
-  const int threads = WIDE ? blockDim.x : 64;
-  const int t = WIDE ? threadIdx.x : threadIdx.x & 63;
-  const int per = WIDE ? 1 : blockDim.x >> 6;
-  const int slot = WIDE ? 0 : threadIdx.x >> 6;
+  constexpr bool WIDE = LANES <= 0;
+  const int threads = WIDE ? blockDim.x : LANES;
+  const int t = WIDE ? threadIdx.x : threadIdx.x % (WIDE ? 1 : LANES);
+  const int per = WIDE ? 1 : blockDim.x / threads;
+  const int slot = WIDE ? 0 : threadIdx.x / threads;
   const int64_t step = (int64_t)gridDim.x * per;
   const int H = a.H;
   const float inv = 1.0f / (float)H;
   int turn = 0;
-  constexpr bool ahead = NV <= 2;   // with 32 elements a thread, weights and next row held over would spill
   Part<WF32, G, NG> w;
-  auto weights = [&] {
-    if (a.w != nullptr) w.load(a.w, 0, H, t, threads); else w.fill(1.0f);
-  };
-  if (ahead) weights();
+  if (a.w != nullptr) w.load(a.w, 0, H, t, threads); else w.fill(1.0f);
   float dw[NG][G], db[NG][G];
 #pragma unroll
   for (int i = 0; i < NG; ++i)
 #pragma unroll
-    for (int k = 0; k < G; ++k) dw[i][k] = db[i][k] = 0.0f;
+    for (int k = 0; k < G; ++k) {
+      dw[i][k] = db[i][k] = 0.0f;
+      if (kept) sums[0][G * (i * threads + t) + k] = sums[1][G * (i * threads + t) + k] = 0.0f;   // 16 a thread: within kNormMaxH
+    }
   int64_t row = (int64_t)blockIdx.x * per + slot;
   Part<XF32, G, NG> nx;
   Part<YF32, G, NG> ng;
@@ -267,12 +279,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_kernel(const NormBwdA
     if (!a.rms) n_mu = a.mean[at];
     n_r = a.rstd[at];
   };
-  if (ahead && row < a.N) fetch(row);
+  if (row < a.N) fetch(row);
   for (; row < a.N; row += step) {
-    if (!ahead) {
-      fetch(row);
-      weights();
-    }
     float x[NG][G], g[NG][G];
     const float mu = n_mu, r = n_r;
 #pragma unroll
@@ -283,22 +291,28 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_kernel(const NormBwdA
         x[i][k] = nx.g[i].at(k);
         g[i][k] = in ? ng.g[i].at(k) : 0.0f;
       }
-    if (ahead && row + step < a.N) fetch(row + step);
+    if (row + step < a.N) fetch(row + step);
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NG; ++i)
 #pragma unroll
       for (int k = 0; k < G; ++k) {
         const float xh = (x[i][k] - mu) * r;
-        dw[i][k] += mul0(g[i][k], xh);
-        db[i][k] += g[i][k];
+        if (kept) {
+          const int j = G * (i * threads + t) + k;
+          sums[0][j] += mul0(g[i][k], xh);
+          sums[1][j] += g[i][k];
+        } else {
+          dw[i][k] += mul0(g[i][k], xh);
+          db[i][k] += g[i][k];
+        }
         const float gw = mul0(g[i][k], w.g[i].at(k));
         c1 += mul0(gw, xh);
         c2 += gw;
         x[i][k] = xh;
         g[i][k] = gw;
       }
-    row_sum2<WIDE>(c1, c2, !a.rms, s, turn);
+    row_sum2<LANES>(c1, c2, !a.rms, s, turn);
     c1 *= inv;
     c2 = a.rms ? 0.0f : c2 * inv;
 #pragma unroll
@@ -310,12 +324,36 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_kernel(const NormBwdA
   if (a.part == nullptr) return;
   float* out = a.part + (int64_t)blockIdx.x * 2 * H;
   if (WIDE) {
+    if (kept) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          const int j = G * (i * threads + t) + k;
+          dw[i][k] = sums[0][j];
+          db[i][k] = sums[1][j];
+        }
+    }
     store_part<true, G, NG>(out, 0, H, t, threads, dw);
     store_part<true, G, NG>(out + H, 0, H, t, threads, db);
     return;
   }
-  for (int i0 = 0; i0 < per; ++i0) {
-    if (slot == i0) {
+  // the rows of a wave by halves, then the waves in order
+  if (LANES < 64) {
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int k = 0; k < G; ++k)
+#pragma unroll
+        for (int x = 32; x >= (WIDE ? 64 : LANES); x >>= 1) {
+          dw[i][k] += __shfl_xor(dw[i][k], x);
+          db[i][k] += __shfl_xor(db[i][k], x);
+        }
+  }
+  const int waves = blockDim.x >> 6;
+  const bool first_rows = (threadIdx.x & 63) < threads;
+  for (int i0 = 0; i0 < waves; ++i0) {
+    if (first_rows && (int)(threadIdx.x >> 6) == i0) {
 #pragma unroll
       for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -326,7 +364,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_bwd_kernel(const NormBwdA
             dw[i][k] += lds[j];
             db[i][k] += lds[H + j];
           }
-          if (i0 < per - 1) {
+          if (i0 < waves - 1) {
             lds[j] = dw[i][k];
             lds[H + j] = db[i][k];
           } else {
@@ -392,30 +430,37 @@ __global__ __launch_bounds__(kRedThreads) void norm_reduce_kernel(const NormRedu
   }
 }
 
-// How rows of H are laid over threads: a wave per row up to 1024 elements
-// (no barrier), above that a block per row with as few elements a thread as
-// 512 threads allow.
+// How rows of H are laid over threads. Up to 1024 elements 16 to 64 lanes of a
+// wave per row (no barrier); above that a block per row, the forward with 16
+// elements a thread (two loads in flight beside the next row's two; 65536 x 2560
+// bf16: 137 us, with 8 168) and the backward, whose sums take registers too,
+// with 8 up to 4096.
 struct Shape {
-  int nv;
-  bool wide;
+  int nv, lanes;
   int block, per;   // threads per block, rows per block
 };
-Shape shape_of(int64_t H) {
-  if (H <= 1024) return {H <= 512 ? 1 : 2, false, 256, 4};
-  const int nv = H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
-  return {nv, true, (int)((H + 8 * nv * 64 - 1) / (8 * nv * 64)) * 64, 1};
+Shape shape_of(int64_t H, bool backward) {
+  if (H <= 1024) {
+    const int lanes = H <= 128 ? 16 : H <= 256 ? 32 : 64;
+    return {H <= 512 ? 1 : 2, lanes, 256, 256 / lanes};
+  }
+  const int nv = H <= 4096 && backward ? 1 : 2;
+  return {nv, H <= 8192 ? kWide : kHuge, (int)((H + 8 * nv * 64 - 1) / (8 * nv * 64)) * 64, 1};
 }
 
 template <class F>
 void with_shape(const Shape& p, F f) {
-  std::true_type yes;
-  std::false_type no;
-  if (!p.wide) {
-    if (p.nv == 1) f(std::integral_constant<int, 1>{}, no);
-    else f(std::integral_constant<int, 2>{}, no);
-  } else if (p.nv == 1) f(std::integral_constant<int, 1>{}, yes);
-  else if (p.nv == 2) f(std::integral_constant<int, 2>{}, yes);
-  else f(std::integral_constant<int, 4>{}, yes);
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, kWide> wide{};
+  constexpr std::integral_constant<int, kHuge> huge{};
+  if (p.lanes == 16) f(one, std::integral_constant<int, 16>{});
+  else if (p.lanes == 32) f(one, std::integral_constant<int, 32>{});
+  else if (p.lanes == 64 && p.nv == 1) f(one, std::integral_constant<int, 64>{});
+  else if (p.lanes == 64) f(two, std::integral_constant<int, 64>{});
+  else if (p.lanes == kWide && p.nv == 1) f(one, wide);
+  else if (p.lanes == kWide) f(two, wide);
+  else f(two, huge);
 }
 
 // The types of x, y and the weights (float32 y comes with float32 x only).
@@ -435,19 +480,19 @@ constexpr int kWavesPerCU = 32;
 // A row per wave or block while that leaves at most a workgroup per CU, then
 // 4 rows each up to 16 waves per CU.
 int norm_bwd_blocks(int64_t N, int64_t H) {
-  const Shape p = shape_of(H);
+  const Shape p = shape_of(H, true);
   const int64_t full = kNumCUs * std::max(1, 16 * 64 / p.block);
   const int64_t rows = (N + p.per - 1) / p.per;
   return (int)std::max<int64_t>(1, std::min(rows, std::max<int64_t>(kNumCUs, std::min((rows + 3) / 4, full))));
 }
 
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
-  const Shape p = shape_of(a.H);
+  const Shape p = shape_of(a.H, false);
   const int64_t blocks = std::min<int64_t>((a.N + p.per - 1) / p.per, kNumCUs * (kWavesPerCU * 64 / p.block));
   trace_begin(stream);
   with_types(a.x_f32, a.y_f32, a.w_f32, [&](auto x, auto y, auto w) {
-    with_shape(p, [&](auto nv, auto wide) {
-      hipLaunchKernelGGL((norm_fwd_kernel<x(), y(), w(), nv(), wide()>), dim3((unsigned)blocks), dim3(p.block), 0,
+    with_shape(p, [&](auto nv, auto lanes) {
+      hipLaunchKernelGGL((norm_fwd_kernel<x(), y(), w(), nv(), lanes()>), dim3((unsigned)blocks), dim3(p.block), 0,
                          stream, a);
     });
   });
@@ -459,12 +504,12 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int blocks, hipStream_t stream) {
-  const Shape p = shape_of(a.H);
-  const size_t lds = p.wide ? 0 : (size_t)2 * a.H * 4;
+  const Shape p = shape_of(a.H, true);
+  const size_t lds = p.lanes <= 0 ? 0 : (size_t)2 * a.H * 4;
   trace_begin(stream);
   with_types(a.x_f32, a.y_f32, a.w_f32, [&](auto x, auto y, auto w) {
-    with_shape(p, [&](auto nv, auto wide) {
-      hipLaunchKernelGGL((norm_bwd_kernel<x(), y(), w(), nv(), wide()>), dim3(blocks), dim3(p.block), lds, stream, a);
+    with_shape(p, [&](auto nv, auto lanes) {
+      hipLaunchKernelGGL((norm_bwd_kernel<x(), y(), w(), nv(), lanes()>), dim3(blocks), dim3(p.block), lds, stream, a);
     });
   });
   const hipError_t e = hipGetLastError();
