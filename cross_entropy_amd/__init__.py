@@ -90,7 +90,9 @@ def _torch():
 
 
 def _ptr(t, name, dtypes, device, numel=None, optional=False):
-    # the usual case first: small calls are bound by what is done here
+    # the usual cases first: small calls are bound by what is done here
+    if t is None and optional:
+        return 0
     try:
         if (t.dtype in dtypes and t.is_cuda and t.device == device and t.is_contiguous()
                 and (numel is None or t.numel() == numel)):
@@ -420,6 +422,16 @@ def _type_of(t, name):
     return code
 
 
+_F32_TYPES = ()
+
+
+def _f32_types():
+    global _F32_TYPES
+    if not _F32_TYPES:
+        _F32_TYPES = (_torch().float32,)
+    return _F32_TYPES
+
+
 _ANY_TYPES = {}
 
 
@@ -454,7 +466,7 @@ def lmhead_logps_distill_fwd(hidden, W, targets, ids, teacher, teacher_lse, chun
     and logp_top [N, K] (float32). ``targets`` (int32 [N]) and ``teacher_lse``
     (float32 [N]) may be None; ``ids`` is int32 [N, K], ``teacher`` float32 or
     bfloat16 [N, K]."""
-    f32 = (_torch().float32,)
+    f32 = _f32_types()
     dev, N, K, args = _distill_args(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature)
     _enqueue(
         dev, _native.raw_distill_fwd, *args, _ptr(kl, "kl", f32, dev, N), _ptr(logp, "logp", f32, dev, N, optional=True), _ptr(lse, "lse", f32, dev, N),
@@ -467,7 +479,7 @@ def lmhead_logps_distill_bwd(hidden, W, targets, ids, teacher, teacher_lse, chun
     """Enqueue the distillation backward into dh [N, H] / dW [V, H], both
     float32 or both bfloat16; ``flags`` as for ``lmhead_logps_bwd_ex``; the
     workspace is that of ``distill_workspace_for`` (True or "bf16")."""
-    f32 = (_torch().float32,)
+    f32 = _f32_types()
     dev, N, K, args = _distill_args(hidden, W, targets, ids, teacher, teacher_lse, chunk_size, temperature)
     if dh.shape != hidden.shape or dW.shape != W.shape:
         raise ValueError("dh must be [N,H] and dW [V,H]")
@@ -547,18 +559,17 @@ _NORM_KINDS = {"layer": _native.NORM_LAYER, "rms": _native.NORM_RMS}
 
 
 def _norm_kind(kind):
-    if kind not in _NORM_KINDS:
+    code = _NORM_KINDS.get(kind)
+    if code is None:
         raise ValueError(f"kind must be 'layer' or 'rms', got {kind!r}")
-    return _NORM_KINDS[kind]
+    return code
 
 
 def _norm_shape(x):
-    if x.dim() < 1:
-        raise ValueError("x must have a last dimension to normalise")
-    H = x.shape[-1]
-    if H < 1:
-        raise ValueError("the last dimension of x must not be empty")
-    return x.numel() // H, H
+    shape = x.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError("x must have a last dimension to normalise, and it must not be empty")
+    return x.numel() // shape[-1], shape[-1]
 
 
 def lmhead_logps_norm_workspace_bytes(N: int, H: int) -> int:
@@ -566,28 +577,29 @@ def lmhead_logps_norm_workspace_bytes(N: int, H: int) -> int:
     return _native.raw_norm_workspace_bytes(N, H)
 
 
-def _vector_type(a, b, names):
+def _vector_type(a, b, name_a, name_b):
     """The one type of two optional vectors (float32 if there is neither)."""
-    if a is not None and b is not None and a.dtype != b.dtype:
-        raise TypeError(f"{names[0]} and {names[1]} must have one dtype, got {a.dtype} and {b.dtype}")
-    some = a if a is not None else b
-    return _native.TYPE_F32 if some is None else _type_of(some, names[0] if a is not None else names[1])
+    if a is None:
+        return _native.TYPE_F32 if b is None else _type_of(b, name_b)
+    if b is not None and a.dtype != b.dtype:
+        raise TypeError(f"{name_a} and {name_b} must have one dtype, got {a.dtype} and {b.dtype}")
+    return _type_of(a, name_a)
 
 
 def lmhead_logps_norm_fwd(x, weight, bias, eps: float, kind: str, y, mean, rstd, stream=None) -> None:
     """Enqueue the norm of x [..., H] into y (x's shape; bfloat16, or float32
     where x is). weight and bias [H] may be None, and mean / rstd (float32,
     one per row, for the backward) too; kind is "layer" or "rms"."""
-    f32 = (_torch().float32,)
+    any_, f32 = _any_types(), _f32_types()
     N, H = _norm_shape(x)
     dev = x.device
     if y.shape != x.shape:
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {tuple(x.shape)}")
     _enqueue(
-        dev, _native.raw_norm_fwd, _ptr(x, "x", _any_types(), dev), _type_of(x, "x"), _ptr(weight, "weight", _any_types(), dev, H, optional=True),
-        _ptr(bias, "bias", _any_types(), dev, H, optional=True), _vector_type(weight, bias, ("weight", "bias")), N, H,
-        eps, _norm_kind(kind), _ptr(y, "y", _any_types(), dev), _type_of(y, "y"),
-        _ptr(mean, "mean", f32, dev, N, optional=True), _ptr(rstd, "rstd", f32, dev, N, optional=True),
+        dev, _native.raw_norm_fwd, _ptr(x, "x", any_, dev), any_[x.dtype],
+        _ptr(weight, "weight", any_, dev, H, True), _ptr(bias, "bias", any_, dev, H, True),
+        _vector_type(weight, bias, "weight", "bias"), N, H, eps, _norm_kind(kind), _ptr(y, "y", any_, dev),
+        any_[y.dtype], _ptr(mean, "mean", f32, dev, N, True), _ptr(rstd, "rstd", f32, dev, N, True),
         _stream(dev, stream))
 
 
@@ -597,23 +609,22 @@ def lmhead_logps_norm_bwd(x, weight, kind: str, mean, rstd, dy, dx, dweight, dbi
     dweight and dbias [H] (float32 or bfloat16); ``flags`` 0 or
     ``_native.BWD_ACCUMULATE_DW`` (add into dweight and dbias). The workspace
     may be None where neither is wanted."""
-    f32 = (_torch().float32,)
+    any_, f32 = _any_types(), _f32_types()
     N, H = _norm_shape(x)
     dev = x.device
     if dy.shape != x.shape or dx.shape != x.shape:
         raise ValueError(f"dy and dx must have x's shape {tuple(x.shape)}, got {tuple(dy.shape)} and {tuple(dx.shape)}")
-    if _type_of(dx, "dx") != _type_of(x, "x"):
+    x_type = _type_of(x, "x")
+    if _type_of(dx, "dx") != x_type:
         raise TypeError(f"dx must have x's dtype {x.dtype}, got {dx.dtype}")
     _enqueue(
-        dev, _native.raw_norm_bwd, _ptr(x, "x", _any_types(), dev), _type_of(x, "x"), _ptr(weight, "weight", _any_types(), dev, H, optional=True),
-        _vector_type(weight, None, ("weight", "")), N, H, _norm_kind(kind),
-        _ptr(mean, "mean", f32, dev, N, optional=True), _ptr(rstd, "rstd", f32, dev, N),
-        _ptr(dy, "dy", _any_types(), dev), _type_of(dy, "dy"), _ptr(dx, "dx", _any_types(), dev),
-        _ptr(dweight, "dweight", _any_types(), dev, H, optional=True),
-        _ptr(dbias, "dbias", _any_types(), dev, H, optional=True),
-        _vector_type(dweight, dbias, ("dweight", "dbias")), flags,
-        _ptr(workspace, "workspace", (_torch().uint8,), dev, optional=True),
-        0 if workspace is None else workspace.numel(), _stream(dev, stream))
+        dev, _native.raw_norm_bwd, _ptr(x, "x", any_, dev), x_type, _ptr(weight, "weight", any_, dev, H, True),
+        _vector_type(weight, None, "weight", ""), N, H, _norm_kind(kind), _ptr(mean, "mean", f32, dev, N, True),
+        _ptr(rstd, "rstd", f32, dev, N), _ptr(dy, "dy", any_, dev), any_[dy.dtype], _ptr(dx, "dx", any_, dev),
+        _ptr(dweight, "dweight", any_, dev, H, True), _ptr(dbias, "dbias", any_, dev, H, True),
+        _vector_type(dweight, dbias, "dweight", "dbias"), flags,
+        _ptr(workspace, "workspace", (_torch().uint8,), dev, None, True), 0 if workspace is None else workspace.numel(),
+        _stream(dev, stream))
 
 
 def norm_workspace_for(x):
