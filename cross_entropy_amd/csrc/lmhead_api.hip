@@ -497,11 +497,22 @@ int bwd_impl(const char* who, const uint16_t* hidden, const uint16_t* W, const i
   const int64_t nb = p.n_tb * p.n_vb;
   // the cotangent-tile counters start at zero (a fill kernel, not a memset:
   // the call may be captured into a graph)
-  hipError_t te = lmh::launch_fill_zero(reinterpret_cast<float*>(ctr), (nb + 1) * 8, s);
-  if (te == hipSuccess && distill) te = lmh::launch_distill_prep(distill->prep, s);
+  hipError_t te;
+  if (distill) {
+    lmh::DistillPrepArgs prep = distill->prep;
+    prep.ctr = ctr;
+    prep.n_ctr = (nb + 1) * 8;
+    prep.tail_in = W + v_tail * H;
+    prep.tail_out = W_tail;
+    prep.tail_rows = (int)(V - v_tail);
+    prep.H = (int)H;
+    te = lmh::launch_distill_prep(prep, s);
+  } else {
+    te = lmh::launch_fill_zero(reinterpret_cast<float*>(ctr), (nb + 1) * 8, s);
+  }
   if (te == hipSuccess)
     te = lmh::launch_transpose(hidden, H, N, H, p.N_pad, p.H_pad, targets, Vtot, ht, p.ld_ht, s);
-  if (te == hipSuccess && v_tail < V) te = lmh::launch_pad_rows(W + v_tail * H, V - v_tail, H, 64, W_tail, s);
+  if (te == hipSuccess && v_tail < V && !distill) te = lmh::launch_pad_rows(W + v_tail * H, V - v_tail, H, 64, W_tail, s);
   if (te != hipSuccess) return fail(LMH_ERR_HIP, "%s: launch failed: %s", who, hipGetErrorString(te));
 
   lmh::BwdStep st{};
@@ -951,7 +962,8 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
     // a hard target without a cotangent takes no part
     hook.prep = {g_logp != nullptr ? targets : nullptr, ids, teacher, teacher_type == LMH_TYPE_F32, teacher_lse, N,
                  (int)V, (int)K, temperature, inv_temperature(temperature), logp, logp_top, g_kl, g_logp, w_tgt, w_ga,
-                 reinterpret_cast<int32_t*>(ws + d.off_id), reinterpret_cast<float*>(ws + d.off_val)};
+                 reinterpret_cast<int32_t*>(ws + d.off_id), reinterpret_cast<float*>(ws + d.off_val),
+                 nullptr, 0, nullptr, nullptr, 0, 0};
     if (d.few) {
       if (workspace_bytes < d.bytes)
         return fail(LMH_ERR_WORKSPACE, "distill_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, d.bytes);

@@ -202,6 +202,16 @@ __global__ __launch_bounds__(64 * kPrepWaves) void distill_prep_kernel(const Dis
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
   const int K = a.K, V = a.V;
+  const int64_t prep_blocks = (a.N + kPrepWaves - 1) / kPrepWaves;
+  if (blockIdx.x >= prep_blocks) {   // the tiles' counters and padded rows
+    const int64_t step = (gridDim.x - prep_blocks) * (int64_t)blockDim.x;
+    const int64_t i0 = (blockIdx.x - prep_blocks) * (int64_t)blockDim.x + threadIdx.x;
+    for (int64_t i = i0; i < a.n_ctr; i += step) a.ctr[i] = 0;
+    const int64_t in = (int64_t)a.tail_rows * a.H / 8, n = a.tail_rows > 0 ? (int64_t)8 * a.H : 0;
+    for (int64_t i = i0; i < n; i += step)
+      reinterpret_cast<uint4*>(a.tail_out)[i] = i < in ? reinterpret_cast<const uint4*>(a.tail_in)[i] : make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
   int* s_id = lds + wave * 2 * K;
   float* s_q = reinterpret_cast<float*>(s_id + K);
   const int64_t tok = min((int64_t)blockIdx.x * kPrepWaves + wave, a.N - 1);   // a wave too many repeats the last token
@@ -460,7 +470,9 @@ hipError_t launch_distill_top(DistillTopArgs a, hipStream_t stream) {
 hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream) {
   const double N = (double)a.N, K = (double)a.K;
   trace_begin(stream);
-  hipLaunchKernelGGL(distill_prep_kernel, dim3((unsigned)((a.N + kPrepWaves - 1) / kPrepWaves)), dim3(64 * kPrepWaves),
+  const int64_t rest = std::max<int64_t>(a.n_ctr, a.tail_rows > 0 ? (int64_t)8 * a.H : 0);
+  const int64_t blocks = (a.N + kPrepWaves - 1) / kPrepWaves + std::min<int64_t>((rest + 255) / 256, 256);
+  hipLaunchKernelGGL(distill_prep_kernel, dim3((unsigned)blocks), dim3(64 * kPrepWaves),
                      (size_t)kPrepWaves * 2 * a.K * 4, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

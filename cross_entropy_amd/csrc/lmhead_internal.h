@@ -166,6 +166,13 @@ struct DistillPrepArgs {
   float* ga;                  // [N]
   int32_t* ent_id;            // [N][K + 1]
   float* ent_val;             // [N][K + 1]
+  // what the tiles need besides, in the same launch: n_ctr zeroed counters, and
+  // W's last tail_rows rows with zero rows up to 64 (none if tail_rows is 0)
+  int* ctr;
+  int64_t n_ctr;
+  const uint16_t* tail_in;
+  uint16_t* tail_out;
+  int tail_rows, H;
 };
 
 // A backward launch, its dh tiles split over the block's vocabulary or (part
