@@ -392,12 +392,13 @@ namespace {
 
 // The distillation's part of a backward: its per-token preparation, launched
 // before everything else, the special entries that overwrite each cotangent
-// block once it is formed, and (splits > 1) its launches with split dh tiles.
-// `bytes` is the whole workspace it needs.
+// block once it is formed, and (k_split > 0) its launches with split gradient
+// tiles. `bytes` is the whole workspace it needs.
 struct DistillHook {
   lmh::DistillPrepArgs prep;
-  int splits, k_split;
+  int k_split, w_k_split;   // vocabulary rows of a dh split; tokens of a dW split (0: dW is not split)
   float* part;
+  float* w_part;
   size_t bytes;
 };
 
@@ -417,31 +418,45 @@ hipError_t launch_distill_block(const DistillHook& h, const lmh::BwdStep& st, bo
     a.v0 = st.z_v0;
     a.Vb = st.z_Vb;
   }
-  hipError_t e;
-  if (h.splits > 1) {
+  lmh::DistillStep d{st, 1, 0, nullptr, 1, 0, nullptr};
+  if (h.k_split > 0) {
     // the block may be shorter than the plan's: as many splits as it fills
-    const int splits = grads ? (int)lmh::ceil_div(lmh::round_up(st.g_Vb, 64), h.k_split) : 1;
-    e = lmh::launch_distill_step({st, splits, h.k_split, h.part}, bf16, s);
+    auto count = [&](int k, int split) { return grads && split > 0 ? (int)lmh::ceil_div(lmh::round_up(k, 64), split) : 1; };
+    d.splits = count(st.g_Vb, h.k_split);
+    d.k_split = h.k_split;
+    d.part = h.part;
+    d.w_splits = count(st.g_Ct, h.w_k_split);
+    d.w_k_split = d.w_splits > 1 ? h.w_k_split : st.g_Ct;
+    d.w_part = h.w_part;
     if (grads) {
-      a.part = h.part;
-      a.splits = splits;
-      a.g_t0 = st.g_t0;
-      a.g_Ct = st.g_Ct;
       a.H = st.H;
       a.V = st.Vtot;
-      a.tgt = st.targets;
+      a.tgt = st.targets + st.g_t0;
+      a.dh.part = d.part;
+      a.dh.splits = d.splits;
+      a.dh.rows = st.g_Ct;
       if (bf16) {
-        a.o = st.o_dh;
+        a.dh.o = st.o_dh;
         a.dead_zero = st.dh_dead_zero;
       } else {
-        a.o.src_kind = st.g_acc_dh ? lmh::kSrcF32 : lmh::kSrcNone;
-        a.o.src = a.o.dst = st.dh + (int64_t)st.g_t0 * st.H;
+        a.dh.o.src_kind = st.g_acc_dh ? lmh::kSrcF32 : lmh::kSrcNone;
+        a.dh.o.src = a.dh.o.dst = st.dh + (int64_t)st.g_t0 * st.H;
         a.dead_zero = !st.g_acc_dh;
       }
     }
-  } else {
-    e = lmh::launch_distill_step({st, 1, 0, nullptr}, bf16, s);
+    if (grads && d.w_splits > 1) {
+      a.dW.part = d.w_part;
+      a.dW.splits = d.w_splits;
+      a.dW.rows = st.g_Vb;
+      if (bf16) {
+        a.dW.o = st.o_dW;
+      } else {
+        a.dW.o.src_kind = st.g_acc_dW ? lmh::kSrcF32 : lmh::kSrcNone;
+        a.dW.o.src = a.dW.o.dst = st.dW + (int64_t)st.g_v0 * st.H;
+      }
+    }
   }
+  const hipError_t e = lmh::launch_distill_step(d, bf16, s);
   return e == hipSuccess ? lmh::launch_distill_post(a, s) : e;
 }
 
@@ -696,11 +711,12 @@ struct DistillPlan {
   size_t fwd_bytes = 0;                                      // the forward: its split records alone
   size_t off_tgt = 0, off_ga = 0, off_id = 0, off_val = 0;   // the backward
   size_t off_part = 0, bytes = 0;                            // its dh splits; its total
-  int splits = 1, k_split = 0;
+  size_t off_w_part = 0;                                     // its dW splits
+  int k_split = 0, w_k_split = 0;                            // 0: not split
   // few tokens: their own kernels
   bool few = false;
   size_t off_hi = 0, off_lo = 0;
-  int dh_strips = 0, dh_rows = 0;
+  int dh_strips = 0, dh_rows = 0, dh_splits = 0;
 };
 
 // When the kernels for few tokens (lmhead_few.hip) run: they fetch W once per
@@ -722,29 +738,38 @@ bool few_backward(int64_t N, int64_t V, int64_t chunk_size) {
   return few_tokens(N, V) && few_padded(N) / (N <= 64 ? 1 : 2) <= chunk_size;
 }
 
-// Splits of the dh tiles over the block's vocabulary. A launch holds the dh
-// tiles (K = Vb), the dW tiles (K = Ct) and the next block's cotangent tiles
-// (K = H); in slices of 64 of K, a CU works off one in about 1 us, so the launch
-// takes all slices over the CUs, but no less than one dh tile's: a small N x H
-// has few dh tiles, each of which walks the whole vocabulary block alone (64
-// tokens, H 2560, V 151936: 10 tiles of 2374 slices, 3.7 ms of 0.3 ms of
-// memory traffic). k splits shorten that walk k times and cost k float32
-// partials of [Ct, H], written and read once at about 4 TB/s.
-int dh_splits(const lmh::BwdPlan& p, int64_t H) {
+// Splits of a launch's gradient tiles over their K (the block's vocabulary for
+// dh, its tokens for dW). A launch holds the dh tiles, the dW tiles and (with
+// more than one block) the next block's cotangent tiles, each of 1.05 us per 64
+// of its K and 16 us around them on a CU (a dh tile of up to twice that: where
+// few token tiles share its rows of W, it waits for memory); it takes all of
+// them over the CUs, but no less than its longest gradient tile and a half. Small blocks have few tiles: 64 tokens, H
+// 2560, V 151936 have 10 dh tiles that each walk 2374 slices alone, 2.5 ms beside
+// 0.3 ms of memory traffic; 2000 tokens of H 512 in blocks of 1792 vocabulary
+// rows, 14 dW tiles of 32 slices. A split costs its tiles' 16 us and a float32
+// partial of the block's gradient, written and read once at about 4 TB/s.
+struct Splits {
+  int dh, dW;
+};
+Splits grad_splits(const lmh::BwdPlan& p, int64_t H) {
   const double T = lmh::kTileRows;
   const double tt = (double)lmh::ceil_div(p.Ct, lmh::kTileRows), vt = (double)lmh::ceil_div(p.Vb, lmh::kTileRows);
   const double ht = (double)lmh::ceil_div(H, lmh::kTileRows);
-  const double all = (tt * ht * p.Vb + vt * ht * p.Ct + tt * vt * H) / 64.0 / lmh::kNumCUs;
-  const double chain = p.Vb / 64.0, part = tt * T * H * 8.0 / 4.0e6;   // us
-  int best = 1;
-  double best_t = std::max(all, chain);
-  for (int k = 2; k <= 64 && chain / k >= 8.0; ++k) {
-    const double t = std::max(all, chain / k) + k * part;
-    if (t < best_t) {
-      best_t = t;
-      best = k;
+  auto tile = [](double k) { return 1.05 * k / 64.0 + 16.0; };   // us
+  const double z = p.n_tb * p.n_vb > 1 ? tile((double)H) : 0.0;
+  Splits best{1, 1};
+  double best_t = 1e300;
+  for (int kd = 1; kd <= 64 && (kd == 1 || p.Vb / kd >= 512); ++kd)
+    for (int kw = 1; kw <= 16 && (kw == 1 || p.Ct / kw >= 256); ++kw) {
+      const double dh = tile((double)p.Vb / kd * (1.0 + 1.0 / tt)), dW = tile((double)p.Ct / kw);
+      const double all = (tt * ht * kd * dh + vt * ht * kw * dW + tt * vt * z) / lmh::kNumCUs;
+      const double part = ((kd > 1 || kw > 1 ? kd * tt : 0.0) + (kw > 1 ? kw * vt : 0.0)) * T * H * 8.0 / 4.0e6;
+      const double t = std::max(std::max(all, z), 1.5 * std::max(dh, dW)) + part;
+      if (t < best_t) {
+        best_t = t;
+        best = {kd, kw};
+      }
     }
-  }
   return best;
 }
 
@@ -788,14 +813,21 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
     const int64_t wgs = (n <= 32 ? 3 : 2) * lmh::kNumCUs / (d.dh_strips * lmh::ceil_div(n, 64));
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(wgs, lmh::ceil_div(V, 128)));
     d.dh_rows = (int)lmh::round_up(lmh::ceil_div(V, most), 32);
-    d.splits = (int)lmh::ceil_div(V, d.dh_rows);
-    d.bytes = d.off_part + room(d.splits * n * H * 4);
+    d.dh_splits = (int)lmh::ceil_div(V, d.dh_rows);
+    d.bytes = d.off_part + room(d.dh_splits * n * H * 4);
     return d;
   }
-  d.splits = dh_splits(p, H);
-  d.k_split = (int)lmh::round_up(lmh::ceil_div(p.Vb, d.splits), 64);
-  d.splits = (int)lmh::ceil_div(lmh::round_up(p.Vb, 64), d.k_split);
-  d.bytes = d.off_part + (d.splits > 1 ? room((int64_t)d.splits * p.Ct * H * 4) : 0);
+  d.bytes = d.off_w_part = d.off_part;
+  const Splits k = grad_splits(p, H);
+  if (k.dh > 1 || k.dW > 1) {
+    d.k_split = (int)lmh::round_up(lmh::ceil_div(p.Vb, k.dh), 64);
+    d.off_w_part = d.off_part + room(lmh::ceil_div(lmh::round_up(p.Vb, 64), d.k_split) * p.Ct * H * 4);
+    d.bytes = d.off_w_part;
+    if (k.dW > 1) {
+      d.w_k_split = (int)lmh::round_up(lmh::ceil_div(p.Ct, k.dW), 64);
+      d.bytes += room(lmh::ceil_div(lmh::round_up(p.Ct, 64), d.w_k_split) * p.Vb * H * 4);
+    }
+  }
   return d;
 }
 
@@ -902,21 +934,21 @@ hipError_t few_bwd(const DistillPlan& d, const lmh::DistillPrepArgs& prep, const
   a.add_dW = (flags & LMH_BWD_ACCUMULATE_DW) != 0;
   a.dh_part = reinterpret_cast<float*>(ws + d.off_part);
   a.dh_strips = d.dh_strips;
-  a.dh_splits = d.splits;
+  a.dh_splits = d.dh_splits;
   a.dh_rows = d.dh_rows;
   e = lmh::launch_few_bwd(a, bf16, s);
   if (e != hipSuccess) return e;
   const bool add = (flags & LMH_BWD_ACCUMULATE_DH) != 0;
   lmh::DistillPostArgs post{};
-  post.part = a.dh_part;
-  post.splits = d.splits;
-  post.g_Ct = a.N;
+  post.dh.part = a.dh_part;
+  post.dh.splits = d.dh_splits;
+  post.dh.rows = a.N;
   post.H = a.H;
   post.V = a.V;
   post.tgt = prep.tgt;
-  post.o.src_kind = !add ? lmh::kSrcNone : bf16 ? lmh::kSrcBf16 : lmh::kSrcF32;
-  post.o.src = post.o.dst = dh;
-  post.o.dst_bf16 = bf16;
+  post.dh.o.src_kind = !add ? lmh::kSrcNone : bf16 ? lmh::kSrcBf16 : lmh::kSrcF32;
+  post.dh.o.src = post.dh.o.dst = dh;
+  post.dh.o.dst_bf16 = bf16;
   post.dead_zero = !add;
   return lmh::launch_distill_post(post, s);
 }
@@ -972,9 +1004,10 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
       if (e != hipSuccess) return fail(LMH_ERR_HIP, "distill_bwd: launch failed: %s", hipGetErrorString(e));
       return ok();
     }
-    hook.splits = d.splits;
     hook.k_split = d.k_split;
+    hook.w_k_split = d.w_k_split;
     hook.part = reinterpret_cast<float*>(ws + d.off_part);
+    hook.w_part = reinterpret_cast<float*>(ws + d.off_w_part);
     hook.bytes = d.bytes;
     tgt = w_tgt;
     ga = w_ga;

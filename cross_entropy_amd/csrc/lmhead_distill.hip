@@ -365,11 +365,34 @@ __device__ __forceinline__ void dw_tile_turned(const BwdStep& s, int vid, char* 
   }
 }
 
+// dW tile of one split of the block's tokens, to its own float32 partial [Vb][H].
+__device__ __forceinline__ void dw_split_tile(const DistillStep& d, int vid, char* lds) {
+  const BwdStep& s = d.step;
+  const int split = vid / s.n_dw;
+  int mt, hb;
+  raster(vid - split * s.n_dw, s.n_dw / s.n_ht, s.n_ht, 4, mt, hb);
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1;
+  const int wn = wave >> 1;
+  const int m0 = mt * kTile;
+  const int h0 = hb * kTile;
+  const int H = s.H;
+  const int k0 = split * d.w_k_split;
+  const int K = min(d.w_k_split, (s.g_Ct + kBK - 1) / kBK * kBK - k0);   // > 0: the host counts the splits
+  const Operand oa{s.g_dz + (int64_t)k0 * s.ld_dz + m0, s.ld_dz, kTile};
+  const Operand ob{s.ht + (int64_t)h0 * s.ld_ht + s.g_t0 + k0, s.ld_ht, kTile};
+  f32x4 acc[kNB][kNB];
+  Pipe pipe;
+  mma_tile<true, 64>(oa, ob, K, lds, acc, pipe, oa.base, ob.base, false);
+  write_acc(d.w_part + (int64_t)split * s.g_Vb * H, H, m0 + wm * 128, s.g_Vb, h0 + wn * 128, H, false, nullptr, 0, 0, acc);
+}
+
 // One backward launch: the head's (each XCD an eighth of the gradient tiles,
 // the kind with the longer K first, then of the next block's cotangent tiles,
 // the last off per-XCD counters and then off the others'), with the dW writer
-// above, and with SPLIT the dh tiles split: where a few dh tiles would
-// otherwise run the whole vocabulary in sequence while the chip idles.
+// above, and with SPLIT the gradient tiles' K split: where a few tiles would
+// otherwise run a whole vocabulary, or many tokens, in sequence while the chip
+// idles.
 template <bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillStep d) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
@@ -378,11 +401,13 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillSte
   const int xcd = blockIdx.x & 7;
   const int loc = blockIdx.x >> 3;
   const int n_dh = s.n_dh * d.splits;
-  const int dw_lo = xcd * s.n_dw / 8;
-  const int dw_cnt = (xcd + 1) * s.n_dw / 8 - dw_lo;
+  const int n_dw = s.n_dw * d.w_splits;
+  const int dw_lo = xcd * n_dw / 8;
+  const int dw_cnt = (xcd + 1) * n_dw / 8 - dw_lo;
   const int dh_lo = xcd * n_dh / 8;
   const int dh_cnt = (xcd + 1) * n_dh / 8 - dh_lo;
-  const bool dh_first = SPLIT || s.g_Vb > s.g_Ct;   // dh tiles run K = Vb, dW tiles K = Ct
+  // dh tiles run K = Vb, dW tiles K = Ct, or a split of it
+  const bool dh_first = SPLIT ? d.k_split > d.w_k_split : s.g_Vb > s.g_Ct;
   const int first_cnt = dh_first ? dh_cnt : dw_cnt;
   if (loc < dh_cnt + dw_cnt) {
     if ((loc < first_cnt) == dh_first) {
@@ -391,7 +416,8 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillSte
       else dh_tile<BF16>(s, vid, lds);
     } else {
       const int vid = dw_lo + (dh_first ? loc - dh_cnt : loc);
-      if constexpr (BF16) dw_tile_turned<BF16>(s, vid, lds);
+      if (SPLIT && d.w_splits > 1) dw_split_tile(d, vid, lds);
+      else if constexpr (BF16) dw_tile_turned<BF16>(s, vid, lds);
       else dw_tile<BF16>(s, vid, lds);
     }
     return;
@@ -404,27 +430,20 @@ __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillSte
   if (tile >= 0) dz_tile(s, tile, lds);
 }
 
-// After each launch, on what it wrote: overwrites the special entries of tokens
-// [t0, t0 + Ct) and vocabulary rows [v0, v0 + Vb) in their cotangent block,
-// and adds up the splits of a block's dh in split order (n4 float4's, o as
-// the bf16-gradient backward's writers take it).
-__global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs a) {
-  const int64_t step = (int64_t)gridDim.x * 256;
-  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t n = a.dz != nullptr ? (int64_t)a.Ct * a.K1 : 0;
-  for (int64_t i = i0; i < n; i += step) {
-    const int64_t at = (int64_t)a.t0 * a.K1 + i;
-    const int id = a.ent_id[at];
-    const int v = id - a.v0;
-    if (id >= 0 && v >= 0 && v < a.Vb) a.dz[i / a.K1 * a.ld_dz + v] = round_bf16(a.ent_val[at]);
-  }
-  if (a.part == nullptr) return;
-  const int h4 = a.H / 4;
-  const int64_t n4 = (int64_t)a.g_Ct * h4;
+// Adds up the splits of a gradient's block in split order, onto what o reads
+// and to where it writes (as the bf16-gradient backward's writers take it);
+// with tgt a masked token's row is written as 0, or left as it is.
+__device__ __forceinline__ void sum_splits(const SplitSum& a, int H, const int32_t* tgt, int V, bool dead_zero, int64_t i0,
+                                           int64_t step) {
+  const int h4 = H / 4;
+  const int64_t n4 = (int64_t)a.rows * h4;
   for (int64_t i = i0; i < n4; i += step) {
-    const int t = a.tgt[a.g_t0 + i / h4];
-    const bool live = t >= 0 && t < a.V;
-    if (!live && !a.dead_zero) continue;
+    bool live = true;
+    if (tgt != nullptr) {
+      const int t = tgt[i / h4];
+      live = t >= 0 && t < V;
+      if (!live && !dead_zero) continue;
+    }
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (live) {
       const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + i;
@@ -448,6 +467,23 @@ __global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs
       static_cast<f32x4*>(a.o.dst)[i] = v;
     }
   }
+}
+
+// After each launch, on what it wrote: overwrites the special entries of tokens
+// [t0, t0 + Ct) and vocabulary rows [v0, v0 + Vb) in their cotangent block, and
+// adds up the splits of the gradients' blocks.
+__global__ __launch_bounds__(256) void distill_post_kernel(const DistillPostArgs a) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = a.dz != nullptr ? (int64_t)a.Ct * a.K1 : 0;
+  for (int64_t i = i0; i < n; i += step) {
+    const int64_t at = (int64_t)a.t0 * a.K1 + i;
+    const int id = a.ent_id[at];
+    const int v = id - a.v0;
+    if (id >= 0 && v >= 0 && v < a.Vb) a.dz[i / a.K1 * a.ld_dz + v] = round_bf16(a.ent_val[at]);
+  }
+  if (a.dh.part != nullptr) sum_splits(a.dh, a.H, a.tgt, a.V, a.dead_zero != 0, i0, step);
+  if (a.dW.part != nullptr) sum_splits(a.dW, a.H, nullptr, 0, false, i0, step);
 }
 
 }  // namespace
@@ -483,10 +519,10 @@ hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream) {
 template <bool BF16, bool SPLIT>
 static hipError_t launch_step(const DistillStep& d, hipStream_t stream) {
   const BwdStep& st = d.step;
-  const int n_z = st.z_ntt * st.z_nvt, n_dh = st.n_dh * d.splits;
+  const int n_z = st.z_ntt * st.z_nvt, n_dh = st.n_dh * d.splits, n_dw = st.n_dw * d.w_splits;
   int per = 0;
   for (int x = 0; x < 8; ++x)
-    per = std::max(per, ((x + 1) * st.n_dw / 8 - x * st.n_dw / 8) + ((x + 1) * n_dh / 8 - x * n_dh / 8) +
+    per = std::max(per, ((x + 1) * n_dw / 8 - x * n_dw / 8) + ((x + 1) * n_dh / 8 - x * n_dh / 8) +
                             ((x + 1) * n_z / 8 - x * n_z / 8) + (n_z > 0 ? kStealSlots : 0));
   if (per == 0) return hipSuccess;
   const int n_g = st.n_dw + st.n_dh;
@@ -497,7 +533,7 @@ static hipError_t launch_step(const DistillStep& d, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kDistillStep, stream, n_g ? 4.0 * gc * gv * H : 0.0,
-            (n_g ? 2.0 * gc * gv + 2.0 * (gc + gv) * H + 4.0 * H * (gc * d.splits + gv) : 0.0) +
+            (n_g ? 2.0 * gc * gv + 2.0 * (gc + gv) * H + 4.0 * H * (gc * d.splits + gv * d.w_splits) : 0.0) +
                 (n_z ? 2.0 * zc * zv + 2.0 * (zc + zv) * H + 20.0 * zc : 0.0));
   return hipSuccess;
 }
@@ -509,14 +545,14 @@ hipError_t launch_distill_step(const DistillStep& d, bool bf16, hipStream_t stre
 
 hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream) {
   const int64_t n = a.dz != nullptr ? (int64_t)a.Ct * a.K1 : 0;
-  const int64_t n4 = a.part != nullptr ? (int64_t)a.g_Ct * (a.H / 4) : 0;
-  const int64_t most = std::max(n, n4);
+  auto n4 = [&](const SplitSum& x) { return x.part != nullptr ? (int64_t)x.rows * (a.H / 4) : (int64_t)0; };
+  const int64_t most = std::max(n, std::max(n4(a.dh), n4(a.dW)));
   if (most == 0) return hipSuccess;
   trace_begin(stream);
   hipLaunchKernelGGL(distill_post_kernel, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 4096)), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  trace_end(kDistillPost, stream, 0.0, 4.0 * (double)n + 16.0 * (double)n4 * (a.splits + 1));
+  trace_end(kDistillPost, stream, 0.0, 4.0 * (double)n + 16.0 * ((double)n4(a.dh) * (a.dh.splits + 1) + (double)n4(a.dW) * (a.dW.splits + 1)));
   return hipSuccess;
 }
 

@@ -175,17 +175,27 @@ struct DistillPrepArgs {
   int tail_rows, H;
 };
 
-// A backward launch, its dh tiles split over the block's vocabulary or (part
-// NULL, splits 1) not.
+// A backward launch with its gradient tiles' K split: the dh tiles over the
+// block's vocabulary, the dW tiles (w_splits > 1) over its tokens; or (part
+// NULL, splits 1) neither.
 struct DistillStep {
   BwdStep step;
-  int splits;        // splits of the launch's dh tiles
-  int k_split;       // vocabulary rows of each (a multiple of 64)
-  float* part;       // [splits][g_Ct][H] float32
+  int splits, k_split;       // splits of the launch's dh tiles, of k_split vocabulary rows (a multiple of 64)
+  float* part;               // [splits][g_Ct][H] float32
+  int w_splits, w_k_split;   // splits of its dW tiles, of w_k_split tokens (a multiple of 64)
+  float* w_part;             // [w_splits][g_Vb][H] float32
+};
+
+// Sum of the splits of one gradient's block of `rows` rows: part [splits][rows]
+// [H] float32 (NULL: nothing to sum), to and from o.
+struct SplitSum {
+  const float* part;
+  int splits, rows;
+  GradOut o;
 };
 
 // What follows each launch: the special entries into the cotangent block that
-// it formed (dz, or NULL), and the sum of its dh splits (part, or NULL).
+// it formed (dz, or NULL), and the sums of its splits.
 struct DistillPostArgs {
   const int32_t* ent_id;
   const float* ent_val;
@@ -193,11 +203,10 @@ struct DistillPostArgs {
   uint16_t* dz;
   int64_t ld_dz;
   int t0, Ct, v0, Vb;
-  const float* part;
-  int splits, g_t0, g_Ct, H, V;
-  const int32_t* tgt;
-  GradOut o;
-  int dead_zero;     // masked tokens' rows are written as 0, else left as they are
+  SplitSum dh, dW;
+  int H, V;
+  const int32_t* tgt;   // of dh's first row on
+  int dead_zero;     // masked tokens' dh rows are written as 0, else left as they are
 };
 
 // The distillation for few tokens (lmhead_few.hip).

@@ -351,8 +351,8 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  *                lmhead_logps_bwd_bf16
  * The workspace holds the head's backward workspace (chunk_size bounds the
  * cotangent block as there), 8 N + 8 N (K + 1) bytes of the tokens' special
- * entries and, where a block's dh is summed in splits, at most 64 float32
- * partials of it. A call of few tokens (64, or 256 of at most 8192 ids) whose
+ * entries and, where a block's gradients are summed in splits, at most 64
+ * float32 partials of its dh and 16 of its dW. A call of few tokens (64, or 256 of at most 8192 ids) whose
  * whole cotangent chunk_size allows holds that instead, as two bf16 words up to 64 tokens,
  * and at most 50 MB of float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
  * LMH_WS_FWD, LMH_WS_BWD or LMH_WS_BWD_BF16. A smaller size than the query
@@ -442,8 +442,8 @@ const char* lmhead_logps_version(void);
  *   6 bwd_step_bf16_kernel (bwd_step_kernel writing bf16 gradients)
  *   7 distill_top_kernel   (distillation: student's log-probs at the teacher's ids, loss)
  *   8 distill_prep_kernel  (distillation backward: per-token cotangents and special entries)
- *   9 distill_step_kernel  (bwd_step_kernel with its dh tiles split, either gradient type)
- *  10 distill_post_kernel  (special entries into a cotangent block, sum of dh splits)
+ *   9 distill_step_kernel  (bwd_step_kernel for the distillation, its tiles' K split where they are few)
+ *  10 distill_post_kernel  (special entries into a cotangent block, sums of splits)
  *  11 few_stats_kernel     (distillation of few tokens: forward statistics)
  *  12 few_dz_kernel        (its cotangent)
  *  13 few_grads_kernel     (its gradient products)

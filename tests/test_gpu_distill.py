@@ -129,6 +129,9 @@ CASES = [
     (256, 64, 1025, 3, 128, 1.0, "bf16", False, True),
     (257, 64, 1025, 3, 512, 1.0, "bf16", False, True),
     (40, 128, 3000, 6, 31, 1.0, "f32", False, True),      # few tokens, beyond what chunk_size allows of their own
+    (3000, 128, 600, 4, 600, 1.0, "f32", False, True),    # split dW products
+    (3000, 192, 9000, 5, 200, 1.0, "bf16", True, True),   # both split, several blocks each way
+    (1100, 64, 2500, 3, 64, 2.0, "f32", False, True),
     (130, 64, 70, 100, 32, 1.0, "f32", False, True),      # more entries than the vocabulary has ids
 ]
 
@@ -349,18 +352,18 @@ def test_distill_extreme_teacher_logits():
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("V", [900, 12000])      # 12000: split dh products
-def test_distill_adds_into_gradients(t, V):
+@pytest.mark.parametrize("N,V", [(330, 900), (330, 12000), (2000, 700)])   # split dh products; split dW products
+def test_distill_adds_into_gradients(t, N, V):
     import torch
     import cross_entropy_amd as lm
-    args = _case(12, 330, 128, V, 7, hard=True)
+    args = _case(12, N, 128, V, 7, hard=True)
     hd, Wd, tg, idd, td, tl = _put(*args)
     ty = torch.float32 if t == "f32" else torch.bfloat16
-    g_kl, g_logp = _g(3, 330, True)
+    g_kl, g_logp = _g(3, N, True)
     kl, logp, lse, top = lm.distill_forward(hd, Wd, tg, idd, td, 64, tl)
     given = (hd, Wd, tg, idd, td, 64, logp, lse, top, dev(g_kl), dev(g_logp), tl)
     dh0, dW0 = lm.distill_backward(*given)
-    ph, pW = torch.randn(330, 128, device="cuda").to(ty), torch.randn(V, 128, device="cuda").to(ty)
+    ph, pW = torch.randn(N, 128, device="cuda").to(ty), torch.randn(V, 128, device="cuda").to(ty)
     dh, dW = ph.clone(), pW.clone()
     lm.distill_backward(*given, dh=dh, dW=dW, accumulate=True)
     torch.cuda.synchronize()
