@@ -41,9 +41,11 @@ def log(msg: str) -> None:
 
 def kernel_source_hash() -> str:
     import hashlib
-    path = os.path.join(ROOT, "cross_entropy_amd", "csrc", "lmhead_kernels.hip")
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    h = hashlib.sha256()
+    for name in ("lmhead_kernels.hip", "lmhead_tile.h"):
+        with open(os.path.join(ROOT, "cross_entropy_amd", "csrc", name), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
 
 
 def stored_counters():
