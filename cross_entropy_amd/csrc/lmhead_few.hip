@@ -385,7 +385,7 @@ __device__ __forceinline__ void few_dw(const FewArgs& a, int vid, char* lds) {
 #pragma unroll
     for (int c = 0; c < h_each; ++c)
       *reinterpret_cast<u32x4*>(turn + (64 * c + lane) / h_per * h_pitch + 16 * (lane % h_per)) = x[c];
-    __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+    wave_order();
     // a transposed read hands lane j the columns that lane j / 4 points at, element j % 4
 #pragma unroll
     for (int b = 0; b < BL; ++b) {
@@ -395,7 +395,7 @@ __device__ __forceinline__ void few_dw(const FewArgs& a, int vid, char* lds) {
       v.s4567 = ds_read_tr(p + 4 * h_pitch);
       ht[b][k] = __builtin_bit_cast(bf16x8, v);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
   }
   const int groups = (V + 15) / 16;
   const int g_lo = (int)((int64_t)split * groups / a.dw_splits), g_hi = (int)((int64_t)(split + 1) * groups / a.dw_splits);
@@ -454,7 +454,7 @@ __device__ __forceinline__ void few_dw(const FewArgs& a, int vid, char* lds) {
         reinterpret_cast<f32x4*>(p)[1] = y;
       }
     }
-    __builtin_amdgcn_wave_barrier();   // one wave's LDS operations run in order
+    wave_order();
 #pragma unroll
     for (int i = 0; i < stores; ++i) {
       const int r = (64 * i + lane) / per_row, piece = lane % per_row;
@@ -462,7 +462,7 @@ __device__ __forceinline__ void few_dw(const FewArgs& a, int vid, char* lds) {
       if (checked && (16 * g + r >= V || h0 + 16 / bytes * piece >= H)) continue;
       *reinterpret_cast<u32x4*>(static_cast<char*>(a.dW) + ((int64_t)(16 * g + r) * H + h0) * bytes + 16 * piece) = v;
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
   };
   load(g_lo);
   const int whole = h0 + cols <= H ? min(g_hi, V / 16) : g_lo;   // groups whose every store lies inside

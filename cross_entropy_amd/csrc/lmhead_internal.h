@@ -1,5 +1,6 @@
 // lmhead_internal.h -- launch descriptors shared by the C ABI (lmhead_api.hip)
-// and the kernels (lmhead_kernels.hip, lmhead_distill.hip, lmhead_norm.hip).
+// and the kernels (lmhead_kernels.hip, lmhead_distill.hip, lmhead_few.hip,
+// lmhead_norm.hip).
 // Not part of the public interface.
 #pragma once
 

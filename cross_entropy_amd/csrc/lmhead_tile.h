@@ -74,6 +74,14 @@ __device__ __forceinline__ void raster(int vid, int n_m, int n_n, int group, int
 // on the scalar unit.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// Orders a wave's LDS accesses across its lanes: what one lane wrote before is
+// what another reads after. The hardware runs a wave's LDS operations in order, so
+// only the compiler is held.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Pin a 4-register accumulator block in AGPRs up to this point: the
 // epilogue's reads of it then become copies right here, instead of one bulk
 // copy of all 256 accumulators into VGPRs at the end of the loop.
