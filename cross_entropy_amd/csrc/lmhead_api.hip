@@ -721,15 +721,22 @@ struct DistillPlan {
 
 // When the kernels for few tokens (lmhead_few.hip) run: they fetch W once per
 // 64 tokens, where the 256 x 256 tiles fetch it once per 256 but spend a whole
-// tile's time on what little there is. Up to 64 tokens always, up to 256 for a
-// small vocabulary. Measured (us, few / tiles), forward: H 2560, V 151936: 64
-// tokens 170 / 234, 128 tokens 251 / 227; 256 tokens, H 2560: V 8000 41 / 65, V
-// 32000 118 / 68. Backward: 64 tokens, H 2560, V 151936 632 / 809; 128 tokens
-// 839 / 813, and 46 / 69 at H 512, V 8000; 256 tokens: 44 / 64 at H 256, V 4096,
-// 107 / 120 at H 2560, V 8000, 240 / 194 at H 4096, V 16000.
-constexpr int64_t kFewVocabulary = 8192;
+// tile's time on what little there is. One tile of 64 tokens always; more, up
+// to 256 tokens, where the vocabulary is small enough for the product of the
+// two. Measured (us, few / tiles):
+//   tokens  H     V       forward   backward
+//   64      2560  151936  160/220   645/711
+//   128     2560  151936  248/221   771/736
+//   128     2560  32000   63/63     183/181
+//   128     4096  16000   54/87     124/177
+//   192     512   30000   30/28     83/76
+//   192     2560  16000   50/62     136/138
+//   256     2560  16000   62/62     159/142
+//   256     2560  8000    38/62     95/123
+//   256     512   8000    16/26     50/73
+constexpr int64_t kFewRows = 49152;   // 64-token tiles times vocabulary
 bool few_tokens(int64_t N, int64_t V) {
-  return N <= 64 ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && V <= kFewVocabulary;
+  return N <= 64 ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && lmh::ceil_div(N, 64) * V <= kFewRows;
 }
 // The backward holds the tokens' whole cotangent, as two bf16 words up to 64
 // tokens and one above, which chunk_size has to allow.

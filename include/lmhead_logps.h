@@ -352,9 +352,9 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  * The workspace holds the head's backward workspace (chunk_size bounds the
  * cotangent block as there), 8 N + 8 N (K + 1) bytes of the tokens' special
  * entries and, where a block's gradients are summed in splits, at most 64
- * float32 partials of its dh and 16 of its dW. A call of few tokens (64, or 256 of at most 8192 ids) whose
- * whole cotangent chunk_size allows holds that instead, as two bf16 words up to 64 tokens,
- * and at most 50 MB of float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
+ * float32 partials of its dh and 16 of its dW. A call of few tokens (64; 128 of at most 24576 ids, 192 of
+ * 16384, 256 of 12288) whose whole cotangent chunk_size allows holds that instead, as two bf16 words up to
+ * 64 tokens, and at most 50 MB of float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
  * LMH_WS_FWD, LMH_WS_BWD or LMH_WS_BWD_BF16. A smaller size than the query
  * gives is refused. Results do not depend on anything but the arguments:
  * no atomics take part in sums.

@@ -102,7 +102,7 @@ def test_distill_workspace():
     assert q(40, 64, 1000, 5, (1 << 63) - 1, 2) == q(40, 64, 1000, 5, 1 << 40, 2)
     # every size on the way between the kernels' limits
     for N in (0, 1, 16, 17, 32, 33, 64, 65, 128, 129, 192, 193, 256, 257, 5000):
-        for V in (1, 63, 8191, 8192, 8193, 151936, (1 << 23) - 256):
+        for V in (1, 63, 8192, 12288, 12289, 16384, 16385, 24576, 24577, 151936, (1 << 23) - 256):
             for chunk in (1, 31, 32, 64, 4096):
                 sizes = [q(N, 64, V, 3, chunk, kind) for kind in (0, 1, 2)]
                 assert 0 < sizes[0] <= sizes[1] <= sizes[2]

@@ -128,6 +128,13 @@ CASES = [
     (200, 512, 8000, 32, 128, 1.0, "f32", True, True),
     (256, 64, 1025, 3, 128, 1.0, "bf16", False, True),
     (257, 64, 1025, 3, 512, 1.0, "bf16", False, True),
+    (128, 128, 24576, 6, 64, 1.0, "bf16", True, True),    # more tokens of a smaller vocabulary, at its limit and past it
+    (128, 128, 24577, 6, 64, 1.0, "f32", False, True),
+    (100, 576, 20000, 9, 64, 0.7, "f32", True, True),
+    (192, 64, 16384, 6, 96, 1.0, "f32", False, True),
+    (150, 320, 16385, 6, 512, 1.0, "bf16", True, False),
+    (256, 192, 12288, 6, 128, 1.0, "f32", True, True),
+    (250, 64, 12289, 6, 128, 2.0, "bf16", False, True),
     (40, 128, 3000, 6, 31, 1.0, "f32", False, True),      # few tokens, beyond what chunk_size allows of their own
     (3000, 128, 600, 4, 600, 1.0, "f32", False, True),    # split dW products
     (3000, 192, 9000, 5, 200, 1.0, "bf16", True, True),   # both split, several blocks each way
