@@ -738,11 +738,21 @@ constexpr int64_t kFewRows = 49152;   // 64-token tiles times vocabulary
 bool few_tokens(int64_t N, int64_t V) {
   return N <= 64 ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && lmh::ceil_div(N, 64) * V <= kFewRows;
 }
+// The chunk that the backward's blocks are sized by: chunk_size, but blocks hold
+// at least two 256 x 256 cotangent tiles per CU (2^25 entries, 134 MB in both
+// buffers, 0.05% of the card's memory). Below that a launch has less than a
+// round of tiles, and the blocks' launches run one after the other. Measured (us
+// at blocks of 8 / 32 / 64 / 128 / 256 MB): 2000 x 512 x 8000 423 / 188 / 147 /
+// 132 / 131; 1357 x 1024 x 50257 1824 / 790 / 559 / 448 / 437; 16000 x 256 x 12000
+// 4312 / 1279 / 880 / 549 / 476; 300 x 2048 x 100000 1804 / 756 / 615 / 611 / 621.
+constexpr int64_t kLeastBlock = 2 * (int64_t)lmh::kNumCUs * lmh::kTileRows * lmh::kTileRows;
+int64_t block_chunk(int64_t V, int64_t chunk_size) { return std::max(chunk_size, lmh::ceil_div(kLeastBlock, V)); }
+
 // The backward holds the tokens' whole cotangent, as two bf16 words up to 64
-// tokens and one above, which chunk_size has to allow.
+// tokens and one above, which the block's size has to allow.
 int64_t few_padded(int64_t N) { return N <= 32 ? 32 : lmh::round_up(N, 64); }
 bool few_backward(int64_t N, int64_t V, int64_t chunk_size) {
-  return few_tokens(N, V) && few_padded(N) / (N <= 64 ? 1 : 2) <= chunk_size;
+  return few_tokens(N, V) && few_padded(N) / (N <= 64 ? 1 : 2) <= block_chunk(V, chunk_size);
 }
 
 // Splits of a launch's gradient tiles over their K (the block's vocabulary for
@@ -750,10 +760,10 @@ bool few_backward(int64_t N, int64_t V, int64_t chunk_size) {
 // more than one block) the next block's cotangent tiles, each of 1.05 us per 64
 // of its K and 16 us around them on a CU (a dh tile of up to twice that: where
 // few token tiles share its rows of W, it waits for memory); it takes all of
-// them over the CUs, but no less than its longest gradient tile and a half. Small blocks have few tiles: 64 tokens, H
-// 2560, V 151936 have 10 dh tiles that each walk 2374 slices alone, 2.5 ms beside
-// 0.3 ms of memory traffic; 2000 tokens of H 512 in blocks of 1792 vocabulary
-// rows, 14 dW tiles of 32 slices. A split costs its tiles' 16 us and a float32
+// them over the CUs, but no less than its longest gradient tile and a half. Small
+// blocks have few tiles: 512 tokens, H 2560, V 151936 have 20 dh tiles that each
+// walk 2374 slices, 2.5 ms alone (split, the whole call takes 1.26); 2000 tokens,
+// H 512, V 8000 64 dW tiles of 32 slices. A split costs its tiles' 16 us and a float32
 // partial of the block's gradient, written and read once at about 4 TB/s.
 struct Splits {
   int dh, dW;
@@ -804,7 +814,7 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
   d.few = few_backward(n, V, chunk_size);
   lmh::BwdPlan p;
   if (!d.few) {
-    p = lmh::plan_backward(N, H, V, chunk_size);
+    p = lmh::plan_backward(N, H, V, block_chunk(V, chunk_size));
     d.off_tgt = kind == LMH_WS_BWD_BF16 ? p.bytes_bf16 : p.bytes;
   }
   d.off_ga = d.off_tgt + room(n * 4);
@@ -1019,7 +1029,7 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
     tgt = w_tgt;
     ga = w_ga;
   }
-  return bwd_impl("distill_bwd", hidden, W, tgt, N, H, V, 0, V, chunk_size, temperature, lse, nullptr, ga, nullptr,
+  return bwd_impl("distill_bwd", hidden, W, tgt, N, H, V, 0, V, block_chunk(V, chunk_size), temperature, lse, nullptr, ga, nullptr,
                   dh, dW, flags, bf16, workspace, workspace_bytes, stream, N > 0 ? &hook : nullptr);
 }
 

@@ -115,9 +115,9 @@ CASES = [
     (256, 256, 4096, 8, 128, 1.0, "f32", False, True),
     (300, 128, 1000, 16, 64, 2.0, "f32", True, True),
     (513, 256, 4097, 33, 4096, 1.0, "bf16", True, True),
-    (700, 320, 3001, 64, 7, 1.0, "f32", True, False),     # several blocks, vocabulary outer for bf16
+    (700, 320, 3001, 64, 7, 1.0, "f32", True, False),     # a chunk_size below every block
     (2100, 128, 777, 17, 64, 1.0, "bf16", False, True),   # N > V: token blocks outer
-    (70, 128, 20011, 12, 30, 1.0, "f32", True, True),     # split dh products, several vocabulary blocks, a ragged last
+    (70, 128, 20011, 12, 30, 1.0, "f32", True, True),     # split dh products, a ragged last
     (300, 192, 9000, 5, 4096, 2.0, "bf16", False, True),  # split over two token tiles in one block
     (1, 64, 40000, 1, 1, 1.0, "f32", False, True),
     (33, 320, 2000, 7, 64, 1.0, "bf16", False, True),     # few tokens at each count of their tiles
@@ -135,9 +135,9 @@ CASES = [
     (150, 320, 16385, 6, 512, 1.0, "bf16", True, False),
     (256, 192, 12288, 6, 128, 1.0, "f32", True, True),
     (250, 64, 12289, 6, 128, 2.0, "bf16", False, True),
-    (40, 128, 3000, 6, 31, 1.0, "f32", False, True),      # few tokens, beyond what chunk_size allows of their own
+    (40, 128, 3000, 6, 31, 1.0, "f32", False, True),      # a chunk_size below the tokens
     (3000, 128, 600, 4, 600, 1.0, "f32", False, True),    # split dW products
-    (3000, 192, 9000, 5, 200, 1.0, "bf16", True, True),   # both split, several blocks each way
+    (3000, 192, 9000, 5, 200, 1.0, "bf16", True, True),   # both split
     (1100, 64, 2500, 3, 64, 2.0, "f32", False, True),
     (130, 64, 70, 100, 32, 1.0, "f32", False, True),      # more entries than the vocabulary has ids
 ]
@@ -146,6 +146,20 @@ CASES = [
 @pytest.mark.parametrize("N,H,V,K,C,T,t_type,tail,hard", CASES)
 def test_distill(N, H, V, K, C, T, t_type, tail, hard):
     what = f"N={N} H={H} V={V} K={K} C={C} T={T} {t_type} tail={tail} hard={hard}"
+    log(f"[distill] {what}")
+    _check(_case(N + V + K, N, H, V, K, T, t_type, tail, hard), T, C, t_type, what=what)
+
+
+@pytest.mark.parametrize("N,H,V,K,C,T,t_type,tail,hard", [
+    (500, 64, 140001, 5, 7, 1.0, "f32", True, True),       # three vocabulary blocks, split dh products, a ragged last
+    (2500, 64, 15001, 4, 64, 2.0, "bf16", False, True),    # two, dW products split too
+    (15000, 64, 2500, 3, 64, 1.0, "f32", False, False),    # N > V: two token blocks, both split
+    (12000, 64, 8001, 2, 1000, 1.0, "f32", True, True),    # two blocks each way
+    (4000, 1536, 9000, 6, 64, 1.0, "bf16", True, True),    # two vocabulary blocks, nothing split
+    (9000, 1536, 4000, 6, 64, 1.0, "f32", False, True),    # two token blocks, nothing split
+])
+def test_distill_several_blocks(N, H, V, K, C, T, t_type, tail, hard):
+    what = f"blocks N={N} H={H} V={V} K={K} C={C} T={T} {t_type} tail={tail} hard={hard}"
     log(f"[distill] {what}")
     _check(_case(N + V + K, N, H, V, K, T, t_type, tail, hard), T, C, t_type, what=what)
 
@@ -359,7 +373,7 @@ def test_distill_extreme_teacher_logits():
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("N,V", [(330, 900), (330, 12000), (2000, 700)])   # split dh products; split dW products
+@pytest.mark.parametrize("N,V", [(330, 900), (330, 12000), (2000, 700), (500, 70001), (15000, 2500)])   # split dh, dW products; two blocks
 def test_distill_adds_into_gradients(t, N, V):
     import torch
     import cross_entropy_amd as lm
