@@ -1121,14 +1121,16 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
   const size_t need = sums ? norm_part_bytes(N, H) : 0;
   if (workspace_bytes < need)
     return fail(LMH_ERR_WORKSPACE, "norm_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, need);
-  float* part = sums ? static_cast<float*>(workspace) : nullptr;
+  const bool columns = sums && lmh::norm_by_columns(N);
+  const bool partial = sums && !columns;
   lmh::NormReduceArgs red = empty;
-  red.part = part;
+  red.part = partial ? static_cast<float*>(workspace) : nullptr;
   red.blocks = lmh::norm_bwd_blocks(N, H);
   hipError_t e = lmh::launch_norm_bwd({x, weight, mean, rstd, dy, x_type == LMH_TYPE_F32, y_type == LMH_TYPE_F32,
-                                       w_type == LMH_TYPE_F32, kind == LMH_NORM_RMS, N, (int)H, dx, part},
-                                      red.blocks, s);
-  if (e == hipSuccess && sums) e = lmh::launch_norm_reduce(red, s);
+                                       w_type == LMH_TYPE_F32, kind == LMH_NORM_RMS, N, (int)H, dx, red.blocks,
+                                       const_cast<float*>(red.part), columns ? dweight : nullptr,
+                                       columns ? dbias : nullptr, red.g_f32, accumulate}, s);
+  if (e == hipSuccess && partial) e = lmh::launch_norm_reduce(red, s);
   if (e != hipSuccess) return fail(LMH_ERR_HIP, "norm_bwd: launch failed: %s", hipGetErrorString(e));
   return ok();
 }

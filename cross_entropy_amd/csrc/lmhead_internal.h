@@ -267,7 +267,11 @@ struct NormBwdArgs {
   int64_t N;
   int H;
   void* dx;
-  float* part;        // [blocks][2][H] partial sums of dw and db, or NULL: neither is wanted
+  int row_blocks;     // workgroups that walk rows (norm_bwd_blocks)
+  float* part;        // [row_blocks][2][H] partial sums of dw and db, or NULL: not wanted, or
+  void* dw;           // these are summed in this launch (norm_by_columns), where not NULL
+  void* db;
+  bool g_f32, accumulate;
 };
 
 struct NormReduceArgs {
@@ -279,6 +283,7 @@ struct NormReduceArgs {
 };
 
 int norm_bwd_blocks(int64_t N, int64_t H);   // workgroups (partial rows) of the norm's backward
+bool norm_by_columns(int64_t N);             // whether dw and db are summed in its launch
 
 // Kernel ids of the tracing facility (lmhead_trace.hip).
 enum KernelId {
@@ -307,7 +312,7 @@ hipError_t launch_distill_prep(const DistillPrepArgs& a, hipStream_t stream);
 hipError_t launch_distill_step(const DistillStep& d, bool bf16, hipStream_t stream);
 hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream);
-hipError_t launch_norm_bwd(const NormBwdArgs& a, int blocks, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t stream);
 
 }  // namespace lmh

@@ -239,16 +239,97 @@ __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_fwd_kernel(c
   }
 }
 
+// dw or db of one column, as norm_reduce_kernel and the columns' workgroups store it.
+__device__ __forceinline__ void store_sum(void* out, bool f32, bool accumulate, int c, float u) {
+  if (out == nullptr) return;
+  if (f32) {
+    float* o = static_cast<float*>(out) + c;
+    *o = accumulate ? *o + u : u;
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(out) + c;
+    *o = narrow(accumulate ? widen(*o) + u : u);
+  }
+}
+
+// dw and db of 32 columns over all rows, read from x and dy themselves: 8 lanes
+// of 4 columns a row, each thread the rows blockDim / 8 apart, then the lanes of
+// a column by halves and the waves in order.
+constexpr int kSumCols = 32;
+template <bool XF32, bool YF32>
+__device__ __forceinline__ void norm_columns(const NormBwdArgs& a, int block, float* lds) {
+  const int lane = threadIdx.x & 63;
+  const int H = a.H;
+  const int c = block * kSumCols + 4 * (lane & 7);
+  float dw[4] = {0.0f, 0.0f, 0.0f, 0.0f}, db[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t step = blockDim.x / 8;
+  const char* px = static_cast<const char*>(a.x) + (int64_t)c * (XF32 ? 4 : 2);
+  const char* pg = static_cast<const char*>(a.dy) + (int64_t)c * (YF32 ? 4 : 2);
+  const int64_t bx = (int64_t)H * (XF32 ? 4 : 2), bg = (int64_t)H * (YF32 ? 4 : 2);
+  if (c + 3 < H) {
+#pragma unroll 4
+    for (int64_t row = threadIdx.x / 8; row < a.N; row += step) {
+      Group<XF32, 4> x;
+      Group<YF32, 4> g;
+      x.raw = *reinterpret_cast<const decltype(x.raw)*>(px + row * bx);
+      g.raw = *reinterpret_cast<const decltype(g.raw)*>(pg + row * bg);
+      const float mu = a.rms ? 0.0f : a.mean[row], r = a.rstd[row];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dw[k] += mul0(g.at(k), (x.at(k) - mu) * r);
+        db[k] += g.at(k);
+      }
+    }
+  } else {
+    for (int64_t row = threadIdx.x / 8; row < a.N; row += step) {
+      const float mu = a.rms ? 0.0f : a.mean[row], r = a.rstd[row];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (c + k >= H) continue;
+        const float x = XF32 ? reinterpret_cast<const float*>(px + row * bx)[k]
+                             : widen(reinterpret_cast<const uint16_t*>(px + row * bx)[k]);
+        const float g = YF32 ? reinterpret_cast<const float*>(pg + row * bg)[k]
+                             : widen(reinterpret_cast<const uint16_t*>(pg + row * bg)[k]);
+        dw[k] += mul0(g, (x - mu) * r);
+        db[k] += g;
+      }
+    }
+  }
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int x = 8; x <= 32; x <<= 1) {
+      dw[k] += __shfl_xor(dw[k], x);
+      db[k] += __shfl_xor(db[k], x);
+    }
+    if (lane < 8) {
+      lds[wave * 2 * kSumCols + 4 * lane + k] = dw[k];
+      lds[wave * 2 * kSumCols + kSumCols + 4 * lane + k] = db[k];
+    }
+  }
+  __syncthreads();
+  const int col = block * kSumCols + threadIdx.x % kSumCols;
+  if (threadIdx.x >= 2 * kSumCols || col >= H) return;
+  float u = lds[threadIdx.x];
+  for (int i = 1; i < waves; ++i) u += lds[i * 2 * kSumCols + threadIdx.x];
+  store_sum(threadIdx.x < kSumCols ? a.dw : a.db, a.g_f32, a.accumulate, col, u);
+}
+
 // Backward: rows are walked likewise and each thread keeps its columns' sums
 // of dw and db in registers; at the end the rows of a block are added through
 // LDS in order and the block writes one partial row of each ([blocks][2][H]),
-// which norm_reduce_kernel sums in block order. A zero in dy contributes a
+// which norm_reduce_kernel sums in block order; with few rows, workgroups past
+// the rows' own sum the columns instead, and there are no partial rows. A zero in dy contributes a
 // zero whatever x, the statistics and w hold there (mul0), so a masked token,
 // whose dy row is 0, adds nothing and gets dx = 0 even where its x is NaN.
 template <bool XF32, bool YF32, bool WF32, int NV, int LANES>
 __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int G = XF32 ? 4 : 8, NG = 8 * NV / G;
-  extern __shared__ float lds[];   // [2][H]: the block's dw and db (LANES > 0)
+  extern __shared__ float lds[];   // [2][H]: the block's dw and db (LANES > 0); a columns' workgroup: [waves][2][32]
+  if ((int)blockIdx.x >= a.row_blocks) {
+    norm_columns<XF32, YF32>(a, (int)blockIdx.x - a.row_blocks, lds);
+    return;
+  }
   // 1024 threads have 128 registers each, which the sums would overflow: there
   // they live in LDS, each thread's at its own columns
   constexpr bool kept = LANES == kHuge;
@@ -259,7 +340,7 @@ __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(c
   const int t = WIDE ? threadIdx.x : threadIdx.x % (WIDE ? 1 : LANES);
   const int per = WIDE ? 1 : blockDim.x / threads;
   const int slot = WIDE ? 0 : threadIdx.x / threads;
-  const int64_t step = (int64_t)gridDim.x * per;
+  const int64_t step = (int64_t)a.row_blocks * per;
   const int H = a.H;
   const float inv = 1.0f / (float)H;
   int turn = 0;
@@ -422,16 +503,7 @@ __global__ __launch_bounds__(kRedThreads) void norm_reduce_kernel(const NormRedu
   float u = s2[0][col];
 #pragma unroll
   for (int i = 1; i < kRedGroups / 8; ++i) u += s2[i][col];
-  void* out = at < a.H ? a.dw : a.db;
-  const int c = at < a.H ? at : at - a.H;
-  if (out == nullptr) return;
-  if (a.g_f32) {
-    float* o = static_cast<float*>(out) + c;
-    *o = a.accumulate ? *o + u : u;
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(out) + c;
-    *o = narrow(a.accumulate ? widen(*o) + u : u);
-  }
+  store_sum(at < a.H ? a.dw : a.db, a.g_f32, a.accumulate, at < a.H ? at : at - a.H, u);
 }
 
 // How rows of H are laid over threads. Up to 1024 elements 16 to 64 lanes of a
@@ -507,9 +579,20 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
   return hipSuccess;
 }
 
-hipError_t launch_norm_bwd(const NormBwdArgs& a, int blocks, hipStream_t stream) {
+// Whether the columns' workgroups read x and dy again (one launch) instead of
+// the rows' leaving partial sums (two). Measured in a graph (us, columns /
+// partial sums, bf16): 64 rows of 256 2.9 / 7.3, of 2560 3.1 / 6.0; 256 rows of 1024
+// 4.3 / 10.0, of 8192 8.9 / 13.6; 512 rows of 2560 8.3 / 9.6, of 16384 25.0 / 25.4;
+// 1024 rows of 256 9.8 / 7.6, of 2560 14.5 / 11.6. A call that enqueues them
+// one by one saves 3 us of the second launch besides.
+constexpr int64_t kColumnRows = 512;
+bool norm_by_columns(int64_t N) { return N <= kColumnRows; }
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   const Shape p = shape_of(a.H, true);
-  const size_t lds = p.lanes <= 0 ? 0 : (size_t)2 * a.H * 4;
+  const bool columns = a.dw != nullptr || a.db != nullptr;
+  const int blocks = a.row_blocks + (columns ? (a.H + kSumCols - 1) / kSumCols : 0);
+  const size_t lds = columns ? (size_t)p.block * kSumCols / 8 : p.lanes <= 0 ? 0 : (size_t)2 * a.H * 4;
   trace_begin(stream);
   with_types(a.x_f32, a.y_f32, a.w_f32, [&](auto x, auto y, auto w) {
     with_shape(p, [&](auto nv, auto lanes) {

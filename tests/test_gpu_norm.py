@@ -61,10 +61,10 @@ def _check(x, w, b, dy, kind, eps=1e-6, y_t="bf16", g_t=None, what=""):
 
 @pytest.mark.parametrize("H", [1, 2, 7, 8, 9, 63, 64, 65, 320, 511, 512, 513, 1001, 1536, 2048, 2559, 2560, 2561, 4096,
                                5000, 6143, 8192, 8200, 12289, 16383, 16384])
-@pytest.mark.parametrize("N", [1, 3, 70])
+@pytest.mark.parametrize("N", [1, 3, 70, 513])
 def test_norm_sizes(N, H):
     """Every row shape of the kernels and its edges, both kinds, in turn with
-    the types."""
+    the types; the weight's gradient by columns and (513 rows) by partial sums."""
     k = H + N
     x_t, y_t = (("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32"))[k % 3]
     w_t = ("bf16", "f32")[k // 3 % 2]
@@ -84,9 +84,9 @@ def test_norm_types(x_t, y_t, w_t, g_t):
         _check(x, w, b, dy, kind, y_t=y_t, g_t=g_t, what=f"{kind} {x_t} {y_t} {w_t}")
 
 
-@pytest.mark.parametrize("N,H", [(4096, 256), (17000, 128), (5003, 2564)])
+@pytest.mark.parametrize("N,H", [(512, 33), (512, 2560), (4096, 256), (17000, 128), (5003, 2564)])
 def test_norm_many_rows(N, H):
-    """More rows than workgroups: every thread walks several."""
+    """Threads that walk several rows."""
     log(f"[norm] N={N} H={H}")
     x, w, b, dy = _data(N, N, H, "bf16", "bf16", "bf16")
     _check(x, w, b, dy, "layer", g_t="f32", what=f"N={N} H={H}")
@@ -111,8 +111,8 @@ def test_norm_masked_rows_do_not_spread():
     other rows' outputs do not see them."""
     import torch
     import cross_entropy_amd as lm
-    for H in (200, 4096):
-        x, w, b, dy = _data(7, 90, H, "f32", "f32", "f32")
+    for N, H in ((90, 200), (90, 4096), (600, 200), (600, 4096)):
+        x, w, b, dy = _data(7, N, H, "f32", "f32", "f32")
         bad = torch.tensor([0, 31, 32, 89], device="cuda")
         dy[bad] = 0.0
         y, mean, rstd = lm.norm_forward(x, w, b)
@@ -125,7 +125,7 @@ def test_norm_masked_rows_do_not_spread():
         y2, mean2, rstd2 = lm.norm_forward(x2, w, b)
         got = lm.norm_backward(x2, w, mean2, rstd2, dy, with_bias=True)
         torch.cuda.synchronize()
-        keep = torch.ones(90, dtype=torch.bool, device="cuda")
+        keep = torch.ones(N, dtype=torch.bool, device="cuda")
         keep[bad] = False
         assert torch.equal(y[keep], y2[keep])
         assert not torch.isfinite(y2[bad]).all(1).any()
@@ -172,10 +172,11 @@ def test_norm_beyond_32_bit_offsets():
             assert torch.equal(a, b)
 
 
-def test_norm_adds_into_gradients():
+@pytest.mark.parametrize("N", [501, 700])
+def test_norm_adds_into_gradients(N):
     import torch
     import cross_entropy_amd as lm
-    x, w, b, dy = _data(11, 501, 384, "bf16", "bf16", "bf16")
+    x, w, b, dy = _data(11, N, 384, "bf16", "bf16", "bf16")
     y, mean, rstd = lm.norm_forward(x, w, b)
     dx, dw, db = lm.norm_backward(x, w, mean, rstd, dy, with_bias=True, grad_dtype=torch.float32)
     for t in (torch.float32, torch.bfloat16):
