@@ -395,8 +395,8 @@ __device__ __forceinline__ void dw_split_tile(const DistillStep& d, int vid, cha
 // the last off per-XCD counters and then off the others'), with the dW writer
 // above, and with SPLIT the gradient tiles' K split: where a few tiles would
 // otherwise run a whole vocabulary, or many tokens, in sequence while the chip
-// idles. Bound by the matrix units: 4096 tokens, H 2560, V 151936 run at 1,390
-// TFLOP/s in the middle launches (764 us each), 1,365 over the whole call.
+// idles. Bound by the matrix units: 4096 tokens, H 2560, V 151936 run at 1,360
+// to 1,390 TFLOP/s in the middle launches (764 to 782 us each).
 template <bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void distill_step_kernel(const DistillStep d) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
