@@ -558,13 +558,14 @@ def test_head_front_end_with_norm():
     assert w.grad is None and torch.isfinite(frozen.grad).all()
 
 
-def test_captured_step_replays():
+@pytest.mark.parametrize("N,V", [(180, 900), (700, 9000), (600, 70001)])   # few tokens; split; two blocks
+def test_captured_step_replays(N, V):
     """Norm, distillation and both backward passes in one captured graph, on
     its own workspaces: every replay gives the eager bits, with eager work
     between the replays and new values in the same buffers."""
     import torch
     import cross_entropy_amd as lm
-    N, H, V, K = 180, 128, 900, 9
+    H, K = 128, 9
     h, W, targets, ids, t, _ = _case(18, N, H, V, K, hard=True)
     x = dev(bf16_bits_to_f32(h))
     w = dev(np.linspace(0.5, 1.5, H).astype(np.float32))
@@ -609,14 +610,15 @@ def test_captured_step_replays():
         assert all(torch.equal(a, b) for a, b in zip(got, outs)), i
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("N,rows", [(40, 500), (300, 900)])
+def test_two_streams_at_once(N, rows):
     """Calls on two streams with workspaces of their own, started together,
     give the lone calls' bits."""
     import torch
     import cross_entropy_amd as lm
-    puts = [_put(*_case(20 + i, 300, 128, 1300, 8, hard=True)) for i in range(2)]
-    gk, gl = (dev(a) for a in _g(8, 300, True))
-    xs = [torch.randn(500, 640, device="cuda") for _ in range(2)]
+    puts = [_put(*_case(20 + i, N, 128, 1300, 8, hard=True)) for i in range(2)]
+    gk, gl = (dev(a) for a in _g(8, N, True))
+    xs = [torch.randn(rows, 640, device="cuda") for _ in range(2)]
 
     def run(i):
         hd, Wd, tg, idd, td, tl = puts[i]
