@@ -820,7 +820,11 @@ def lmhead_distill(hidden, W, ids, teacher, chunk_size: int, targets=None, teach
     and ``teacher`` (bfloat16 or float32) are [N, K]; ids outside [0, V) are
     missing entries. Gradients flow to hidden and W (and, with ``norm`` as for
     ``lmhead_logps``, to the norm's weight and bias); the teacher gets none.
-    Multiply kl by temperature squared for gradients of temperature 1's size."""
+    Multiply kl by temperature squared for gradients of temperature 1's size.
+    ``chunk_size`` bounds the backward's cotangent block as for the head, but
+    blocks of up to 2^25 entries (134 MB) are always taken. A backward pass may
+    be captured into a graph where no eager graph of the same leaves is alive
+    (torch ends the process otherwise, whatever the function)."""
     global _DISTILL_FN
     if _DISTILL_FN is None:
         _DISTILL_FN = _distill_function()
