@@ -675,6 +675,33 @@ def norm_backward(x, weight, mean, rstd, dy, kind: str = "layer", with_weight: b
     return dx, dweight, dbias
 
 
+_ONCE_FN = None
+
+
+def _once(*grads):
+    """What a front end's backward returns: the library's gradients carry no
+    graph, so where one is being recorded (create_graph) they are joined to a
+    node that refuses a second backward. As constants they would leave a loss
+    on them (a gradient penalty) without its gradient, and say nothing."""
+    torch = _torch()
+    if not torch.is_grad_enabled():
+        return grads
+    global _ONCE_FN
+    if _ONCE_FN is None:
+        class _Once(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, joined, grad):
+                return grad.detach()
+
+            @staticmethod
+            def backward(ctx, g):
+                raise RuntimeError("the gradients of lmhead_distill and lmhead_norm take no second backward")
+
+        _ONCE_FN = _Once
+    joined = torch.empty(0, requires_grad=True)
+    return tuple(None if g is None else _ONCE_FN.apply(joined, g) for g in grads)
+
+
 def _autograd_function():
     torch = _torch()
 
@@ -742,9 +769,9 @@ def _distill_function():
             dh, dW = distill_backward(hidden, W, targets, ids, teacher, ctx.chunk_size, logp, lse, logp_top, gk, gl,
                                       teacher_lse, temperature=ctx.temperature,
                                       grad_dtype=torch.bfloat16 if bf16 else torch.float32)
-            return (dh.to(hidden.dtype) if ctx.needs_input_grad[0] else None,
-                    dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
-                    None, None, None, None, None, None)
+            return _once(dh.to(hidden.dtype) if ctx.needs_input_grad[0] else None,
+                         dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
+                         None, None, None, None, None, None)
 
     return _LmheadDistill
 
@@ -770,7 +797,7 @@ def _norm_function():
             want_w, want_b = ctx.needs_input_grad[1], ctx.needs_input_grad[2]
             dx, dw, db = norm_backward(x, weight, mean, rstd, dy.detach().contiguous(), ctx.kind, with_weight=want_w,
                                        with_bias=want_b, grad_dtype=ctx.bias if weight is None else weight.dtype)
-            return dx if ctx.needs_input_grad[0] else None, dw, db, None, None, None
+            return _once(dx if ctx.needs_input_grad[0] else None, dw, db, None, None, None)
 
     return _LmheadNorm
 
@@ -785,7 +812,7 @@ def lmhead_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "layer
     float32 (``out_dtype=torch.bfloat16`` gives the head its dtype from a
     float32 stream); gradients flow to x, weight and bias. A row whose incoming
     gradient is 0 (a token that the head masks) adds nothing to any gradient,
-    whatever it holds."""
+    whatever it holds. A second backward, through the gradients, is refused."""
     global _NORM_FN
     if _NORM_FN is None:
         _NORM_FN = _norm_function()
@@ -824,7 +851,8 @@ def lmhead_distill(hidden, W, ids, teacher, chunk_size: int, targets=None, teach
     ``chunk_size`` bounds the backward's cotangent block as for the head, but
     blocks of up to 2^25 entries (134 MB) are always taken. A backward pass may
     be captured into a graph where no eager graph of the same leaves is alive
-    (torch ends the process otherwise, whatever the function)."""
+    (torch ends the process otherwise, whatever the function). A second backward,
+    through the gradients, is refused."""
     global _DISTILL_FN
     if _DISTILL_FN is None:
         _DISTILL_FN = _distill_function()
