@@ -695,7 +695,7 @@ def _once(*grads):
 
             @staticmethod
             def backward(ctx, g):
-                raise RuntimeError("the gradients of lmhead_distill and lmhead_norm take no second backward")
+                raise RuntimeError("the gradients of lmhead_logps, lmhead_distill and lmhead_norm take no second backward")
 
         _ONCE_FN = _Once
     joined = torch.empty(0, requires_grad=True)
@@ -737,9 +737,9 @@ def _autograd_function():
             dh, dW = backward(hidden, W, targets, ctx.chunk_size, lse, ent if ge is not None else None, gl, ge,
                               temperature=ctx.temperature,
                               grad_dtype=torch.bfloat16 if bf16 else torch.float32)
-            return (dh.to(hidden.dtype) if ctx.needs_input_grad[0] else None,
-                    dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
-                    None, None, None, None)
+            return _once(dh.to(hidden.dtype) if ctx.needs_input_grad[0] else None,
+                         dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
+                         None, None, None, None)
 
     return _LmheadLogps
 
@@ -833,7 +833,8 @@ def lmhead_logps(hidden, W, targets, chunk_size: int, temperature: Optional[floa
     ``lmhead_logps_bwd`` on the saved lse / entropy (the logits are recomputed,
     never stored). Masked targets (outside [0, V)) give zeros. With ``norm``,
     hidden is the stream in front of the final norm (bfloat16 or float32), and
-    gradients flow to it and to the norm's weight and bias."""
+    gradients flow to it and to the norm's weight and bias. A second backward,
+    through the gradients, is refused."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()

@@ -19,6 +19,18 @@ def _distill_backward(hidden, W, targets, ids, teacher, chunk_size, logp, lse, l
     return dz @ W, dz.t() @ hidden
 
 
+def _head_forward(hidden, W, targets, chunk_size, with_entropy=True, temperature=None):
+    z = hidden @ W.t()
+    return z.pow(2).sum(1), z.sum(1) if with_entropy else None, z[:, 0]
+
+
+def _head_backward(hidden, W, targets, chunk_size, lse, entropy, g_logp, g_ent=None, temperature=None, grad_dtype=None):
+    dz = 2 * g_logp[:, None] * (hidden @ W.t())
+    if g_ent is not None:
+        dz = dz + g_ent[:, None]
+    return dz @ W, dz.t() @ hidden
+
+
 def _norm_forward(x, weight=None, bias=None, eps=1e-6, kind="layer", out_dtype=None):
     return x * weight + bias, None, x.new_ones(len(x))
 
@@ -63,3 +75,15 @@ def _once(loss, leaves):
 @pytest.mark.parametrize("loss,shapes", [(_distill, ((3, 4), (5, 4))), (_norm, ((3, 4), (4,)))])
 def test_second_order_gradients_are_refused(plain, loss, shapes):
     _once(loss, _leaves(*shapes))
+
+
+@pytest.mark.parametrize("with_entropy", [True, False])
+def test_second_order_gradients_of_the_head_are_refused(monkeypatch, with_entropy):
+    monkeypatch.setattr(lm, "forward", torch.no_grad()(_head_forward))
+    monkeypatch.setattr(lm, "backward", torch.no_grad()(_head_backward))
+
+    def head(h, W):
+        out = lm.lmhead_logps(h, W, torch.zeros(len(h), dtype=torch.int32), 8, with_entropy=with_entropy)
+        return out[0].sum() + out[1].sum() if with_entropy else out.sum()
+
+    _once(head, _leaves((3, 4), (5, 4)))
