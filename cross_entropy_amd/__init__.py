@@ -142,6 +142,17 @@ def _stream(device, stream):
     return stream.cuda_stream
 
 
+def _enqueue(dev, raw, *args):
+    """Call ``raw`` with the tensors' device current (a launch goes to the
+    current device where the stream is the default one) and check its status."""
+    torch = _torch()
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _native.check(raw(*args))
+    else:
+        with torch.cuda.device(dev):
+            _native.check(raw(*args))
+
+
 def lmhead_logps_workspace_bytes(N: int, H: int, V: int, chunk_size: int, with_backward=True) -> int:
     """Workspace bytes: with_backward False (forward only), True (forward and
     the float32-gradient backward) or "bf16" (also the bf16-gradient backward)."""
@@ -190,14 +201,14 @@ def _fwd_args(hidden, W, targets, chunk_size, logp, entropy, lse, workspace, str
 def lmhead_logps_fwd(hidden, W, targets, chunk_size: int, logp, entropy, lse, workspace, stream=None) -> None:
     """Enqueue the forward on ``stream`` (default: torch's current stream)."""
     ptrs, outs = _fwd_args(hidden, W, targets, chunk_size, logp, entropy, lse, workspace, stream)
-    _native.check(_native.raw_fwd(*ptrs, *outs))
+    _enqueue(hidden.device, _native.raw_fwd, *ptrs, *outs)
 
 
 def lmhead_logps_fwd_temp(hidden, W, targets, chunk_size: int, temperature: float, logp, entropy, lse, workspace,
                           stream=None) -> None:
     """Enqueue the tempered forward (logits / temperature) on ``stream``."""
     ptrs, outs = _fwd_args(hidden, W, targets, chunk_size, logp, entropy, lse, workspace, stream)
-    _native.check(_native.raw_fwd_temp(*ptrs, temperature, *outs))
+    _enqueue(hidden.device, _native.raw_fwd_temp, *ptrs, temperature, *outs)
 
 
 def lmhead_logps_fwd_noalloc(hidden, W, targets, chunk_size: int, temperature: float, logp, entropy, lse,
@@ -207,11 +218,12 @@ def lmhead_logps_fwd_noalloc(hidden, W, targets, chunk_size: int, temperature: f
     torch = _torch()
     N, H, V = _shapes(hidden, W, targets)
     dev = hidden.device
-    _native.check(_native.raw_fwd_noalloc(
+    _enqueue(
+        dev, _native.raw_fwd_noalloc,
         _ptr(hidden, "hidden", _bf16_types(), dev), _ptr(W, "W", _bf16_types(), dev),
         _ptr(targets, "targets", (torch.int32,), dev), N, H, V, chunk_size, temperature,
         _ptr(logp, "logp", (torch.float32,), dev, N), _ptr(entropy, "entropy", (torch.float32,), dev, N, optional=True),
-        _ptr(lse, "lse", (torch.float32,), dev, N), _stream(dev, stream)))
+        _ptr(lse, "lse", (torch.float32,), dev, N), _stream(dev, stream))
 
 
 def _bwd_args(hidden, W, targets, chunk_size, lse, entropy, g_logp, g_ent, dh, dW, workspace, stream,
@@ -247,7 +259,7 @@ def lmhead_logps_bwd(hidden, W, targets, chunk_size: int, lse, entropy, g_logp, 
                      stream=None) -> None:
     """Enqueue the backward on ``stream`` (default: torch's current stream)."""
     ptrs, rest = _bwd_args(hidden, W, targets, chunk_size, lse, entropy, g_logp, g_ent, dh, dW, workspace, stream)
-    _native.check(_native.raw_bwd(*ptrs, *rest))
+    _enqueue(hidden.device, _native.raw_bwd, *ptrs, *rest)
 
 
 def lmhead_logps_bwd_temp(hidden, W, targets, chunk_size: int, temperature: float, lse, entropy, g_logp, g_ent,
@@ -255,7 +267,7 @@ def lmhead_logps_bwd_temp(hidden, W, targets, chunk_size: int, temperature: floa
     """Enqueue the tempered backward on ``stream``; lse and entropy come from
     the tempered forward with the same temperature."""
     ptrs, rest = _bwd_args(hidden, W, targets, chunk_size, lse, entropy, g_logp, g_ent, dh, dW, workspace, stream)
-    _native.check(_native.raw_bwd_temp(*ptrs, temperature, *rest))
+    _enqueue(hidden.device, _native.raw_bwd_temp, *ptrs, temperature, *rest)
 
 
 def lmhead_logps_bwd_ex(hidden, W, targets, chunk_size: int, temperature: float, lse, entropy, g_logp, g_ent,
@@ -263,7 +275,7 @@ def lmhead_logps_bwd_ex(hidden, W, targets, chunk_size: int, temperature: float,
     """Enqueue the backward with flags (``_native.BWD_ACCUMULATE_DH`` /
     ``BWD_ACCUMULATE_DW``: add into dh / dW instead of overwriting)."""
     ptrs, rest = _bwd_args(hidden, W, targets, chunk_size, lse, entropy, g_logp, g_ent, dh, dW, workspace, stream)
-    _native.check(_native.raw_bwd_ex(*ptrs, temperature, *rest[:6], flags, *rest[6:]))
+    _enqueue(hidden.device, _native.raw_bwd_ex, *ptrs, temperature, *rest[:6], flags, *rest[6:])
 
 
 def lmhead_logps_bwd_bf16(hidden, W, targets, chunk_size: int, temperature: float, lse, entropy, g_logp, g_ent,
@@ -273,7 +285,7 @@ def lmhead_logps_bwd_bf16(hidden, W, targets, chunk_size: int, temperature: floa
     workspace is sized with ``with_backward="bf16"``."""
     ptrs, rest = _bwd_args(hidden, W, targets, chunk_size, lse, entropy, g_logp, g_ent, dh, dW, workspace, stream,
                            grad_types=_bf16_types())
-    _native.check(_native.raw_bwd_bf16(*ptrs, temperature, *rest[:6], flags, *rest[6:]))
+    _enqueue(hidden.device, _native.raw_bwd_bf16, *ptrs, temperature, *rest[:6], flags, *rest[6:])
 
 
 def lmhead_logps_fwd_shard(hidden, W_shard, targets, vocab_offset: int, V_total: int, chunk_size: int,
@@ -282,11 +294,12 @@ def lmhead_logps_fwd_shard(hidden, W_shard, targets, vocab_offset: int, V_total:
     torch = _torch()
     N, H, V = _shapes(hidden, W_shard, targets)
     dev = hidden.device
-    _native.check(_native.raw_fwd_shard(
+    _enqueue(
+        dev, _native.raw_fwd_shard,
         _ptr(hidden, "hidden", _bf16_types(), dev), _ptr(W_shard, "W_shard", _bf16_types(), dev),
         _ptr(targets, "targets", (torch.int32,), dev), N, H, V, vocab_offset, V_total, chunk_size, temperature,
         _ptr(partial, "partial", (torch.float32,), dev, 4 * N), _ptr(workspace, "workspace", (torch.uint8,), dev),
-        workspace.numel(), _stream(dev, stream)))
+        workspace.numel(), _stream(dev, stream))
 
 
 def lmhead_logps_merge_shards(partials, targets, V_total: int, temperature: float, logp, entropy, lse,
@@ -297,11 +310,12 @@ def lmhead_logps_merge_shards(partials, targets, V_total: int, temperature: floa
         raise ValueError("partials must be [P, N, 4]")
     P, N = int(partials.shape[0]), int(partials.shape[1])
     dev = partials.device
-    _native.check(_native.raw_merge_shards(
+    _enqueue(
+        dev, _native.raw_merge_shards,
         _ptr(partials, "partials", (torch.float32,), dev), P, _ptr(targets, "targets", (torch.int32,), dev, N),
         N, V_total, temperature, _ptr(logp, "logp", (torch.float32,), dev, N),
         _ptr(entropy, "entropy", (torch.float32,), dev, N, optional=True), _ptr(lse, "lse", (torch.float32,), dev, N),
-        _stream(dev, stream)))
+        _stream(dev, stream))
 
 
 def lmhead_logps_bwd_shard(hidden, W_shard, targets, vocab_offset: int, V_total: int, chunk_size: int,
@@ -311,8 +325,8 @@ def lmhead_logps_bwd_shard(hidden, W_shard, targets, vocab_offset: int, V_total:
     ptrs, rest = _bwd_args(hidden, W_shard, targets, chunk_size, lse, entropy, g_logp, g_ent, dh, dW_shard,
                            workspace, stream)
     hid, Wp, tg, N, H, V, C = ptrs
-    _native.check(_native.raw_bwd_shard(hid, Wp, tg, N, H, V, vocab_offset, V_total, C, temperature, *rest[:6],
-                                        flags, *rest[6:]))
+    _enqueue(hidden.device, _native.raw_bwd_shard, hid, Wp, tg, N, H, V, vocab_offset, V_total, C, temperature,
+             *rest[:6], flags, *rest[6:])
 
 
 def workspace_for(hidden, W, chunk_size: int, with_backward=True):
@@ -384,17 +398,6 @@ def backward(hidden, W, targets, chunk_size: int, lse, entropy, g_logp, g_ent: O
         lmhead_logps_bwd_temp(hidden, W, targets, chunk_size, temperature, lse, entropy, g_logp, g_ent, dh, dW,
                               workspace, stream)
     return dh, dW
-
-
-def _enqueue(dev, raw, *args):
-    """Call ``raw`` with the tensors' device current (a launch goes to the
-    current device where the stream is the default one) and check its status."""
-    torch = _torch()
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _native.check(raw(*args))
-    else:
-        with torch.cuda.device(dev):
-            _native.check(raw(*args))
 
 
 def _allocating(device, stream):

@@ -87,3 +87,59 @@ def test_second_order_gradients_of_the_head_are_refused(monkeypatch, with_entrop
         return out[0].sum() + out[1].sum() if with_entropy else out.sum()
 
     _once(head, _leaves((3, 4), (5, 4)))
+
+
+class _On1:
+    """The parts of a tensor on cuda:1 that the calls look at."""
+    is_cuda, device = True, torch.device("cuda", 1)
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, torch.Size(shape)
+
+    dim = lambda self: len(self.shape)                 # noqa: E731
+    numel = lambda self: self.shape.numel()            # noqa: E731
+    is_contiguous = lambda self: True                  # noqa: E731
+    data_ptr = lambda self: 64                         # noqa: E731
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """A launch on the default stream goes to the current device: every call
+    makes its tensors' one current, and leaves the caller's as it was."""
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d.index
+
+        def __enter__(self):
+            self.back, now[0] = now[0], self.d
+
+        def __exit__(self, *exc):
+            now[0] = self.back
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    raws = ("fwd", "fwd_temp", "fwd_noalloc", "fwd_shard", "merge_shards", "bwd", "bwd_temp", "bwd_ex", "bwd_bf16",
+            "bwd_shard", "distill_fwd", "distill_bwd", "norm_fwd", "norm_bwd")
+    for name in raws:
+        monkeypatch.setattr(lm._native, "raw_" + name, lambda *a, name=name: seen.append((name, now[0])) or 0)
+    f32, bf16, i32 = torch.float32, torch.bfloat16, torch.int32
+    h, W, ws = _On1(bf16, 4, 64), _On1(bf16, 9, 64), _On1(torch.uint8, 100)
+    t, s, top, ids = _On1(i32, 4), _On1(f32, 4), _On1(f32, 4, 3), _On1(i32, 4, 3)
+    dh, dW, v = _On1(f32, 4, 64), _On1(f32, 9, 64), _On1(f32, 64)
+    out = dict(stream=0)
+    lm.lmhead_logps_fwd(h, W, t, 8, s, s, s, ws, **out)
+    lm.lmhead_logps_fwd_temp(h, W, t, 8, 0.7, s, s, s, ws, **out)
+    lm.lmhead_logps_fwd_noalloc(h, W, t, 8, 0.7, s, s, s, **out)
+    lm.lmhead_logps_fwd_shard(h, W, t, 0, 18, 8, 1.0, _On1(f32, 4, 4), ws, **out)
+    lm.lmhead_logps_merge_shards(_On1(f32, 2, 4, 4), t, 18, 1.0, s, s, s, **out)
+    lm.lmhead_logps_bwd(h, W, t, 8, s, s, s, s, dh, dW, ws, **out)
+    lm.lmhead_logps_bwd_temp(h, W, t, 8, 0.7, s, s, s, s, dh, dW, ws, **out)
+    lm.lmhead_logps_bwd_ex(h, W, t, 8, 0.7, s, s, s, s, dh, dW, 0, ws, **out)
+    lm.lmhead_logps_bwd_bf16(h, W, t, 8, 0.7, s, s, s, s, h, W, 0, ws, **out)
+    lm.lmhead_logps_bwd_shard(h, W, t, 0, 18, 8, 1.0, s, s, s, s, dh, dW, 0, ws, **out)
+    lm.lmhead_logps_distill_fwd(h, W, t, ids, top, s, 8, 1.0, s, s, s, top, ws, **out)
+    lm.lmhead_logps_distill_bwd(h, W, t, ids, top, s, 8, 1.0, s, s, top, s, s, dh, dW, 0, ws, **out)
+    lm.lmhead_logps_norm_fwd(dh, v, v, 1e-6, "layer", dh, s, s, **out)
+    lm.lmhead_logps_norm_bwd(dh, v, "layer", s, s, dh, dh, v, v, 0, ws, **out)
+    assert sorted(seen) == sorted((name, 1) for name in raws) and now == [0]
