@@ -153,6 +153,18 @@ def _enqueue(dev, raw, *args):
             _native.check(raw(*args))
 
 
+def _allocating(device, stream):
+    """Context in which tensors are allocated for work on ``stream`` (None: the
+    current one): from that stream's own pool, so that neither their earlier
+    nor their later use elsewhere overlaps it."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def lmhead_logps_workspace_bytes(N: int, H: int, V: int, chunk_size: int, with_backward=True) -> int:
     """Workspace bytes: with_backward False (forward only), True (forward and
     the float32-gradient backward) or "bf16" (also the bf16-gradient backward)."""
@@ -346,11 +358,12 @@ def forward(hidden, W, targets, chunk_size: int, with_entropy: bool = True, work
     torch = _torch()
     N = hidden.shape[0]
     dev = hidden.device
-    logp = torch.empty(N, dtype=torch.float32, device=dev)
-    lse = torch.empty(N, dtype=torch.float32, device=dev)
-    ent = torch.empty(N, dtype=torch.float32, device=dev) if with_entropy else None
-    if workspace is None:
-        workspace = workspace_for(hidden, W, chunk_size, with_backward=False)
+    with _allocating(dev, stream):
+        logp = torch.empty(N, dtype=torch.float32, device=dev)
+        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        ent = torch.empty(N, dtype=torch.float32, device=dev) if with_entropy else None
+        if workspace is None:
+            workspace = workspace_for(hidden, W, chunk_size, with_backward=False)
     if temperature is None:
         lmhead_logps_fwd(hidden, W, targets, chunk_size, logp, ent, lse, workspace, stream)
     else:
@@ -375,19 +388,19 @@ def backward(hidden, W, targets, chunk_size: int, lse, entropy, g_logp, g_ent: O
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
     if accumulate and (dh is None or dW is None):
         raise ValueError("accumulate needs both dh and dW buffers")
-    if dh is None:
-        dh = torch.empty((N, H), dtype=grad_dtype, device=dev)
-    if dW is None:
-        dW = torch.empty((V, H), dtype=grad_dtype, device=dev)
-    if grad_dtype == torch.bfloat16:
+    with _allocating(dev, stream):
+        if dh is None:
+            dh = torch.empty((N, H), dtype=grad_dtype, device=dev)
+        if dW is None:
+            dW = torch.empty((V, H), dtype=grad_dtype, device=dev)
         if workspace is None:
-            workspace = workspace_for(hidden, W, chunk_size, with_backward="bf16")
+            workspace = workspace_for(hidden, W, chunk_size,
+                                      with_backward="bf16" if grad_dtype == torch.bfloat16 else True)
+    if grad_dtype == torch.bfloat16:
         flags = (_native.BWD_ACCUMULATE_DH | _native.BWD_ACCUMULATE_DW) if accumulate else 0
         lmhead_logps_bwd_bf16(hidden, W, targets, chunk_size, 1.0 if temperature is None else temperature, lse,
                               entropy, g_logp, g_ent, dh, dW, flags, workspace, stream)
         return dh, dW
-    if workspace is None:
-        workspace = workspace_for(hidden, W, chunk_size, with_backward=True)
     if accumulate:
         flags = _native.BWD_ACCUMULATE_DH | _native.BWD_ACCUMULATE_DW
         lmhead_logps_bwd_ex(hidden, W, targets, chunk_size, 1.0 if temperature is None else temperature, lse,
@@ -398,18 +411,6 @@ def backward(hidden, W, targets, chunk_size: int, lse, entropy, g_logp, g_ent: O
         lmhead_logps_bwd_temp(hidden, W, targets, chunk_size, temperature, lse, entropy, g_logp, g_ent, dh, dW,
                               workspace, stream)
     return dh, dW
-
-
-def _allocating(device, stream):
-    """Context in which tensors are allocated for work on ``stream`` (None: the
-    current one): from that stream's own pool, so that neither their earlier
-    nor their later use elsewhere overlaps it."""
-    torch = _torch()
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
 
 
 def lmhead_logps_distill_workspace_bytes(N: int, H: int, V: int, K: int, chunk_size: int, with_backward=True) -> int:

@@ -143,3 +143,32 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     lm.lmhead_logps_norm_fwd(dh, v, v, 1e-6, "layer", dh, s, s, **out)
     lm.lmhead_logps_norm_bwd(dh, v, "layer", s, s, dh, dh, v, v, 0, ws, **out)
     assert sorted(seen) == sorted((name, 1) for name in raws) and now == [0]
+
+
+def test_helpers_allocate_for_the_calls_stream(monkeypatch):
+    """Outputs and workspaces of the helpers given a stream come from that
+    stream's own pool: from the current stream's, a workspace freed on return
+    could be handed out while the call still runs."""
+    inside, made = [0], []
+
+    class Pool:
+        def __enter__(self):
+            inside[0] += 1
+
+        def __exit__(self, *exc):
+            inside[0] -= 1
+
+    def empty(*shape, dtype=None, device=None, **kw):
+        made.append(inside[0])
+        return _On1(dtype, *(shape[0] if isinstance(shape[0], tuple) else shape))
+
+    monkeypatch.setattr(lm, "_allocating", lambda device, stream: Pool())
+    monkeypatch.setattr(lm, "_enqueue", lambda dev, raw, *a: None)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(lm._native, "raw_workspace_bytes", lambda *a: 64)
+    h, W, t, s = _On1(torch.bfloat16, 4, 64), _On1(torch.bfloat16, 9, 64), _On1(torch.int32, 4), _On1(torch.float32, 4)
+    for temperature in (None, 0.7):
+        lm.forward(h, W, t, 8, stream=7, temperature=temperature)
+        for dtype in (torch.float32, torch.bfloat16):
+            lm.backward(h, W, t, 8, s, s, s, stream=7, temperature=temperature, grad_dtype=dtype)
+    assert len(made) == 2 * (4 + 2 * 3) and all(made)
