@@ -1,0 +1,58 @@
+"""The distillation's kernels for few tokens where the other tests do not take
+them: gradients added into."""
+import pytest
+
+import ops_reference as R
+from gpu_common import dev, log
+from synthetic import bf16_bits_to_f32
+from test_gpu_distill import _case, _check, _g, _put
+
+pytestmark = pytest.mark.gpu
+
+ADD = [(20, 777), (50, 1003), (120, 900), (180, 1025), (250, 700)]   # each K of the products, a ragged vocabulary
+
+
+def _forward(args):
+    import cross_entropy_amd as lm
+    hd, Wd, tg, idd, td, tl = _put(*args)
+    kl, logp, lse, top = lm.distill_forward(hd, Wd, tg, idd, td, 64, tl)
+    return (hd, Wd, tg, idd, td), tl, (logp, lse, top)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("N,V", ADD)
+def test_few_tokens_add_into_gradients(t, N, V):
+    """Added into, a gradient is the float32 sum of what the buffer held and of
+    the gradient's own float32 value, rounded once: bit for bit."""
+    import torch
+    import cross_entropy_amd as lm
+    H = 192                                  # no multiple of a wave's 128 columns, nor of a workgroup's 256
+    log(f"[distill] add N={N} V={V} {t}")
+    args = _case(40 + N, N, H, V, 7, hard=True)
+    given, tl, (logp, lse, top) = _forward(args)
+    gk, gl = (dev(a) for a in _g(41, N, True))
+    ty = torch.float32 if t == "f32" else torch.bfloat16
+    ws = lm.distill_workspace_for(given[0], given[1], given[3], 64, "bf16")
+    own_h, own_W = lm.distill_backward(*given, 64, logp, lse, top, gk, gl, tl)      # float32, not added
+    masked = dev(~R.Distill(bf16_bits_to_f32(args[0]), bf16_bits_to_f32(args[1]), *args[2:], 1.0).used)
+    assert masked.any()
+    for flags in (1, 2, 3):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(flags)
+        ph, pW = (torch.randn(s, H, device="cuda", generator=gen).to(ty) for s in (N, V))
+        room_h = torch.cat([ph, torch.full((3, H), 7.0, device="cuda", dtype=ty)])   # rows behind, left as they were
+        room_W = torch.cat([pW, torch.full((3, H), 7.0, device="cuda", dtype=ty)])
+        dh, dW = room_h[:N], room_W[:V]
+        lm.lmhead_logps_distill_bwd(*given, tl, 64, 1.0, logp, lse, top, gk, gl, dh, dW, flags, ws)
+        torch.cuda.synchronize()
+        want_h, want_W = own_h.to(ty), own_W.to(ty)
+        if flags & 1:
+            want_h = (ph.float() + own_h).to(ty)
+            assert torch.equal(dh[masked], ph[masked])
+        else:
+            assert (dh[masked] == 0).all()
+        if flags & 2:
+            want_W = (pW.float() + own_W).to(ty)
+        assert torch.equal(dh[~masked], want_h[~masked]), flags
+        assert torch.equal(dW, want_W), flags
+        assert (room_h[N:] == 7).all() and (room_W[V:] == 7).all()
