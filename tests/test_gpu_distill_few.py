@@ -1,5 +1,5 @@
 """The distillation's kernels for few tokens where the other tests do not take
-them: gradients added into."""
+them: gradients added into, each count of row blocks."""
 import pytest
 
 import ops_reference as R
@@ -56,3 +56,12 @@ def test_few_tokens_add_into_gradients(t, N, V):
         assert torch.equal(dh[~masked], want_h[~masked]), flags
         assert torch.equal(dW, want_W), flags
         assert (room_h[N:] == 7).all() and (room_W[V:] == 7).all()
+
+
+@pytest.mark.parametrize("V", [50001, 90001, 120011, 151936, 200003])   # 2 to 5 row blocks a wave, and a second round
+@pytest.mark.parametrize("N", [7, 24, 50])
+def test_few_tokens_of_a_large_vocabulary(N, V):
+    what = f"few N={N} V={V}"
+    log(f"[distill] {what}")
+    hard = N != 24
+    _check(_case(N + V, N, 64, V, 9, t_type="f32", tail=N == 50, hard=hard), C=512, what=what)
