@@ -1,10 +1,12 @@
 """The distillation's kernels for few tokens where the other tests do not take
-them: gradients added into, each count of row blocks."""
+them: gradients added into, each count of row blocks, the second word of the
+cotangent."""
 import pytest
 
 import ops_reference as R
 from gpu_common import dev, log
 from synthetic import bf16_bits_to_f32
+from test_distill_words import WORDS, two_words, words_case
 from test_gpu_distill import _case, _check, _g, _put
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +67,13 @@ def test_few_tokens_of_a_large_vocabulary(N, V):
     log(f"[distill] {what}")
     hard = N != 24
     _check(_case(N + V, N, 64, V, 9, t_type="f32", tail=N == 50, hard=hard), C=512, what=what)
+
+
+@pytest.mark.parametrize("N,H,V,K", WORDS)
+def test_few_tokens_keep_two_words(N, H, V, K, monkeypatch):
+    """Up to 64 tokens the cotangent is held as its rounding to bf16 and what
+    that left, rounded: the bound of two words, which one word does not keep
+    (tests/test_distill_words.py)."""
+    log(f"[distill] two words N={N} H={H} V={V} K={K}")
+    two_words(monkeypatch, N, V)
+    _check(words_case(N, H, V, K), grads=("f32",), what=f"two words N={N} V={V}")
