@@ -238,7 +238,9 @@ __global__ __launch_bounds__(256, 2) void few_stats_kernel(const FewArgs a) {
           if (row < V) mx = nan_max(mx, acc[i][j][r]);
           if (row == tgt[j]) st[j].zt = acc[i][j][r];
         }
-      const float m = mx * a.sc;   // sc > 0: max commutes with the scaling
+      // sc > 0: max commutes with the scaling. Lanes without a row keep kNegBig: scaled by
+      // an sc above 3.4e8 it would be -inf, whose merge with another such record is NaN.
+      const float m = nan_max(kNegBig, mx * a.sc);
       float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < MB; ++i)

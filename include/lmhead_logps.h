@@ -315,7 +315,8 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  * and, beside it from the same pass, logp = z[target] / T - lse of a hard
  * target. Neither call holds the [tokens, vocab] logits. kl is the loss at
  * temperature T without the customary factor T^2 (the caller's cotangent
- * carries it).
+ * carries it). Scores z / T of up to 2^30 either way are taken, as by the
+ * head: the steps of larger ones in float32 are beyond what an exponential holds.
  *   targets      int32 [N]    hard targets, or NULL for none; outside [0, V)
  *                             the token has none (logp 0)
  *   ids          int32 [N,K]  teacher's ids; an id outside [0, V) marks a

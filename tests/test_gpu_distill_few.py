@@ -7,7 +7,7 @@ import ops_reference as R
 from gpu_common import dev, log
 from synthetic import bf16_bits_to_f32
 from test_distill_words import WORDS, two_words, words_case
-from test_gpu_distill import _case, _check, _g, _put
+from test_gpu_distill import _case, _check, _forward_check, _g, _put
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,14 @@ def test_few_tokens_keep_two_words(N, H, V, K, monkeypatch):
     log(f"[distill] two words N={N} H={H} V={V} K={K}")
     two_words(monkeypatch, N, V)
     _check(words_case(N, H, V, K), grads=("f32",), what=f"two words N={N} V={V}")
+
+
+@pytest.mark.parametrize("N", [3, 20, 50, 300])   # the kernels for few tokens at each tile of theirs, and the tiles
+@pytest.mark.parametrize("V", [5, 70, 300])
+def test_scores_of_a_small_temperature(N, V):
+    """T = 2^-28: the scale to base 2 takes the stand-in for a missing row's
+    logit beyond float32, which must not reach the rows that are there."""
+    T, K = 2.0 ** -28, 3
+    log(f"[distill] T=2^-28 N={N} V={V}")
+    args = _case(70 + N + V, N, 64, V, K, T, hard=True, pad=0.0, lean=False)
+    _forward_check(args, _put(*args), T, 64, f"T=2^-28 N={N} V={V}")
