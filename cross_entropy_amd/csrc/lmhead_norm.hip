@@ -25,11 +25,30 @@
 namespace lmh {
 namespace {
 
-// v_mul_legacy_f32: +0 when either factor is 0 (NaN and inf included), else IEEE
+// v_mul_legacy_f32: +0 when either factor is 0 (NaN and inf included), else IEEE.
+// A zero of dy is to contribute 0 whatever lies beside it, at no cost; a NaN or an
+// infinity of dy beside a 0 is to give NaN, and what it reaches is taken again.
 extern "C" __device__ float lmh_norm_fmul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
 __device__ __forceinline__ float mul0(float a, float b) { return lmh_norm_fmul_legacy(a, b); }
 
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+template <bool F32>
+__device__ __forceinline__ float element(const void* p, int64_t i) {
+  return F32 ? static_cast<const float*>(p)[i] : widen(static_cast<const uint16_t*>(p)[i]);
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
+// a column's sum of dy xh over rows row, row + step, ..., IEEE's product for
+// every element of dy but a zero
+template <bool XF32, bool YF32>
+__device__ float ieee_column(const NormBwdArgs& a, int j, int64_t row, int64_t step) {
+  float u = 0.0f;
+  for (; row < a.N; row += step) {
+    const float dy = element<YF32>(a.dy, row * a.H + j);
+    if (dy != 0.0f) u += dy * ((element<XF32>(a.x, row * a.H + j) - (a.rms ? 0.0f : a.mean[row])) * a.rstd[row]);
+  }
+  return u;
+}
 __device__ __forceinline__ uint16_t narrow(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return (uint32_t)narrow(lo) | ((uint32_t)narrow(hi) << 16);
@@ -294,6 +313,9 @@ __device__ __forceinline__ void norm_columns(const NormBwdArgs& a, int block, fl
       }
     }
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (__builtin_expect(!finite(db[k]), 0)) dw[k] = ieee_column<XF32, YF32>(a, c + k, threadIdx.x / 8, step);
   const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -322,6 +344,9 @@ __device__ __forceinline__ void norm_columns(const NormBwdArgs& a, int block, fl
 // the rows' own sum the columns instead, and there are no partial rows. A zero in dy contributes a
 // zero whatever x, the statistics and w hold there (mul0), so a masked token,
 // whose dy row is 0, adds nothing and gets dx = 0 even where its x is NaN.
+// The same product drops a NaN or an infinity of dy beside a 0 of xh or w: at the
+// end a workgroup (or wave) that met one forms again what that reaches, as IEEE
+// has it. Asking costs 0.1 us of a small call and 1% of a large one.
 template <bool XF32, bool YF32, bool WF32, int NV, int LANES>
 __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int G = XF32 ? 4 : 8, NG = 8 * NV / G;
@@ -354,7 +379,9 @@ __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(c
       dw[i][k] = db[i][k] = 0.0f;
       if (kept) sums[0][G * (i * threads + t) + k] = sums[1][G * (i * threads + t) + k] = 0.0f;   // 16 a thread: within kNormMaxH
     }
-  int64_t row = (int64_t)blockIdx.x * per + slot;
+  const int64_t first = (int64_t)blockIdx.x * per + slot;
+  int64_t row = first;
+  bool bad = false;   // something here is not finite
   Part<XF32, G, NG> nx;
   Part<YF32, G, NG> ng;
   float n_mu = 0.0f, n_r = 0.0f;
@@ -400,11 +427,66 @@ __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(c
     row_sum2<LANES>(c1, c2, !a.rms, s, turn);
     c1 *= inv;
     c2 = a.rms ? 0.0f : c2 * inv;
+    bad |= !(finite(c1) && finite(c2)) || r == 0.0f;   // r is 0 beside an infinite x
 #pragma unroll
     for (int i = 0; i < NG; ++i)
 #pragma unroll
       for (int k = 0; k < G; ++k) x[i][k] = mul0(r, (g[i][k] - c2) - mul0(x[i][k], c1));
     store_part<XF32, G, NG>(a.dx, row, H, t, threads, x);
+  }
+#pragma unroll
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int k = 0; k < G; ++k) bad |= !finite(kept ? sums[1][G * (i * threads + t) + k] : db[i][k]);
+  if (__builtin_expect(WIDE ? __syncthreads_or(bad) : __any(bad), 0)) {
+    int tc = t;
+    int64_t from = first;
+    asm volatile("" : "+v"(tc), "+v"(from));   // nothing of this is worth a register of the loop above
+    // the columns with such a dy, whose db is not finite, and the rows with such a
+    // dy or x, whose c1 is not or whose r is 0: element by element
+    if (a.part != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          const int j = G * (i * threads + tc) + k;
+          if (finite(kept ? sums[1][j] : db[i][k])) continue;
+          const float u = ieee_column<XF32, YF32>(a, j, from, step);
+          if (kept) sums[0][j] = u;
+          else dw[i][k] = u;
+        }
+    }
+    for (row = from; row < a.N; row += step) {
+      const float mu = a.rms ? 0.0f : a.mean[row], r = a.rstd[row];
+      auto each = [&](auto f) {   // f(column, dy, xh, dy weight)
+#pragma unroll 1
+        for (int e = 0; e < NG * G; ++e) {
+          const int j = G * (e / G * threads + tc) + e % G;
+          if (j >= H) continue;
+          const float dy = element<YF32>(a.dy, row * H + j);
+          const float wt = a.w != nullptr ? element<WF32>(a.w, j) : 1.0f;
+          f(j, dy, (element<XF32>(a.x, row * H + j) - mu) * r, dy != 0.0f ? dy * wt : 0.0f);
+        }
+      };
+      float c1 = 0.0f, c2 = 0.0f, some = 0.0f, none = 0.0f;
+      each([&](int, float dy, float xh, float gw) {
+        if (dy != 0.0f) {
+          c1 += gw * xh;
+          some = 1.0f;
+        }
+        c2 += gw;
+      });
+      row_sum2<LANES>(c1, c2, !a.rms, s, turn);
+      row_sum2<LANES>(some, none, false, s, turn);
+      c1 *= inv;
+      c2 = a.rms ? 0.0f : c2 * inv;
+      if (some == 0.0f || (finite(c1) && finite(c2) && r != 0.0f)) continue;   // masked, or no different above
+      each([&](int j, float, float xh, float gw) {
+        const float v = r * ((gw - c2) - xh * c1);
+        if (XF32) static_cast<float*>(a.dx)[row * H + j] = v;
+        else static_cast<uint16_t*>(a.dx)[row * H + j] = narrow(v);
+      });
+    }
   }
   if (a.part == nullptr) return;
   float* out = a.part + (int64_t)blockIdx.x * 2 * H;

@@ -404,8 +404,10 @@ int lmhead_logps_distill_bwd(const uint16_t* hidden, const uint16_t* W, const in
  * dbias are summed in an order that N and H fix. An element of dy that is 0
  * contributes 0 whatever x, the statistics and the weight hold there, so a
  * masked token (dy row 0) gets dx = 0 and adds nothing even where its x is
- * NaN. The backward's workspace (lmhead_logps_norm_workspace_bytes; needed
- * only where dweight or dbias is wanted) holds the partial sums.
+ * NaN. Everything else follows IEEE evaluation: a NaN or an infinity in dy
+ * reaches dx and dweight also where xh or the weight is 0. The backward's
+ * workspace (lmhead_logps_norm_workspace_bytes; needed only where dweight or
+ * dbias is wanted) holds the partial sums.
  * N = 0: the forward does nothing, the backward writes dweight = dbias = 0
  * (unless adding). Errors: LMH_ERR_NULL, LMH_ERR_SHAPE (N < 0, H < 1),
  * LMH_ERR_ARGS (unknown kind, type or flag; float32 y from bf16 x; eps < 0 or
