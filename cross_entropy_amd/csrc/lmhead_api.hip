@@ -825,7 +825,8 @@ DistillPlan plan_distill(int64_t N, int64_t H, int64_t V, int64_t K, int64_t chu
     d.off_hi = d.off_part;
     d.off_lo = d.off_hi + room(V * few_padded(n) * 2);
     d.off_part = d.off_lo + (n <= 64 ? room(V * few_padded(n) * 2) : 0);
-    // two workgroups a CU, of at least 128 vocabulary rows each
+    // two workgroups a CU (three of up to 32 tokens), of at least 128 vocabulary rows
+    // each; one split where the strips of a long row alone are more
     d.dh_strips = (int)lmh::ceil_div(H, 256);
     const int64_t wgs = (n <= 32 ? 3 : 2) * lmh::kNumCUs / (d.dh_strips * lmh::ceil_div(n, 64));
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(wgs, lmh::ceil_div(V, 128)));

@@ -354,9 +354,11 @@ int lmhead_logps_fwd_noalloc(const uint16_t* hidden, const uint16_t* W, const in
  * cotangent block as there, but blocks of up to 2^25 entries, 134 MB, are always
  * taken), 8 N + 8 N (K + 1) bytes of the tokens' special
  * entries and, where a block's gradients are summed in splits, at most 64
- * float32 partials of its dh and 16 of its dW. A call of few tokens (64; 128 of at most 24576 ids, 192 of
- * 16384, 256 of 12288) whose whole cotangent the block allows holds that instead, as two bf16 words up to
- * 64 tokens, and at most 50 MB of float32 partials of dh. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
+ * float32 partials of its dh and 16 of its dW. A call of few tokens (64; 128 of
+ * at most 24576 ids, 192 of 16384, 256 of 12288) whose whole cotangent the block
+ * allows holds that instead, as two bf16 words up to 64 tokens, and float32
+ * partials of dh: at most 32 MiB of them, or one of 4 N H bytes where that is
+ * more. lmhead_logps_distill_workspace_bytes sizes it: with_backward is
  * LMH_WS_FWD, LMH_WS_BWD or LMH_WS_BWD_BF16. A smaller size than the query
  * gives is refused. Results do not depend on anything but the arguments:
  * no atomics take part in sums.
