@@ -88,3 +88,42 @@ def test_scores_of_a_small_temperature(N, V):
     log(f"[distill] T=2^-28 N={N} V={V}")
     args = _case(70 + N + V, N, 64, V, K, T, hard=True, pad=0.0, lean=False)
     _forward_check(args, _put(*args), T, 64, f"T=2^-28 N={N} V={V}")
+
+
+def test_front_end_gradients_in_a_captured_step():
+    """lmhead_distill with norm=, forward and backward, captured with no eager
+    graph of its leaves alive: every replay gives the eager gradients."""
+    import torch
+    import cross_entropy_amd as lm
+    for N, V in ((40, 700), (300, 900)):
+        log(f"[distill] captured front end N={N} V={V}")
+        h, W, targets, ids, t, _ = _case(80, N, 128, V, 6, hard=True)
+        hd, Wd, tg, idd, td, _ = _put(h, W, targets, ids, t, None)
+        x, Wb = hd.view(torch.bfloat16).float(), Wd.view(torch.bfloat16)
+        w = torch.linspace(0.5, 1.5, 128, device="cuda")
+
+        def step(leaves):
+            kl, logp = lm.lmhead_distill(leaves[0], leaves[1], idd, td, 64, tg, norm=lm.Norm(leaves[2], kind="rms"))
+            return torch.autograd.grad(kl.sum() - 0.5 * logp.sum(), leaves)
+
+        fresh = lambda: [a.clone().requires_grad_() for a in (x, Wb, w)]   # noqa: E731
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(fresh())
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        leaves = fresh()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(leaves)
+        for i in range(3):
+            with torch.no_grad():
+                leaves[0].mul_(1.2)
+            for g in got:
+                g.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            want = step([a.detach().clone().requires_grad_() for a in leaves])
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), i
