@@ -17,7 +17,8 @@
 //
 // Up to 64 tokens the cotangent is held as two bf16 words (its rounding and
 // what that left): its products then cost twice the matrix instructions, which
-// are idle there, and carry 16 bits instead of 8.
+// are idle there, and carry 16 bits instead of 8. Above, it is one word, as the
+// tiles' (a second would double what the gradients' kernels read of it).
 //
 // Measured with H = 2560, V = 151936 (778 MB of W; a copy reaches 5.0 TB/s): the
 // forward's pass 143 us for one token and 147 us for 64 (5.4 TB/s); in the backward
@@ -607,6 +608,8 @@ __global__ __launch_bounds__(256, 2) void few_grads_kernel(const FewArgs a) {
 // Row blocks (of 16) per wave: as few as let two workgroups a CU cover the
 // vocabulary at once, so that no CU is left a second round (V = 151936: 475
 // workgroups of 5 blocks a wave take 143 us for one token, 594 of 4 take 162).
+// Above V = 163840 a second round starts: the whole forward of one token takes
+// 217 us at 200003 and 283 at 262144, where W at the copy's rate takes 205 and 268.
 constexpr int kMostBlocks = 5;
 int few_blocks(int64_t V) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kMostBlocks, (V + 128 * kNumCUs - 1) / (128 * kNumCUs)));

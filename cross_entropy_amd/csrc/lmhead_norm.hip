@@ -12,8 +12,8 @@
 // arithmetic is float32; bf16 outputs are rounded once, when stored.
 //
 // Measured (bf16, layer norm; a copy of 2 GB reaches 5.0 TB/s): 65536 x 2560
-// forward 137 us (4.9 TB/s), backward 186 us (5.4 TB/s, 5 us of it the sums of the
-// partial rows); 65536 x 256 12.5 and 24 us; one row 2.8 us forward.
+// forward 137 us (4.9 TB/s), backward 189 us (5.3 TB/s) and 5 us for the sums of
+// the partial rows; 65536 x 256 12.5 and 24 us; one row 2.7 us forward.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -356,7 +356,9 @@ __global__ __launch_bounds__(LANES == kHuge ? 1024 : 512) void norm_bwd_kernel(c
     return;
   }
   // 1024 threads have 128 registers each, which the sums would overflow: there
-  // they live in LDS, each thread's at its own columns
+  // they live in LDS, each thread's at its own columns. Float32 rows still spill one
+  // to four registers, outside the loop over rows: 4096 x 16384 take 168 us with float32
+  // dy (4.8 TB/s), 148 with bf16 (4.5); bf16 rows 92 (4.4)
   constexpr bool kept = LANES == kHuge;
   __shared__ __attribute__((aligned(16))) float sums[2][kept ? kNormMaxH : 4];
   __shared__ float s[2][kMaxWaves][2];
