@@ -25,9 +25,14 @@ Entry points mirror the C ABI:
                          logits, and the log-prob of a hard target beside it)
     lmhead_logps_norm_fwd / lmhead_logps_norm_bwd  (the layer or RMS norm in
                          front of the head)
-with allocating helpers for the last two pairs (``distill_forward``,
-``distill_backward``, ``norm_forward``, ``norm_backward``) and autograd front
-ends (``lmhead_distill``, ``lmhead_norm``);
+    lmhead_logps_embed_fwd / lmhead_logps_embed_bwd  (the vocabulary table as an
+                         embedding, and its gradient from sorted tokens)
+    lmhead_logps_beam_step / lmhead_logps_beam_reorder  (beam search's step over
+                         the head's never-held logits, and its states' reordering)
+with allocating helpers for the last four pairs (``distill_forward``,
+``distill_backward``, ``norm_forward``, ``norm_backward``, ``embed_forward``,
+``embed_backward``, ``beam_step``, ``beam_reorder``) and autograd front ends
+(``lmhead_distill``, ``lmhead_norm``, ``lmhead_embed``);
 two allocating helpers for the head, ``forward`` and ``backward`` (``temperature=``
 selects the tempered calls, ``dh=`` / ``dW=`` with ``accumulate=`` add into
 caller buffers), and ``lmhead_logps``, a ``torch.autograd.Function`` front
@@ -37,6 +42,7 @@ norm too (``norm=Norm(...)``: hidden is then the stream in front of it).
 from __future__ import annotations
 
 import contextlib
+import math
 from typing import Any, NamedTuple, Optional, Tuple
 
 from . import _native
@@ -61,9 +67,16 @@ __all__ = [
     "lmhead_logps_norm_workspace_bytes",
     "lmhead_logps_norm_fwd",
     "lmhead_logps_norm_bwd",
+    "lmhead_logps_embed_workspace_bytes",
+    "lmhead_logps_embed_fwd",
+    "lmhead_logps_embed_bwd",
+    "lmhead_logps_beam_workspace_bytes",
+    "lmhead_logps_beam_step",
+    "lmhead_logps_beam_reorder",
     "lmhead_logps",
     "lmhead_distill",
     "lmhead_norm",
+    "lmhead_embed",
     "Norm",
     "forward",
     "backward",
@@ -71,9 +84,15 @@ __all__ = [
     "distill_backward",
     "norm_forward",
     "norm_backward",
+    "embed_forward",
+    "embed_backward",
+    "beam_step",
+    "beam_reorder",
     "workspace_for",
     "distill_workspace_for",
     "norm_workspace_for",
+    "embed_workspace_for",
+    "beam_workspace_for",
     "version",
 ]
 
@@ -679,6 +698,205 @@ def norm_backward(x, weight, mean, rstd, dy, kind: str = "layer", with_weight: b
     return dx, dweight, dbias
 
 
+def lmhead_logps_embed_workspace_bytes(N: int, H: int, V: int) -> int:
+    """Workspace bytes of the embedding's backward."""
+    return _native.raw_embed_workspace_bytes(N, H, V)
+
+
+_I32_TYPES = ()
+
+
+def _i32_types():
+    global _I32_TYPES
+    if not _I32_TYPES:
+        _I32_TYPES = (_torch().int32,)
+    return _I32_TYPES
+
+
+def _embed_shape(ids, W, y, name):
+    if W.dim() != 2:
+        raise ValueError(f"the table must be [V, H], got {tuple(W.shape)}")
+    V, H = W.shape
+    if y.shape != (*ids.shape, H):
+        raise ValueError(f"{name} has shape {tuple(y.shape)}, expected {(*ids.shape, H)}")
+    return ids.numel(), H, V
+
+
+def lmhead_logps_embed_fwd(W, ids, scale: float, y, stream=None) -> None:
+    """Enqueue the embedding lookup: y [..., H] = scale * W[ids], W [V, H] and
+    y float32 or bfloat16 (in any combination), ids int32 [...]. Ids outside
+    [0, V) give zeros."""
+    any_ = _any_types()
+    N, H, V = _embed_shape(ids, W, y, "y")
+    dev = W.device
+    _enqueue(
+        dev, _native.raw_embed_fwd, _ptr(W, "W", any_, dev), any_[W.dtype], _ptr(ids, "ids", _i32_types(), dev), N, H, V,
+        scale, _ptr(y, "y", any_, dev), any_[y.dtype], _stream(dev, stream))
+
+
+def lmhead_logps_embed_bwd(ids, dy, scale: float, dW, flags: int, workspace, stream=None) -> None:
+    """Enqueue the embedding's backward into dW [V, H] (float32 or bfloat16):
+    ``flags`` 0 writes all of it, ``_native.BWD_ACCUMULATE_DW`` adds into it
+    and touches only the rows of words that occur (a tied table, whose head's
+    backward wrote dW before). dy is [..., H]; the workspace is that of
+    ``embed_workspace_for``."""
+    any_ = _any_types()
+    N, H, V = _embed_shape(ids, dW, dy, "dy")
+    dev = dW.device
+    _enqueue(
+        dev, _native.raw_embed_bwd, _ptr(ids, "ids", _i32_types(), dev), _ptr(dy, "dy", any_, dev), any_[dy.dtype], N, H, V,
+        scale, _ptr(dW, "dW", any_, dev), any_[dW.dtype], flags, _ptr(workspace, "workspace", (_torch().uint8,), dev),
+        workspace.numel(), _stream(dev, stream))
+
+
+def embed_workspace_for(ids, W):
+    """Allocate a workspace for the embedding's backward (W: the table or its
+    gradient)."""
+    torch = _torch()
+    V, H = W.shape
+    return torch.empty(lmhead_logps_embed_workspace_bytes(ids.numel(), H, V), dtype=torch.uint8, device=W.device)
+
+
+def embed_forward(W, ids, scale: float = 1.0, out_dtype=None, stream=None):
+    """Allocate y [..., H] (in ``out_dtype``, default W's) and run the lookup."""
+    torch = _torch()
+    with _allocating(W.device, stream):
+        y = torch.empty((*ids.shape, W.shape[1]), dtype=W.dtype if out_dtype is None else out_dtype, device=W.device)
+    lmhead_logps_embed_fwd(W, ids, scale, y, stream)
+    return y
+
+
+def embed_backward(ids, dy, vocab: Optional[int] = None, scale: float = 1.0, workspace=None, stream=None, dW=None,
+                   accumulate: bool = False, grad_dtype=None):
+    """Run the embedding's backward: dW [vocab, H], allocated in
+    ``grad_dtype`` (default float32) unless given; with ``accumulate`` the
+    given buffer is added into."""
+    torch = _torch()
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dW buffer")
+        if vocab is None:
+            raise ValueError("vocab (the table's rows) or dW is needed")
+    with _allocating(dy.device, stream):
+        if dW is None:
+            dW = torch.empty((vocab, dy.shape[-1]), dtype=torch.float32 if grad_dtype is None else grad_dtype,
+                             device=dy.device)
+        if workspace is None:
+            workspace = embed_workspace_for(ids, dW)
+    lmhead_logps_embed_bwd(ids, dy, scale, dW, _native.BWD_ACCUMULATE_DW if accumulate else 0, workspace, stream)
+    return dW
+
+
+def lmhead_logps_beam_workspace_bytes(N: int, H: int, V: int, beams: int, candidates: int) -> int:
+    """Workspace bytes of a beam step."""
+    return _native.raw_beam_workspace_bytes(N, H, V, beams, candidates)
+
+
+def lmhead_logps_beam_step(hidden, W, scores, ended, allowed, beams: int, temperature: float, top_scores, top_ids,
+                           top_parents, lse, workspace, stream=None) -> None:
+    """Enqueue one step of beam search over the rows of hidden [N, H], in
+    groups of ``beams`` rows: the best candidates' scores (float32), words and
+    parent rows (int32), each [N / beams, candidates], and lse [N]. ``scores``
+    is float32 [N]; ``ended`` (int32 [N]: a row with an id in [0, V) has that
+    id, at its unchanged score, as its only candidate) and ``allowed`` (int32
+    [N, ceil(V / 32)]: the bits of the words that a row may take) may be None."""
+    f32, i32 = _f32_types(), _i32_types()
+    if hidden.dim() != 2 or W.dim() != 2 or hidden.shape[1] != W.shape[1]:
+        raise ValueError(f"hidden [N,H] and W [V,H] must share H: {tuple(hidden.shape)} vs {tuple(W.shape)}")
+    N, H = hidden.shape
+    V = W.shape[0]
+    if top_scores.dim() != 2 or beams < 1 or top_scores.shape[0] * beams != N:
+        raise ValueError(f"top_scores must be [N / beams, candidates] with N = {N} and beams = {beams}, got "
+                         f"{tuple(top_scores.shape)}")
+    groups, C = top_scores.shape
+    dev = hidden.device
+    _enqueue(
+        dev, _native.raw_beam_step, _ptr(hidden, "hidden", _bf16_types(), dev), _ptr(W, "W", _bf16_types(), dev),
+        _ptr(scores, "scores", f32, dev, N), _ptr(ended, "ended", i32, dev, N, True),
+        _ptr(allowed, "allowed", i32, dev, N * ((V + 31) // 32), True), N, H, V, beams, C, temperature,
+        _ptr(top_scores, "top_scores", f32, dev), _ptr(top_ids, "top_ids", i32, dev, groups * C),
+        _ptr(top_parents, "top_parents", i32, dev, groups * C), _ptr(lse, "lse", f32, dev, N),
+        _ptr(workspace, "workspace", (_torch().uint8,), dev), workspace.numel(), _stream(dev, stream))
+
+
+def beam_workspace_for(hidden, W, beams: int, candidates: int):
+    """Allocate a workspace for beam steps of this shape."""
+    torch = _torch()
+    nbytes = lmhead_logps_beam_workspace_bytes(hidden.shape[0], hidden.shape[1], W.shape[0], beams, candidates)
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=hidden.device)
+
+
+def beam_step(hidden, W, scores, beams: int, candidates: Optional[int] = None, ended=None, allowed=None,
+              temperature: float = 1.0, norm: Optional["Norm"] = None, workspace=None, stream=None) -> Tuple:
+    """Allocate outputs and run one step of beam search: (top_scores, top_ids,
+    top_parents, lse), the first three [N / beams, candidates]. ``candidates``
+    defaults to 2 * beams, which holds ``beams`` that have not just ended. With
+    ``norm``, hidden is the stream in front of the final norm (bfloat16 or
+    float32)."""
+    torch = _torch()
+    N, dev = hidden.shape[0], hidden.device
+    if candidates is None:
+        candidates = 2 * beams
+    if beams < 1 or N % beams:
+        raise ValueError(f"hidden has {N} rows, which are no groups of {beams} beams")
+    if norm is not None:
+        hidden, _, _ = norm_forward(hidden, norm.weight, norm.bias, norm.eps, norm.kind, torch.bfloat16, stream)
+    with _allocating(dev, stream):
+        top_scores = torch.empty((N // beams, candidates), dtype=torch.float32, device=dev)
+        top_ids, top_parents = (torch.empty((N // beams, candidates), dtype=torch.int32, device=dev) for _ in range(2))
+        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = beam_workspace_for(hidden, W, beams, candidates)
+    lmhead_logps_beam_step(hidden, W, scores, ended, allowed, beams, temperature, top_scores, top_ids, top_parents, lse,
+                           workspace, stream)
+    return top_scores, top_ids, top_parents, lse
+
+
+def lmhead_logps_beam_reorder(states, parents, beams: int, out, lengths=None, row_dim: int = 0,
+                              length_dim: Optional[int] = None, stream=None) -> None:
+    """Enqueue the reordering of beams' states, of any dtype, whose dimension
+    ``row_dim`` holds the N rows: row j of ``out`` (``states`` itself, or a
+    tensor like it) takes over row parents[j] (int32 [N]; one outside j's group
+    of ``beams`` rows leaves row j as it is). With ``lengths`` (int32 [N], by
+    row of states) only the first lengths[parents[j]] steps of dimension
+    ``length_dim`` (default: the one after ``row_dim``) are, and the rest of out
+    stays."""
+    dims = states.dim()
+    if dims == 0 or not -dims <= row_dim < dims:
+        raise ValueError(f"row_dim {row_dim} is no dimension of states {tuple(states.shape)}")
+    row_dim %= dims
+    shape = states.shape
+    if out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    if out.dtype != states.dtype:
+        raise TypeError(f"out must have states' dtype {states.dtype}, got {out.dtype}")
+    if lengths is None:
+        if length_dim is not None:
+            raise ValueError("length_dim is given without lengths")
+        runs = steps = 1
+        step_bytes = math.prod(shape[row_dim + 1:]) * states.element_size()
+    else:
+        length_dim = row_dim + 1 if length_dim is None else length_dim + dims if length_dim < 0 else length_dim
+        if not row_dim < length_dim < dims:
+            raise ValueError(f"lengths need a dimension of states {tuple(shape)} after row_dim {row_dim}, got {length_dim}")
+        runs, steps = math.prod(shape[row_dim + 1:length_dim]), shape[length_dim]
+        step_bytes = math.prod(shape[length_dim + 1:]) * states.element_size()
+    N, dev, types, i32 = shape[row_dim], states.device, (states.dtype,), _i32_types()
+    _enqueue(
+        dev, _native.raw_beam_reorder, _ptr(states, "states", types, dev), _ptr(out, "out", types, dev),
+        _ptr(parents, "parents", i32, dev, N), _ptr(lengths, "lengths", i32, dev, N, True), math.prod(shape[:row_dim]), N,
+        beams, runs, steps, step_bytes, _stream(dev, stream))
+
+
+def beam_reorder(states, parents, beams: int, out=None, lengths=None, row_dim: int = 0,
+                 length_dim: Optional[int] = None, stream=None):
+    """Reorder beams' states in place, or into ``out``; returns the reordered
+    tensor."""
+    out = states if out is None else out
+    lmhead_logps_beam_reorder(states, parents, beams, out, lengths, row_dim, length_dim, stream)
+    return out
+
+
 _ONCE_FN = None
 
 
@@ -699,7 +917,7 @@ def _once(*grads):
 
             @staticmethod
             def backward(ctx, g):
-                raise RuntimeError("the gradients of lmhead_logps, lmhead_distill and lmhead_norm take no second backward")
+                raise RuntimeError("the gradients of lmhead_logps, lmhead_distill, lmhead_norm and lmhead_embed take no second backward")
 
         _ONCE_FN = _Once
     joined = torch.empty(0, requires_grad=True)
@@ -806,9 +1024,48 @@ def _norm_function():
     return _LmheadNorm
 
 
+def _embed_function():
+    torch = _torch()
+
+    class _LmheadEmbed(torch.autograd.Function):
+        """The embedding lookup with its backward through the library; keeps
+        the ids."""
+
+        @staticmethod
+        def forward(ctx, W, ids, scale, out_dtype):
+            ctx.scale, ctx.vocab, ctx.dtype = scale, W.shape[0], W.dtype
+            ctx.save_for_backward(ids)
+            return embed_forward(W, ids, scale, out_dtype)
+
+        @staticmethod
+        def backward(ctx, dy):
+            ids, = ctx.saved_tensors
+            dW = None
+            if ctx.needs_input_grad[0]:
+                dW = embed_backward(ids, dy.detach().contiguous(), ctx.vocab, ctx.scale, grad_dtype=ctx.dtype)
+            return _once(dW, None, None, None)
+
+    return _LmheadEmbed
+
+
 _FN = None
 _DISTILL_FN = None
 _NORM_FN = None
+_EMBED_FN = None
+
+
+def lmhead_embed(W, ids, scale: float = 1.0, out_dtype=None):
+    """Differentiable embedding lookup: ``scale * W[ids]`` [..., H] in
+    ``out_dtype`` (default W's; float32 for a float32 stream), for W [V, H]
+    float32 or bfloat16 and ids int32 [...] of any shape; ids outside [0, V) give
+    zeros and no gradient. W's gradient comes whole, in W's dtype (a trainer that
+    keeps a tied table's gradient in a buffer of its own adds to the rows that
+    occur alone with ``embed_backward(..., dW=buffer, accumulate=True)``). A
+    second backward, through the gradients, is refused."""
+    global _EMBED_FN
+    if _EMBED_FN is None:
+        _EMBED_FN = _embed_function()
+    return _EMBED_FN.apply(W, ids, scale, out_dtype)
 
 
 def lmhead_norm(x, weight=None, bias=None, eps: float = 1e-6, kind: str = "layer", out_dtype=None):

@@ -42,6 +42,12 @@ EXPORTED = (
     "lmhead_logps_norm_workspace_bytes",
     "lmhead_logps_norm_fwd",
     "lmhead_logps_norm_bwd",
+    "lmhead_logps_embed_workspace_bytes",
+    "lmhead_logps_embed_fwd",
+    "lmhead_logps_embed_bwd",
+    "lmhead_logps_beam_workspace_bytes",
+    "lmhead_logps_beam_step",
+    "lmhead_logps_beam_reorder",
     "lmhead_logps_last_error",
     "lmhead_logps_version",
     "lmhead_logps_trace_enable",
@@ -130,6 +136,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.lmhead_logps_norm_bwd.argtypes = [p, i32, p, i32, i64, i64, i32, p, p, p, i32, p, p, p, i32, ctypes.c_uint, p,
                                           sz, p]
     lib.lmhead_logps_norm_bwd.restype = ctypes.c_int
+    lib.lmhead_logps_embed_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+    lib.lmhead_logps_embed_workspace_bytes.restype = ctypes.c_int
+    lib.lmhead_logps_embed_fwd.argtypes = [p, i32, p, i64, i64, i64, f32, p, i32, p]
+    lib.lmhead_logps_embed_fwd.restype = ctypes.c_int
+    lib.lmhead_logps_embed_bwd.argtypes = [p, p, i32, i64, i64, i64, f32, p, i32, ctypes.c_uint, p, sz, p]
+    lib.lmhead_logps_embed_bwd.restype = ctypes.c_int
+    lib.lmhead_logps_beam_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+    lib.lmhead_logps_beam_workspace_bytes.restype = ctypes.c_int
+    lib.lmhead_logps_beam_step.argtypes = [p, p, p, p, p, i64, i64, i64, i64, i64, f32, p, p, p, p, p, sz, p]
+    lib.lmhead_logps_beam_step.restype = ctypes.c_int
+    lib.lmhead_logps_beam_reorder.argtypes = [p, p, p, p, i64, i64, i64, i64, i64, i64, p]
+    lib.lmhead_logps_beam_reorder.restype = ctypes.c_int
     lib.lmhead_logps_last_error.argtypes = []
     lib.lmhead_logps_last_error.restype = ctypes.c_char_p
     lib.lmhead_logps_version.argtypes = []
@@ -313,10 +331,58 @@ def raw_norm_bwd(x, x_type, weight, w_type, N, H, kind, mean, rstd, dy, y_type, 
                                         int(workspace_bytes), stream or None)
 
 
+def raw_embed_workspace_bytes(N: int, H: int, V: int) -> int:
+    out = ctypes.c_size_t(0)
+    check(load().lmhead_logps_embed_workspace_bytes(int(N), int(H), int(V), ctypes.byref(out)))
+    return int(out.value)
+
+
+def raw_embed_fwd(W, w_type, ids, N, H, V, scale, y, y_type, stream) -> int:
+    """Call lmhead_logps_embed_fwd with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_embed_fwd(W or None, int(w_type), ids or None, int(N), int(H), int(V), float(scale),
+                                         y or None, int(y_type), stream or None)
+
+
+def raw_embed_bwd(ids, dy, y_type, N, H, V, scale, dW, g_type, flags, workspace, workspace_bytes, stream) -> int:
+    """Call lmhead_logps_embed_bwd with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_embed_bwd(ids or None, dy or None, int(y_type), int(N), int(H), int(V), float(scale),
+                                         dW or None, int(g_type), int(flags), workspace or None, int(workspace_bytes),
+                                         stream or None)
+
+
+BEAM_MAX_BEAMS = 64
+BEAM_MAX_CANDIDATES = 64
+
+
+def raw_beam_workspace_bytes(N: int, H: int, V: int, beams: int, candidates: int) -> int:
+    out = ctypes.c_size_t(0)
+    check(load().lmhead_logps_beam_workspace_bytes(int(N), int(H), int(V), int(beams), int(candidates),
+                                                   ctypes.byref(out)))
+    return int(out.value)
+
+
+def raw_beam_step(hidden, W, scores, ended, allowed, N, H, V, beams, candidates, temperature, top_scores, top_ids,
+                  top_parents, lse, workspace, workspace_bytes, stream) -> int:
+    """Call lmhead_logps_beam_step with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_beam_step(hidden or None, W or None, scores or None, ended or None, allowed or None,
+                                         int(N), int(H), int(V), int(beams), int(candidates), float(temperature),
+                                         top_scores or None, top_ids or None, top_parents or None, lse or None,
+                                         workspace or None, int(workspace_bytes), stream or None)
+
+
+def raw_beam_reorder(states, out, parents, lengths, planes, rows, beams, runs, steps, step_bytes, stream) -> int:
+    """Call lmhead_logps_beam_reorder with integer addresses (0 = NULL); returns the status."""
+    return load().lmhead_logps_beam_reorder(states or None, out or None, parents or None, lengths or None, int(planes),
+                                            int(rows), int(beams), int(runs), int(steps), int(step_bytes),
+                                            stream or None)
+
+
 TRACE_KERNELS = ("fwd_stats_kernel", "fwd_merge_kernel", "bwd_step_kernel", "transpose_kernel",
                  "fill_zero_kernel", "pad_rows_kernel", "bwd_step_bf16_kernel", "distill_top_kernel",
                  "distill_prep_kernel", "distill_step_kernel", "distill_post_kernel", "few_stats_kernel",
-                 "few_dz_kernel", "few_grads_kernel", "norm_fwd_kernel", "norm_bwd_kernel", "norm_reduce_kernel")
+                 "few_dz_kernel", "few_grads_kernel", "norm_fwd_kernel", "norm_bwd_kernel", "norm_reduce_kernel",
+                 "embed_fwd_kernel", "embed_sort_kernel", "embed_rows_kernel", "embed_join_kernel",
+                 "beam_logits_kernel", "beam_select_kernel", "beam_score_kernel", "beam_reorder_kernel")
 
 
 def trace_enable(on: bool) -> None:

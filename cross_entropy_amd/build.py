@@ -27,8 +27,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_NAME = "liblmhead_logps.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["lmhead_api.hip", "lmhead_kernels.hip", "lmhead_distill.hip", "lmhead_few.hip", "lmhead_norm.hip", "lmhead_trace.hip"]
-HEADERS = ["lmhead_internal.h", "lmhead_tile.h", os.path.join("..", "..", "include", "lmhead_logps.h")]
+SOURCES = ["lmhead_api.hip", "lmhead_kernels.hip", "lmhead_distill.hip", "lmhead_few.hip", "lmhead_norm.hip",
+           "lmhead_embed.hip", "lmhead_beam.hip", "lmhead_trace.hip"]
+HEADERS = ["lmhead_internal.h", "lmhead_tile.h", "lmhead_few.h", os.path.join("..", "..", "include", "lmhead_logps.h")]
 
 # Packed-fp32 VALU ops are kept out of the generated code on purpose.
 HIP_FLAGS = [

@@ -1137,3 +1137,281 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The vocabulary table as an embedding.
+namespace {
+
+static_assert(lmh::kMostBeams == LMH_BEAM_MAX_BEAMS && lmh::kMostCandidates == LMH_BEAM_MAX_CANDIDATES, "limits in the header");
+
+int check_embed(const char* who, int64_t N, int64_t H, int64_t V) {
+  if (N < 0 || N >= (int64_t(1) << 31))
+    return fail(LMH_ERR_SHAPE, "%s: N must be in [0, 2^31), got %lld", who, (long long)N);
+  if (H <= 0 || H >= (int64_t(1) << 20))
+    return fail(LMH_ERR_SHAPE, "%s: H must be in (0, 2^20), got %lld", who, (long long)H);
+  if (V <= 0 || V >= (int64_t(1) << 31))
+    return fail(LMH_ERR_SHAPE, "%s: V must be in (0, 2^31), got %lld", who, (long long)V);
+  return LMH_OK;
+}
+
+// The gradient's sort: words in classes by their lowest bits, 256 (one
+// workgroup a CU) or as many as keep a class's counters within LDS.
+struct EmbedPlan {
+  int classes = lmh::kNumCUs, shift = 8, words = 0;
+  size_t off_order = 0, off_pieces = 0, off_longs = 0, off_touched = 0, off_part = 0, bytes = 0;
+};
+EmbedPlan plan_embed(int64_t N, int64_t H, int64_t V) {
+  EmbedPlan p;
+  while (lmh::ceil_div(V, p.classes) > lmh::kMostClassWords) p.classes *= 2, ++p.shift;
+  p.words = (int)lmh::ceil_div(V, p.classes);
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t here = at;
+    at += (size_t)lmh::round_up(bytes, 256);
+    return here;
+  };
+  take(12 * (int64_t)p.classes);
+  p.off_order = take(4 * N);
+  p.off_pieces = take(16 * N);
+  p.off_longs = take(16 * (N / lmh::kPiece + 1));
+  p.off_touched = take((int64_t)p.classes * p.words);
+  p.off_part = take(N > lmh::kPiece ? 2 * lmh::ceil_div(N, lmh::kPiece) * H * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lmhead_logps_embed_workspace_bytes(int64_t N, int64_t H, int64_t V, size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(LMH_ERR_NULL, "bytes_out is NULL");
+  int rc = check_embed("embed", N, H, V);
+  if (rc == LMH_OK) rc = check_backward_size(N, V);
+  if (rc != LMH_OK) return rc;
+  *bytes_out = plan_embed(N, H, V).bytes;
+  return ok();
+}
+
+int lmhead_logps_embed_fwd(const void* W, int w_type, const int32_t* ids, int64_t N, int64_t H, int64_t V, float scale,
+                           void* y, int y_type, void* stream) {
+  const int rc = check_embed("embed_fwd", N, H, V);
+  if (rc != LMH_OK) return rc;
+  if (!known_type(w_type) || !known_type(y_type))
+    return fail(LMH_ERR_ARGS, "embed_fwd: unknown type among W %d, y %d", w_type, y_type);
+  if (!std::isfinite(scale)) return fail(LMH_ERR_ARGS, "embed_fwd: scale must be finite, got %g", (double)scale);
+  if (N == 0) return ok();
+  if (!W || !ids || !y) return fail(LMH_ERR_NULL, "embed_fwd: W, ids and y must be non-NULL");
+  if (!aligned(W, type_size(w_type)) || !aligned(ids, 4) || !aligned(y, type_size(y_type)))
+    return fail(LMH_ERR_UNSUPPORTED, "embed_fwd: a pointer is not aligned to its elements");
+  const hipError_t e = lmh::launch_embed_fwd({W, ids, w_type == LMH_TYPE_F32, y_type == LMH_TYPE_F32, N, (int)H, (int)V,
+                                              scale, y}, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "embed_fwd: launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64_t N, int64_t H, int64_t V, float scale,
+                           void* dW, int g_type, unsigned flags, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_embed("embed_bwd", N, H, V);
+  if (rc == LMH_OK) rc = check_backward_size(N, V);
+  if (rc != LMH_OK) return rc;
+  if (!known_type(y_type) || !known_type(g_type))
+    return fail(LMH_ERR_ARGS, "embed_bwd: unknown type among dy %d, dW %d", y_type, g_type);
+  if (!std::isfinite(scale)) return fail(LMH_ERR_ARGS, "embed_bwd: scale must be finite, got %g", (double)scale);
+  if (flags & ~(unsigned)LMH_BWD_ACCUMULATE_DW) return fail(LMH_ERR_ARGS, "embed_bwd: unknown flags 0x%x", flags);
+  const bool add = (flags & LMH_BWD_ACCUMULATE_DW) != 0;
+  if (N == 0 && add) return ok();
+  if (!dW || !workspace || (N > 0 && (!ids || !dy)))
+    return fail(LMH_ERR_NULL, "embed_bwd: ids, dy, dW and workspace must be non-NULL");
+  if (!aligned(ids, 4) || !aligned(dy, type_size(y_type)) || !aligned(dW, type_size(g_type)) || !aligned(workspace, 16))
+    return fail(LMH_ERR_UNSUPPORTED, "embed_bwd: a pointer is not aligned to its elements (workspace: 16 bytes)");
+  const EmbedPlan p = plan_embed(N, H, V);
+  if (workspace_bytes < p.bytes)
+    return fail(LMH_ERR_WORKSPACE, "embed_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, p.bytes);
+  char* ws = static_cast<char*>(workspace);
+  lmh::EmbedBwdArgs a{};
+  a.ids = ids;
+  a.dy = dy;
+  a.y_f32 = y_type == LMH_TYPE_F32;
+  a.g_f32 = g_type == LMH_TYPE_F32;
+  a.add = add;
+  a.N = (int)N;
+  a.H = (int)H;
+  a.V = (int)V;
+  a.scale = scale;
+  a.dW = dW;
+  a.classes = p.classes;
+  a.class_shift = p.shift;
+  a.class_words = p.words;
+  a.counts = reinterpret_cast<int32_t*>(ws);
+  a.order = reinterpret_cast<int32_t*>(ws + p.off_order);
+  a.pieces = reinterpret_cast<int4*>(ws + p.off_pieces);
+  a.longs = reinterpret_cast<int4*>(ws + p.off_longs);
+  a.touched = reinterpret_cast<uint8_t*>(ws + p.off_touched);
+  a.part = reinterpret_cast<float*>(ws + p.off_part);
+  const hipError_t e = lmh::launch_embed_bwd(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "embed_bwd: launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Beam search on the head.
+namespace {
+
+int check_beam(int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidates) {
+  const int rc = check_shape(N, H, V, 1);
+  if (rc != LMH_OK) return rc;
+  if (beams < 1 || beams > LMH_BEAM_MAX_BEAMS)
+    return fail(LMH_ERR_SHAPE, "beams must be in [1, %d], got %lld", LMH_BEAM_MAX_BEAMS, (long long)beams);
+  if (N % beams != 0)
+    return fail(LMH_ERR_SHAPE, "N (%lld) must be a multiple of beams (%lld)", (long long)N, (long long)beams);
+  if (candidates < 1 || candidates > LMH_BEAM_MAX_CANDIDATES)
+    return fail(LMH_ERR_SHAPE, "candidates must be in [1, %d], got %lld", LMH_BEAM_MAX_CANDIDATES, (long long)candidates);
+  if (N >= (int64_t(1) << 23) || beams * V >= (int64_t(1) << 31))
+    return fail(LMH_ERR_UNSUPPORTED, "beam_step: N (%lld) must stay below 2^23 and beams * V (%lld) below 2^31",
+                (long long)N, (long long)(beams * V));
+  return LMH_OK;
+}
+
+struct BeamPlan {
+  bool few = false;
+  int splits = 0, n_tt = 0, n_vt = 0, per_section = 0;
+  int64_t n_sections = 0, n_blocks = 0, ld = 0;
+  size_t off_sections = 0, off_blocks = 0, off_lse = 0, off_chosen = 0, off_used = 0, off_ticket = 0, off_exact = 0, bytes = 0;
+};
+BeamPlan plan_beam(int64_t N, int64_t H, int64_t V, int64_t beams) {
+  BeamPlan p;
+  p.few = few_tokens(N, V);
+  if (p.few) {
+    p.splits = lmh::few_splits(V);
+    p.n_sections = p.splits;
+    p.per_section = lmh::few_rows(V) / 16;
+  } else {
+    const lmh::FwdPlan f = lmh::plan_forward(N, H, V);
+    p.splits = f.S;
+    p.n_tt = f.n_tt;
+    p.n_vt = f.n_vt;
+    p.n_sections = lmh::ceil_div(V, 128);
+    p.per_section = 8;
+  }
+  p.n_blocks = lmh::ceil_div(V, 16);
+  p.ld = lmh::round_up(std::max<int64_t>(N, 1), 64);
+  const int64_t groups = N / beams;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t here = at;
+    at += (size_t)lmh::round_up(bytes, 256);
+    return here;
+  };
+  take(8 * p.splits * p.ld);
+  p.off_sections = take(4 * p.n_sections * p.ld);
+  p.off_blocks = take(4 * p.n_blocks * p.ld);
+  p.off_lse = take(8 * N);
+  p.off_chosen = take(4 * lmh::kMostKept * groups);
+  p.off_used = take(4 * groups);
+  p.off_ticket = take(4 * groups);
+  p.off_exact = take(8 * 16 * lmh::kMostKept * groups);
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lmhead_logps_beam_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidates,
+                                      size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(LMH_ERR_NULL, "bytes_out is NULL");
+  const int rc = check_beam(N, H, V, beams, candidates);
+  if (rc != LMH_OK) return rc;
+  *bytes_out = plan_beam(N, H, V, beams).bytes;
+  return ok();
+}
+
+int lmhead_logps_beam_step(const uint16_t* hidden, const uint16_t* W, const float* scores, const int32_t* ended,
+                           const int32_t* allowed, int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidates,
+                           float temperature, float* top_scores, int32_t* top_ids, int32_t* top_parents, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_beam(N, H, V, beams, candidates);
+  if (rc == LMH_OK) rc = check_temperature(temperature);
+  if (rc != LMH_OK) return rc;
+  if (N == 0) return ok();
+  if (!hidden || !W || !scores || !top_scores || !top_ids || !top_parents || !lse || !workspace)
+    return fail(LMH_ERR_NULL, "beam_step: hidden, W, scores, top_scores, top_ids, top_parents, lse and workspace must be non-NULL");
+  if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(workspace, 16) || !aligned(scores, 4) || !aligned(ended, 4) ||
+      !aligned(allowed, 4) || !aligned(top_scores, 4) || !aligned(top_ids, 4) || !aligned(top_parents, 4) || !aligned(lse, 4))
+    return fail(LMH_ERR_UNSUPPORTED,
+                "beam_step: hidden, W and workspace need 16-byte alignment, the others that of their elements");
+  const BeamPlan p = plan_beam(N, H, V, beams);
+  if (workspace_bytes < p.bytes)
+    return fail(LMH_ERR_WORKSPACE, "beam_step: workspace of %zu bytes, %zu needed", workspace_bytes, p.bytes);
+  char* ws = static_cast<char*>(workspace);
+  lmh::BeamArgs b{};
+  b.hidden = hidden;
+  b.W = W;
+  b.scores = scores;
+  b.ended = ended;
+  b.allowed = allowed;
+  b.mask_ld = lmh::ceil_div(V, 32);
+  b.N = (int)N;
+  b.H = (int)H;
+  b.V = (int)V;
+  b.beams = (int)beams;
+  b.C = (int)candidates;
+  b.keep = (int)candidates + lmh::kSpare;
+  b.sc = temper_scale(temperature);
+  b.invT = inv_temperature(temperature);
+  b.T = (double)temperature;
+  b.back = 1.0 / ((double)b.sc * (double)temperature);
+  b.few = p.few;
+  b.splits = p.splits;
+  b.n_tt = p.n_tt;
+  b.n_vt = p.n_vt;
+  b.n_sections = p.n_sections;
+  b.n_blocks = p.n_blocks;
+  b.per_section = p.per_section;
+  b.ld = p.ld;
+  b.records = reinterpret_cast<float2*>(ws);
+  b.sections = reinterpret_cast<float*>(ws + p.off_sections);
+  b.blocks = reinterpret_cast<float*>(ws + p.off_blocks);
+  b.lse64 = reinterpret_cast<double*>(ws + p.off_lse);
+  b.chosen = reinterpret_cast<uint32_t*>(ws + p.off_chosen);
+  b.used = reinterpret_cast<int32_t*>(ws + p.off_used);
+  b.ticket = reinterpret_cast<int32_t*>(ws + p.off_ticket);
+  b.exact = reinterpret_cast<double*>(ws + p.off_exact);
+  b.top_scores = top_scores;
+  b.top_ids = top_ids;
+  b.top_parents = top_parents;
+  b.lse = lse;
+  const hipError_t e = lmh::launch_beam_step(b, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "beam_step: launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int lmhead_logps_beam_reorder(const void* states, void* out, const int32_t* parents, const int32_t* lengths,
+                              int64_t planes, int64_t rows, int64_t beams, int64_t runs, int64_t steps,
+                              int64_t step_bytes, void* stream) {
+  if (beams < 1 || beams > LMH_BEAM_MAX_BEAMS)
+    return fail(LMH_ERR_SHAPE, "beam_reorder: beams must be in [1, %d], got %lld", LMH_BEAM_MAX_BEAMS, (long long)beams);
+  if (planes < 0 || rows < 0 || runs < 0 || steps < 0 || step_bytes < 0 || rows % beams != 0)
+    return fail(LMH_ERR_SHAPE, "beam_reorder: planes, rows (a multiple of beams), runs, steps and step_bytes must be >= 0");
+  if (planes == 0 || rows == 0 || runs == 0 || steps == 0 || step_bytes == 0) return ok();
+  int64_t bytes = 1;
+  for (int64_t n : {planes, rows, runs, steps, step_bytes})
+    if (__builtin_mul_overflow(bytes, n, &bytes) || bytes >= (int64_t(1) << 43) || rows >= (int64_t(1) << 31))
+      return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: the states hold 2^43 bytes or more");
+  if (!states || !out || !parents) return fail(LMH_ERR_NULL, "beam_reorder: states, out and parents must be non-NULL");
+  if (!aligned(parents, 4) || !aligned(lengths, 4))
+    return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a pointer is not aligned to its elements");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(states), b = reinterpret_cast<uintptr_t>(out);
+  if (a != b && (a < b ? b - a : a - b) < (uintptr_t)bytes)
+    return fail(LMH_ERR_ARGS, "beam_reorder: out overlaps the states without being them");
+  const hipError_t e = lmh::launch_beam_reorder({states, out, parents, lengths, planes, rows, (int)beams, runs, steps,
+                                                 step_bytes, 0, 0, 0}, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(LMH_ERR_HIP, "beam_reorder: launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+}  // extern "C"

@@ -1,6 +1,6 @@
 // lmhead_internal.h -- launch descriptors shared by the C ABI (lmhead_api.hip)
 // and the kernels (lmhead_kernels.hip, lmhead_distill.hip, lmhead_few.hip,
-// lmhead_norm.hip).
+// lmhead_norm.hip, lmhead_embed.hip, lmhead_beam.hip).
 // Not part of the public interface.
 #pragma once
 
@@ -237,6 +237,7 @@ struct FewArgs {
   int dh_strips, dh_splits, dh_rows;
 };
 
+int few_rows(int64_t V);     // vocabulary rows of a split
 int few_splits(int64_t V);   // records per token of the forward
 hipError_t launch_few_stats(FewArgs a, hipStream_t stream);
 hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream);   // the cotangent, dW and the partials of dh
@@ -285,11 +286,89 @@ struct NormReduceArgs {
 int norm_bwd_blocks(int64_t N, int64_t H);   // workgroups (partial rows) of the norm's backward
 bool norm_by_columns(int64_t N);             // whether dw and db are summed in its launch
 
+// The vocabulary table as an embedding (lmhead_embed.hip).
+struct EmbedFwdArgs {
+  const void* W;
+  const int32_t* ids;
+  bool w_f32, y_f32;
+  int64_t N;
+  int H, V;
+  float scale;
+  void* y;
+};
+
+constexpr int kPiece = 64;             // most tokens of a word that one wave sums
+constexpr int kMostClasses = 4096;     // workgroups of the sort, a power of two of them
+constexpr int kMostClassWords = 2048;  // words of a class
+
+struct EmbedBwdArgs {
+  const int32_t* ids;
+  const void* dy;
+  bool y_f32, g_f32, add;
+  int N, H, V;
+  float scale;
+  void* dW;
+  int classes, class_shift, class_words;   // word v: class v % classes, place v >> class_shift in it
+  int32_t* counts;     // [classes][3]: pieces, tokens of lower classes, long words
+  int32_t* order;      // [N] tokens by word
+  int4* pieces;        // [N] (first place in order, tokens, word, partial row or -1), a class's from its first token on
+  int4* longs;         // [N / kPiece + 1] (first place, tokens, word, 0) of the words of several pieces
+  uint8_t* touched;    // [classes][class_words] whether the word has a token
+  float* part;         // [2 ceil(N / kPiece)][H] partial rows
+};
+
+// A step of beam search (lmhead_beam.hip).
+constexpr int kMostBeams = 64;
+constexpr int kMostCandidates = 64;
+constexpr int kSpare = 16;                          // blocks looked at beyond the candidates
+constexpr int kMostKept = kMostCandidates + kSpare;
+
+struct BeamArgs {
+  const uint16_t* hidden;
+  const uint16_t* W;
+  const float* scores;
+  const int32_t* ended;     // or NULL
+  const int32_t* allowed;   // [N][mask_ld] bits, or NULL
+  int64_t mask_ld;
+  int N, H, V, beams, C, keep;   // keep: C + kSpare
+  float sc, invT;           // log2(e) / T, 1 / T
+  double T, back;           // T; 1 / (sc T)
+  bool few;                 // the streaming kernels
+  int splits, n_tt, n_vt;   // records per row; the tiles
+  int64_t n_sections, n_blocks;
+  int per_section;          // blocks of 16 words
+  int64_t ld;               // rows of the arrays below, padded
+  float2* records;          // [splits][ld]
+  float* sections;          // [n_sections][ld] largest allowed logit
+  float* blocks;            // [n_blocks][ld]
+  double* lse64;            // [N]
+  uint32_t* chosen;         // [groups][kMostKept] row in the group * n_blocks + block
+  int32_t* used;            // [groups] how many of them
+  int32_t* ticket;          // [groups]
+  double* exact;            // [groups][kMostKept][16] logits
+  float* top_scores;
+  int32_t* top_ids;
+  int32_t* top_parents;
+  float* lse;
+};
+
+struct ReorderArgs {
+  const void* states;
+  void* out;
+  const int32_t* parents;
+  const int32_t* lengths;   // or NULL
+  int64_t planes, rows;
+  int beams;
+  int64_t runs, steps, step_bytes;
+  int64_t run_bytes, places, units;   // set by the launcher
+};
+
 // Kernel ids of the tracing facility (lmhead_trace.hip).
 enum KernelId {
   kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
   kDistillTop, kDistillPrep, kDistillStep, kDistillPost,
-  kFewStats, kFewDz, kFewGrads, kNormFwd, kNormBwd, kNormReduce, kNumKernels
+  kFewStats, kFewDz, kFewGrads, kNormFwd, kNormBwd, kNormReduce,
+  kEmbedFwd, kEmbedSort, kEmbedRows, kEmbedJoin, kBeamLogits, kBeamSelect, kBeamScore, kBeamReorder, kNumKernels
 };
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);
@@ -314,5 +393,9 @@ hipError_t launch_distill_post(const DistillPostArgs& a, hipStream_t stream);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t stream);
+hipError_t launch_embed_fwd(const EmbedFwdArgs& a, hipStream_t stream);
+hipError_t launch_embed_bwd(const EmbedBwdArgs& a, hipStream_t stream);
+hipError_t launch_beam_step(const BeamArgs& a, hipStream_t stream);
+hipError_t launch_beam_reorder(ReorderArgs a, hipStream_t stream);
 
 }  // namespace lmh

@@ -428,6 +428,99 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
                           void* dx, void* dweight, void* dbias, int g_type, unsigned flags,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The vocabulary table as an embedding:
+ *   y_i = scale W[id_i],    dW_v = scale sum over the tokens i with id_i = v of dy_i
+ *   W     [V,H] of w_type; y and dy [N,H] of y_type; dW [V,H] of g_type (each
+ *         LMH_TYPE_BF16 or LMH_TYPE_F32, in any combination)
+ *   ids   int32 [N]; an id outside [0, V) (padding, -1) gives a y row of 0 and
+ *         adds nothing to dW, whatever its dy row holds (NaN and inf included)
+ *   scale finite, applied in float32 (in the gradient, to the sums)
+ *   flags of the backward: 0 writes all of dW, rows without a token as 0;
+ *         LMH_BWD_ACCUMULATE_DW adds into it and leaves rows without a token
+ *         untouched: with tied tables, the gradient that the head's backward
+ *         wrote becomes the table's whole gradient
+ * H in [1, 2^20), odd sizes too; every pointer aligned to its elements (the
+ * workspace to 16 bytes). Sums are float32, taken over a word's tokens in the
+ * order of the tokens (in pieces of 64 whose sums are then added in order), so
+ * results depend on the arguments alone; bf16 gradients are rounded once, a
+ * previous bf16 value being widened first. N = 0: the forward does nothing, the
+ * backward writes dW = 0 (unless adding). Errors: LMH_ERR_NULL, LMH_ERR_SHAPE,
+ * LMH_ERR_ARGS (unknown type or flag; scale not finite), LMH_ERR_WORKSPACE,
+ * LMH_ERR_UNSUPPORTED (a misaligned pointer; in the backward and its size query
+ * N or V above 2^23 - 256), LMH_ERR_HIP. Outputs must not overlap inputs. Stream
+ * semantics as for every call here.
+ */
+int lmhead_logps_embed_workspace_bytes(int64_t N, int64_t H, int64_t V, size_t* bytes_out);   /* the backward's */
+int lmhead_logps_embed_fwd(const void* W, int w_type, const int32_t* ids, int64_t N, int64_t H, int64_t V,
+                           float scale, void* y, int y_type, void* stream);
+int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64_t N, int64_t H, int64_t V,
+                           float scale, void* dW, int g_type, unsigned flags,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One step of beam search on the head's never-held logits. The N rows are
+ * groups of `beams` neighbouring rows (a group is a request). A candidate of a
+ * group is one of its rows r and a word v, with the score
+ *   scores[r] + z_v - lse_r,    z = W hidden_r / T,  lse_r = log sum_v exp z_v,
+ * and the `candidates` best of each group come out, the best first; equal ones
+ * by the lowest row and then the lowest word.
+ *   hidden   bf16 [N,H], W bf16 [V,H], as for the head (16-byte aligned)
+ *   scores   f32 [N]  the beams' scores so far. A row whose score is not
+ *                     finite is given up: it has no candidates
+ *   ended    int32 [N] or NULL: a row with an id in [0, V) here has ended; its
+ *                     only candidate is that id at its unchanged score
+ *   allowed  int32 [N, ceil(V/32)] or NULL: bit v % 32 of word v / 32 says
+ *                     whether the row may take v (lse is that of the whole
+ *                     vocabulary all the same); an ended row's bits are not read
+ *                     for its candidate
+ *   temperature       as for the head
+ *   top_scores  f32   [N / beams, candidates]  out
+ *   top_ids     int32 [N / beams, candidates]  out: the words
+ *   top_parents int32 [N / beams, candidates]  out: the rows, in [0, N)
+ *                     Where a group has fewer candidates: -inf, -1, -1
+ *   lse      f32 [N]  out: of z; 0 for rows given up or ended, whose hidden row
+ *                     may hold anything
+ * A word of logit -inf is no candidate, and a row whose lse is not finite (a
+ * NaN or an infinity among its logits) has none. The order of candidates is that
+ * of 64-bit scores of logits summed in 64 bits, so it does not depend on the
+ * kernels' summation order; lse and the scores carry lse's float32 sums (about 1e-7
+ * of them: two candidates of different rows closer than that may change places).
+ * The choice looks at 16 blocks of 16 words more than there are candidates where
+ * float32 does not tell their largest logits apart; in a group with more near ties
+ * than that it may miss one.
+ * The workspace holds 4 N V / 16 bytes of the blocks' largest logits and smaller
+ * arrays; lmhead_logps_beam_workspace_bytes sizes it.
+ * Errors: those of the head's calls, plus LMH_ERR_SHAPE when beams is not in [1,
+ * LMH_BEAM_MAX_BEAMS], candidates not in [1, LMH_BEAM_MAX_CANDIDATES] or N not a
+ * multiple of beams, and LMH_ERR_UNSUPPORTED where N >= 2^23 or beams V >= 2^31.
+ *
+ * lmhead_logps_beam_reorder: the beams' states after the step. Rows of
+ * `states` [planes][rows][runs][steps][step_bytes] (bytes of any type) are
+ * taken over by the rows that have them as parent:
+ *   out[p][j][q][0 : n] = states[p][parents[j]][q][0 : n],
+ *   n = lengths[parents[j]] (at most steps), or steps without lengths
+ * The rest of out is left as it is: the steps from n on, and whole rows whose
+ * parent lies outside the row's own group of `beams` rows (-1 included). out may
+ * be `states` itself (the rows that stay are then neither read nor written) and
+ * must not overlap it else.
+ *   parents  int32 [rows];  lengths int32 [rows] or NULL (steps in use, by row of
+ *            states; below 0 as 0)
+ * Errors: LMH_ERR_SHAPE, LMH_ERR_NULL, LMH_ERR_ARGS (an overlap),
+ * LMH_ERR_UNSUPPORTED (2^43 bytes or more; a misaligned pointer), LMH_ERR_HIP.
+ */
+#define LMH_BEAM_MAX_BEAMS 64
+#define LMH_BEAM_MAX_CANDIDATES 64
+int lmhead_logps_beam_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidates,
+                                      size_t* bytes_out);
+int lmhead_logps_beam_step(const uint16_t* hidden, const uint16_t* W, const float* scores, const int32_t* ended,
+                           const int32_t* allowed, int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidates,
+                           float temperature, float* top_scores, int32_t* top_ids, int32_t* top_parents, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+int lmhead_logps_beam_reorder(const void* states, void* out, const int32_t* parents, const int32_t* lengths,
+                              int64_t planes, int64_t rows, int64_t beams, int64_t runs, int64_t steps,
+                              int64_t step_bytes, void* stream);
+
 /* Thread-local message of the calling thread's last failing call ("" if none). */
 const char* lmhead_logps_last_error(void);
 
@@ -456,6 +549,14 @@ const char* lmhead_logps_version(void);
  *  14 norm_fwd_kernel
  *  15 norm_bwd_kernel
  *  16 norm_reduce_kernel   (dweight and dbias from their partial sums)
+ *  17 embed_fwd_kernel
+ *  18 embed_sort_kernel    (embedding backward: tokens by word)
+ *  19 embed_rows_kernel    (its sums, and the rows without a token)
+ *  20 embed_join_kernel    (its words of many tokens)
+ *  21 beam_logits_kernel   (beam step: log-sum-exps and blocks' largest logits)
+ *  22 beam_select_kernel   (the blocks that hold the best candidates)
+ *  23 beam_score_kernel    (their logits in 64 bits, the candidates)
+ *  24 beam_reorder_kernel
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch
