@@ -1279,7 +1279,7 @@ struct BeamPlan {
   bool few = false;
   int splits = 0, n_tt = 0, n_vt = 0, per_section = 0;
   int64_t n_sections = 0, n_blocks = 0, ld = 0;
-  size_t off_sections = 0, off_blocks = 0, off_lse = 0, off_chosen = 0, off_used = 0, off_ticket = 0, off_exact = 0, bytes = 0;
+  size_t off_sections = 0, off_blocks = 0, off_lse = 0, off_chosen = 0, off_used = 0, off_exact = 0, bytes = 0;
 };
 BeamPlan plan_beam(int64_t N, int64_t H, int64_t V, int64_t beams) {
   BeamPlan p;
@@ -1289,7 +1289,7 @@ BeamPlan plan_beam(int64_t N, int64_t H, int64_t V, int64_t beams) {
     p.n_sections = p.splits;
     p.per_section = lmh::few_rows(V) / 16;
   } else {
-    const lmh::FwdPlan f = lmh::plan_forward(N, H, V);
+    const lmh::FwdPlan f = lmh::plan_forward(N, H, V, lmh::kNumCUs);
     p.splits = f.S;
     p.n_tt = f.n_tt;
     p.n_vt = f.n_vt;
@@ -1297,7 +1297,8 @@ BeamPlan plan_beam(int64_t N, int64_t H, int64_t V, int64_t beams) {
     p.per_section = 8;
   }
   p.n_blocks = lmh::ceil_div(V, 16);
-  p.ld = lmh::round_up(std::max<int64_t>(N, 1), 64);
+  // the tiles store whole: rows to 256, words to 256 (sections and blocks of them)
+  p.ld = lmh::round_up(std::max<int64_t>(N, 1), p.few ? 64 : lmh::kTileRows);
   const int64_t groups = N / beams;
   size_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -1306,12 +1307,11 @@ BeamPlan plan_beam(int64_t N, int64_t H, int64_t V, int64_t beams) {
     return here;
   };
   take(8 * p.splits * p.ld);
-  p.off_sections = take(4 * p.n_sections * p.ld);
-  p.off_blocks = take(4 * p.n_blocks * p.ld);
+  p.off_sections = take(4 * std::max<int64_t>(p.n_sections, 2 * p.n_vt) * p.ld);
+  p.off_blocks = take(4 * std::max<int64_t>(p.n_blocks, 16 * p.n_vt) * p.ld);
   p.off_lse = take(8 * N);
   p.off_chosen = take(4 * lmh::kMostKept * groups);
   p.off_used = take(4 * groups);
-  p.off_ticket = take(4 * groups);
   p.off_exact = take(8 * 16 * lmh::kMostKept * groups);
   p.bytes = at;
   return p;
@@ -1379,7 +1379,6 @@ int lmhead_logps_beam_step(const uint16_t* hidden, const uint16_t* W, const floa
   b.lse64 = reinterpret_cast<double*>(ws + p.off_lse);
   b.chosen = reinterpret_cast<uint32_t*>(ws + p.off_chosen);
   b.used = reinterpret_cast<int32_t*>(ws + p.off_used);
-  b.ticket = reinterpret_cast<int32_t*>(ws + p.off_ticket);
   b.exact = reinterpret_cast<double*>(ws + p.off_exact);
   b.top_scores = top_scores;
   b.top_ids = top_ids;

@@ -122,45 +122,65 @@ __global__ __launch_bounds__(256, 2) void beam_few_kernel(const FewArgs a, const
   }
 }
 
-// Many rows: the head's forward tiles; a section is a wave's 128 vocabulary rows.
+// Of four blocks' largest logits, of which a lane holds a part of each (the
+// lanes of a row of 16 tokens four words each), the whole of one block in each
+// quarter of the wave: quarter q gets block kQuarterBlock[q]. Three exchanges
+// where a butterfly per block takes eight.
+__device__ __forceinline__ float swap_max(float a, float b, bool halves) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  const unsigned x = __float_as_uint(a), y = __float_as_uint(b);
+  const u32x2 r = halves ? __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(x, y, false, false))
+                         : __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(x, y, false, false));
+  return max_drop(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+__device__ __forceinline__ float four_blocks(float b0, float b1, float b2, float b3) {
+  return swap_max(swap_max(b0, b1, true), swap_max(b2, b3, true), false);
+}
+__device__ __forceinline__ int quarter_block(int q) { return (q & 1) * 2 + (q >> 1); }
+
+// Many rows: the head's forward tiles; a section is a wave's 128 vocabulary
+// rows. The arrays hold whole tiles of rows and of words, so every store is in
+// place; what lies past N or V is not read.
 template <bool MASK>
-__global__ __launch_bounds__(kThreads) void beam_tile_kernel(const BeamArgs b) {
+__global__ __launch_bounds__(kThreads) void beam_tile_kernel(
+    const uint16_t* __restrict__ hidden, const uint16_t* __restrict__ W, const int32_t* __restrict__ allowed, int mask_ld, int N,
+    int H, int V, int S, int n_tt, int n_vt, float sc, float2* __restrict__ records, float* __restrict__ sections,
+    float* __restrict__ blocks, int ld) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   const int vid = xcd_remap(blockIdx.x, gridDim.x);
-  const int S = b.splits;
-  if (vid >= b.n_tt * S) return;
+  if (vid >= n_tt * S) return;
   const int tt = vid / S;
   const int s = vid - tt * S;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
   const int wm = wave & 1;
   const int wn = wave >> 1;
-  const int q = lane >> 4;
   const int tok0 = tt * kTile;
-  const int N = b.N, H = b.H, V = b.V;
-  const float sc = b.sc;
   float m2[kNB], s1[kNB];
 #pragma unroll
   for (int j = 0; j < kNB; ++j) m2[j] = kNegBig, s1[j] = 0.0f;
-  const Operand ob{b.hidden + (int64_t)tok0 * H, H, min(kTile, N - tok0)};
+  const Operand ob{hidden + (int64_t)tok0 * H, H, min(kTile, N - tok0)};
   Pipe pipe;
-  for (int vt = s; vt < b.n_vt; vt += S) {
+  for (int vt = s; vt < n_vt; vt += S) {
     const int v0 = vt * kTile;
-    const Operand oa{b.W + (int64_t)v0 * H, H, min(kTile, V - v0)};
+    const Operand oa{W + (int64_t)v0 * H, H, min(kTile, V - v0)};
     const int v1 = v0 + S * kTile;
-    const bool more = vt + S < b.n_vt && min(kTile, V - v1) == oa.rows;
+    const bool more = vt + S < n_vt && min(kTile, V - v1) == oa.rows;
     f32x4 acc[kNB][kNB];
-    mma_tile<false, 96>(oa, ob, H, lds, acc, pipe, b.W + (int64_t)(more ? v1 : v0) * H, ob.base, more);
+    mma_tile<false, 96>(oa, ob, H, lds, acc, pipe, W + (int64_t)(more ? v1 : v0) * H, ob.base, more);
     const int vrow0 = v0 + wm * 128;
     const bool ragged = vrow0 + 128 > V;
+    const int q = lane >> 4;
+    const int tok = tok0 + wn * 128 + (lane & 15);
+    float* to = blocks + (int64_t)((vrow0 >> 4) + quarter_block(q)) * ld + tok;
+    float* sec = sections + (int64_t)(vrow0 >> 7) * ld + tok;
 #pragma unroll
     for (int j = 0; j < kNB; ++j) {
-      const int tok = tok0 + wn * 128 + j * 16 + (lane & 15);
-      uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+      uint32_t words[4];
       if (MASK) {
-        const int32_t* row = b.allowed + (int64_t)min(tok, N - 1) * b.mask_ld;
+        const int32_t* row = allowed + (int64_t)min(tok + 16 * j, N - 1) * mask_ld;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) words[w] = (uint32_t)row[min((vrow0 >> 5) + w, (int)b.mask_ld - 1)];
+        for (int w = 0; w < 4; ++w) words[w] = (uint32_t)row[min((vrow0 >> 5) + w, mask_ld - 1)] >> (4 * q);
       }
       float z[kNB][4];
 #pragma unroll
@@ -175,34 +195,49 @@ __global__ __launch_bounds__(kThreads) void beam_tile_kernel(const BeamArgs b) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) z[i][r] = (vrow0 + acc_row(i, r, lane) < V) ? z[i][r] : kNegBig;
       }
-      float mx = z[0][0], top = -INFINITY;
-      float best[kNB];
-#pragma unroll
-      for (int i = 0; i < kNB; ++i) {
-        best[i] = -INFINITY;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          mx = nan_max(mx, z[i][r]);
-          bool in = !ragged || vrow0 + acc_row(i, r, lane) < V;
-          if (MASK) in = in && ((words[i >> 1] >> (16 * (i & 1) + 4 * q + r)) & 1);
-          best[i] = max_drop(best[i], in ? z[i][r] : -INFINITY);
-        }
-        best[i] = max_drop(best[i], __shfl_xor(best[i], 16));
-        best[i] = max_drop(best[i], __shfl_xor(best[i], 32));
-        top = max_drop(top, best[i]);
-        const int vb = vrow0 + 16 * i;
-        if (q == (i & 3) && vb < V && tok < N) b.blocks[(int64_t)(vb >> 4) * b.ld + tok] = best[i];
-      }
-      if (q == 0 && vrow0 < V && tok < N) b.sections[(int64_t)(vrow0 >> 7) * b.ld + tok] = top;
-      const float mnew = nan_max(m2[j], mx * sc);
-      float e = s1[j] * fast_exp2(m2[j] - mnew);
+      float mx = z[0][0];
 #pragma unroll
       for (int i = 0; i < kNB; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float x = fast_exp2(fmaf(z[i][r], sc, -mnew));
-          e += !ragged || vrow0 + acc_row(i, r, lane) < V ? x : 0.0f;
+        for (int r = 0; r < 4; ++r) mx = nan_max(mx, z[i][r]);
+      float whole[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float best[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * h + e;
+          float x[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[r] = z[i][r];
+            if (MASK) x[r] = (words[i >> 1] >> (16 * (i & 1) + r)) & 1 ? x[r] : -INFINITY;
+          }
+          best[e] = max_drop(max_drop(x[0], x[1]), max_drop(x[2], x[3]));
         }
+        whole[h] = four_blocks(best[0], best[1], best[2], best[3]);
+        to[(int64_t)(4 * h) * ld + 16 * j] = whole[h];
+      }
+      float top = max_drop(whole[0], whole[1]);
+      top = swap_max(top, top, true);
+      top = swap_max(top, top, false);
+      if (q == 0) sec[16 * j] = top;
+      const float mnew = nan_max(m2[j], mx * sc);
+      float e = s1[j] * fast_exp2(m2[j] - mnew);
+      if (!ragged) {
+#pragma unroll
+        for (int i = 0; i < kNB; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) e += fast_exp2(fmaf(z[i][r], sc, -mnew));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kNB; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = fast_exp2(fmaf(z[i][r], sc, -mnew));
+            e += vrow0 + acc_row(i, r, lane) < V ? x : 0.0f;
+          }
+      }
       m2[j] = mnew;
       s1[j] = e;
       __builtin_amdgcn_sched_barrier(0);
@@ -229,8 +264,8 @@ __global__ __launch_bounds__(kThreads) void beam_tile_kernel(const BeamArgs b) {
     for (int j = 0; j < kNB; ++j) {
       const float2 o = xch[(wn * kNB + j) * 16 + lane];
       const float m = nan_max(m2[j], o.x);
-      const int tok = tok0 + wn * 128 + j * 16 + lane;
-      if (tok < N) b.records[(int64_t)s * b.ld + tok] = make_float2(m, s1[j] * fast_exp2(m2[j] - m) + o.y * fast_exp2(o.x - m));
+      records[(int64_t)s * ld + tok0 + wn * 128 + j * 16 + lane] =
+          make_float2(m, s1[j] * fast_exp2(m2[j] - m) + o.y * fast_exp2(o.x - m));
     }
   }
 }
@@ -250,67 +285,92 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 __device__ __forceinline__ uint32_t index_of(uint64_t key) { return ~(uint32_t)key; }
 
 constexpr int kSelThreads = 1024;
-constexpr int kSelItems = 16;                                 // items of a thread at once
-constexpr int kSelList = 4 * kSelItems * kMostKept + kMostKept;   // candidates that can pass the threshold, and those kept
+constexpr int kSelTeams = 128;    // of 8 threads each
+constexpr int kSelList = 2048;
 
-// The `keep` largest keys of items 0 .. n - 1 into list[0 ..], sorted; returns
-// how many there are. get(i) gives an item's key, 0 for none. Each group of
-// four threads has a largest key, and the keep-th largest of those 256 is a
-// threshold that at least `keep` items reach, and few more do.
+// The `keep` largest keys of items 0 .. n - 1 into kept[0 ..], sorted; returns
+// how many there are (keep, or all that are not 0). get(i) gives an item's key, 0
+// for none. Every team has a largest key, and the keep-th largest of those is a
+// threshold that at least `keep` items reach, and few more do as a rule: those
+// are ranked. Should more than the list holds reach it (most of the best items
+// lie with few teams), the best are taken one after the other.
+static_assert(kMostKept <= kSelTeams, "a threshold exists");
 struct Selection {
   uint64_t list[kSelList];
+  uint64_t most[kSelTeams];
   uint64_t kept[kMostKept];
-  uint64_t most[kSelThreads / 4];
   uint64_t limit;
   int count;
 };
 template <class F>
 __device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, F get) {
-  const int tid = threadIdx.x;
-  int have = 0;
-  for (uint32_t base = 0; base < n; base += kSelThreads * kSelItems) {
-    uint64_t key[kSelItems], most = 0;
+  const uint32_t tid = threadIdx.x;
+  auto largest = [&](uint64_t below) {
+    uint64_t most = 0;
+    for (uint32_t base = tid; base < n; base += 4 * kSelThreads) {
+      uint64_t key[4];
 #pragma unroll
-    for (int k = 0; k < kSelItems; ++k) {
-      const uint32_t i = base + tid + kSelThreads * k;
-      key[k] = i < n ? get(i) : 0;
+      for (int k = 0; k < 4; ++k) key[k] = base + kSelThreads * k < n ? get(base + kSelThreads * k) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) most = key[k] < below ? max(most, key[k]) : most;
     }
 #pragma unroll
-    for (int k = 0; k < kSelItems; ++k) most = max(most, key[k]);
-    most = max(most, (uint64_t)__shfl_xor((unsigned long long)most, 1));
-    most = max(most, (uint64_t)__shfl_xor((unsigned long long)most, 2));
-    if ((tid & 3) == 0) s.most[tid >> 2] = most;
-    if (tid == 0) {
-      s.limit = 0;
-      s.count = have;
-    }
-    __syncthreads();
-    if (tid < kSelThreads / 4) {
-      const uint64_t mine = s.most[tid];
-      int rank = 0;
-#pragma unroll 8
-      for (int k = 0; k < kSelThreads / 4; ++k) rank += s.most[k] > mine;
-      if (rank == keep - 1) s.limit = mine;   // keys differ, so one has this rank, or (all zeros behind it) the limit stays 0
-    }
-    __syncthreads();
-    uint64_t limit = max(s.limit, (uint64_t)1);
-    if (have == keep) limit = max(limit, s.kept[keep - 1]);
-    if (tid < have) s.list[tid] = s.kept[tid];
-#pragma unroll
-    for (int k = 0; k < kSelItems; ++k)
-      if (key[k] >= limit) s.list[atomicAdd(&s.count, 1)] = key[k];
-    __syncthreads();
-    const int found = s.count;
-    for (int i = tid; i < found; i += kSelThreads) {
-      const uint64_t mine = s.list[i];
-      int rank = 0;
-      for (int k = 0; k < found; ++k) rank += s.list[k] > mine;
-      if (rank < keep) s.kept[rank] = mine;
-    }
-    have = min(found, keep);
-    __syncthreads();
+    for (int x = 1; x < kSelThreads / kSelTeams; x <<= 1) most = max(most, (uint64_t)__shfl_xor((unsigned long long)most, x));
+    return most;
+  };
+  const uint64_t most = largest(~(uint64_t)0);
+  if (tid % (kSelThreads / kSelTeams) == 0) s.most[tid / (kSelThreads / kSelTeams)] = most;
+  if (tid == 0) {
+    s.limit = 1;
+    s.count = 0;
   }
-  return have;
+  __syncthreads();
+  if (tid < kSelTeams) {
+    const uint64_t mine = s.most[tid];
+    int rank = 0;
+#pragma unroll 16
+    for (int k = 0; k < kSelTeams; ++k) rank += s.most[k] > mine;
+    if (rank == keep - 1 && mine > 0) s.limit = mine;
+  }
+  __syncthreads();
+  const uint64_t limit = s.limit;
+  for (uint32_t base = tid; base < n; base += 4 * kSelThreads) {
+    uint64_t key[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) key[k] = base + kSelThreads * k < n ? get(base + kSelThreads * k) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (key[k] >= limit) {
+        const int at = atomicAdd(&s.count, 1);
+        if (at < kSelList) s.list[at] = key[k];
+      }
+  }
+  __syncthreads();
+  const int found = s.count;
+  if (found > kSelList) {
+    uint64_t below = ~(uint64_t)0;
+    for (int r = 0; r < keep; ++r) {
+      __syncthreads();   // s.most and s.limit have been read
+      const uint64_t team = largest(below);
+      if (tid % (kSelThreads / kSelTeams) == 0) s.most[tid / (kSelThreads / kSelTeams)] = team;
+      __syncthreads();
+      uint64_t best = 0;
+      for (int k = 0; k < kSelTeams; ++k) best = max(best, s.most[k]);
+      if (tid == 0) s.kept[r] = best;
+      below = best;
+    }
+    __syncthreads();
+    return keep;   // more than kSelList items are not 0
+  }
+  for (int i = tid; i < found; i += kSelThreads) {
+    const uint64_t mine = s.list[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int k = 0; k < found; ++k) rank += s.list[k] > mine;
+    if (rank < keep) s.kept[rank] = mine;
+  }
+  __syncthreads();
+  return min(found, keep);
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -318,19 +378,16 @@ __device__ __forceinline__ double wave_sum(double v) {
   for (int x = 32; x >= 1; x >>= 1) v += __shfl_xor(v, x);
   return v;
 }
-
-// A row that takes part: neither given up (a score that is not finite) nor ended.
+__device__ __forceinline__ bool finite(double v) { return fabs(v) < INFINITY; }
 __device__ __forceinline__ bool ended_row(const BeamArgs& b, int64_t tok) {
   return b.ended != nullptr && b.ended[tok] >= 0 && b.ended[tok] < b.V;
 }
-__device__ __forceinline__ bool finite(double v) { return fabs(v) < INFINITY; }
 
 __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs b) {
   __shared__ Selection sel;
   __shared__ double base[kMostBeams];
-  __shared__ float shift[kMostBeams], size[kMostBeams];
+  __shared__ float size[kMostBeams], shift[kMostBeams];
   __shared__ uint32_t section[kMostKept];
-  __shared__ double ref;
   __shared__ float slack;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -339,42 +396,51 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
   for (int r = wave; r < G; r += kSelThreads / 64) {
     const int64_t tok = row0 + r;
     float m = kNegBig;
-    for (int s = lane; s < b.splits; s += 64) m = nan_max(m, b.records[s * b.ld + tok].x);
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) m = nan_max(m, __shfl_xor(m, x));
     double sum = 0.0;
-    for (int s = lane; s < b.splits; s += 64) {
-      const float2 p = b.records[s * b.ld + tok];
-      sum += (double)p.y * exp2((double)p.x - (double)m);
+    for (int s0 = lane; s0 < b.splits; s0 += 64 * 8) {
+      float2 p[8];
+      float mx = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        p[k] = s0 + 64 * k < b.splits ? b.records[(int64_t)(s0 + 64 * k) * b.ld + tok] : make_float2(kNegBig, 0.0f);
+        mx = nan_max(mx, p[k].x);
+      }
+      sum *= (double)fast_exp2(m - mx);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += (double)p[k].y * (double)fast_exp2(p[k].x - mx);
+      m = mx;
     }
-    sum = wave_sum(sum);
+    float mx = m;
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) mx = nan_max(mx, __shfl_xor(mx, x));
+    sum = wave_sum(sum * (double)fast_exp2(m - mx));
     if (lane == 0) {
       const float score = b.scores[tok];
       // records are in base 2 of logits scaled by the float32 sc: back = 1 / (sc T) undoes both
-      const double lse = m == INFINITY ? INFINITY : (double)m * b.back + log(sum);
+      const double lse = mx == INFINITY ? INFINITY : (double)mx * b.back + log(sum);
       const bool part = finite(score) && !ended_row(b, tok);
       const bool live = part && finite(lse);
       base[r] = live ? (double)score - lse : -INFINITY;
-      size[r] = live ? (float)((double)m * b.back) : 0.0f;
+      size[r] = live ? (float)((double)mx * b.back) : 0.0f;
       b.lse64[tok] = lse;
       b.lse[tok] = part ? (float)lse : 0.0f;
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    double best = -INFINITY;
-    float most = 0.0f;
-    for (int r = 0; r < G; ++r) {
-      if (!finite(base[r])) continue;
-      best = max(best, base[r] + (double)size[r]);
-      most = max(most, fabsf(size[r]));
+  if (wave == 0) {
+    // values relative to about the best candidate, where float32 is finest
+    const double mine = lane < G ? base[lane] : -INFINITY;
+    const float large = lane < G ? size[lane] : 0.0f;
+    double ref = mine + (double)large;
+    float most = fabsf(large);
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) {
+      ref = fmax(ref, __shfl_xor(ref, x));
+      most = fmaxf(most, __shfl_xor(most, x));
     }
-    ref = best;
-    slack = (most + b.invT) * 0x1p-13f;   // far more than the tiles' sums are off
+    if (lane < G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
+    if (lane == 0) slack = (most + b.invT) * 0x1p-13f;   // far more than the tiles' sums are off
   }
-  __syncthreads();
-  // values relative to about the best candidate, where float32 is finest
-  if (tid < G) shift[tid] = finite(base[tid]) ? (float)(base[tid] - ref) : -INFINITY;
   __syncthreads();
   const int keep = b.keep;
   const uint32_t n_sec = (uint32_t)b.n_sections;   // beams * V stays below 2^31
@@ -394,151 +460,160 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     const uint32_t r = at / n_sec, blk = (at - r * n_sec) * per + i % per;
     return blk < n_blocks ? key(b.blocks[(int64_t)blk * b.ld + row0 + r], r, r * n_blocks + blk) : (uint64_t)0;
   });
-  if (tid < n2) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
-  if (tid == 0) {
-    int used = min(n2, b.C);
-    while (used < n2 && value_of(sel.kept[used]) >= value_of(sel.kept[b.C - 1]) - slack) ++used;
-    b.used[group] = used;
-    b.ticket[group] = 0;
-  }
+  // those of the first C, and of the spare ones that are as good within the slack
+  const bool in = tid < n2 && (tid < b.C || value_of(sel.kept[tid]) >= value_of(sel.kept[b.C - 1]) - slack);
+  if (in) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
+  const int used = __syncthreads_count(in);   // values fall, so these are the first ones
+  if (tid == 0) b.used[group] = used;
 }
 
-// A workgroup per chosen block: its 16 logits in 64 bits. The last one of the
-// group ranks the candidates.
-constexpr int kScoreThreads = 256;
-constexpr int kMostFound = 16 * kMostKept + kMostBeams;
-__global__ __launch_bounds__(kScoreThreads) void beam_score_kernel(const BeamArgs b) {
-  __shared__ double z_max[kMostKept], logsum[kMostBeams];
-  __shared__ double value[kMostFound];
-  __shared__ uint32_t index[kMostFound];
-  __shared__ double limit;
-  __shared__ int count, last;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t group = blockIdx.x / b.keep, row0 = group * b.beams;
-  const int used = b.used[group];
+// A workgroup per chosen block: its 16 logits in 64 bits, four a wave.
+__global__ __launch_bounds__(256) void beam_score_kernel(const BeamArgs b) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t group = blockIdx.x / b.keep;
   const int k = (int)(blockIdx.x - group * b.keep);
-  if (k >= max(used, 1)) return;
-  const int G = b.beams, V = b.V, H = b.H, C = b.C;
-  if (k < used) {
-    const uint32_t at = b.chosen[group * kMostKept + k];
-    const int r = at / (uint32_t)b.n_blocks;
-    const int v0 = (int)(at - (uint32_t)r * (uint32_t)b.n_blocks) * 16;
-    const uint4* h = reinterpret_cast<const uint4*>(b.hidden + (row0 + r) * H);
-    const uint4* w[4];
-    double acc[4];
+  if (k >= b.used[group]) return;
+  const int H8 = b.H / 8;
+  const uint32_t at = b.chosen[group * kMostKept + k];
+  const uint32_t r = at / (uint32_t)b.n_blocks;
+  const int v0 = (int)(at - r * (uint32_t)b.n_blocks) * 16;
+  const uint4* h = reinterpret_cast<const uint4*>(b.hidden + (group * b.beams + r) * b.H);
+  const uint4* w[4];
+  double acc[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      w[e] = reinterpret_cast<const uint4*>(b.W + (int64_t)min(v0 + 4 * wave + e, V - 1) * H);
-      acc[e] = 0.0;
+  for (int e = 0; e < 4; ++e) {
+    w[e] = reinterpret_cast<const uint4*>(b.W + (int64_t)min(v0 + 4 * wave + e, b.V - 1) * b.H);
+    acc[e] = 0.0;
+  }
+  constexpr int D = 3;
+  for (int c = lane; c < H8; c += 64 * D) {
+    uint4 x[D], y[D][4];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {   // past the end: the last chunk of h times 0
+      const int at = min(c + 64 * d, H8 - 1);
+      x[d] = h[at];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[d][e] = w[e][at];
     }
-    for (int c = lane; c < H / 8; c += 64) {
-      const uint4 x = h[c];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-      uint4 y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = w[e][c];
+    for (int d = 0; d < D; ++d) {
+      if (c + 64 * d >= H8) continue;
+      const uint32_t xs[4] = {x[d].x, x[d].y, x[d].z, x[d].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+        const uint32_t ys[4] = {y[d][e].x, y[d][e].y, y[d][e].z, y[d][e].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // a product of two bf16 is exact in float32 (but for its range: 64 bits)
+        for (int i = 0; i < 4; ++i) {
           acc[e] = fma((double)__uint_as_float(xs[i] << 16), (double)__uint_as_float(ys[i] << 16), acc[e]);
           acc[e] = fma((double)__uint_as_float(xs[i] & 0xFFFF0000u), (double)__uint_as_float(ys[i] & 0xFFFF0000u), acc[e]);
         }
       }
     }
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double z = wave_sum(acc[e]);
-      if (lane == 0) b.exact[(group * kMostKept + k) * 16 + 4 * wave + e] = z;
-    }
+  for (int e = 0; e < 4; ++e) {
+    const double z = wave_sum(acc[e]);
+    if (lane == 0) b.exact[(group * kMostKept + k) * 16 + 4 * wave + e] = z;
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(&b.ticket[group], 1) == max(used, 1) - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
+}
 
-  auto allowed = [&](int r, int64_t v) {
-    return v < V && (b.allowed == nullptr || ((uint32_t)b.allowed[(row0 + r) * b.mask_ld + (v >> 5)] >> (v & 31)) & 1);
-  };
-  auto place = [&](int i, int& r, int64_t& v0) {
-    const uint32_t at = b.chosen[group * kMostKept + i];
-    r = at / (uint32_t)b.n_blocks;
-    v0 = (int64_t)(at - (uint32_t)r * (uint32_t)b.n_blocks) * 16;
-  };
-  const double* exact = b.exact + group * kMostKept * 16;
-  if (tid < used) {
-    int r;
-    int64_t v0;
-    place(tid, r, v0);
-    double m = -INFINITY;
-    for (int e = 0; e < 16; ++e)
-      if (allowed(r, v0 + e)) m = fmax(m, exact[16 * tid + e]);
-    z_max[tid] = m;
-  }
+// A workgroup per group: the candidates of the chosen blocks, and the ended
+// rows, in order.
+constexpr int kRankThreads = 256;
+constexpr int kMostFound = 16 * kMostKept + kMostBeams;
+__global__ __launch_bounds__(kRankThreads) void beam_rank_kernel(const BeamArgs b) {
+  __shared__ double z_max[kMostKept], logsum[kMostBeams], best[kMostKept];
+  __shared__ uint32_t row_of[kMostKept], word_of[kMostKept];
+  __shared__ int first[kMostBeams];
+  __shared__ double value[kMostFound];
+  __shared__ uint32_t index[kMostFound];
+  __shared__ double limit;
+  __shared__ int count;
+  const int tid = threadIdx.x;
+  const int64_t group = blockIdx.x, row0 = group * b.beams;
+  const int G = b.beams, V = b.V, C = b.C, used = b.used[group];
+  if (tid < G) first[tid] = kMostKept;
   if (tid == 0) {
     count = 0;
     limit = -INFINITY;
   }
+  if (tid < used) {
+    const uint32_t at = b.chosen[group * kMostKept + tid], r = at / (uint32_t)b.n_blocks;
+    row_of[tid] = r;
+    word_of[tid] = (at - r * (uint32_t)b.n_blocks) * 16;
+  }
+  __syncthreads();
+  // sixteen lanes a block
+  constexpr int rounds = (16 * kMostKept + kRankThreads - 1) / kRankThreads;
+  double z[rounds];
+#pragma unroll
+  for (int q = 0; q < rounds; ++q) {
+    const int i = q * kRankThreads + tid, k = i >> 4;
+    z[q] = -INFINITY;
+    if (k < used) {
+      const uint32_t v = word_of[k] + (i & 15);
+      const bool may = v < (uint32_t)V && (b.allowed == nullptr ||
+                                           ((uint32_t)b.allowed[(row0 + row_of[k]) * b.mask_ld + (v >> 5)] >> (v & 31)) & 1);
+      if (may) z[q] = b.exact[group * kMostKept * 16 + i];
+    }
+    double m = z[q];
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) m = fmax(m, __shfl_xor(m, x));
+    if (k < used && (i & 15) == 0) {
+      z_max[k] = m;
+      atomicMin(&first[row_of[k]], k);
+    }
+  }
   __syncthreads();
   if (tid < G) {
     double lse = b.lse64[row0 + tid];
-    for (int i = 0; i < used; ++i) {
-      int r;
-      int64_t v0;
-      place(i, r, v0);
-      if (r != tid) continue;
-      const double was = b.blocks[(v0 >> 4) * b.ld + row0 + r];
-      lse += log1p(exp(z_max[i] / b.T - lse) - exp(was / b.T - lse));
-      break;
+    const int k = first[tid];
+    if (k < used) {
+      const double was = b.blocks[(int64_t)(word_of[k] >> 4) * b.ld + row0 + tid];
+      lse += log1p(exp(z_max[k] / b.T - lse) - exp(was / b.T - lse));
     }
     logsum[tid] = lse;
   }
   __syncthreads();
-  auto score_of = [&](int r, double z) { return (double)b.scores[row0 + r] + (z / b.T - logsum[r]); };
+  auto score_of = [&](int r, double x) { return (double)b.scores[row0 + r] + (x / b.T - logsum[r]); };
   // C blocks hold a candidate each that reaches the C-th largest of their best
-  if (tid < used) {
-    int r;
-    int64_t v0;
-    place(tid, r, v0);
-    value[tid] = score_of(r, z_max[tid]);
-  }
+  if (tid < used) best[tid] = score_of(row_of[tid], z_max[tid]);
   __syncthreads();
   if (tid < used) {
+    const double mine = best[tid];
     int rank = 0;
-    for (int i = 0; i < used; ++i) rank += value[i] > value[tid] || (value[i] == value[tid] && i < tid);
-    if (rank == C - 1) limit = value[tid];
+#pragma unroll 8
+    for (int i = 0; i < used; ++i) rank += best[i] > mine || (best[i] == mine && i < tid);
+    if (rank == C - 1) limit = mine;
   }
   __syncthreads();
-  for (int i = tid; i < 16 * used; i += kScoreThreads) {
-    int r;
-    int64_t v0;
-    place(i >> 4, r, v0);
-    const int64_t v = v0 + (i & 15);
-    if (!allowed(r, v)) continue;
-    const double x = score_of(r, exact[i]);
+#pragma unroll
+  for (int q = 0; q < rounds; ++q) {
+    const int i = q * kRankThreads + tid, k = i >> 4;
+    if (k >= used) continue;
+    const double x = score_of(row_of[k], z[q]);
     if (x > -INFINITY && x >= limit) {
       const int at = atomicAdd(&count, 1);
       value[at] = x;
-      index[at] = (uint32_t)(r * (int64_t)V + v);
+      index[at] = row_of[k] * (uint32_t)V + word_of[k] + (i & 15);
     }
   }
-  for (int r = tid; r < G; r += kScoreThreads) {
-    const float s = b.scores[row0 + r];
-    if (!ended_row(b, row0 + r) || !finite(s)) continue;
-    const int at = atomicAdd(&count, 1);
-    value[at] = s;
-    index[at] = (uint32_t)(r * (int64_t)V + b.ended[row0 + r]);
+  if (tid < G) {
+    const float s = b.scores[row0 + tid];
+    if (ended_row(b, row0 + tid) && finite(s)) {
+      const int at = atomicAdd(&count, 1);
+      value[at] = s;
+      index[at] = (uint32_t)tid * (uint32_t)V + (uint32_t)b.ended[row0 + tid];
+    }
   }
   __syncthreads();
   const int found = count;
-  for (int i = tid; i < found; i += kScoreThreads) {
+  for (int i = tid; i < found; i += kRankThreads) {
     const double x = value[i];
     const uint32_t at = index[i];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < found; ++j) rank += value[j] > x || (value[j] == x && index[j] < at);
     if (rank < C) {
       const int64_t to = group * C + rank;
@@ -547,7 +622,7 @@ __global__ __launch_bounds__(kScoreThreads) void beam_score_kernel(const BeamArg
       b.top_parents[to] = (int32_t)(row0 + at / (uint32_t)V);
     }
   }
-  for (int i = found + tid; i < C; i += kScoreThreads) {
+  for (int i = found + tid; i < C; i += kRankThreads) {
     const int64_t to = group * C + i;
     b.top_scores[to] = -INFINITY;
     b.top_ids[to] = -1;
@@ -578,8 +653,11 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
     });
   } else {
     const dim3 grid((unsigned)(((int64_t)b.n_tt * b.splits + 7) / 8 * 8));
-    if (b.allowed != nullptr) hipLaunchKernelGGL((beam_tile_kernel<true>), grid, dim3(kThreads), 0, stream, b);
-    else hipLaunchKernelGGL((beam_tile_kernel<false>), grid, dim3(kThreads), 0, stream, b);
+    auto tiles = [&](auto mask) {
+      hipLaunchKernelGGL((beam_tile_kernel<mask()>), grid, dim3(kThreads), 0, stream, b.hidden, b.W, b.allowed, (int)b.mask_ld, b.N,
+                         b.H, b.V, b.splits, b.n_tt, b.n_vt, b.sc, b.records, b.sections, b.blocks, (int)b.ld);
+    };
+    b.allowed != nullptr ? tiles(std::true_type{}) : tiles(std::false_type{});
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -591,10 +669,15 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
   if (e != hipSuccess) return e;
   trace_end(kBeamSelect, stream, 0.0, 8.0 * b.splits * N + 4.0 * N * b.n_sections);
   trace_begin(stream);
-  hipLaunchKernelGGL(beam_score_kernel, dim3((unsigned)(b.keep * groups)), dim3(kScoreThreads), 0, stream, b);
+  hipLaunchKernelGGL(beam_score_kernel, dim3((unsigned)(b.keep * groups)), dim3(256), 0, stream, b);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kBeamScore, stream, 32.0 * groups * b.C * H, 34.0 * groups * b.C * H);
+  trace_begin(stream);
+  hipLaunchKernelGGL(beam_rank_kernel, dim3((unsigned)groups), dim3(kRankThreads), 0, stream, b);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kBeamRank, stream, 0.0, 140.0 * groups * b.C);
   return hipSuccess;
 }
 

@@ -344,7 +344,6 @@ struct BeamArgs {
   double* lse64;            // [N]
   uint32_t* chosen;         // [groups][kMostKept] row in the group * n_blocks + block
   int32_t* used;            // [groups] how many of them
-  int32_t* ticket;          // [groups]
   double* exact;            // [groups][kMostKept][16] logits
   float* top_scores;
   int32_t* top_ids;
@@ -368,7 +367,7 @@ enum KernelId {
   kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
   kDistillTop, kDistillPrep, kDistillStep, kDistillPost,
   kFewStats, kFewDz, kFewGrads, kNormFwd, kNormBwd, kNormReduce,
-  kEmbedFwd, kEmbedSort, kEmbedRows, kEmbedJoin, kBeamLogits, kBeamSelect, kBeamScore, kBeamReorder, kNumKernels
+  kEmbedFwd, kEmbedSort, kEmbedRows, kEmbedJoin, kBeamLogits, kBeamSelect, kBeamScore, kBeamRank, kBeamReorder, kNumKernels
 };
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);

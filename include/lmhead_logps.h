@@ -489,8 +489,9 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  * The choice looks at 16 blocks of 16 words more than there are candidates where
  * float32 does not tell their largest logits apart; in a group with more near ties
  * than that it may miss one.
- * The workspace holds 4 N V / 16 bytes of the blocks' largest logits and smaller
- * arrays; lmhead_logps_beam_workspace_bytes sizes it.
+ * The workspace holds 4 N V / 16 bytes of the blocks' largest logits (N rounded
+ * up to 64, or to 256 above 64) and smaller arrays;
+ * lmhead_logps_beam_workspace_bytes sizes it.
  * Errors: those of the head's calls, plus LMH_ERR_SHAPE when beams is not in [1,
  * LMH_BEAM_MAX_BEAMS], candidates not in [1, LMH_BEAM_MAX_CANDIDATES] or N not a
  * multiple of beams, and LMH_ERR_UNSUPPORTED where N >= 2^23 or beams V >= 2^31.
@@ -555,8 +556,9 @@ const char* lmhead_logps_version(void);
  *  20 embed_join_kernel    (its words of many tokens)
  *  21 beam_logits_kernel   (beam step: log-sum-exps and blocks' largest logits)
  *  22 beam_select_kernel   (the blocks that hold the best candidates)
- *  23 beam_score_kernel    (their logits in 64 bits, the candidates)
- *  24 beam_reorder_kernel
+ *  23 beam_score_kernel    (their logits in 64 bits)
+ *  24 beam_rank_kernel     (the candidates in order)
+ *  25 beam_reorder_kernel
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch

@@ -131,10 +131,11 @@ def test_beam_workspace():
     for N in (0, 1, 4, 64, 65, 128, 256, 257, 1024, 100000):
         for V in (1, 16, 17, 4096, 12289, 151936, 1 << 22):
             b = q(N, 2560, V, 1, 8)
-            ld = up(max(N, 1), 64)
-            assert 4 * ld * -(-V // 16) <= b
-            # blocks of 16 words, sections and records of at least 64, and the groups' chosen blocks
-            assert b <= ld * (4 * (V / 16 + 1) + 12 * (V / 64 + 128)) + N * (8 + 80 * 132 + 8) + 4096
+            assert 4 * N * -(-V // 16) <= b
+            # for rows rounded up to 64, or 256 above 64 of them: blocks of 16 words, sections and records of at least
+            # 64, all of whole tiles of 256; and the groups' chosen blocks
+            ld, v = up(max(N, 1), 64 if N <= 64 else 256), up(V, 256)
+            assert b <= ld * (4 * v / 16 + 12 * (v / 64 + 256)) + N * (8 + 80 * 132 + 8) + 4096
 
 
 def _br(**kw):
