@@ -381,7 +381,8 @@ TRACE_KERNELS = ("fwd_stats_kernel", "fwd_merge_kernel", "bwd_step_kernel", "tra
                  "fill_zero_kernel", "pad_rows_kernel", "bwd_step_bf16_kernel", "distill_top_kernel",
                  "distill_prep_kernel", "distill_step_kernel", "distill_post_kernel", "few_stats_kernel",
                  "few_dz_kernel", "few_grads_kernel", "norm_fwd_kernel", "norm_bwd_kernel", "norm_reduce_kernel",
-                 "embed_fwd_kernel", "embed_sort_kernel", "embed_rows_kernel", "embed_join_kernel",
+                 "embed_fwd_kernel", "embed_few_kernel", "embed_sort_kernel", "embed_rows_kernel",
+                 "embed_join_kernel",
                  "beam_logits_kernel", "beam_select_kernel", "beam_score_kernel", "beam_rank_kernel",
                  "beam_reorder_kernel")
 

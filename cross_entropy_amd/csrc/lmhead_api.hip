@@ -1157,11 +1157,13 @@ int check_embed(const char* who, int64_t N, int64_t H, int64_t V) {
 // The gradient's sort: words in classes by their lowest bits, 256 (one
 // workgroup a CU) or as many as keep a class's counters within LDS.
 struct EmbedPlan {
+  bool few = false;
   int classes = lmh::kNumCUs, shift = 8, words = 0;
   size_t off_order = 0, off_pieces = 0, off_longs = 0, off_touched = 0, off_part = 0, bytes = 0;
 };
-EmbedPlan plan_embed(int64_t N, int64_t H, int64_t V) {
+EmbedPlan plan_embed(int64_t N, int64_t H, int64_t V, bool add) {
   EmbedPlan p;
+  p.few = N <= lmh::kFewIds && (add || V <= lmh::kFewWords);
   while (lmh::ceil_div(V, p.classes) > lmh::kMostClassWords) p.classes *= 2, ++p.shift;
   p.words = (int)lmh::ceil_div(V, p.classes);
   size_t at = 0;
@@ -1170,11 +1172,12 @@ EmbedPlan plan_embed(int64_t N, int64_t H, int64_t V) {
     at += (size_t)lmh::round_up(bytes, 256);
     return here;
   };
-  take(12 * (int64_t)p.classes);
-  p.off_order = take(4 * N);
-  p.off_pieces = take(16 * N);
-  p.off_longs = take(16 * (N / lmh::kPiece + 1));
-  p.off_touched = take((int64_t)p.classes * p.words);
+  const bool sorted = !p.few;
+  take(sorted ? 12 * (int64_t)p.classes : 0);
+  p.off_order = take(sorted ? 4 * N : 0);
+  p.off_pieces = take(sorted ? 16 * N : 0);
+  p.off_longs = take(16 * (sorted ? N / lmh::kPiece + 1 : N));
+  p.off_touched = take(sorted ? (int64_t)p.classes * p.words : 0);
   p.off_part = take(N > lmh::kPiece ? 2 * lmh::ceil_div(N, lmh::kPiece) * H * 4 : 0);
   p.bytes = at;
   return p;
@@ -1189,7 +1192,7 @@ int lmhead_logps_embed_workspace_bytes(int64_t N, int64_t H, int64_t V, size_t* 
   int rc = check_embed("embed", N, H, V);
   if (rc == LMH_OK) rc = check_backward_size(N, V);
   if (rc != LMH_OK) return rc;
-  *bytes_out = plan_embed(N, H, V).bytes;
+  *bytes_out = std::max(plan_embed(N, H, V, false).bytes, plan_embed(N, H, V, true).bytes);
   return ok();
 }
 
@@ -1221,11 +1224,11 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
   if (flags & ~(unsigned)LMH_BWD_ACCUMULATE_DW) return fail(LMH_ERR_ARGS, "embed_bwd: unknown flags 0x%x", flags);
   const bool add = (flags & LMH_BWD_ACCUMULATE_DW) != 0;
   if (N == 0 && add) return ok();
-  if (!dW || !workspace || (N > 0 && (!ids || !dy)))
+  const EmbedPlan p = plan_embed(N, H, V, add);
+  if (!dW || (!workspace && p.bytes > 0) || (N > 0 && (!ids || !dy)))
     return fail(LMH_ERR_NULL, "embed_bwd: ids, dy, dW and workspace must be non-NULL");
   if (!aligned(ids, 4) || !aligned(dy, type_size(y_type)) || !aligned(dW, type_size(g_type)) || !aligned(workspace, 16))
     return fail(LMH_ERR_UNSUPPORTED, "embed_bwd: a pointer is not aligned to its elements (workspace: 16 bytes)");
-  const EmbedPlan p = plan_embed(N, H, V);
   if (workspace_bytes < p.bytes)
     return fail(LMH_ERR_WORKSPACE, "embed_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, p.bytes);
   char* ws = static_cast<char*>(workspace);
@@ -1235,6 +1238,7 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
   a.y_f32 = y_type == LMH_TYPE_F32;
   a.g_f32 = g_type == LMH_TYPE_F32;
   a.add = add;
+  a.few = p.few;
   a.N = (int)N;
   a.H = (int)H;
   a.V = (int)V;
@@ -1401,6 +1405,9 @@ int lmhead_logps_beam_reorder(const void* states, void* out, const int32_t* pare
   for (int64_t n : {planes, rows, runs, steps, step_bytes})
     if (__builtin_mul_overflow(bytes, n, &bytes) || bytes >= (int64_t(1) << 43) || rows >= (int64_t(1) << 31))
       return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: the states hold 2^43 bytes or more");
+  const int64_t run = steps * step_bytes, places = planes * (rows / beams) * runs * lmh::ceil_div(run, 16);
+  if (run >= (int64_t(1) << 36) || planes * rows >= (int64_t(1) << 30) || places >= (int64_t(1) << 36))
+    return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a run of 2^36 bytes or more, 2^30 rows of all planes or 2^36 places of 16 bytes in a beam's runs");
   if (!states || !out || !parents) return fail(LMH_ERR_NULL, "beam_reorder: states, out and parents must be non-NULL");
   if (!aligned(parents, 4) || !aligned(lengths, 4))
     return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a pointer is not aligned to its elements");

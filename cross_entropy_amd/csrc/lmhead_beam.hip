@@ -288,9 +288,10 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelTeams = 128;    // of 8 threads each
 constexpr int kSelList = 2048;
 
-// The `keep` largest keys of items 0 .. n - 1 into kept[0 ..], sorted; returns
-// how many there are (keep, or all that are not 0). get(i) gives an item's key, 0
-// for none. Every team has a largest key, and the keep-th largest of those is a
+// The `keep` largest keys into kept[0 ..], sorted; returns how many there are
+// (keep, or all that are not 0). A thread has `per` items: key(k, load(k)) is
+// the key of its k-th, 0 for none, and first[] holds what load gives for the
+// first U. Every team has a largest key, and the keep-th largest of those is a
 // threshold that at least `keep` items reach, and few more do as a rule: those
 // are ranked. Should more than the list holds reach it (most of the best items
 // lie with few teams), the best are taken one after the other.
@@ -298,61 +299,69 @@ static_assert(kMostKept <= kSelTeams, "a threshold exists");
 struct Selection {
   uint64_t list[kSelList];
   uint64_t most[kSelTeams];
+  int rank[kSelTeams];
   uint64_t kept[kMostKept];
   uint64_t limit;
   int count;
 };
-template <class F>
-__device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, F get) {
-  const uint32_t tid = threadIdx.x;
+template <int U, class L, class K>
+__device__ __forceinline__ int select_best(Selection& s, int per, int keep, const float (&first)[U], L load, K key) {
+  const int tid = threadIdx.x;
+  constexpr int team = kSelThreads / kSelTeams;
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (k < per) f(key(k, first[k]));
+    for (int base = U; base < per; base += U) {
+      float z[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) z[k] = load(base + k);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (base + k < per) f(key(base + k, z[k]));
+    }
+  };
   auto largest = [&](uint64_t below) {
     uint64_t most = 0;
-    for (uint32_t base = tid; base < n; base += 4 * kSelThreads) {
-      uint64_t key[4];
+    each([&](uint64_t k) { most = k < below ? max(most, k) : most; });
 #pragma unroll
-      for (int k = 0; k < 4; ++k) key[k] = base + kSelThreads * k < n ? get(base + kSelThreads * k) : 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) most = key[k] < below ? max(most, key[k]) : most;
-    }
-#pragma unroll
-    for (int x = 1; x < kSelThreads / kSelTeams; x <<= 1) most = max(most, (uint64_t)__shfl_xor((unsigned long long)most, x));
+    for (int x = 1; x < team; x <<= 1) most = max(most, (uint64_t)__shfl_xor((unsigned long long)most, x));
     return most;
   };
   const uint64_t most = largest(~(uint64_t)0);
-  if (tid % (kSelThreads / kSelTeams) == 0) s.most[tid / (kSelThreads / kSelTeams)] = most;
+  if (tid % team == 0) s.most[tid / team] = most;
+  if (tid < kSelTeams) s.rank[tid] = 0;
   if (tid == 0) {
     s.limit = 1;
     s.count = 0;
   }
   __syncthreads();
-  if (tid < kSelTeams) {
-    const uint64_t mine = s.most[tid];
+  {
+    // the teams' ranks, 16 comparisons a thread
+    const uint64_t mine = s.most[tid % kSelTeams];
     int rank = 0;
-#pragma unroll 16
-    for (int k = 0; k < kSelTeams; ++k) rank += s.most[k] > mine;
-    if (rank == keep - 1 && mine > 0) s.limit = mine;
+#pragma unroll
+    for (int k = 0; k < kSelTeams / team; ++k) rank += s.most[tid / kSelTeams * (kSelTeams / team) + k] > mine;
+    if (rank > 0) atomicAdd(&s.rank[tid % kSelTeams], rank);
   }
   __syncthreads();
+  if (tid < kSelTeams && s.rank[tid] == keep - 1 && s.most[tid] > 0) s.limit = s.most[tid];
+  __syncthreads();
   const uint64_t limit = s.limit;
-  for (uint32_t base = tid; base < n; base += 4 * kSelThreads) {
-    uint64_t key[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) key[k] = base + kSelThreads * k < n ? get(base + kSelThreads * k) : 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (key[k] >= limit) {
-        const int at = atomicAdd(&s.count, 1);
-        if (at < kSelList) s.list[at] = key[k];
-      }
-  }
+  each([&](uint64_t k) {
+    if (k >= limit) {
+      const int at = atomicAdd(&s.count, 1);
+      if (at < kSelList) s.list[at] = k;
+    }
+  });
   __syncthreads();
   const int found = s.count;
   if (found > kSelList) {
     uint64_t below = ~(uint64_t)0;
     for (int r = 0; r < keep; ++r) {
-      __syncthreads();   // s.most and s.limit have been read
-      const uint64_t team = largest(below);
-      if (tid % (kSelThreads / kSelTeams) == 0) s.most[tid / (kSelThreads / kSelTeams)] = team;
+      __syncthreads();   // s.most has been read
+      const uint64_t mine = largest(below);
+      if (tid % team == 0) s.most[tid / team] = mine;
       __syncthreads();
       uint64_t best = 0;
       for (int k = 0; k < kSelTeams; ++k) best = max(best, s.most[k]);
@@ -362,12 +371,15 @@ __device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, F
     __syncthreads();
     return keep;   // more than kSelList items are not 0
   }
-  for (int i = tid; i < found; i += kSelThreads) {
-    const uint64_t mine = s.list[i];
+  for (int i0 = 0; i0 < found; i0 += kSelThreads / 16) {   // 16 threads a candidate
+    const int i = i0 + (tid >> 4);
+    const uint64_t mine = i < found ? s.list[i] : 0;
     int rank = 0;
-#pragma unroll 8
-    for (int k = 0; k < found; ++k) rank += s.list[k] > mine;
-    if (rank < keep) s.kept[rank] = mine;
+#pragma unroll 4
+    for (int k = tid & 15; k < found; k += 16) rank += s.list[k] > mine;
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) rank += __shfl_xor(rank, x);
+    if (i < found && (tid & 15) == 0 && rank < keep) s.kept[rank] = mine;
   }
   __syncthreads();
   return min(found, keep);
@@ -393,6 +405,19 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t group = blockIdx.x, row0 = group * b.beams;
   const int G = b.beams;
+  // a thread looks at sections of one row: its first ones are on their way
+  // while the records are merged
+  constexpr int U = 12;
+  const uint32_t n_sec = (uint32_t)b.n_sections;   // beams * V stays below 2^31
+  const int rows_at_once = kSelThreads / G;
+  const int my_row = tid % G, my_sec = tid / G;
+  const int per_a = my_sec < rows_at_once ? ((int)n_sec - my_sec + rows_at_once - 1) / rows_at_once : 0;
+  const float* sections = b.sections + row0 + my_row + min((uint32_t)my_sec, n_sec - 1) * b.ld;
+  const int64_t stride = rows_at_once * b.ld;
+  auto load_a = [&](int k) { return sections[max(0, min(k, per_a - 1)) * stride]; };
+  float first[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) first[k] = load_a(k);
   for (int r = wave; r < G; r += kSelThreads / 64) {
     const int64_t tok = row0 + r;
     float m = kNegBig;
@@ -443,23 +468,34 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
   }
   __syncthreads();
   const int keep = b.keep;
-  const uint32_t n_sec = (uint32_t)b.n_sections;   // beams * V stays below 2^31
   auto key = [&](float z, int r, uint32_t index) {
     const float x = shift[r];
     return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
   };
-  const int n1 = select_best(sel, n_sec * G, keep, [&](uint32_t i) {
-    const uint32_t s = i / (uint32_t)G, r = i - s * (uint32_t)G;
-    return key(b.sections[(int64_t)s * b.ld + row0 + r], r, r * n_sec + s);
+  const int n1 = select_best(sel, per_a, keep, first, load_a, [&](int k, float z) {
+    return key(z, my_row, (uint32_t)my_row * n_sec + (uint32_t)(my_sec + k * rows_at_once));
   });
   if (tid < n1) section[tid] = index_of(sel.kept[tid]);
   __syncthreads();
+  // the blocks of those sections
   const uint32_t per = b.per_section, n_blocks = (uint32_t)b.n_blocks;
-  const int n2 = select_best(sel, (uint32_t)n1 * per, keep, [&](uint32_t i) {
+  const uint32_t n2_items = (uint32_t)n1 * per;
+  constexpr int UB = 2;
+  uint32_t at_row[UB], at_block[UB];
+  float z[UB];
+#pragma unroll
+  for (int k = 0; k < UB; ++k) {   // kMostKept sections of at most 20 blocks
+    const uint32_t i = tid + kSelThreads * k;
+    at_row[k] = at_block[k] = 0;
+    z[k] = -INFINITY;
+    if (i >= n2_items) continue;
     const uint32_t at = section[i / per];
-    const uint32_t r = at / n_sec, blk = (at - r * n_sec) * per + i % per;
-    return blk < n_blocks ? key(b.blocks[(int64_t)blk * b.ld + row0 + r], r, r * n_blocks + blk) : (uint64_t)0;
-  });
+    at_row[k] = at / n_sec;
+    at_block[k] = (at - at_row[k] * n_sec) * per + i % per;
+    if (at_block[k] < n_blocks) z[k] = b.blocks[(int64_t)at_block[k] * b.ld + row0 + at_row[k]];
+  }
+  const int n2 = select_best(sel, UB, keep, z, [&](int) { return -INFINITY; },
+                             [&](int k, float v) { return key(v, at_row[k], at_row[k] * n_blocks + at_block[k]); });
   // those of the first C, and of the spare ones that are as good within the slack
   const bool in = tid < n2 && (tid < b.C || value_of(sel.kept[tid]) >= value_of(sel.kept[b.C - 1]) - slack);
   if (in) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
@@ -683,96 +719,97 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
 
 // ---------------------------------------------------------------------------
 // Reordering: rows of `runs` runs of `run_bytes` each, of which the first
-// lengths[parent] * step_bytes are in use (all without lengths). A thread owns
-// the 16 bytes at one place of a run for the whole group, reads what the
-// group's rows need of them and writes it: in place, every read of them comes
-// before any write, without a wait between threads. Groups above kReorderRows
-// rows go through LDS in place, and in batches of rows else.
+// lengths[parent] * step_bytes are in use (all without lengths). A wave takes 64
+// places of 16 bytes, at which it first reads what up to 16 rows of the group
+// take over, and then writes it. In place every read of a place so comes before
+// any write: larger groups take several waves of a workgroup and a barrier
+// between. Which row takes from which, and how much, is the same for all lanes.
 namespace {
 
 typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(1)));
 
-__device__ __forceinline__ u32x4a load16(const char* p, int n) {
-  if (n >= 16) return *reinterpret_cast<const u32x4a*>(p);
-  u32x4a v = {0, 0, 0, 0};
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-    if (k < n) v[k >> 2] |= (uint32_t)(uint8_t)p[k] << (8 * (k & 3));
-  return v;
-}
-__device__ __forceinline__ void store16(char* p, int n, u32x4a v) {
-  if (n >= 16) {
-    *reinterpret_cast<u32x4a*>(p) = v;
-    return;
+// The first n < 16 bytes at p, the lowest byte first, and back.
+__device__ __forceinline__ u32x4a load_bytes(const char* p, uint32_t n) {
+  uint64_t lo = 0, hi = 0;
+  for (uint32_t k = n; k-- > 0;) {
+    hi = (hi << 8) | (lo >> 56);
+    lo = (lo << 8) | (uint8_t)p[k];
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-    if (k < n) p[k] = (char)(v[k >> 2] >> (8 * (k & 3)));
+  return u32x4a{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+__device__ __forceinline__ void store_bytes(char* p, uint32_t n, u32x4a v) {
+  uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+  for (uint32_t k = 0; k < n; ++k) {
+    p[k] = (char)lo;
+    lo = (lo >> 8) | (hi << 56);
+    hi >>= 8;
+  }
 }
 
-constexpr int kReorderRows = 16;
-
-// bytes in use of the run that row j of the group takes over from row `from`,
-// 0 where it takes none
-__device__ __forceinline__ int64_t used_bytes(const ReorderArgs& a, int64_t from) {
-  if (a.lengths == nullptr) return a.run_bytes;
-  const int64_t n = a.lengths[from];
-  return (n < 0 ? 0 : n > a.steps ? a.steps : n) * a.step_bytes;
-}
-
-template <bool LDS>
+// TAIL: bytes in use are no multiple of 16 everywhere; those of a row's last
+// place are taken one by one.
+template <int RB, int WR, bool TAIL, bool STREAM>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(const ReorderArgs a) {
-  extern __shared__ u32x4 held[];   // LDS: [threads][beams]
-  const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (unit >= a.units) return;
-  // unit = ((plane, group), run, place)
-  const int64_t run_of = unit / a.places;
-  const int64_t at = (unit - run_of * a.places) * 16;
-  const int64_t pg = run_of / a.runs, run = run_of - pg * a.runs;
-  const int64_t groups = a.rows / a.beams;
-  const int64_t plane = pg / groups, group = pg - plane * groups;
-  const int64_t row0 = group * a.beams, row_bytes = a.runs * a.run_bytes;
-  const int64_t base = (plane * a.rows + row0) * row_bytes + run * a.run_bytes + at;
-  const char* in = static_cast<const char*>(a.states) + base;
-  char* out = static_cast<char*>(a.out) + base;
-  const bool place = a.states == a.out;
+  constexpr int CW = 4 / WR;   // waves side by side
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave % WR;
   const int G = a.beams;
-  // the bytes at this place that row j takes over, and from which row
-  auto source = [&](int j, int& from) {
-    const int64_t p = (int64_t)a.parents[row0 + j] - row0;
-    from = (int)p;
-    if (p < 0 || p >= G || (place && p == j)) return 0;
-    const int64_t n = used_bytes(a, row0 + p) - at;
-    return n <= 0 ? 0 : n >= 16 ? 16 : (int)n;
-  };
-  if (LDS) {
-    u32x4* mine = held + (int64_t)threadIdx.x * G;
-    for (int j = 0; j < G; ++j) {
-      int from;
-      const int n = source(j, from);
-      if (n > 0) mine[j] = load16(in + from * row_bytes, n);
+  const bool place = a.states == a.out;
+  // block = ((plane, group), places)
+  const uint32_t block = (uint32_t)xcd_remap(blockIdx.x, gridDim.x), pg = block / a.blocks, groups = (uint32_t)(a.rows / G);
+  if (pg >= a.planes * groups) return;
+  const int64_t plane = pg / groups, row0 = (int64_t)(pg - (uint32_t)plane * groups) * G;
+  const int64_t row_bytes = a.runs * a.run_bytes;
+  const int64_t base = (plane * a.rows + row0) * row_bytes;
+  const char* in = static_cast<const char*>(a.states) + base;
+  char* out = static_cast<char*>(a.out) + base + part * RB * row_bytes;
+  int from[RB];
+  uint32_t whole[RB], rest[RB];   // places of a run that the row takes over, and bytes of one more
+#pragma unroll
+  for (int j = 0; j < RB; ++j) {
+    const int row = part * RB + j;
+    const int p = row < G ? (int)(a.parents[row0 + row] - row0) : -1;   // rows stay below 2^31
+    const bool takes = p >= 0 && p < G && !(place && p == row);
+    from[j] = takes ? p : 0;
+    int64_t n = takes ? a.run_bytes : 0;
+    if (takes && a.lengths != nullptr) {
+      const int64_t len = a.lengths[row0 + p];
+      n = (len < 0 ? 0 : len > a.steps ? a.steps : len) * a.step_bytes;
     }
-    for (int j = 0; j < G; ++j) {
-      int from;
-      const int n = source(j, from);
-      if (n > 0) store16(out + j * row_bytes, n, mine[j]);
-    }
-    return;
+    whole[j] = (uint32_t)(n >> 4);
+    rest[j] = (uint32_t)n & 15;
   }
-  for (int j0 = 0; j0 < G; j0 += kReorderRows) {
-    u32x4a v[kReorderRows];
-    int n[kReorderRows];
+  const int64_t units = a.runs * a.places;
+  const int64_t unit = (int64_t)(block - pg * a.blocks) * (64 * CW) + (wave / WR) * 64 + lane;
+  uint32_t at = (uint32_t)unit;   // the place in the run; a run has less than 2^32
+  int64_t offset = unit * 16;     // in the row
+  if (a.runs > 1) {
+    const int64_t run = units >> 32 ? unit / a.places : (int64_t)((uint32_t)unit / (uint32_t)a.places);
+    at = (uint32_t)(unit - run * a.places);
+    offset = run * a.run_bytes + (int64_t)at * 16;
+  }
+  if (unit >= units) at = ~0u;   // past the row: nothing is in use there
+  u32x4a v[RB];
 #pragma unroll
-    for (int j = 0; j < kReorderRows; ++j) {
-      n[j] = 0;
-      if (j0 + j >= G) continue;
-      int from;
-      n[j] = source(j0 + j, from);
-      if (n[j] > 0) v[j] = load16(in + from * row_bytes, n[j]);
+  for (int j = 0; j < RB; ++j) {
+    if (j > 0 && from[j] == from[j - 1] && whole[j] == whole[j - 1] && rest[j] == rest[j - 1]) {
+      v[j] = v[j - 1];   // children of one parent come one after the other
+      continue;
     }
+    const char* p = in + from[j] * row_bytes + offset;
+    if (at < whole[j]) v[j] = *reinterpret_cast<const u32x4a*>(p);
+    else if (TAIL && at == whole[j]) v[j] = load_bytes(p, rest[j]);
+  }
+  if (WR > 1 && place) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kReorderRows; ++j)
-      if (n[j] > 0) store16(out + (j0 + j) * row_bytes, n[j], v[j]);
+  for (int j = 0; j < RB; ++j) {
+    char* p = out + j * row_bytes + offset;
+    if (at < whole[j]) {
+      if (STREAM) __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4a*>(p));
+      else *reinterpret_cast<u32x4a*>(p) = v[j];
+    }
+    if (TAIL && at == whole[j]) store_bytes(p, rest[j], v[j]);
   }
 }
 
@@ -781,16 +818,29 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(const ReorderArgs a) 
 hipError_t launch_beam_reorder(ReorderArgs a, hipStream_t stream) {
   a.run_bytes = a.steps * a.step_bytes;
   a.places = (a.run_bytes + 15) / 16;
-  a.units = a.planes * (a.rows / a.beams) * a.runs * a.places;
-  if (a.units == 0) return hipSuccess;
+  const int64_t groups = a.planes * (a.rows / a.beams), places = a.runs * a.places;
+  if (groups * places == 0) return hipSuccess;
   trace_begin(stream);
-  if (a.states == a.out && a.beams > kReorderRows) {
-    const int threads = 64;
-    hipLaunchKernelGGL((beam_reorder_kernel<true>), dim3((unsigned)((a.units + threads - 1) / threads)), dim3(threads),
-                       (size_t)threads * a.beams * 16, stream, a);
-  } else {
-    hipLaunchKernelGGL((beam_reorder_kernel<false>), dim3((unsigned)((a.units + 255) / 256)), dim3(256), 0, stream, a);
-  }
+  const bool streamed = (double)a.planes * a.rows * a.runs * a.run_bytes > kStreamed;
+  auto launch = [&](auto rb, auto wr) {
+    const int64_t at_once = 64 * (4 / wr());
+    a.blocks = (uint32_t)((places + at_once - 1) / at_once);
+    const dim3 grid((unsigned)((groups * a.blocks + 7) / 8 * 8));
+    auto kind = [&](auto tail, auto past) {
+      hipLaunchKernelGGL((beam_reorder_kernel<rb(), wr(), tail(), past()>), grid, dim3(256), 0, stream, a);
+    };
+    std::true_type yes;
+    std::false_type no;
+    if (a.step_bytes % 16 != 0) streamed ? kind(yes, yes) : kind(yes, no);
+    else streamed ? kind(no, yes) : kind(no, no);
+  };
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 16> most{};
+  if (a.beams <= 4) launch(std::integral_constant<int, 4>{}, one);
+  else if (a.beams <= 8) launch(std::integral_constant<int, 8>{}, one);
+  else if (a.beams <= 16) launch(most, one);
+  else if (a.beams <= 32) launch(most, std::integral_constant<int, 2>{});
+  else launch(most, std::integral_constant<int, 4>{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kBeamReorder, stream, 0.0, 2.0 * a.planes * a.rows * a.runs * (double)a.run_bytes);

@@ -4,26 +4,35 @@
 //   y_i  = scale W[id_i]                      (0 for an id outside [0, V))
 //   dW_v (+)= scale sum_{i: id_i = v} dy_i
 //
-// The gradient's sums run over the tokens of a word in the tokens' order, so
-// the tokens are first sorted by word (stably), and no atomics take part in
-// sums: results depend on the arguments alone.
+// The gradient's sums run over the tokens of a word in the tokens' order, in
+// pieces of at most kPiece tokens whose sums are then added in order, and no
+// atomics take part in sums: results depend on the arguments alone. Two ways
+// lead there.
 //
+// Many tokens, sorted by word first (stably):
 //   sort   workgroup c owns the words v with v mod NC = c. Words that follow one
 //          another fall to different workgroups, so a table sorted by frequency
 //          loads them alike. Each scans all ids (its 16 waves a sixteenth each),
 //          counts those of its words in LDS and those of lower classes (which is
 //          where its part of the order begins: no word passes between
 //          workgroups), and scans again to place its tokens.
-//   rows   a word's tokens are cut into pieces of at most kPiece; a wave sums one
-//          piece over 512 columns, straight into dW where it is the word's only
-//          one, into a float32 partial row else. Rows without a token are zeroed.
+//   rows   a wave sums one piece over 64 groups of columns, straight into dW
+//          where it is the word's only one, into a float32 partial row else, and
+//          in between zeroes rows without a token.
 //   join   partial rows of the words of several pieces, in order.
+//
+// Up to kFewIds tokens, counted: a workgroup per token looks at all ids for its
+// own word and knows from the counts whether a piece begins with its token, of
+// which tokens, and where the piece lies in the sorted order; other workgroups
+// look for the words of 64 rows each and zero the rest. N^2 comparisons, but one
+// launch, or two where a word may have several pieces.
 //
 // All sums are float32; a bf16 gradient is rounded once, when stored.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lmhead_internal.h"
 
@@ -35,46 +44,61 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return (uint32_t)narrow(lo) | ((uint32_t)narrow(hi) << 16);
 }
 
-// Eight elements of a row, at their own alignment: rows of an odd length start
-// off any larger boundary, which global memory accepts.
+// G elements of a row, at their own alignment: rows of an odd length start off
+// any larger boundary, which global memory accepts. G is 8 (16 bytes a lane)
+// where both sides are bf16 and 4 (16 bytes of the float32 side) else, so that
+// a wave's accesses cover whole lines of the larger side. TAIL: rows are no
+// multiple of G, and their last elements are taken one by one.
 template <int WORDS>
 struct __attribute__((packed, aligned(2))) Raw {
   uint32_t w[WORDS];
 };
-template <bool F32>
-struct Eight {
-  Raw<F32 ? 8 : 4> raw;
-  // n < 8: the last elements of a row
+template <bool F32, int G, bool TAIL>
+struct Part {
+  static constexpr int kWords = G * (F32 ? 4 : 2) / 4;
+  Raw<kWords> raw;
+  // n < G: the last elements of a row
   __device__ __forceinline__ void load(const void* row, int at, int n) {
-    if (n >= 8) {
-      raw = *reinterpret_cast<const Raw<F32 ? 8 : 4>*>(static_cast<const char*>(row) + (int64_t)at * (F32 ? 4 : 2));
+    if (!TAIL || n >= G) {
+      raw = *reinterpret_cast<const Raw<kWords>*>(static_cast<const char*>(row) + (int64_t)at * (F32 ? 4 : 2));
       return;
     }
-    uint32_t u[8];
+    uint32_t u[G];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < G; ++k) {
       u[k] = 0;
       if (k < n) u[k] = F32 ? static_cast<const uint32_t*>(row)[at + k] : static_cast<const uint16_t*>(row)[at + k];
     }
 #pragma unroll
-    for (int k = 0; k < (F32 ? 8 : 4); ++k) raw.w[k] = F32 ? u[k] : u[2 * k & 7] | (u[(2 * k + 1) & 7] << 16);
+    for (int k = 0; k < kWords; ++k) raw.w[k] = F32 ? u[k] : u[2 * k % G] | (u[(2 * k + 1) % G] << 16);
   }
   __device__ __forceinline__ float at(int k) const {
     if (F32) return __uint_as_float(raw.w[k]);
     const uint32_t w = raw.w[k / 2];
     return __uint_as_float((k & 1) ? (w & 0xFFFF0000u) : (w << 16));
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
+  __device__ __forceinline__ void set(const float (&v)[G]) {
 #pragma unroll
-    for (int k = 0; k < 8; k += F32 ? 1 : 2) raw.w[F32 ? k : k / 2] = F32 ? __float_as_uint(v[k]) : narrow2(v[k], v[k + 1]);
+    for (int k = 0; k < G; k += F32 ? 1 : 2) raw.w[F32 ? k : k / 2] = F32 ? __float_as_uint(v[k]) : narrow2(v[k], v[k + 1]);
   }
+  // STREAM: past the caches, for what they cannot hold anyway
+  template <bool STREAM = false>
   __device__ __forceinline__ void store(void* row, int at, int n) const {
-    if (n >= 8) {
-      *reinterpret_cast<Raw<F32 ? 8 : 4>*>(static_cast<char*>(row) + (int64_t)at * (F32 ? 4 : 2)) = raw;
+    if (!TAIL || n >= G) {
+      char* to = static_cast<char*>(row) + (int64_t)at * (F32 ? 4 : 2);
+      if constexpr (STREAM) {
+        typedef uint32_t words __attribute__((ext_vector_type(kWords), aligned(2)));
+        words w;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = raw.w[k];
+        __builtin_nontemporal_store(w, reinterpret_cast<words*>(to));
+      } else {
+        *reinterpret_cast<Raw<kWords>*>(to) = raw;
+      }
       return;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < G; ++k) {
       if (k >= n) break;
       if (F32) static_cast<uint32_t*>(row)[at + k] = raw.w[k];
       else static_cast<uint16_t*>(row)[at + k] = (uint16_t)(raw.w[k / 2] >> (16 * (k & 1)));
@@ -82,15 +106,16 @@ struct Eight {
   }
 };
 
-// Forward: a thread takes U groups of 8 elements, 256 apart in the row-major
+// Forward: a thread takes U groups of G elements, 256 apart in the row-major
 // order of all of them.
-template <bool WF32, bool YF32, int U>
+template <bool WF32, bool YF32, bool TAIL, bool STREAM, int U>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedFwdArgs a) {
-  const int per = (a.H + 7) / 8;   // groups of a row
+  constexpr int G = WF32 || YF32 ? 4 : 8;
+  const int per = (a.H + G - 1) / G;   // groups of a row
   const int64_t g0 = (int64_t)blockIdx.x * (256 * U);
   const int64_t row0 = g0 / per;
   const uint32_t off = (uint32_t)(g0 - row0 * per) + threadIdx.x;
-  Eight<WF32> in[U];
+  Part<WF32, G, TAIL> in[U];
   int64_t row[U];
   int col[U];
   bool live[U];
@@ -99,7 +124,7 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedFwdArgs a) {
     const uint32_t local = off + 256 * u;
     const uint32_t r = local / (uint32_t)per;
     row[u] = row0 + r;
-    col[u] = 8 * (int)(local - r * (uint32_t)per);
+    col[u] = G * (int)(local - r * (uint32_t)per);
     const int id = a.ids[min(row[u], a.N - 1)];
     live[u] = id >= 0 && id < a.V;
     in[u].load(static_cast<const char*>(a.W) + (int64_t)(live[u] ? id : 0) * a.H * (WF32 ? 4 : 2), col[u], a.H - col[u]);
@@ -107,19 +132,19 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedFwdArgs a) {
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (row[u] >= a.N) continue;
-    float v[8];
+    float v[G];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = live[u] ? in[u].at(k) * a.scale : 0.0f;
-    Eight<YF32> out;
+    for (int k = 0; k < G; ++k) v[k] = live[u] ? in[u].at(k) * a.scale : 0.0f;
+    Part<YF32, G, TAIL> out;
     out.set(v);
-    out.store(static_cast<char*>(a.y) + row[u] * a.H * (YF32 ? 4 : 2), col[u], a.H - col[u]);
+    out.template store<STREAM>(static_cast<char*>(a.y) + row[u] * a.H * (YF32 ? 4 : 2), col[u], a.H - col[u]);
   }
 }
 
 constexpr int kSortWaves = 16;
 
 // Exclusive sum over the workgroup's threads; total is the whole sum. `red`
-// holds kSortWaves words.
+// holds a word per wave.
 __device__ __forceinline__ int block_scan(int x, int* red, int& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int s = x;
@@ -140,37 +165,70 @@ __device__ __forceinline__ int block_scan(int x, int* red, int& total) {
   return base + s - x;
 }
 
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The tokens of the class that a wave found in its part of the ids, while they
+// fit: what it places them from then, and not from the ids again.
 template <int LC>
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const EmbedBwdArgs a) {
   __shared__ int cnt[kSortWaves][LC];   // tokens of the class's word l in the wave's part, then where the wave's next goes
   __shared__ int red[kSortWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kFound = LC > 1024 ? 192 : 512;   // within 160 KB of LDS
+  __shared__ int2 found[kSortWaves][kFound];      // (token, word)
+  const int tid = threadIdx.x, lane = tid & 63;
   const int c = blockIdx.x, mask = a.classes - 1, shift = a.class_shift;
+  // the part of the ids that a wave takes, turned by the class: workgroups side by side read different ones
+  const int wave = __builtin_amdgcn_readfirstlane(((tid >> 6) + c) % kSortWaves);
   const int lc = a.class_words;   // <= LC
   for (int i = tid; i < kSortWaves * LC; i += 64 * kSortWaves) (&cnt[0][0])[i] = 0;
   __syncthreads();
   const int part = (a.N + kSortWaves - 1) / kSortWaves;
   const int i0 = min(a.N, wave * part), i1 = min(a.N, i0 + part);
-  int lower = 0;
-#pragma unroll 4
-  for (int i = i0 + lane; i < i1; i += 64) {
-    const int id = a.ids[i];
-    const bool live = id >= 0 && id < a.V;
-    const int k = id & mask;
-    lower += live && k < c;
-    if (live && k == c) atomicAdd(&cnt[wave][id >> shift], 1);
-  }
+  constexpr int D = 16;   // vectors of 64 ids in flight
+  int lower = 0, n_found = 0;
+  // whole batches are loaded without a bound, which costs as much as all the
+  // rest: the scan is bound by the vector unit
+  auto scan = [&](int i, auto whole) {
+    const int32_t* from = a.ids + i;
+    int id[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) id[d] = whole() ? from[64 * d + lane] : a.ids[min(i + 64 * d + lane, i1 - 1)];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const bool live = (uint32_t)id[d] < (uint32_t)a.V && (whole() || i + 64 * d + lane < i1);
+      const int k = id[d] & mask;
+      lower += __popcll(__ballot(live && k < c));   // on the scalar unit
+      const bool mine = live && k == c;
+      const uint64_t all = __ballot(mine);
+      if (all == 0) continue;
+      const int at = n_found + __popcll(all & ((1ull << lane) - 1));
+      if (mine) {
+        atomicAdd(&cnt[wave][id[d] >> shift], 1);
+        if (at < kFound) found[wave][at] = make_int2(i + 64 * d + lane, id[d]);
+      }
+      n_found += __popcll(all);
+    }
+  };
+  int at_id = i0;
+  for (; at_id + 64 * D <= i1; at_id += 64 * D) scan(at_id, std::true_type{});
+  if (at_id < i1) scan(at_id, std::false_type{});
   int below;
-  block_scan(lower, red, below);
-  // the class's words in order: their tokens' places, and their pieces
+  block_scan(lane == 0 ? lower : 0, red, below);
+  // the class's words in order: their tokens' places
   constexpr int per = (LC + 64 * kSortWaves - 1) / (64 * kSortWaves);
-  int tot[per], n_tok = 0, n_pc = 0, n_lg = 0;
+  int of[per][kSortWaves], tot[per], n_tok = 0, n_pc = 0, n_lg = 0;
 #pragma unroll
   for (int k = 0; k < per; ++k) {
     const int l = tid * per + k;
     tot[k] = 0;
-    if (l < lc)
-      for (int w = 0; w < kSortWaves; ++w) tot[k] += cnt[w][l];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      of[k][w] = l < lc ? cnt[w][l] : 0;
+      tot[k] += of[k][w];
+    }
     n_tok += tot[k];
     n_pc += (tot[k] + kPiece - 1) / kPiece;
     n_lg += tot[k] > kPiece;
@@ -179,201 +237,464 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const Embed
   int at = below + block_scan(n_tok, red, own);
   int pc = below + block_scan(n_pc, red, pieces);
   int lg = below / kPiece + block_scan(n_lg, red, longs);
-#pragma unroll
-  for (int k = 0; k < per; ++k) {
-    const int l = tid * per + k;
-    if (l >= lc) break;
-    const int64_t v = ((int64_t)l << shift) + c;
-    if (v < a.V) a.touched[(int64_t)c * lc + l] = tot[k] > 0;
+  {
     int to = at;
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int n = cnt[w][l];
-      cnt[w][l] = to;
-      to += n;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      const int l = tid * per + k;
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        if (l < lc) cnt[w][l] = to;
+        to += of[k][w];
+      }
     }
-    const bool several = tot[k] > kPiece;
-    if (several) a.longs[lg++] = make_int4(at, tot[k], (int)v, 0);
-    for (int r = 0; r < tot[k]; r += kPiece)
-      a.pieces[pc++] = make_int4(at + r, min(kPiece, tot[k] - r), (int)v,
-                                 several ? 2 * ((at + r) / kPiece) + (r == 0) : -1);
-    at += tot[k];
   }
+  __syncthreads();
+  // the pieces, and which rows have a token: after the last barrier, none of
+  // which then waits for these stores
   if (tid == 0) {
     a.counts[3 * c] = pieces;
     a.counts[3 * c + 1] = below;
     a.counts[3 * c + 2] = longs;
   }
-  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < per; ++k) {
+    const int l = tid * per + k;
+    const int v = (l << shift) + c;
+    if (l < lc && v < a.V) a.touched[(int64_t)c * lc + l] = tot[k] > 0;
+    const bool several = tot[k] > kPiece;
+    if (tot[k] > 0 && !several) a.pieces[pc] = make_int4(at, tot[k], v, -1);
+    if (several) a.longs[lg++] = make_int4(at, tot[k], v, 0);
+    // a long word's pieces are listed by the whole wave
+    uint64_t todo = __ballot(several);
+    while (todo != 0) {
+      const int who = __builtin_ctzll(todo);
+      todo &= todo - 1;
+      const int from = __builtin_amdgcn_readlane(at, who), n = __builtin_amdgcn_readlane(tot[k], who);
+      const int word = __builtin_amdgcn_readlane(v, who), to_pc = __builtin_amdgcn_readlane(pc, who);
+      for (int r = lane * kPiece; r < n; r += 64 * kPiece)
+        a.pieces[to_pc + r / kPiece] = make_int4(from + r, min(kPiece, n - r), word, 2 * ((from + r) / kPiece) + (r == 0));
+    }
+    pc += (tot[k] + kPiece - 1) / kPiece;
+    at += tot[k];
+  }
   // The wave's tokens to their places: a wave's counters are its own, and
   // tokens of one word among the 64 in flight go in lane order.
-  for (int i = i0; i < i1; i += 64) {
-    const int id = i + lane < i1 ? a.ids[i + lane] : -1;
-    const bool mine = id >= 0 && id < a.V && (id & mask) == c;
+  auto place = [&](bool mine, int token, int id) {
     uint64_t todo = __ballot(mine);
     while (todo != 0) {
       const int word = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
       const uint64_t same = __ballot(mine && id == word);
       const int to = cnt[wave][word >> shift];
-      if (mine && id == word) a.order[to + __popcll(same & ((1ull << lane) - 1))] = i + lane;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      if (mine && id == word) a.order[to + __popcll(same & ((1ull << lane) - 1))] = token;
+      wave_fence();
       if (lane == 0) cnt[wave][word >> shift] = to + __popcll(same);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_fence();
       todo &= ~same;
     }
+  };
+  if (n_found <= kFound) {
+    for (int k = 0; k < n_found; k += 64) {
+      const int2 f = found[wave][min(k + lane, n_found - 1)];
+      place(k + lane < n_found, f.x, f.y);
+    }
+    return;
+  }
+  for (int i = i0; i < i1; i += 64 * D) {
+    int id[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) id[d] = a.ids[min(i + 64 * d + lane, i1 - 1)];   // a branch per load would wait for each
+#pragma unroll
+    for (int d = 0; d < D; ++d) id[d] = i + 64 * d + lane < i1 ? id[d] : -1;
+#pragma unroll
+    for (int d = 0; d < D; ++d) place(id[d] >= 0 && id[d] < a.V && (id[d] & mask) == c, i + 64 * d + lane, id[d]);
   }
 }
 
 // scale times the sum, onto what the row holds where it is added to.
-template <bool GF32>
-__device__ __forceinline__ void put_row(const EmbedBwdArgs& a, int64_t v, int col, int n, float (&s)[8]) {
-  char* row = static_cast<char*>(a.dW) + v * a.H * (GF32 ? 4 : 2);
-  Eight<GF32> out;
-  if (a.add) {
+template <bool GF32, int G, bool TAIL>
+__device__ __forceinline__ void put_row(void* dW, bool add, float scale, int H, int64_t v, int col, int n, float (&s)[G]) {
+  char* row = static_cast<char*>(dW) + v * H * (GF32 ? 4 : 2);
+  Part<GF32, G, TAIL> out;
+  if (add) {
     out.load(row, col, n);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] = fmaf(s[k], a.scale, out.at(k));
+    for (int k = 0; k < G; ++k) s[k] = fmaf(s[k], scale, out.at(k));
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] *= a.scale;
+    for (int k = 0; k < G; ++k) s[k] *= scale;
   }
   out.set(s);
   out.store(row, col, n);
 }
 
-constexpr int kZeroRows = 8;   // rows that a wave looks at together
+// Sums the rows row_of(0) .. row_of(count - 1) of dy over CB groups of columns
+// (col, col + 64 G, ...) and stores them: into dW's row v, or (slot >= 0) into a
+// partial row. A group past the row reads its beginning along and is not stored.
+template <bool YF32, bool GF32, int G, bool TAIL, bool STREAM, int CB, class F>
+__device__ __forceinline__ void sum_piece(const EmbedBwdArgs& a, int col, int count, int64_t v, int slot, F row_of) {
+  const int H = a.H;
+  int at[CB];
+  float s[CB][G];
+  Part<GF32, G, TAIL> old[CB];
+  const bool add = a.add && slot < 0;
+  char* into = static_cast<char*>(a.dW) + v * H * (GF32 ? 4 : 2);
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    at[c] = col + 64 * G * c < H ? col + 64 * G * c : 0;
+#pragma unroll
+    for (int k = 0; k < G; ++k) s[c][k] = 0.0f;
+    if (add) old[c].load(into, at[c], H - at[c]);
+  }
+  auto row = [&](int t) { return static_cast<const char*>(a.dy) + (int64_t)row_of(t) * H * (YF32 ? 4 : 2); };
+  constexpr int D = 8 / CB;
+  int t = 0;
+  for (; t + D <= count; t += D) {
+    Part<YF32, G, TAIL> x[D][CB];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int c = 0; c < CB; ++c) x[d][c].load(row(t + d), at[c], H - at[c]);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int k = 0; k < G; ++k) s[c][k] += x[d][c].at(k);
+  }
+  for (; t < count; ++t) {
+    Part<YF32, G, TAIL> x[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) x[c].load(row(t), at[c], H - at[c]);
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int k = 0; k < G; ++k) s[c][k] += x[c].at(k);
+  }
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    if (col + 64 * G * c >= H) continue;
+    const int n = H - at[c];
+    if (slot >= 0) {
+      Part<true, G, TAIL> out;
+      out.set(s[c]);
+      out.store(a.part + (int64_t)slot * H, at[c], n);
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < G; ++k) s[c][k] = add ? fmaf(s[c][k], a.scale, old[c].at(k)) : s[c][k] * a.scale;
+    Part<GF32, G, TAIL> out;
+    out.set(s[c]);
+    out.template store<STREAM>(into, at[c], n);
+  }
+}
 
-template <bool YF32, bool GF32>
-__global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedBwdArgs a) {
-  __shared__ int first[kMostClasses + 1];   // pieces of the classes before
+// Zeroes the rows v of dW without a token (has(v) is 0 for them), as workgroup
+// `me` of `blocks`: the table as it lies, 16 bytes a thread and 4 KB a
+// workgroup at once, the workgroups side by side. Walked by rows, it takes 141
+// us where this takes 115 (778 MB). The flags of the next kZeroAhead places are
+// on their way while the last ones' are used.
+constexpr int kZeroAhead = 8;
+template <bool GF32, class F>
+__device__ __forceinline__ void zero_rows(const EmbedBwdArgs& a, int me, int blocks, F has) {
+  constexpr int size = GF32 ? 4 : 2;
+  typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
+  const uint32_t row_bytes = (uint32_t)a.H * size;
+  const int64_t bytes = (int64_t)a.V * row_bytes;
+  const uint32_t step = (uint32_t)blocks * 4096, step_rows = step / row_bytes, step_rest = step - step_rows * row_bytes;
+  const uint32_t first = (uint32_t)me * 4096 + threadIdx.x * 16;
+  uint32_t row = first / row_bytes, rest = first - row * row_bytes;   // of the next place whose flag is fetched
+  int64_t at = first;
+  uint32_t rows[kZeroAhead], rests[kZeroAhead];
+  bool keep[kZeroAhead];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int k = 0; k < kZeroAhead; ++k) {
+      rows[k] = row;
+      rests[k] = rest;
+      keep[k] = has((int)min(row, (uint32_t)a.V - 1)) != 0;
+      row += step_rows;
+      rest += step_rest;
+      if (rest >= row_bytes) {
+        rest -= row_bytes;
+        ++row;
+      }
+    }
+  };
+  fetch();
+  while (at < bytes) {
+    uint32_t r[kZeroAhead], o[kZeroAhead];
+    bool kept[kZeroAhead];
+#pragma unroll
+    for (int k = 0; k < kZeroAhead; ++k) {
+      r[k] = rows[k];
+      o[k] = rests[k];
+      kept[k] = keep[k];
+    }
+    fetch();
+#pragma unroll
+    for (int k = 0; k < kZeroAhead; ++k, at += step) {
+      if (at >= bytes) break;
+      char* to = static_cast<char*>(a.dW) + at;
+      if (o[k] + 16 <= row_bytes) {
+        if (!kept[k]) __builtin_nontemporal_store(words{0, 0, 0, 0}, reinterpret_cast<words*>(to));
+        continue;
+      }
+      // across the end of a row: element by element
+      uint32_t v = r[k], left = row_bytes - o[k];
+      bool full = kept[k];
+      for (uint32_t e = 0; e < 16 && at + e < bytes; e += size) {
+        if (left == 0) {
+          full = has((int)++v) != 0;
+          left = row_bytes;
+        }
+        if (!full) {
+          if (GF32) *reinterpret_cast<uint32_t*>(to + e) = 0;
+          else *reinterpret_cast<uint16_t*>(to + e) = 0;
+        }
+        left -= size;
+      }
+    }
+  }
+}
+
+// The partial rows of a long word (first place in the order, tokens) over one
+// wave's columns, by a workgroup: its waves take runs of neighbouring pieces,
+// whose sums are added in order.
+constexpr int kJoinWaves = 8;
+template <bool GF32, bool TAIL>
+__device__ __forceinline__ void join_row(const EmbedBwdArgs& a, int first, int tokens, int64_t v, int col, float4 (&xch)[kJoinWaves][64]) {
+  constexpr int G = 4;
+  const int H = a.H, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool in = col < H;
+  col = in ? col : 0;
+  const int n = H - col;
+  const int pieces = (tokens + kPiece - 1) / kPiece, slot = first / kPiece;
+  const int run = (pieces + kJoinWaves - 1) / kJoinWaves, p0 = wave * run, p1 = min(pieces, p0 + run);
+  float s[G] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int p = p0; p < p1; ++p) {
+    Part<true, G, TAIL> x;
+    x.load(a.part + (int64_t)(2 * (slot + p) + (p == 0)) * H, col, n);
+#pragma unroll
+    for (int k = 0; k < G; ++k) s[k] += x.at(k);
+  }
+  xch[wave][lane] = make_float4(s[0], s[1], s[2], s[3]);
+  __syncthreads();
+  if (wave == 0 && in) {
+#pragma unroll
+    for (int w = 1; w < kJoinWaves; ++w) {
+      const float4 o = xch[w][lane];
+      s[0] += o.x;
+      s[1] += o.y;
+      s[2] += o.z;
+      s[3] += o.w;
+    }
+    put_row<GF32, G, TAIL>(a.dW, a.add, a.scale, H, v, col, n, s);
+  }
+  __syncthreads();   // read before the next word's
+}
+
+constexpr int kRowGroups = 1;   // groups of columns that a wave sums at once
+constexpr int kRowsPerCU = 5;   // workgroups that fit
+constexpr int kZeroBlocks = kNumCUs;   // those that zero rows, one a CU beside four that sum
+
+// The first kZeroBlocks workgroups zero rows, unless dW is added to; the others
+// sum pieces.
+template <bool YF32, bool GF32, bool TAIL>
+__global__ __launch_bounds__(256, kRowsPerCU) void embed_rows_kernel(const EmbedBwdArgs a) {
+  constexpr int G = YF32 || GF32 ? 4 : 8;
+  __shared__ int first[kMostClasses];   // pieces of the classes before
   __shared__ int red[4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int H = a.H;
+  const int zero_blocks = a.add ? 0 : kZeroBlocks;
+  if ((int)blockIdx.x < zero_blocks) {
+    zero_rows<GF32>(a, blockIdx.x, kZeroBlocks, [&](int v) {
+      return a.touched[(int64_t)(v & (a.classes - 1)) * a.class_words + (v >> a.class_shift)];
+    });
+    return;
+  }
   int total;
   {
-    const int per = (a.classes + 255) / 256;
+    const int per = a.classes / 256;
     int n = 0;
-    for (int k = 0; k < per; ++k) n += tid * per + k < a.classes ? a.counts[3 * (tid * per + k)] : 0;
+    for (int k = 0; k < per; ++k) n += a.counts[3 * (tid * per + k)];
     int at = block_scan(n, red, total);
     for (int k = 0; k < per; ++k) {
-      if (tid * per + k >= a.classes) break;
       first[tid * per + k] = at;
       at += a.counts[3 * (tid * per + k)];
     }
     __syncthreads();
   }
-  const int chunks = (H + 511) / 512;
-  const int64_t units = (int64_t)total * chunks;
-  const int64_t waves = (int64_t)gridDim.x * 4, me = (int64_t)blockIdx.x * 4 + wave;
-  for (int64_t u = me; u < units; u += waves) {
-    const int g = (int)(u / chunks);
-    int col = ((int)(u - (int64_t)g * chunks) * 64 + lane) * 8;
-    const bool in = col < H;
-    col = in ? col : 0;   // lanes past the row read along: every lane's token is read by the others
-    int c = 0;   // the last class that begins at or before g
-    for (int step = a.classes >> 1; step > 0; step >>= 1)
+  // piece g: the last class that begins at or before it, of the first 256 by
+  // steps of `per` at once
+  const int per = a.classes / 256;
+  int mark[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mark[k] = first[(64 * k + lane) * per];
+  auto piece = [&](int g) {
+    if (g >= total) return make_int4(0, 1, 0, -1);
+    int c = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c += __popcll(__ballot(mark[k] <= g));
+    c *= per;
+    for (int step = per >> 1; step > 0; step >>= 1)
       if (first[c + step] <= g) c += step;
-    const int4 p = a.pieces[a.counts[3 * c + 1] + g - first[c]];
-    const int mine = a.order[p.x + min(lane, p.y - 1)];
-    const int n = H - col;
-    float s[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] = 0.0f;
-    auto row = [&](int t) { return static_cast<const char*>(a.dy) + (int64_t)__builtin_amdgcn_readlane(mine, t) * H * (YF32 ? 4 : 2); };
-    constexpr int D = 4;
-    int t = 0;
-    for (; t + D <= p.y; t += D) {
-      Eight<YF32> x[D];
-#pragma unroll
-      for (int d = 0; d < D; ++d) x[d].load(row(t + d), col, n);
-#pragma unroll
-      for (int d = 0; d < D; ++d)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[k] += x[d].at(k);
-    }
-    for (; t < p.y; ++t) {
-      Eight<YF32> x;
-      x.load(row(t), col, n);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += x.at(k);
-    }
-    if (!in) continue;
-    if (p.w < 0) {
-      put_row<GF32>(a, p.z, col, n, s);
-    } else {
-      Eight<true> out;
-      out.set(s);
-      out.store(a.part + (int64_t)p.w * H, col, n);
-    }
-  }
-  if (a.add) return;
-  const int64_t groups = (a.V + kZeroRows - 1) / kZeroRows;
-  for (int64_t u = me; u < groups; u += waves) {
-    const int64_t v = u * kZeroRows + (lane & (kZeroRows - 1));
-    bool empty = lane < kZeroRows && v < a.V;
-    if (empty) empty = a.touched[(v & (a.classes - 1)) * a.class_words + (v >> a.class_shift)] == 0;
-    uint64_t todo = __ballot(empty);
-    while (todo != 0) {
-      const int r = __builtin_ctzll(todo);
-      todo &= todo - 1;
-      char* row = static_cast<char*>(a.dW) + (u * kZeroRows + r) * H * (GF32 ? 4 : 2);
-      Eight<GF32> none;
-      const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      none.set(zero);
-      for (int col = lane * 8; col < H; col += 512) none.store(row, col, H - col);
-    }
+    return a.pieces[a.counts[3 * c + 1] + g - first[c]];
+  };
+  auto tokens = [&](const int4& p) { return a.order[p.x + min(lane, p.y - 1)]; };
+  const int chunks = (a.H + 64 * G * kRowGroups - 1) / (64 * G * kRowGroups);
+  const int waves = ((int)gridDim.x - zero_blocks) * 4, me = ((int)blockIdx.x - zero_blocks) * 4 + wave;   // `chunks` waves at least
+  const int step = waves / chunks;
+  int g = me / chunks;
+  const int col = ((me - g * chunks) * 64 * kRowGroups + lane) * G;
+  if (g >= step || g >= total) return;
+  // the piece after the next and the next one's tokens are on their way while a
+  // piece is summed
+  int4 p0 = piece(g), p1 = piece(g + step);
+  int t0 = tokens(p0);
+  for (; g < total; g += step) {
+    const int4 p2 = piece(g + 2 * step);
+    const int t1 = tokens(p1);
+    sum_piece<YF32, GF32, G, TAIL, true, kRowGroups>(a, col, p0.y, p0.z, p0.w, [&](int t) { return __builtin_amdgcn_readlane(t0, t); });
+    p0 = p1;
+    p1 = p2;
+    t0 = t1;
   }
 }
 
-// A workgroup per class: the partial rows of its long words, in order.
-template <bool GF32>
-__global__ __launch_bounds__(256) void embed_join_kernel(const EmbedBwdArgs a) {
-  const int c = blockIdx.x;
+// A class's long words; kJoinParts workgroups share their columns.
+constexpr int kJoinParts = 8;
+template <bool GF32, bool TAIL>
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedBwdArgs a) {
+  __shared__ float4 xch[kJoinWaves][64];
+  const int c = blockIdx.x / kJoinParts;
   const int n_long = a.counts[3 * c + 2], base = a.counts[3 * c + 1] / kPiece;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int H = a.H, chunks = (H + 511) / 512;
-  for (int u = wave; u < n_long * chunks; u += 4) {
+  const int chunks = (a.H + 255) / 256;
+  for (int u = blockIdx.x % kJoinParts; u < n_long * chunks; u += kJoinParts) {
     const int4 w = a.longs[base + u / chunks];
-    const int col = (u % chunks * 64 + lane) * 8;
-    const int n = H - col;
-    if (n <= 0) continue;
-    const int pieces = (w.y + kPiece - 1) / kPiece, slot = w.x / kPiece;
-    Eight<true> x;
-    x.load(a.part + (int64_t)(2 * slot + 1) * H, col, n);
-    float s[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] = x.at(k);
-#pragma unroll 4
-    for (int p = 1; p < pieces; ++p) {
-      x.load(a.part + (int64_t)(2 * (slot + p)) * H, col, n);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += x.at(k);
+    join_row<GF32, TAIL>(a, w.x, w.y, w.z, (u % chunks * 64 + (threadIdx.x & 63)) * 4, xch);
+  }
+}
+
+// Few tokens, a workgroup per token: if a piece begins with it, its sum. Each
+// wave looks at a fourth of the ids, 64 neighbours at a time.
+constexpr int kFewPer = kFewIds / 256;
+template <bool YF32, bool GF32, bool TAIL>
+__global__ __launch_bounds__(256) void embed_few_kernel(const EmbedBwdArgs a) {
+  constexpr int G = YF32 || GF32 ? 4 : 8;
+  extern __shared__ uint32_t seen[];   // bits of the words that occur
+  __shared__ int4 red[4];
+  __shared__ int list[kPiece];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = a.N;
+  const int zero_blocks = (int)gridDim.x - N;   // the first ones, so that they spread over the CUs
+  if ((int)blockIdx.x < zero_blocks) {
+    for (int w = tid; w < (a.V + 31) / 32; w += 256) seen[w] = 0;
+    __syncthreads();
+    for (int i = tid; i < N; i += 256) {
+      const int id = a.ids[i];
+      if (id >= 0 && id < a.V) atomicOr(&seen[id >> 5], 1u << (id & 31));
     }
-    put_row<GF32>(a, w.z, col, n, s);
+    __syncthreads();
+    zero_rows<GF32>(a, blockIdx.x, zero_blocks, [&](int v) { return (seen[v >> 5] >> (v & 31)) & 1; });
+    return;
+  }
+  const int i = (int)blockIdx.x - zero_blocks, word = a.ids[i];
+  if (N > kPiece && tid == 0) a.longs[i] = make_int4(0, 0, 0, 0);   // thread 0 fills it below, if at all
+  if (word < 0 || word >= a.V) return;
+  const int lane = tid & 63, vectors = (N + 255) / 256, j0 = wave * vectors * 64;
+  int id[kFewPer];
+#pragma unroll
+  for (int k = 0; k < kFewPer; ++k)
+    if (k < vectors) id[k] = a.ids[min(j0 + 64 * k + lane, N - 1)];
+#pragma unroll
+  for (int k = 0; k < kFewPer; ++k) id[k] = k < vectors && j0 + 64 * k + lane < min(N, j0 + 64 * vectors) ? id[k] : -1;
+  int same = 0, before = 0, less = 0;
+#pragma unroll
+  for (int k = 0; k < kFewPer; ++k) {
+    same += __popcll(__ballot(id[k] == word));
+    before += __popcll(__ballot(id[k] == word && j0 + 64 * k + lane < i));
+    less += __popcll(__ballot(id[k] >= 0 && id[k] < word));
+  }
+  if (lane == 0) red[wave] = make_int4(same, before, less, 0);
+  __syncthreads();
+  int total = 0, ahead = 0, smaller = 0, rank = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int4 r = red[w];
+    if (w < wave) rank += r.x;
+    total += r.x;
+    ahead += r.y;
+    smaller += r.z;
+  }
+  if (ahead % kPiece != 0) return;
+#pragma unroll
+  for (int k = 0; k < kFewPer; ++k) {
+    const uint64_t all = __ballot(id[k] == word);
+    if (all == 0) continue;
+    const int at = rank + __popcll(all & ((1ull << lane) - 1)) - ahead;
+    if (id[k] == word && at >= 0 && at < kPiece) list[at] = j0 + 64 * k + lane;
+    rank += __popcll(all);
+  }
+  __syncthreads();
+  const bool several = total > kPiece;
+  if (several && ahead == 0 && tid == 0) a.longs[i] = make_int4(smaller, total, word, 0);
+  const int count = min(kPiece, total - ahead);
+  const int mine = list[min(lane, count - 1)];
+  const int slot = several ? 2 * ((smaller + ahead) / kPiece) + (ahead == 0) : -1;
+  for (int col = (wave * 64 + lane) * G; col - lane * G < a.H; col += 256 * G)
+    sum_piece<YF32, GF32, G, TAIL, false, 1>(a, col, count, word, slot, [&](int t) { return __builtin_amdgcn_readlane(mine, t); });
+}
+
+// A workgroup per 64 tokens and 256 columns: the long words among them.
+template <bool GF32, bool TAIL>
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_few_join_kernel(const EmbedBwdArgs a) {
+  __shared__ float4 xch[kJoinWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int chunks = (a.H + 255) / 256;
+  const int block = blockIdx.x / chunks, col = ((int)(blockIdx.x - block * chunks) * 64 + lane) * 4;
+  const int i = block * 64 + lane;
+  const int4 w = i < a.N ? a.longs[i] : make_int4(0, 0, 0, 0);
+  uint64_t todo = __ballot(w.y > 0);   // every wave looks at the same tokens
+  while (todo != 0) {
+    const int l = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    join_row<GF32, TAIL>(a, __builtin_amdgcn_readlane(w.x, l), __builtin_amdgcn_readlane(w.y, l), __builtin_amdgcn_readlane(w.z, l), col, xch);
   }
 }
 
 }  // namespace
 
-hipError_t launch_embed_fwd(const EmbedFwdArgs& a, hipStream_t stream) {
-  const int64_t groups = a.N * ((a.H + 7) / 8);
-  const double N = (double)a.N, H = a.H;
-  trace_begin(stream);
-  auto launch = [&](auto w, auto y, auto u) {
-    const int64_t blocks = (groups + 256 * u() - 1) / (256 * u());
-    hipLaunchKernelGGL((embed_fwd_kernel<w(), y(), u()>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
-  };
-  auto sized = [&](auto w, auto y) {
-    if (groups <= 256 * 2 * kNumCUs) launch(w, y, std::integral_constant<int, 1>{});
-    else launch(w, y, std::integral_constant<int, 4>{});
-  };
+namespace {
+template <class F>
+void with_types(bool a, bool b, bool tail, F f) {
   std::true_type yes;
   std::false_type no;
-  if (a.w_f32) a.y_f32 ? sized(yes, yes) : sized(yes, no);
-  else a.y_f32 ? sized(no, yes) : sized(no, no);
+  auto second = [&](auto x) {
+    auto third = [&](auto y) { tail ? f(x, y, yes) : f(x, y, no); };
+    b ? third(yes) : third(no);
+  };
+  a ? second(yes) : second(no);
+}
+}  // namespace
+
+hipError_t launch_embed_fwd(const EmbedFwdArgs& a, hipStream_t stream) {
+  const int G = a.w_f32 || a.y_f32 ? 4 : 8;
+  const int64_t groups = a.N * ((a.H + G - 1) / G);
+  const double N = (double)a.N, H = a.H;
+  trace_begin(stream);
+  with_types(a.w_f32, a.y_f32, a.H % G != 0, [&](auto w, auto y, auto tail) {
+    auto launch = [&](auto stream_y, auto u) {
+      const int64_t blocks = (groups + 256 * u() - 1) / (256 * u());
+      hipLaunchKernelGGL((embed_fwd_kernel<w(), y(), tail(), stream_y(), u()>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    };
+    if (N * H * (a.y_f32 ? 4 : 2) > kStreamed) launch(std::true_type{}, std::integral_constant<int, 2>{});
+    else launch(std::false_type{}, std::integral_constant<int, 1>{});
+  });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kEmbedFwd, stream, N * H, N * H * ((a.w_f32 ? 4 : 2) + (a.y_f32 ? 4 : 2)) + 4.0 * N);
@@ -381,34 +702,54 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, hipStream_t stream) {
-  const double N = (double)a.N, H = a.H, V = (double)a.V;
+  const double N = (double)a.N, H = a.H, V = (double)a.V, g = a.g_f32 ? 4.0 : 2.0;
+  const double rows_bytes = N * H * (a.y_f32 ? 4 : 2) + (a.add ? std::min(N, V) * 2.0 : V) * H * g;
+  const int G = a.y_f32 || a.g_f32 ? 4 : 8;
+  const bool tail = a.H % G != 0;
+  const int chunks = (a.H + 64 * G * kRowGroups - 1) / (64 * G * kRowGroups), chunks4 = (a.H + 255) / 256;
+  hipError_t e;
+  if (a.few) {
+    trace_begin(stream);
+    const int blocks = a.N + (a.add ? 0 : (int)std::min<int64_t>(kZeroBlocks, ((int64_t)a.V * a.H * (int)g + 4095) / 4096));
+    with_types(a.y_f32, a.g_f32, tail, [&](auto y, auto gf, auto t) {
+      hipLaunchKernelGGL((embed_few_kernel<y(), gf(), t()>), dim3((unsigned)blocks), dim3(256), a.add ? 0 : (a.V + 31) / 32 * 4, stream, a);
+    });
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    trace_end(kEmbedFew, stream, N * H, rows_bytes);
+    if (a.N <= kPiece) return hipSuccess;   // no word has several pieces
+    trace_begin(stream);
+    with_types(a.g_f32, false, a.H % 4 != 0, [&](auto gf, auto, auto t) {
+      hipLaunchKernelGGL((embed_few_join_kernel<gf(), t()>), dim3((unsigned)((a.N + 63) / 64 * chunks4)), dim3(64 * kJoinWaves), 0,
+                         stream, a);
+    });
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    trace_end(kEmbedJoin, stream, 0.0, 16.0 * N);
+    return hipSuccess;
+  }
   trace_begin(stream);
   if (a.class_words <= 640)
     hipLaunchKernelGGL((embed_sort_kernel<640>), dim3(a.classes), dim3(64 * kSortWaves), 0, stream, a);
   else
     hipLaunchKernelGGL((embed_sort_kernel<kMostClassWords>), dim3(a.classes), dim3(64 * kSortWaves), 0, stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  trace_end(kEmbedSort, stream, 0.0, 24.0 * N + V);
-  std::true_type yes;
-  std::false_type no;
-  const int chunks = (a.H + 511) / 512;
-  const int64_t units = std::max<int64_t>((int64_t)a.N * chunks, a.add ? 0 : (a.V + kZeroRows - 1) / kZeroRows);
-  trace_begin(stream);
-  auto rows = [&](auto y, auto g) {
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((units + 3) / 4, 8 * kNumCUs));
-    hipLaunchKernelGGL((embed_rows_kernel<y(), g()>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
-  };
-  if (a.y_f32) a.g_f32 ? rows(yes, yes) : rows(yes, no);
-  else a.g_f32 ? rows(no, yes) : rows(no, no);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const double g = a.g_f32 ? 4.0 : 2.0;
-  trace_end(kEmbedRows, stream, N * H, N * H * (a.y_f32 ? 4 : 2) + (a.add ? std::min(N, V) * 2.0 : V) * H * g);
-  if (a.N <= kPiece) return hipSuccess;   // no word has several pieces
+  trace_end(kEmbedSort, stream, 0.0, 24.0 * N + V);
+  const int64_t units = std::max<int64_t>((int64_t)a.N, 1) * chunks;
+  const int64_t most = kRowsPerCU * kNumCUs - (a.add ? 0 : kZeroBlocks);
+  const int64_t blocks = std::max<int64_t>((chunks + 3) / 4, std::min<int64_t>((units + 3) / 4, most)) + (a.add ? 0 : kZeroBlocks);
   trace_begin(stream);
-  if (a.g_f32) hipLaunchKernelGGL((embed_join_kernel<true>), dim3(a.classes), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((embed_join_kernel<false>), dim3(a.classes), dim3(256), 0, stream, a);
+  with_types(a.y_f32, a.g_f32, tail, [&](auto y, auto gf, auto t) {
+    hipLaunchKernelGGL((embed_rows_kernel<y(), gf(), t()>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+  });
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  trace_end(kEmbedRows, stream, N * H, rows_bytes);
+  trace_begin(stream);
+  with_types(a.g_f32, false, a.H % 4 != 0, [&](auto gf, auto, auto t) {
+    hipLaunchKernelGGL((embed_join_kernel<gf(), t()>), dim3(a.classes * kJoinParts), dim3(64 * kJoinWaves), 0, stream, a);
+  });
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   trace_end(kEmbedJoin, stream, 0.0, 12.0 * a.classes);

@@ -12,6 +12,7 @@ namespace lmh {
 
 constexpr int kTileRows = 256;   // output tile edge of every MMA kernel
 constexpr int kNumCUs = 256;     // MI355X: 8 XCDs x 32 CUs
+constexpr double kStreamed = 32 << 20;   // bytes of output, all XCDs' L2s, above which moved rows are stored past the caches
 
 // Forward: token tiles x vocabulary splits of the tile kernel, then the merge.
 struct FwdPlan {
@@ -297,14 +298,16 @@ struct EmbedFwdArgs {
   void* y;
 };
 
-constexpr int kPiece = 64;             // most tokens of a word that one wave sums
+constexpr int kPiece = 32;             // most tokens of a word that one wave sums
+constexpr int kFewIds = 2048;          // tokens up to which they are counted and not sorted,
+constexpr int kFewWords = 163840;      // and words, where the rows of those that do not occur are zeroed
 constexpr int kMostClasses = 4096;     // workgroups of the sort, a power of two of them
 constexpr int kMostClassWords = 2048;  // words of a class
 
 struct EmbedBwdArgs {
   const int32_t* ids;
   const void* dy;
-  bool y_f32, g_f32, add;
+  bool y_f32, g_f32, add, few;   // few: counted, not sorted
   int N, H, V;
   float scale;
   void* dW;
@@ -312,7 +315,8 @@ struct EmbedBwdArgs {
   int32_t* counts;     // [classes][3]: pieces, tokens of lower classes, long words
   int32_t* order;      // [N] tokens by word
   int4* pieces;        // [N] (first place in order, tokens, word, partial row or -1), a class's from its first token on
-  int4* longs;         // [N / kPiece + 1] (first place, tokens, word, 0) of the words of several pieces
+  int4* longs;         // (first place, tokens, word, 0) of the words of several pieces: a class's from its first token's
+                       // place / kPiece on; of few tokens, by the word's first token, zeros at the others
   uint8_t* touched;    // [classes][class_words] whether the word has a token
   float* part;         // [2 ceil(N / kPiece)][H] partial rows
 };
@@ -359,7 +363,8 @@ struct ReorderArgs {
   int64_t planes, rows;
   int beams;
   int64_t runs, steps, step_bytes;
-  int64_t run_bytes, places, units;   // set by the launcher
+  int64_t run_bytes, places;   // set by the launcher: of a run; its places of 16 bytes
+  uint32_t blocks;             // workgroups of a group
 };
 
 // Kernel ids of the tracing facility (lmhead_trace.hip).
@@ -367,7 +372,7 @@ enum KernelId {
   kFwdStats = 0, kFwdMerge, kBwdStep, kTranspose, kFill, kPadRows, kBwdStepBf16,
   kDistillTop, kDistillPrep, kDistillStep, kDistillPost,
   kFewStats, kFewDz, kFewGrads, kNormFwd, kNormBwd, kNormReduce,
-  kEmbedFwd, kEmbedSort, kEmbedRows, kEmbedJoin, kBeamLogits, kBeamSelect, kBeamScore, kBeamRank, kBeamReorder, kNumKernels
+  kEmbedFwd, kEmbedFew, kEmbedSort, kEmbedRows, kEmbedJoin, kBeamLogits, kBeamSelect, kBeamScore, kBeamRank, kBeamReorder, kNumKernels
 };
 void trace_begin(hipStream_t stream);
 void trace_end(int kernel, hipStream_t stream, double flops, double bytes);

@@ -508,7 +508,9 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  *   parents  int32 [rows];  lengths int32 [rows] or NULL (steps in use, by row of
  *            states; below 0 as 0)
  * Errors: LMH_ERR_SHAPE, LMH_ERR_NULL, LMH_ERR_ARGS (an overlap),
- * LMH_ERR_UNSUPPORTED (2^43 bytes or more; a misaligned pointer), LMH_ERR_HIP.
+ * LMH_ERR_UNSUPPORTED (2^43 bytes or more, 2^36 of a run, 2^30 rows of all
+ * planes, 2^36 places of 16 bytes in one row of every group; a misaligned
+ * pointer), LMH_ERR_HIP.
  */
 #define LMH_BEAM_MAX_BEAMS 64
 #define LMH_BEAM_MAX_CANDIDATES 64
@@ -551,14 +553,15 @@ const char* lmhead_logps_version(void);
  *  15 norm_bwd_kernel
  *  16 norm_reduce_kernel   (dweight and dbias from their partial sums)
  *  17 embed_fwd_kernel
- *  18 embed_sort_kernel    (embedding backward: tokens by word)
- *  19 embed_rows_kernel    (its sums, and the rows without a token)
- *  20 embed_join_kernel    (its words of many tokens)
- *  21 beam_logits_kernel   (beam step: log-sum-exps and blocks' largest logits)
- *  22 beam_select_kernel   (the blocks that hold the best candidates)
- *  23 beam_score_kernel    (their logits in 64 bits)
- *  24 beam_rank_kernel     (the candidates in order)
- *  25 beam_reorder_kernel
+ *  18 embed_few_kernel     (embedding backward of few tokens: its sums)
+ *  19 embed_sort_kernel    (embedding backward: tokens by word)
+ *  20 embed_rows_kernel    (its sums, and the rows without a token)
+ *  21 embed_join_kernel    (its words of many tokens)
+ *  22 beam_logits_kernel   (beam step: log-sum-exps and blocks' largest logits)
+ *  23 beam_select_kernel   (the blocks that hold the best candidates)
+ *  24 beam_score_kernel    (their logits in 64 bits)
+ *  25 beam_rank_kernel     (the candidates in order)
+ *  26 beam_reorder_kernel
  * lmhead_logps_trace_enable(on) clears the totals and starts (on != 0) or
  * stops recording. lmhead_logps_trace_read(kernel, ...) waits for the
  * recorded launches to finish and returns, for that kernel, the launch
