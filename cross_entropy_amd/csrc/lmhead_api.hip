@@ -1279,6 +1279,14 @@ int check_beam(int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidate
   return LMH_OK;
 }
 
+// When the streaming kernels run: they fetch W once per 128 rows, where the
+// tiles take as long for one row as for 256. Measured (us, H 2560, streaming /
+// tiles): 128 rows at 151936 words 200/205, at 32000 39/51, at 8000 22/48; 256
+// rows at 151936 294/217, at 32000 73/52, at 8000 23/48.
+bool few_beams(int64_t N, int64_t V) {
+  return N <= 128 ? V < (int64_t(1) << 23) : N <= lmh::kFewTokens && V <= 24576;
+}
+
 struct BeamPlan {
   bool few = false;
   int splits = 0, n_tt = 0, n_vt = 0, per_section = 0;
@@ -1287,11 +1295,12 @@ struct BeamPlan {
 };
 BeamPlan plan_beam(int64_t N, int64_t H, int64_t V, int64_t beams) {
   BeamPlan p;
-  p.few = few_tokens(N, V);
+  p.few = few_beams(N, V);
   if (p.few) {
-    p.splits = lmh::few_splits(V);
+    const int rows = lmh::beam_few_rows(N, V);
+    p.splits = (int)lmh::ceil_div(V, rows);
     p.n_sections = p.splits;
-    p.per_section = lmh::few_rows(V) / 16;
+    p.per_section = rows / 16;
   } else {
     const lmh::FwdPlan f = lmh::plan_forward(N, H, V, lmh::kNumCUs);
     p.splits = f.S;

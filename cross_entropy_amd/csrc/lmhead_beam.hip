@@ -43,14 +43,16 @@ __device__ __forceinline__ uint32_t allowed16(const BeamArgs& a, int64_t tok, in
 }
 
 // Few rows: the workgroup's 64 MB vocabulary rows, one record and one section.
+// Tiles of 16 NB tokens: up to 128, where the distillation's stop at 64.
 template <int MB, int NB, bool MASK>
 __global__ __launch_bounds__(256, 2) void beam_few_kernel(const FewArgs a, const BeamArgs b) {
   __shared__ __attribute__((aligned(16))) char lds[few_lds<NB>()];
   __shared__ float4 xch[4][16 * NB];
   const int lane = threadIdx.x & 63;
   const int wave = wave_id();
-  const FewTile t = few_tile(a, xcd_remap(blockIdx.x, gridDim.x), a.splits);
-  if (t.split < 0) return;
+  const int vid = xcd_remap(blockIdx.x, gridDim.x), tok0 = vid % a.tiles * (16 * NB);
+  const FewTile t{tok0, min(16 * NB, a.N - tok0), vid / a.tiles};
+  if (t.split >= a.splits) return;
   const int r0 = (t.split * 4 + wave) * 16 * MB;
   const int V = a.V;
   const int q = lane >> 4;
@@ -138,6 +140,11 @@ __device__ __forceinline__ float four_blocks(float b0, float b1, float b2, float
 }
 __device__ __forceinline__ int quarter_block(int q) { return (q & 1) * 2 + (q >> 1); }
 
+// Four words of a row's mask, wherever they begin.
+struct __attribute__((packed, aligned(4))) Words4 {
+  uint32_t w[4];
+};
+
 // Many rows: the head's forward tiles; a section is a wave's 128 vocabulary
 // rows. The arrays hold whole tiles of rows and of words, so every store is in
 // place; what lies past N or V is not read.
@@ -174,13 +181,36 @@ __global__ __launch_bounds__(kThreads) void beam_tile_kernel(
     const int tok = tok0 + wn * 128 + (lane & 15);
     float* to = blocks + (int64_t)((vrow0 >> 4) + quarter_block(q)) * ld + tok;
     float* sec = sections + (int64_t)(vrow0 >> 7) * ld + tok;
+    // the masks of a row's 128 words: of the next row while one is looked at
+    const int word0 = min(vrow0 >> 5, max(mask_ld - 4, 0));   // four words in place, of which `skip` come before
+    const int skip = (vrow0 >> 5) - word0;
+    auto masks_of = [&](int j) {
+      const int32_t* row = allowed + (int64_t)min(tok + 16 * j, N - 1) * mask_ld + word0;
+      if (mask_ld >= 4) return *reinterpret_cast<const Words4*>(row);
+      Words4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w.w[k] = k < mask_ld ? (uint32_t)row[min(k, mask_ld - 1)] : 0;
+      return w;
+    };
+    Words4 ahead{};
+    if (MASK) ahead = masks_of(0);
 #pragma unroll
     for (int j = 0; j < kNB; ++j) {
       uint32_t words[4];
       if (MASK) {
-        const int32_t* row = allowed + (int64_t)min(tok + 16 * j, N - 1) * mask_ld;
+        const Words4 now = ahead;
+        if (j + 1 < kNB) ahead = masks_of(j + 1);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) words[w] = (uint32_t)row[min((vrow0 >> 5) + w, mask_ld - 1)] >> (4 * q);
+        for (int w = 0; w < 4; ++w) words[w] = now.w[w] >> (4 * q);
+        if (skip > 0) {   // the last tile's
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t x = 0;
+#pragma unroll
+            for (int k = w + 1; k < 4; ++k) x = w + skip == k ? now.w[k] : x;
+            words[w] = x >> (4 * q);
+          }
+        }
       }
       float z[kNB][4];
 #pragma unroll
@@ -271,6 +301,62 @@ __global__ __launch_bounds__(kThreads) void beam_tile_kernel(
 }
 
 // ---------------------------------------------------------------------------
+// Reductions over lanes on the vector unit (data-parallel primitives and lane
+// swaps; __shfl_xor takes a trip through LDS for each step). Every lane of a
+// group of W ends with the same bits: each step combines the same two values in
+// both of the lanes that exchange them, lower half first where that matters.
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp_of(T v) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+  }
+}
+template <int HALF, class T, class F>
+__device__ __forceinline__ T swapped(T v, F op) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  auto swap = [](uint32_t x) {
+    return HALF == 32 ? __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(x, x, false, false))
+                      : __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(x, x, false, false));
+  };
+  if constexpr (sizeof(T) == 4) {
+    const u32x2 r = swap(__builtin_bit_cast(uint32_t, v));
+    const uint32_t x = r.x, y = r.y;   // a bit_cast of r.y itself would read r.x
+    return op(__builtin_bit_cast(T, x), __builtin_bit_cast(T, y));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const u32x2 lo = swap((uint32_t)u), hi = swap((uint32_t)(u >> 32));
+    return op(__builtin_bit_cast(T, (uint64_t)hi.x << 32 | lo.x), __builtin_bit_cast(T, (uint64_t)hi.y << 32 | lo.y));
+  }
+}
+// op is commutative in its bits (a sum or a maximum of two values)
+template <int W, class T, class F>
+__device__ __forceinline__ T reduce(T v, F op) {
+  v = op(v, dpp_of<0xB1>(v));                       // quad_perm 1 0 3 2
+  v = op(v, dpp_of<0x4E>(v));                       // quad_perm 2 3 0 1
+  if constexpr (W >= 8) v = op(v, dpp_of<0x141>(v));   // row_half_mirror
+  if constexpr (W >= 16) v = op(v, dpp_of<0x140>(v));  // row_mirror
+  if constexpr (W >= 32) v = swapped<16>(v, op);
+  if constexpr (W >= 64) v = swapped<32>(v, op);
+  return v;
+}
+struct Sum {
+  template <class T>
+  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
+  __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
+};
+struct NanMax {
+  __device__ __forceinline__ float operator()(float a, float b) const { return nan_max(a, b); }
+};
+
+// ---------------------------------------------------------------------------
 // Keys: a float's order as an unsigned number, above the complement of its
 // index, so that larger keys are better candidates and no two are equal.
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t index) {
@@ -324,9 +410,7 @@ __device__ __forceinline__ int select_best(Selection& s, int per, int keep, cons
   auto largest = [&](uint64_t below) {
     uint64_t most = 0;
     each([&](uint64_t k) { most = k < below ? max(most, k) : most; });
-#pragma unroll
-    for (int x = 1; x < team; x <<= 1) most = max(most, (uint64_t)__shfl_xor((unsigned long long)most, x));
-    return most;
+    return reduce<team>(most, Max());
   };
   const uint64_t most = largest(~(uint64_t)0);
   if (tid % team == 0) s.most[tid / team] = most;
@@ -377,19 +461,14 @@ __device__ __forceinline__ int select_best(Selection& s, int per, int keep, cons
     int rank = 0;
 #pragma unroll 4
     for (int k = tid & 15; k < found; k += 16) rank += s.list[k] > mine;
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) rank += __shfl_xor(rank, x);
+    rank = reduce<16>(rank, Sum());
     if (i < found && (tid & 15) == 0 && rank < keep) s.kept[rank] = mine;
   }
   __syncthreads();
   return min(found, keep);
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int x = 32; x >= 1; x >>= 1) v += __shfl_xor(v, x);
-  return v;
-}
+__device__ __forceinline__ double wave_sum(double v) { return reduce<64>(v, Sum()); }
 __device__ __forceinline__ bool finite(double v) { return fabs(v) < INFINITY; }
 __device__ __forceinline__ bool ended_row(const BeamArgs& b, int64_t tok) {
   return b.ended != nullptr && b.ended[tok] >= 0 && b.ended[tok] < b.V;
@@ -405,16 +484,23 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t group = blockIdx.x, row0 = group * b.beams;
   const int G = b.beams;
-  // a thread looks at sections of one row: its first ones are on their way
-  // while the records are merged
+  // a thread looks at sections of one row, or where a team would otherwise miss
+  // most rows, of all in turn: the best row's fall to all teams then. Its first
+  // ones are on their way while the records are merged
   constexpr int U = 12;
   const uint32_t n_sec = (uint32_t)b.n_sections;   // beams * V stays below 2^31
   const int rows_at_once = kSelThreads / G;
-  const int my_row = tid % G, my_sec = tid / G;
+  const int my_sec = tid / G;
+  const uint32_t my_row = tid - my_sec * G, turn = G > 16;
+  const uint32_t recip = G > 1 ? 0xFFFFFFFFu / (uint32_t)G + 1 : 0;   // x / G of small x as a product
+  auto row_at = [&](uint32_t k) {
+    const uint32_t x = my_row + k * turn;
+    return (int)(x - __umulhi(x, recip) * (uint32_t)G);
+  };
   const int per_a = my_sec < rows_at_once ? ((int)n_sec - my_sec + rows_at_once - 1) / rows_at_once : 0;
-  const float* sections = b.sections + row0 + my_row + min((uint32_t)my_sec, n_sec - 1) * b.ld;
+  const float* sections = b.sections + row0 + min((uint32_t)my_sec, n_sec - 1) * b.ld;
   const int64_t stride = rows_at_once * b.ld;
-  auto load_a = [&](int k) { return sections[max(0, min(k, per_a - 1)) * stride]; };
+  auto load_a = [&](int k) { return sections[max(0, min(k, per_a - 1)) * stride + row_at(k)]; };
   float first[U];
 #pragma unroll
   for (int k = 0; k < U; ++k) first[k] = load_a(k);
@@ -435,9 +521,7 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
       for (int k = 0; k < 8; ++k) sum += (double)p[k].y * (double)fast_exp2(p[k].x - mx);
       m = mx;
     }
-    float mx = m;
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) mx = nan_max(mx, __shfl_xor(mx, x));
+    const float mx = reduce<64>(m, NanMax());
     sum = wave_sum(sum * (double)fast_exp2(m - mx));
     if (lane == 0) {
       const float score = b.scores[tok];
@@ -456,13 +540,8 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     // values relative to about the best candidate, where float32 is finest
     const double mine = lane < G ? base[lane] : -INFINITY;
     const float large = lane < G ? size[lane] : 0.0f;
-    double ref = mine + (double)large;
-    float most = fabsf(large);
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) {
-      ref = fmax(ref, __shfl_xor(ref, x));
-      most = fmaxf(most, __shfl_xor(most, x));
-    }
+    const double ref = reduce<64>(mine + (double)large, Max());
+    const float most = reduce<64>(fabsf(large), NanMax());
     if (lane < G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
     if (lane == 0) slack = (most + b.invT) * 0x1p-13f;   // far more than the tiles' sums are off
   }
@@ -473,7 +552,8 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
   };
   const int n1 = select_best(sel, per_a, keep, first, load_a, [&](int k, float z) {
-    return key(z, my_row, (uint32_t)my_row * n_sec + (uint32_t)(my_sec + k * rows_at_once));
+    const int r = row_at(k);
+    return key(z, r, (uint32_t)r * n_sec + (uint32_t)(my_sec + k * rows_at_once));
   });
   if (tid < n1) section[tid] = index_of(sel.kept[tid]);
   __syncthreads();
@@ -593,9 +673,7 @@ __global__ __launch_bounds__(kRankThreads) void beam_rank_kernel(const BeamArgs 
                                            ((uint32_t)b.allowed[(row0 + row_of[k]) * b.mask_ld + (v >> 5)] >> (v & 31)) & 1);
       if (may) z[q] = b.exact[group * kMostKept * 16 + i];
     }
-    double m = z[q];
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) m = fmax(m, __shfl_xor(m, x));
+    const double m = reduce<16>(z[q], Max());
     if (k < used && (i & 15) == 0) {
       z_max[k] = m;
       atomicMin(&first[row_of[k]], k);
@@ -668,6 +746,10 @@ __global__ __launch_bounds__(kRankThreads) void beam_rank_kernel(const BeamArgs 
 
 }  // namespace
 
+// Vocabulary rows of a workgroup of the streaming kernels: above 64 tokens at
+// most 192, whose accumulators leave registers for two workgroups a CU.
+int beam_few_rows(int64_t N, int64_t V) { return N <= 64 ? few_rows(V) : std::min(few_rows(V), 192); }
+
 hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
   const double N = b.N, H = b.H, V = b.V;
   const int64_t groups = b.N / b.beams;
@@ -680,13 +762,19 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
     a.H = b.H;
     a.V = b.V;
     a.sc = b.sc;
-    a.tiles = (b.N + 63) / 64;
     a.splits = b.splits;
-    with_sizes(few_blocks(b.V), b.N <= 16 ? 1 : b.N <= 32 ? 2 : 4, [&](auto mb, auto nb) {
+    auto launch = [&](auto mb, auto nb) {
+      a.tiles = (b.N + 16 * nb() - 1) / (16 * nb());
       const dim3 grid(few_grid((int64_t)a.tiles * a.splits));
       if (b.allowed != nullptr) hipLaunchKernelGGL((beam_few_kernel<mb(), nb(), true>), grid, dim3(256), 0, stream, a, b);
       else hipLaunchKernelGGL((beam_few_kernel<mb(), nb(), false>), grid, dim3(256), 0, stream, a, b);
-    });
+    };
+    constexpr std::integral_constant<int, 8> eight{};
+    const int mb = beam_few_rows(b.N, b.V) / 64;
+    if (b.N <= 64) with_sizes(mb, b.N <= 16 ? 1 : b.N <= 32 ? 2 : 4, launch);
+    else if (mb == 3) launch(std::integral_constant<int, 3>{}, eight);
+    else if (mb == 2) launch(std::integral_constant<int, 2>{}, eight);
+    else launch(std::integral_constant<int, 1>{}, eight);
   } else {
     const dim3 grid((unsigned)(((int64_t)b.n_tt * b.splits + 7) / 8 * 8));
     auto tiles = [&](auto mask) {

@@ -239,6 +239,7 @@ struct FewArgs {
 };
 
 int few_rows(int64_t V);     // vocabulary rows of a split
+int beam_few_rows(int64_t N, int64_t V);   // likewise of the beams' forward, of up to 256 tokens
 int few_splits(int64_t V);   // records per token of the forward
 hipError_t launch_few_stats(FewArgs a, hipStream_t stream);
 hipError_t launch_few_bwd(FewArgs a, bool bf16, hipStream_t stream);   // the cotangent, dW and the partials of dh
