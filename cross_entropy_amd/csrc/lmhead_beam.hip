@@ -747,8 +747,10 @@ __global__ __launch_bounds__(kRankThreads) void beam_rank_kernel(const BeamArgs 
 }  // namespace
 
 // Vocabulary rows of a workgroup of the streaming kernels: above 64 tokens at
-// most 192, whose accumulators leave registers for two workgroups a CU.
-int beam_few_rows(int64_t N, int64_t V) { return N <= 64 ? few_rows(V) : std::min(few_rows(V), 192); }
+// most 128. 192 still leave registers for two workgroups a CU, but those of a
+// large vocabulary then take two rounds, the second half empty (128 tokens, H
+// 2560, V 151936: 198 us where 128 rows take 188 and 64 rows 237).
+int beam_few_rows(int64_t N, int64_t V) { return N <= 64 ? few_rows(V) : std::min(few_rows(V), 128); }
 
 hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
   const double N = b.N, H = b.H, V = b.V;
@@ -772,7 +774,6 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
     constexpr std::integral_constant<int, 8> eight{};
     const int mb = beam_few_rows(b.N, b.V) / 64;
     if (b.N <= 64) with_sizes(mb, b.N <= 16 ? 1 : b.N <= 32 ? 2 : 4, launch);
-    else if (mb == 3) launch(std::integral_constant<int, 3>{}, eight);
     else if (mb == 2) launch(std::integral_constant<int, 2>{}, eight);
     else launch(std::integral_constant<int, 1>{}, eight);
   } else {
@@ -813,6 +814,8 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
 // any write: larger groups take several waves of a workgroup and a barrier
 // between. Which row takes from which, and how much, is the same for all lanes.
 namespace {
+
+constexpr int kReorderRows = 16;
 
 typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(1)));
 
@@ -903,17 +906,24 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(const ReorderArgs a) 
 
 }  // namespace
 
+// Waves of a workgroup that share the group's rows, 16 each.
+static int reorder_waves(int64_t beams) { return beams <= kReorderRows ? 1 : beams <= 2 * kReorderRows ? 2 : 4; }
+
+int64_t reorder_blocks(int64_t planes, int64_t rows, int64_t beams, int64_t runs, int64_t run_bytes) {
+  const int64_t at_once = 64 * (4 / reorder_waves(beams));
+  return planes * (rows / beams) * ((runs * ((run_bytes + 15) / 16) + at_once - 1) / at_once);
+}
+
 hipError_t launch_beam_reorder(ReorderArgs a, hipStream_t stream) {
   a.run_bytes = a.steps * a.step_bytes;
   a.places = (a.run_bytes + 15) / 16;
-  const int64_t groups = a.planes * (a.rows / a.beams), places = a.runs * a.places;
-  if (groups * places == 0) return hipSuccess;
+  const int64_t groups = a.planes * (a.rows / a.beams), blocks = reorder_blocks(a.planes, a.rows, a.beams, a.runs, a.run_bytes);
+  if (blocks == 0) return hipSuccess;
+  a.blocks = (uint32_t)(blocks / groups);
   trace_begin(stream);
   const bool streamed = (double)a.planes * a.rows * a.runs * a.run_bytes > kStreamed;
   auto launch = [&](auto rb, auto wr) {
-    const int64_t at_once = 64 * (4 / wr());
-    a.blocks = (uint32_t)((places + at_once - 1) / at_once);
-    const dim3 grid((unsigned)((groups * a.blocks + 7) / 8 * 8));
+    const dim3 grid((unsigned)((blocks + 7) / 8 * 8));
     auto kind = [&](auto tail, auto past) {
       hipLaunchKernelGGL((beam_reorder_kernel<rb(), wr(), tail(), past()>), grid, dim3(256), 0, stream, a);
     };
@@ -923,11 +933,12 @@ hipError_t launch_beam_reorder(ReorderArgs a, hipStream_t stream) {
     else streamed ? kind(no, yes) : kind(no, no);
   };
   constexpr std::integral_constant<int, 1> one{};
-  constexpr std::integral_constant<int, 16> most{};
+  constexpr std::integral_constant<int, kReorderRows> most{};
+  const int waves = reorder_waves(a.beams);
   if (a.beams <= 4) launch(std::integral_constant<int, 4>{}, one);
   else if (a.beams <= 8) launch(std::integral_constant<int, 8>{}, one);
-  else if (a.beams <= 16) launch(most, one);
-  else if (a.beams <= 32) launch(most, std::integral_constant<int, 2>{});
+  else if (waves == 1) launch(most, one);
+  else if (waves == 2) launch(most, std::integral_constant<int, 2>{});
   else launch(most, std::integral_constant<int, 4>{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -402,5 +402,6 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, hipStream_t stream);
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, hipStream_t stream);
 hipError_t launch_beam_step(const BeamArgs& a, hipStream_t stream);
 hipError_t launch_beam_reorder(ReorderArgs a, hipStream_t stream);
+int64_t reorder_blocks(int64_t planes, int64_t rows, int64_t beams, int64_t runs, int64_t run_bytes);   // its workgroups
 
 }  // namespace lmh

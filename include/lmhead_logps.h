@@ -442,13 +442,13 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
  *         wrote becomes the table's whole gradient
  * H in [1, 2^20), odd sizes too; every pointer aligned to its elements (the
  * workspace to 16 bytes). Sums are float32, taken over a word's tokens in the
- * order of the tokens (in pieces of 64 whose sums are then added in order), so
+ * order of the tokens (in pieces of 32 whose sums are then added in order), so
  * results depend on the arguments alone; bf16 gradients are rounded once, a
  * previous bf16 value being widened first. N = 0: the forward does nothing, the
  * backward writes dW = 0 (unless adding). Errors: LMH_ERR_NULL, LMH_ERR_SHAPE,
  * LMH_ERR_ARGS (unknown type or flag; scale not finite), LMH_ERR_WORKSPACE,
- * LMH_ERR_UNSUPPORTED (a misaligned pointer; in the backward and its size query
- * N or V above 2^23 - 256), LMH_ERR_HIP. Outputs must not overlap inputs. Stream
+ * LMH_ERR_UNSUPPORTED (a misaligned pointer; a forward of N H / 4 >= 2^33; in the
+ * backward and its size query N or V above 2^23 - 256), LMH_ERR_HIP. Outputs must not overlap inputs. Stream
  * semantics as for every call here.
  */
 int lmhead_logps_embed_workspace_bytes(int64_t N, int64_t H, int64_t V, size_t* bytes_out);   /* the backward's */
@@ -490,11 +490,12 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  * float32 does not tell their largest logits apart; in a group with more near ties
  * than that it may miss one.
  * The workspace holds 4 N V / 16 bytes of the blocks' largest logits (N rounded
- * up to 64, or to 256 above 64) and smaller arrays;
+ * up to 64, or to 256 above 128) and smaller arrays;
  * lmhead_logps_beam_workspace_bytes sizes it.
  * Errors: those of the head's calls, plus LMH_ERR_SHAPE when beams is not in [1,
  * LMH_BEAM_MAX_BEAMS], candidates not in [1, LMH_BEAM_MAX_CANDIDATES] or N not a
- * multiple of beams, and LMH_ERR_UNSUPPORTED where N >= 2^23 or beams V >= 2^31.
+ * multiple of beams, and LMH_ERR_UNSUPPORTED where N >= 2^23, beams V >= 2^31 or
+ * N / beams (candidates + 16) >= 2^24.
  *
  * lmhead_logps_beam_reorder: the beams' states after the step. Rows of
  * `states` [planes][rows][runs][steps][step_bytes] (bytes of any type) are
@@ -508,9 +509,9 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  *   parents  int32 [rows];  lengths int32 [rows] or NULL (steps in use, by row of
  *            states; below 0 as 0)
  * Errors: LMH_ERR_SHAPE, LMH_ERR_NULL, LMH_ERR_ARGS (an overlap),
- * LMH_ERR_UNSUPPORTED (2^43 bytes or more, 2^36 of a run, 2^30 rows of all
- * planes, 2^36 places of 16 bytes in one row of every group; a misaligned
- * pointer), LMH_ERR_HIP.
+ * LMH_ERR_UNSUPPORTED (2^43 bytes or more, 2^35 of a run, 2^30 rows, or more than
+ * 2^24 workgroups, of up to 16 beams' 4 KB each: 64 GB of single beams; a
+ * misaligned pointer), LMH_ERR_HIP.
  */
 #define LMH_BEAM_MAX_BEAMS 64
 #define LMH_BEAM_MAX_CANDIDATES 64

@@ -48,6 +48,7 @@ def test_embed_forward_errors():
     assert _ef(w_type=1, W=MIS) == -6
     assert _ef(y_type=1, y=MIS) == -6
     assert _ef(N=0, W=0, ids=0, y=0) == 0
+    assert _ef(N=1 << 28, H=128) == -6
 
 
 def test_embed_backward_errors():
@@ -104,6 +105,7 @@ def test_beam_step_errors():
         assert _bs(candidates=C) == -2
     assert _bs(N=1 << 23) == -6
     assert _bs(beams=64, V=1 << 25) == -6
+    assert _bs(N=1 << 20, beams=1) == -6           # groups times what each scores
     for T in (0.0, -1.0, float("nan"), float("inf"), 1e-40):
         assert _bs(temperature=T) == -5
     for k in ("hidden", "W", "scores", "top_scores", "top_ids", "top_parents", "lse", "workspace"):
@@ -127,13 +129,13 @@ def test_beam_workspace():
             q(*bad)
     assert nat.load().lmhead_logps_beam_workspace_bytes(4, 64, 10, 1, 1, ctypes.cast(None, ctypes.POINTER(ctypes.c_size_t))) == -1
     up = lambda n, m: -(-n // m) * m  # noqa: E731
-    for N in (0, 1, 4, 64, 65, 128, 256, 257, 1024, 100000):
+    for N in (0, 1, 4, 64, 65, 128, 129, 256, 257, 1024, 100000):
         for V in (1, 16, 17, 4096, 12289, 151936, 1 << 22):
             b = q(N, 2560, V, 1, 8)
             assert 4 * N * -(-V // 16) <= b
             # for rows rounded up to 64, or 256 above 64 of them: blocks of 16 words, sections and records of at least
             # 64, all of whole tiles of 256; and the groups' chosen blocks
-            ld, v = up(max(N, 1), 64 if N <= 64 else 256), up(V, 256)
+            ld, v = up(max(N, 1), 64 if N <= 128 else 256), up(V, 256)
             assert b <= ld * (4 * v / 16 + 12 * (v / 64 + 256)) + N * (8 + 80 * 132 + 8) + 4096
 
 
@@ -161,3 +163,7 @@ def test_beam_reorder_errors():
     assert _br(steps=1 << 40) == -6
     assert _br(steps=1 << 62, step_bytes=1 << 62) == -6
     assert _br(rows=1 << 33, steps=1, planes=1) == -6
+    assert _br(rows=1 << 30, steps=1, planes=1) == -6
+    assert _br(steps=1 << 35, step_bytes=1, planes=1) == -6
+    assert _br(beams=1, planes=1, rows=1 << 24, steps=1, step_bytes=1) == -6     # a workgroup each
+    assert _br(beams=1, planes=1 << 10, rows=1 << 14, steps=1, step_bytes=1) == -6
