@@ -1384,7 +1384,7 @@ int lmhead_logps_beam_step(const uint16_t* hidden, const uint16_t* W, const floa
   b.keep = (int)candidates + lmh::kSpare;
   b.sc = temper_scale(temperature);
   b.invT = inv_temperature(temperature);
-  b.T = (double)temperature;
+  b.rT = 1.0 / (double)temperature;
   b.back = 1.0 / ((double)b.sc * (double)temperature);
   b.few = p.few;
   b.splits = p.splits;

@@ -373,14 +373,16 @@ __device__ __forceinline__ uint32_t index_of(uint64_t key) { return ~(uint32_t)k
 constexpr int kSelThreads = 1024;
 constexpr int kSelTeams = 128;    // of 8 threads each
 constexpr int kSelList = 2048;
+constexpr int kSelHeld = 24576;   // items whose values LDS holds (96 KB)
 
-// The `keep` largest keys into kept[0 ..], sorted; returns how many there are
-// (keep, or all that are not 0). A thread has `per` items: key(k, load(k)) is
-// the key of its k-th, 0 for none, and first[] holds what load gives for the
-// first U. Every team has a largest key, and the keep-th largest of those is a
-// threshold that at least `keep` items reach, and few more do as a rule: those
-// are ranked. Should more than the list holds reach it (most of the best items
-// lie with few teams), the best are taken one after the other.
+// The `keep` largest keys of items 0 .. n - 1 into kept[0 ..], sorted; returns
+// how many there are (keep, or all that are not 0). key(i) gives an item's key,
+// 0 for none. A thread looks at neighbouring items, a team at those of eight
+// threads: rows in turn. Every team has a largest key, and the keep-th largest of
+// those is a threshold that at least `keep` items reach, and few more do as a
+// rule: those are ranked. Should more than the list holds reach it (most of the
+// best items lie with few teams), the best are taken one after the other.
+//
 static_assert(kMostKept <= kSelTeams, "a threshold exists");
 struct Selection {
   uint64_t list[kSelList];
@@ -390,76 +392,75 @@ struct Selection {
   uint64_t limit;
   int count;
 };
-template <int U, class L, class K>
-__device__ __forceinline__ int select_best(Selection& s, int per, int keep, const float (&first)[U], L load, K key) {
+template <class K>
+__device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, K key) {
   const int tid = threadIdx.x;
   constexpr int team = kSelThreads / kSelTeams;
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (k < per) f(key(k, first[k]));
-    for (int base = U; base < per; base += U) {
-      float z[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k) z[k] = load(base + k);
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (base + k < per) f(key(base + k, z[k]));
-    }
-  };
+  const uint32_t per = (n + kSelThreads - 1) / kSelThreads;
+  const uint32_t i0 = min(n, tid * per), i1 = min(n, i0 + per);
   auto largest = [&](uint64_t below) {
     uint64_t most = 0;
-    each([&](uint64_t k) { most = k < below ? max(most, k) : most; });
+#pragma unroll 4
+    for (uint32_t i = i0; i < i1; ++i) {
+      const uint64_t k = key(i);
+      most = k < below ? max(most, k) : most;
+    }
     return reduce<team>(most, Max());
   };
-  const uint64_t most = largest(~(uint64_t)0);
-  if (tid % team == 0) s.most[tid / team] = most;
-  if (tid < kSelTeams) s.rank[tid] = 0;
-  if (tid == 0) {
-    s.limit = 1;
-    s.count = 0;
-  }
-  __syncthreads();
-  {
-    // the teams' ranks, 16 comparisons a thread
-    const uint64_t mine = s.most[tid % kSelTeams];
-    int rank = 0;
+  uint64_t below = ~(uint64_t)0;
+  int found = 0;
+#pragma unroll 1
+  for (int r = 0; r < keep; ++r) {   // once, unless the list runs over
+    const uint64_t most = largest(below);
+    if (tid % team == 0) s.most[tid / team] = most;
+    if (tid < kSelTeams) s.rank[tid] = 0;
+    if (tid == 0) {
+      s.limit = 1;
+      s.count = 0;
+    }
+    __syncthreads();
+    {
+      // the teams' ranks, 16 comparisons a thread
+      const uint64_t mine = s.most[tid % kSelTeams];
+      int rank = 0;
 #pragma unroll
-    for (int k = 0; k < kSelTeams / team; ++k) rank += s.most[tid / kSelTeams * (kSelTeams / team) + k] > mine;
-    if (rank > 0) atomicAdd(&s.rank[tid % kSelTeams], rank);
-  }
-  __syncthreads();
-  if (tid < kSelTeams && s.rank[tid] == keep - 1 && s.most[tid] > 0) s.limit = s.most[tid];
-  __syncthreads();
-  const uint64_t limit = s.limit;
-  each([&](uint64_t k) {
-    if (k >= limit) {
+      for (int k = 0; k < kSelTeams / team; ++k) rank += s.most[tid / kSelTeams * (kSelTeams / team) + k] > mine;
+      if (rank > 0) atomicAdd(&s.rank[tid % kSelTeams], rank);
+    }
+    __syncthreads();
+    const int want = found > kSelList ? 0 : keep - 1;
+    if (tid < kSelTeams && s.rank[tid] == want && s.most[tid] > 0) s.limit = s.most[tid];
+    __syncthreads();
+    const uint64_t limit = s.limit;
+    if (found > kSelList) {
+      if (tid == 0) s.kept[r] = limit;
+      below = limit;
+      __syncthreads();   // the limit has been read
+      continue;
+    }
+#pragma unroll 4
+    for (uint32_t i = i0; i < i1; ++i) {
+      const uint64_t k = key(i);
+      if (k < limit) continue;
       const int at = atomicAdd(&s.count, 1);
       if (at < kSelList) s.list[at] = k;
     }
-  });
-  __syncthreads();
-  const int found = s.count;
+    __syncthreads();
+    found = s.count;
+    if (found <= kSelList) break;
+    r = -1;   // one after the other, from the first
+    __syncthreads();
+  }
   if (found > kSelList) {
-    uint64_t below = ~(uint64_t)0;
-    for (int r = 0; r < keep; ++r) {
-      __syncthreads();   // s.most has been read
-      const uint64_t mine = largest(below);
-      if (tid % team == 0) s.most[tid / team] = mine;
-      __syncthreads();
-      uint64_t best = 0;
-      for (int k = 0; k < kSelTeams; ++k) best = max(best, s.most[k]);
-      if (tid == 0) s.kept[r] = best;
-      below = best;
-    }
     __syncthreads();
     return keep;   // more than kSelList items are not 0
   }
-  for (int i0 = 0; i0 < found; i0 += kSelThreads / 16) {   // 16 threads a candidate
-    const int i = i0 + (tid >> 4);
+#pragma unroll 1
+  for (int first = 0; first < found; first += kSelThreads / 16) {   // 16 threads a candidate
+    const int i = first + (tid >> 4);
     const uint64_t mine = i < found ? s.list[i] : 0;
     int rank = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int k = tid & 15; k < found; k += 16) rank += s.list[k] > mine;
     rank = reduce<16>(rank, Sum());
     if (i < found && (tid & 15) == 0 && rank < keep) s.kept[rank] = mine;
@@ -476,53 +477,68 @@ __device__ __forceinline__ bool ended_row(const BeamArgs& b, int64_t tok) {
 
 __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs b) {
   __shared__ Selection sel;
+  __shared__ float held[kSelHeld];
   __shared__ double base[kMostBeams];
   __shared__ float size[kMostBeams], shift[kMostBeams];
-  __shared__ uint32_t section[kMostKept];
+  __shared__ uint32_t sec_row[kMostKept], sec_block[kMostKept];
   __shared__ float slack;
+  __shared__ double rec_sum[kSelThreads];
+  __shared__ float rec_max[kSelThreads];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t group = blockIdx.x, row0 = group * b.beams;
-  const int G = b.beams;
-  // a thread looks at sections of one row, or where a team would otherwise miss
-  // most rows, of all in turn: the best row's fall to all teams then. Its first
-  // ones are on their way while the records are merged
-  constexpr int U = 12;
-  const uint32_t n_sec = (uint32_t)b.n_sections;   // beams * V stays below 2^31
-  const int rows_at_once = kSelThreads / G;
-  const int my_sec = tid / G;
-  const uint32_t my_row = tid - my_sec * G, turn = G > 16;
-  const uint32_t recip = G > 1 ? 0xFFFFFFFFu / (uint32_t)G + 1 : 0;   // x / G of small x as a product
-  auto row_at = [&](uint32_t k) {
-    const uint32_t x = my_row + k * turn;
-    return (int)(x - __umulhi(x, recip) * (uint32_t)G);
+  const uint32_t G = b.beams, n_sec = (uint32_t)b.n_sections, per = b.per_section, n_blocks = (uint32_t)b.n_blocks;
+  const uint32_t n_a = n_sec * G;   // beams * V stays below 2^31: i / G is exact as a product with a reciprocal
+  const uint32_t by_rows = G > 1 ? 0xFFFFFFFFu / G + 1 : 0, by_blocks = per > 1 ? 0xFFFFFFFFu / per + 1 : 0;
+  auto quotient = [](uint32_t i, uint32_t recip) { return recip != 0 ? __umulhi(i, recip) : i; };
+  const float* sections = b.sections + row0;
+  auto section_at = [&](uint32_t i) {
+    const uint32_t s = quotient(i, by_rows);
+    return sections[(int64_t)s * b.ld + (i - s * G)];
   };
-  const int per_a = my_sec < rows_at_once ? ((int)n_sec - my_sec + rows_at_once - 1) / rows_at_once : 0;
-  const float* sections = b.sections + row0 + min((uint32_t)my_sec, n_sec - 1) * b.ld;
-  const int64_t stride = rows_at_once * b.ld;
-  auto load_a = [&](int k) { return sections[max(0, min(k, per_a - 1)) * stride + row_at(k)]; };
-  float first[U];
+  // the sections' values, on their way while the records are merged
+  constexpr int U = 4;
+  float early[U];
 #pragma unroll
-  for (int k = 0; k < U; ++k) first[k] = load_a(k);
-  for (int r = wave; r < G; r += kSelThreads / 64) {
-    const int64_t tok = row0 + r;
+  for (int k = 0; k < U; ++k) early[k] = section_at(min((uint32_t)tid + kSelThreads * k, n_a - 1));
+  // records, rows side by side as they lie (a wave per row would fetch each line
+  // for 8 bytes of it, for every row): a thread's of one row, then the row's
+  {
+    const uint32_t at_once = kSelThreads / G, mine = quotient(tid, by_rows), r = tid - mine * G;
     float m = kNegBig;
     double sum = 0.0;
-    for (int s0 = lane; s0 < b.splits; s0 += 64 * 8) {
-      float2 p[8];
-      float mx = m;
+    if (mine < at_once) {
+#pragma unroll 1
+      for (uint32_t s0 = mine; s0 < (uint32_t)b.splits; s0 += 4 * at_once) {
+        float2 p[4];
+        float mx = m;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        p[k] = s0 + 64 * k < b.splits ? b.records[(int64_t)(s0 + 64 * k) * b.ld + tok] : make_float2(kNegBig, 0.0f);
-        mx = nan_max(mx, p[k].x);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t s = s0 + k * at_once;
+          p[k] = b.records[(int64_t)min(s, (uint32_t)b.splits - 1) * b.ld + row0 + r];
+          if (s >= (uint32_t)b.splits) p[k] = make_float2(kNegBig, 0.0f);
+          mx = nan_max(mx, p[k].x);
+        }
+        sum *= (double)fast_exp2(m - mx);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += (double)p[k].y * (double)fast_exp2(p[k].x - mx);
+        m = mx;
       }
-      sum *= (double)fast_exp2(m - mx);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum += (double)p[k].y * (double)fast_exp2(p[k].x - mx);
-      m = mx;
     }
+    rec_sum[tid] = sum;
+    rec_max[tid] = m;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int r = wave; r < (int)G; r += kSelThreads / 64) {
+    const int64_t tok = row0 + r;
+    const int at_once = kSelThreads / G;
+    float m = kNegBig;
+    for (int k = lane; k < at_once; k += 64) m = nan_max(m, rec_max[k * G + r]);
     const float mx = reduce<64>(m, NanMax());
-    sum = wave_sum(sum * (double)fast_exp2(m - mx));
+    double sum = 0.0;
+    for (int k = lane; k < at_once; k += 64) sum += rec_sum[k * G + r] * (double)fast_exp2(rec_max[k * G + r] - mx);
+    sum = wave_sum(sum);
     if (lane == 0) {
       const float score = b.scores[tok];
       // records are in base 2 of logits scaled by the float32 sc: back = 1 / (sc T) undoes both
@@ -535,47 +551,59 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
       b.lse[tok] = part ? (float)lse : 0.0f;
     }
   }
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+    if (tid + kSelThreads * k < min(n_a, (uint32_t)kSelHeld)) held[tid + kSelThreads * k] = early[k];
+#pragma unroll 1
+  for (uint32_t i = tid + kSelThreads * U; i < min(n_a, (uint32_t)kSelHeld); i += kSelThreads * U) {
+    float z[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) z[k] = section_at(min(i + kSelThreads * k, n_a - 1));
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i + kSelThreads * k < min(n_a, (uint32_t)kSelHeld)) held[i + kSelThreads * k] = z[k];
+  }
   __syncthreads();
   if (wave == 0) {
     // values relative to about the best candidate, where float32 is finest
-    const double mine = lane < G ? base[lane] : -INFINITY;
-    const float large = lane < G ? size[lane] : 0.0f;
+    const double mine = lane < (int)G ? base[lane] : -INFINITY;
+    const float large = lane < (int)G ? size[lane] : 0.0f;
     const double ref = reduce<64>(mine + (double)large, Max());
     const float most = reduce<64>(fabsf(large), NanMax());
-    if (lane < G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
+    if (lane < (int)G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
     if (lane == 0) slack = (most + b.invT) * 0x1p-13f;   // far more than the tiles' sums are off
   }
   __syncthreads();
   const int keep = b.keep;
-  auto key = [&](float z, int r, uint32_t index) {
-    const float x = shift[r];
-    return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
-  };
-  const int n1 = select_best(sel, per_a, keep, first, load_a, [&](int k, float z) {
-    const int r = row_at(k);
-    return key(z, r, (uint32_t)r * n_sec + (uint32_t)(my_sec + k * rows_at_once));
-  });
-  if (tid < n1) section[tid] = index_of(sel.kept[tid]);
-  __syncthreads();
-  // the blocks of those sections
-  const uint32_t per = b.per_section, n_blocks = (uint32_t)b.n_blocks;
-  const uint32_t n2_items = (uint32_t)n1 * per;
-  constexpr int UB = 2;
-  uint32_t at_row[UB], at_block[UB];
-  float z[UB];
+  int kept = 0;
+#pragma unroll 1
+  for (int stage = 0; stage < 2; ++stage) {   // the sections, then the blocks of the best of them
+    const uint32_t n = stage == 0 ? n_a : (uint32_t)kept * per;
+    if (stage == 1) {
+      if (tid < kept) {
+        const uint32_t at = index_of(sel.kept[tid]), r = at / n_sec;
+        sec_row[tid] = r;
+        sec_block[tid] = (at - r * n_sec) * per;
+      }
+      __syncthreads();
 #pragma unroll
-  for (int k = 0; k < UB; ++k) {   // kMostKept sections of at most 20 blocks
-    const uint32_t i = tid + kSelThreads * k;
-    at_row[k] = at_block[k] = 0;
-    z[k] = -INFINITY;
-    if (i >= n2_items) continue;
-    const uint32_t at = section[i / per];
-    at_row[k] = at / n_sec;
-    at_block[k] = (at - at_row[k] * n_sec) * per + i % per;
-    if (at_block[k] < n_blocks) z[k] = b.blocks[(int64_t)at_block[k] * b.ld + row0 + at_row[k]];
+      for (int k = 0; k < 2; ++k) {   // kMostKept sections of at most 20 blocks
+        const uint32_t i = tid + kSelThreads * k;
+        if (i >= n) continue;
+        const uint32_t q = quotient(i, by_blocks), blk = sec_block[q] + (i - q * per);
+        held[i] = blk < n_blocks ? b.blocks[(int64_t)blk * b.ld + row0 + sec_row[q]] : -INFINITY;
+      }
+      __syncthreads();
+    }
+    kept = select_best(sel, n, keep, [&](uint32_t i) {
+      const uint32_t q = quotient(i, stage == 0 ? by_rows : by_blocks), rest = i - q * (stage == 0 ? G : per);
+      const uint32_t r = stage == 0 ? rest : sec_row[q];
+      const uint32_t index = stage == 0 ? r * n_sec + q : r * n_blocks + sec_block[q] + rest;
+      const float x = shift[r], z = i < kSelHeld ? held[i] : section_at(i);
+      return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
+    });
   }
-  const int n2 = select_best(sel, UB, keep, z, [&](int) { return -INFINITY; },
-                             [&](int k, float v) { return key(v, at_row[k], at_row[k] * n_blocks + at_block[k]); });
+  const int n2 = kept;
   // those of the first C, and of the spare ones that are as good within the slack
   const bool in = tid < n2 && (tid < b.C || value_of(sel.kept[tid]) >= value_of(sel.kept[b.C - 1]) - slack);
   if (in) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
@@ -684,13 +712,14 @@ __global__ __launch_bounds__(kRankThreads) void beam_rank_kernel(const BeamArgs 
     double lse = b.lse64[row0 + tid];
     const int k = first[tid];
     if (k < used) {
+      // log1p(e^(z / T - lse) - e^(was / T - lse)); float32 carries it, being some 1e-6 at most
       const double was = b.blocks[(int64_t)(word_of[k] >> 4) * b.ld + row0 + tid];
-      lse += log1p(exp(z_max[k] / b.T - lse) - exp(was / b.T - lse));
+      lse += (double)log1pf(expf((float)(was * b.rT - lse)) * expm1f((float)((z_max[k] - was) * b.rT)));
     }
     logsum[tid] = lse;
   }
   __syncthreads();
-  auto score_of = [&](int r, double x) { return (double)b.scores[row0 + r] + (x / b.T - logsum[r]); };
+  auto score_of = [&](int r, double x) { return (double)b.scores[row0 + r] + (x * b.rT - logsum[r]); };
   // C blocks hold a candidate each that reaches the C-th largest of their best
   if (tid < used) best[tid] = score_of(row_of[tid], z_max[tid]);
   __syncthreads();

@@ -143,26 +143,37 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedFwdArgs a) {
 
 constexpr int kSortWaves = 16;
 
-// Exclusive sum over the workgroup's threads; total is the whole sum. `red`
-// holds a word per wave.
-__device__ __forceinline__ int block_scan(int x, int* red, int& total) {
+// Exclusive sums over the workgroup's threads; total is the whole sum. `red`
+// holds an entry per wave.
+__device__ __forceinline__ int4 plus(int4 a, int4 b) { return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+__device__ __forceinline__ int plus(int a, int b) { return a + b; }
+__device__ __forceinline__ int4 minus(int4 a, int4 b) { return make_int4(a.x - b.x, a.y - b.y, a.z - b.z, a.w - b.w); }
+__device__ __forceinline__ int minus(int a, int b) { return a - b; }
+__device__ __forceinline__ int4 shfl_up(int4 v, int d) {
+  return make_int4(__shfl_up(v.x, d), __shfl_up(v.y, d), __shfl_up(v.z, d), __shfl_up(v.w, d));
+}
+__device__ __forceinline__ int shfl_up(int v, int d) { return __shfl_up(v, d); }
+template <class T, int W>
+__device__ __forceinline__ T block_scan(T x, T (&red)[W], T& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int s = x;
+  T s = x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(s, d);
-    if (lane >= d) s += o;
+    const T o = shfl_up(s, d);
+    if (lane >= d) s = plus(s, o);
   }
   if (lane == 63) red[wave] = s;
   __syncthreads();
-  int base = 0;
-  total = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
-    if (w < wave) base += red[w];
-    total += red[w];
+  T base{};
+  total = T{};
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const T r = red[w];
+    if (w < wave) base = plus(base, r);
+    total = plus(total, r);
   }
   __syncthreads();
-  return base + s - x;
+  return minus(plus(base, s), x);
 }
 
 __device__ __forceinline__ void wave_fence() {
@@ -175,7 +186,7 @@ __device__ __forceinline__ void wave_fence() {
 template <int LC>
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const EmbedBwdArgs a) {
   __shared__ int cnt[kSortWaves][LC];   // tokens of the class's word l in the wave's part, then where the wave's next goes
-  __shared__ int red[kSortWaves];
+  __shared__ int4 red[kSortWaves];
   constexpr int kFound = LC > 1024 ? 192 : 512;   // within 160 KB of LDS
   __shared__ int2 found[kSortWaves][kFound];      // (token, word)
   const int tid = threadIdx.x, lane = tid & 63;
@@ -191,13 +202,14 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const Embed
   int lower = 0, n_found = 0;
   // whole batches are loaded without a bound, which costs as much as all the
   // rest: the scan is bound by the vector unit
-  auto scan = [&](int i, auto whole) {
+  auto scan = [&](int i, auto vectors, auto whole) {
+    constexpr int n = vectors();
     const int32_t* from = a.ids + i;
-    int id[D];
+    int id[n];
 #pragma unroll
-    for (int d = 0; d < D; ++d) id[d] = whole() ? from[64 * d + lane] : a.ids[min(i + 64 * d + lane, i1 - 1)];
+    for (int d = 0; d < n; ++d) id[d] = whole() ? from[64 * d + lane] : a.ids[min(i + 64 * d + lane, i1 - 1)];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
+    for (int d = 0; d < n; ++d) {
       const bool live = (uint32_t)id[d] < (uint32_t)a.V && (whole() || i + 64 * d + lane < i1);
       const int k = id[d] & mask;
       lower += __popcll(__ballot(live && k < c));   // on the scalar unit
@@ -213,12 +225,13 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const Embed
     }
   };
   int at_id = i0;
-  for (; at_id + 64 * D <= i1; at_id += 64 * D) scan(at_id, std::true_type{});
-  if (at_id < i1) scan(at_id, std::false_type{});
-  int below;
-  block_scan(lane == 0 ? lower : 0, red, below);
+#pragma unroll 1
+  for (; at_id + 64 * D <= i1; at_id += 64 * D) scan(at_id, std::integral_constant<int, D>{}, std::true_type{});
+#pragma unroll 1
+  for (; at_id < i1; at_id += 64 * 4) scan(at_id, std::integral_constant<int, 4>{}, std::false_type{});
   // the class's words in order: their tokens' places
   constexpr int per = (LC + 64 * kSortWaves - 1) / (64 * kSortWaves);
+  __syncthreads();   // every wave's tokens are counted
   int of[per][kSortWaves], tot[per], n_tok = 0, n_pc = 0, n_lg = 0;
 #pragma unroll
   for (int k = 0; k < per; ++k) {
@@ -233,10 +246,11 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const Embed
     n_pc += (tot[k] + kPiece - 1) / kPiece;
     n_lg += tot[k] > kPiece;
   }
-  int own, pieces, longs;
-  int at = below + block_scan(n_tok, red, own);
-  int pc = below + block_scan(n_pc, red, pieces);
-  int lg = below / kPiece + block_scan(n_lg, red, longs);
+  // tokens, pieces and long words of the words before, and tokens of lower classes, in one go
+  int4 sum, all;
+  sum = block_scan(make_int4(n_tok, n_pc, n_lg, lane == 0 ? lower : 0), red, all);
+  const int below = all.w, pieces = all.y, longs = all.z;
+  int at = below + sum.x, pc = below + sum.y, lg = below / kPiece + sum.z;
   {
     int to = at;
 #pragma unroll
@@ -300,14 +314,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const Embed
     }
     return;
   }
-  for (int i = i0; i < i1; i += 64 * D) {
-    int id[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) id[d] = a.ids[min(i + 64 * d + lane, i1 - 1)];   // a branch per load would wait for each
-#pragma unroll
-    for (int d = 0; d < D; ++d) id[d] = i + 64 * d + lane < i1 ? id[d] : -1;
-#pragma unroll
-    for (int d = 0; d < D; ++d) place(id[d] >= 0 && id[d] < a.V && (id[d] & mask) == c, i + 64 * d + lane, id[d]);
+#pragma unroll 1
+  for (int i = i0; i < i1; i += 64) {
+    const int id = a.ids[min(i + lane, i1 - 1)];
+    place(i + lane < i1 && id >= 0 && id < a.V && (id & mask) == c, i + lane, id);
   }
 }
 

@@ -337,7 +337,7 @@ struct BeamArgs {
   int64_t mask_ld;
   int N, H, V, beams, C, keep;   // keep: C + kSpare
   float sc, invT;           // log2(e) / T, 1 / T
-  double T, back;           // T; 1 / (sc T)
+  double rT, back;          // 1 / T; 1 / (sc T)
   bool few;                 // the streaming kernels
   int splits, n_tt, n_vt;   // records per row; the tiles
   int64_t n_sections, n_blocks;

@@ -93,6 +93,20 @@ def test_ties_go_to_the_lowest_row_and_word(N, V):
     _reference(case, G, C).check(*_run(case, G, C), "ties", exactly=True)
 
 
+@pytest.mark.parametrize("G,V,C", [(8, 65000, 64), (64, 4000, 64), (32, 30000, 64)])
+def test_best_words_in_a_few_places(G, V, C):
+    """Most of the best words at places that fall to the same threads of the selection, or all with one beam of many."""
+    log(f"few places {G} {V}")
+    rng = np.random.default_rng(G)
+    h = rng.standard_normal((G, 64)).astype(np.float32)
+    W = (0.1 * rng.standard_normal((V, 64))).astype(np.float32)
+    h[:, 0] = 1.0
+    W[:, 0] = np.where(np.arange(V) // 128 % 128 < 79, 10.0, -10.0)
+    scores = np.full(G, -1.0, np.float32) if G == 8 else np.where(np.arange(G) == 5, -1.0, -60.0).astype(np.float32)
+    case = (f32_to_bf16_bits(h), f32_to_bf16_bits(W), scores, None, None)
+    _reference(case, G, C).check(*_run(case, G, C), f"{G} {V}")
+
+
 def test_words_and_parents_exactly():
     """Without near ties the very words and parents of 64-bit scores come out."""
     for seed, (B, G, H, V, C) in enumerate([(1, 4, 128, 2000, 8), (8, 8, 64, 3000, 16), (40, 8, 64, 2500, 16)]):
