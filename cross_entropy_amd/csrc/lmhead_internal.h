@@ -12,6 +12,7 @@ namespace lmh {
 
 constexpr int kTileRows = 256;   // output tile edge of every MMA kernel
 constexpr int kNumCUs = 256;     // MI355X: 8 XCDs x 32 CUs
+constexpr double kMemoryCache = 256 << 20;   // bytes that the cache in front of HBM holds
 constexpr double kStreamed = 32 << 20;   // bytes of output, all XCDs' L2s, above which moved rows are stored past the caches
 
 // Forward: token tiles x vocabulary splits of the tile kernel, then the merge.

@@ -242,6 +242,31 @@ def test_reorder(shape, row_dim, length_dim, G, t, kind):
     assert np.array_equal(place, R.reorder(states, states, parents, G, lengths, row_dim, length_dim))
 
 
+@pytest.mark.parametrize("beams", [4, 8, 16, 32, 64])
+@pytest.mark.parametrize("L,D", [(257, 64), (251, 67)])
+def test_reorder_of_large_states(beams, L, D):
+    """States larger than the caches near the units hold (33 MB upwards), which are stored past them."""
+    import torch
+    import cross_entropy_amd as lm
+    log(f"reorder large {beams} {L} {D}")
+    gen = torch.Generator(device="cuda").manual_seed(beams)
+    N, planes, heads = 128, 3, 7
+    x = torch.randint(0, 250, (planes, N, heads, L, D), device="cuda", dtype=torch.uint8, generator=gen)
+    other = torch.randint(0, 250, x.shape, device="cuda", dtype=torch.uint8, generator=gen)
+    first = torch.arange(N, device="cuda") // beams * beams
+    parents = (first + torch.randint(0, beams, (N,), device="cuda", generator=gen)).int()
+    lengths = torch.randint(0, L + 1, (N,), device="cuda", generator=gen).int()
+    for n in (None, lengths):
+        took = x[:, parents.long()]
+        short = None if n is None else (torch.arange(L, device="cuda")[None] >= n[parents.long()][:, None])[None, :, None, :, None]
+        for onto in (other, x):
+            want = took if n is None else torch.where(short, onto, took)
+            state = x.clone()
+            out = state if onto is x else other.clone()
+            got = lm.beam_reorder(state, parents, beams, out=out, lengths=n, row_dim=1, length_dim=None if n is None else 3)
+            assert torch.equal(got, want), (n is None, onto is x)
+
+
 def test_reorder_at_odd_addresses():
     """States that begin at any byte, and runs of any length."""
     import torch

@@ -151,6 +151,52 @@ def test_infinities_and_zeros_in_the_gradient():
     check(got, want, e, "dW")
 
 
+@pytest.mark.parametrize("w,y", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("H", [1000, 1001])
+def test_lookup_of_many_tokens(H, w, y):
+    """y larger than the caches near the units hold (33 MB upwards), which is stored past them."""
+    import torch
+    import cross_entropy_amd as lm
+    log(f"embed_fwd large {H} {w} {y}")
+    rng = np.random.default_rng(H)
+    N, V = 17000, 300
+    W, ids, scale = _values(rng, (V, H), w), _ids(rng, N, V), 11.3137
+    got = lm.embed_forward(_put(W, w), dev(ids), scale, _type(y)).double()
+    table, e = (torch.from_numpy(x).cuda() for x in R.embed(W, np.arange(V, dtype=np.int32), scale, y))
+    live = dev(((ids >= 0) & (ids < V)))[:, None]
+    at = dev(np.where((ids >= 0) & (ids < V), ids, 0)).long()
+    assert bool((torch.where(live, (got - table[at]).abs() - e[at], got.abs()) <= 0).all())
+
+
+@pytest.mark.parametrize("y,g", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("H", [1000, 1001])
+def test_gradient_of_many_tokens(H, y, g):
+    """dy larger than every cache (270 MB upwards), which is loaded past them; the bound is that of R.embed_grad."""
+    import torch
+    import cross_entropy_amd as lm
+    log(f"embed_bwd large {H} {y} {g}")
+    rng = np.random.default_rng(H)
+    N, V, scale = 136000 if y == "bf16" else 68000, 9000, 0.75
+    ids = dev(_ids(rng, N, V, heavy=0.01))
+    gen = torch.Generator(device="cuda").manual_seed(H)
+    dy = torch.randn(N, H, device="cuda", generator=gen).to(_type(y))
+    old = torch.randn(V, H, device="cuda", generator=gen).to(_type(g))
+    live = (ids >= 0) & (ids < V)
+    at = ids[live].long()
+    total, size = (torch.zeros(V, H, device="cuda", dtype=torch.float64) for _ in range(2))
+    total.index_add_(0, at, dy[live].double())
+    size.index_add_(0, at, dy[live].double().abs())
+    n = torch.bincount(at, minlength=V)[:, None]
+    for add in (False, True):
+        got = lm.embed_backward(ids, dy, scale=scale, dW=old.clone(), accumulate=add).double()
+        want, e = scale * total, scale * size * (n + 1) * R.U
+        if add:
+            want = want + old.double()
+            e = e + R.U * (want.abs() + e)
+        e = e * (1 + R.HALF[g]) + R.HALF[g] * want.abs() + R.TINY
+        assert bool(((got - want).abs() <= torch.where(n > 0, e, 0.0)).all()), add
+
+
 def test_front_end_gradients():
     """lmhead_embed against autograd of its definition, and against differences."""
     import torch
