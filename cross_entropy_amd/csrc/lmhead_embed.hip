@@ -322,10 +322,15 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const Embed
     }
     return;
   }
+  // more than were kept (a word of every tenth token, say): all ids once more
 #pragma unroll 1
-  for (int i = i0; i < i1; i += 64) {
-    const int id = a.ids[min(i + lane, i1 - 1)];
-    place(i + lane < i1 && id >= 0 && id < a.V && (id & mask) == c, i + lane, id);
+  for (int i = i0; i < i1; i += 64 * D) {
+    int id[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) id[d] = a.ids[min(i + 64 * d + lane, i1 - 1)];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      place(i + 64 * d + lane < i1 && (uint32_t)id[d] < (uint32_t)a.V && (id[d] & mask) == c, i + 64 * d + lane, id[d]);
   }
 }
 
