@@ -17,7 +17,11 @@
 //           free of the order of the tiles' float32 sums, which differs between
 //           kernels and would decide between near candidates. kSpare blocks
 //           more than C are looked at where their float32 maxima lie within
-//           that error. The last workgroup of a group ranks its candidates.
+//           that error
+//   rank    a workgroup per group orders the candidates of its blocks. A launch
+//           of its own: the last of a group's scoring workgroups would do it
+//           without, but each of them then makes its stores visible to the whole
+//           card first, which takes longer
 //
 // A row's log-sum-exp is the float32 one, corrected by what the 64-bit logit of
 // its best candidate changes, which holds most of its mass as a rule. By that
@@ -43,7 +47,10 @@ __device__ __forceinline__ uint32_t allowed16(const BeamArgs& a, int64_t tok, in
 }
 
 // Few rows: the workgroup's 64 MB vocabulary rows, one record and one section.
-// Tiles of 16 NB tokens: up to 128, where the distillation's stop at 64.
+// Tiles of 16 NB tokens: up to 128, where the distillation's stop at 64. Bound by
+// the read of W: 64 rows at H 2560, V 151936 (778 MB) take 154 us, 5.05 TB/s,
+// as a copy; 4 rows at 1024 x 50257 (103 MB) 27 us, 3.8 TB/s, of which 6 are
+// the launch's rise and fall.
 template <int MB, int NB, bool MASK>
 __global__ __launch_bounds__(256, 2) void beam_few_kernel(const FewArgs a, const BeamArgs b) {
   __shared__ __attribute__((aligned(16))) char lds[few_lds<NB>()];
@@ -147,7 +154,10 @@ struct __attribute__((packed, aligned(4))) Words4 {
 
 // Many rows: the head's forward tiles; a section is a wave's 128 vocabulary
 // rows. The arrays hold whole tiles of rows and of words, so every store is in
-// place; what lies past N or V is not read.
+// place; what lies past N or V is not read. Bound by the matrix units: 1024
+// rows at H 2560, V 151936 take 680 us (1,170 TFLOP/s) and with masks 727 to 768;
+// the block maxima and statistics of a tile are a tenth of its time, on a
+// SIMD's only wave.
 template <bool MASK>
 __global__ __launch_bounds__(kThreads) void beam_tile_kernel(
     const uint16_t* __restrict__ hidden, const uint16_t* __restrict__ W, const int32_t* __restrict__ allowed, int mask_ld, int N,
@@ -475,6 +485,10 @@ __device__ __forceinline__ bool ended_row(const BeamArgs& b, int64_t tok) {
   return b.ended != nullptr && b.ended[tok] >= 0 && b.ended[tok] < b.V;
 }
 
+// Bound by the chain of its steps (loads, records' sums, two choices of some ten
+// barriers each), not by bytes: 12 us for one group of 4 beams at 50257 words,
+// 15 for 8 of 8 at 151936, 26 for 64 of 16. One workgroup a group: a group's
+// sections lie within 100 KB or so, and several would need a launch more.
 __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs b) {
   __shared__ Selection sel;
   __shared__ float held[kSelHeld];
@@ -611,7 +625,11 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
   if (tid == 0) b.used[group] = used;
 }
 
-// A workgroup per chosen block: its 16 logits in 64 bits, four a wave.
+// A workgroup per chosen block: its 16 logits in 64 bits, four a wave. Products
+// of bf16 values are exact in float64, the sums off by 1e-16 of their terms. One
+// trip to memory where there are few (4.6 us for 24 blocks of H 1024), gathered
+// rows where there are many (27 us for 2048 blocks of H 2560, 6 TB/s with those
+// that share rows).
 __global__ __launch_bounds__(256) void beam_score_kernel(const BeamArgs b) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -663,7 +681,8 @@ __global__ __launch_bounds__(256) void beam_score_kernel(const BeamArgs b) {
 }
 
 // A workgroup per group: the candidates of the chosen blocks, and the ended
-// rows, in order.
+// rows, in order: all pairs of the few that reach the C-th best block's maximum.
+// A chain of steps like select's: 4.9 us for 8 candidates, 12 for 64 groups of 32.
 constexpr int kRankThreads = 256;
 constexpr int kMostFound = 16 * kMostKept + kMostBeams;
 __global__ __launch_bounds__(kRankThreads) void beam_rank_kernel(const BeamArgs b) {
@@ -842,6 +861,13 @@ hipError_t launch_beam_step(const BeamArgs& b, hipStream_t stream) {
 // take over, and then writes it. In place every read of a place so comes before
 // any write: larger groups take several waves of a workgroup and a barrier
 // between. Which row takes from which, and how much, is the same for all lanes.
+// Bound by memory: 64 beams' caches of 34 MB, in use in part (1.30 GB read and
+// written in place), 304 us, 4.3 TB/s; 24 states of 1024
+// rows of 16 KB into other buffers (631 MB, parents read once for all their
+// children) 118 us, 5.3 TB/s; a history of 512 words 2.4 us.
+// Outputs larger than the near caches are stored past them (states 118 us instead
+// of 128, caches 307 of 322); loads past them as well take 3% less at 1.3 GB but
+// 10 to 30% more where the far cache still holds the states (64 MB: 21 us to 17).
 namespace {
 
 constexpr int kReorderRows = 16;
