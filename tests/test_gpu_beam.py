@@ -172,6 +172,27 @@ def test_small_temperatures_and_large_logits():
     _reference(case, 4, 8).check(*_run(case, 4, 8), "large")
 
 
+@pytest.mark.parametrize("B,G,H,V,C", [(3, 4, 64, 3000, 16), (1, 64, 64, 9000, 64), (24, 16, 64, 4000, 40), (40, 8, 128, 30000, 20)])
+@pytest.mark.parametrize("far", [-1e4, -1e9, float(np.finfo(np.float32).min)])
+def test_scores_far_apart(B, G, H, V, C, far):
+    """Beams that a caller holds back by a very low score, in groups whose other beams have fewer words left than there
+    are candidates: the best of the held back ones come next, by what 64 bits tell apart at that score."""
+    log(f"far apart {B} {G} {V} {far}")
+    h, W, scores, _, _ = _case(G + V, B, G, H, V)
+    rng = np.random.default_rng(V)
+    N = B * G
+    scores = np.where(np.isfinite(scores), scores, -20).astype(np.float32)
+    scores.reshape(B, G)[:, 1:] = far               # first steps: one beam, the others held back
+    scores.reshape(B, G)[:, 2::3] *= 0.75           # at two distances
+    a = np.zeros((N, -(-V // 32)), np.int32)
+    some = rng.integers(0, a.shape[1], (N, 3))
+    np.put_along_axis(a, some, rng.integers(0, 2**31, some.shape).astype(np.int32) & 0x00010001, 1)
+    a.reshape(B, G, -1)[:, -1] = -1
+    case = (h, W, scores, None, a)
+    for T in (1.0, 0.5):
+        _reference(case, G, C, T).check(*_run(case, G, C, T), f"{B} x {G} {V} {far} {T}")
+
+
 def test_step_with_norm_and_workspaces():
     import torch
     import cross_entropy_amd as lm
