@@ -533,26 +533,29 @@ __device__ __forceinline__ void join_row(const EmbedBwdArgs& a, int first, int t
 }
 
 constexpr int kRowGroups = 1;   // groups of columns that a wave sums at once
-constexpr int kRowsPerCU = 5;   // workgroups that fit
+constexpr int kRowsPerCU = 5, kAddsPerCU = 8;   // workgroups that fit, zeroing rows beside them or adding
 constexpr int kZeroBlocks = kNumCUs;   // those that zero rows, one a CU beside four that sum
 
 // The first kZeroBlocks workgroups zero rows, unless dW is added to; the others
 // sum pieces. Bound by memory where there is much of it: 65536 rows of 2560
 // into 151936 rows take 247 us for 1.10 GB (4.4 TB/s; 336 MB of gathered rows of
 // 5 KB, 778 MB of stores, 115 us of them by themselves), 131072 rows added to 34000
-// rows 200 us for 1.0 GB (5.1 TB/s). 4096 rows added to 2250 take 13 us for 42 MB,
-// a wave's two or three pieces one after the other. Six or eight workgroups a CU
-// take 0 to 6% less for the largest and 6 to 10% more for the smallest; 128
-// zeroing workgroups 289 us, 512 300 (with uniform words).
-template <bool YF32, bool GF32, bool TAIL, bool STREAM_IN>
-__global__ __launch_bounds__(256, kRowsPerCU) void embed_rows_kernel(const EmbedBwdArgs a) {
+// rows 186 us for 1.0 GB (5.5 TB/s). 4096 rows added to 2250 take 13 us for 42 MB,
+// a wave's one or two pieces one after the other. ADD has eight workgroups a CU
+// (131072 rows 186 us where five take 195) and its classes' places in LDS, which
+// saves a trip to memory a piece. Written, with zeroing beside, both make the
+// frequent words' case slower (65536 rows 242 us, 253 with the places, 262 with
+// eight) and the uniform one faster (262, 248, 222). 128 zeroing workgroups take
+// 289 us, 512 300 (with uniform words).
+template <bool YF32, bool GF32, bool TAIL, bool STREAM_IN, bool ADD>
+__global__ __launch_bounds__(256, ADD ? kAddsPerCU : kRowsPerCU) void embed_rows_kernel(const EmbedBwdArgs a) {
   constexpr int G = YF32 || GF32 ? 4 : 8;
-  __shared__ int first[kMostClasses];   // pieces of the classes before
+  extern __shared__ int first[];   // pieces of the classes before; ADD: and where the class's begin, less those
   __shared__ int red[4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int zero_blocks = a.add ? 0 : kZeroBlocks;
-  if ((int)blockIdx.x < zero_blocks) {
+  constexpr int zero_blocks = ADD ? 0 : kZeroBlocks;
+  if (!ADD && (int)blockIdx.x < zero_blocks) {
     zero_rows<GF32>(a, blockIdx.x, kZeroBlocks, [&](int v) {
       return a.touched[(int64_t)(v & (a.classes - 1)) * a.class_words + (v >> a.class_shift)];
     });
@@ -565,8 +568,10 @@ __global__ __launch_bounds__(256, kRowsPerCU) void embed_rows_kernel(const Embed
     for (int k = 0; k < per; ++k) n += a.counts[3 * (tid * per + k)];
     int at = block_scan(n, red, total);
     for (int k = 0; k < per; ++k) {
-      first[tid * per + k] = at;
-      at += a.counts[3 * (tid * per + k)];
+      const int c = tid * per + k;
+      first[c] = at;
+      if (ADD) first[a.classes + c] = a.counts[3 * c + 1] - at;
+      at += a.counts[3 * c];
     }
     __syncthreads();
   }
@@ -584,7 +589,7 @@ __global__ __launch_bounds__(256, kRowsPerCU) void embed_rows_kernel(const Embed
     c *= per;
     for (int step = per >> 1; step > 0; step >>= 1)
       if (first[c + step] <= g) c += step;
-    return a.pieces[a.counts[3 * c + 1] + g - first[c]];
+    return a.pieces[(ADD ? first[a.classes + c] : a.counts[3 * c + 1] - first[c]) + g];
   };
   auto tokens = [&](const int4& p) { return a.order[p.x + min(lane, p.y - 1)]; };
   const int chunks = (a.H + 64 * G * kRowGroups - 1) / (64 * G * kRowGroups);
@@ -784,16 +789,20 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   trace_end(kEmbedSort, stream, 0.0, 24.0 * N + V);
   const int64_t units = std::max<int64_t>((int64_t)a.N, 1) * chunks;
-  const int64_t most = kRowsPerCU * kNumCUs - (a.add ? 0 : kZeroBlocks);
+  const int64_t most = a.add ? kAddsPerCU * kNumCUs : kRowsPerCU * kNumCUs - kZeroBlocks;
   const int64_t blocks = std::max<int64_t>((chunks + 3) / 4, std::min<int64_t>((units + 3) / 4, most)) + (a.add ? 0 : kZeroBlocks);
   trace_begin(stream);
   with_types(a.y_f32, a.g_f32, tail, [&](auto y, auto gf, auto t) {
-    // dy past the caches where the memory-side one does not hold it: 65536 rows of 5 KB (335 MB) added 105 us instead
-    // of 129, but 16384 rows 173 instead of 143
-    if (N * H * (a.y_f32 ? 4 : 2) > kMemoryCache)
-      hipLaunchKernelGGL((embed_rows_kernel<y(), gf(), t(), true>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((embed_rows_kernel<y(), gf(), t(), false>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    auto launch = [&](auto past, auto add) {
+      hipLaunchKernelGGL((embed_rows_kernel<y(), gf(), t(), past(), add()>), dim3((unsigned)blocks), dim3(256),
+                         (add() ? 8 : 4) * a.classes, stream, a);
+    };
+    std::true_type yes;
+    std::false_type no;
+    // dy past the caches where the memory-side one does not hold it: 65536 rows of 5 KB (335 MB) added 113 us instead
+    // of 128, but 16384 rows 38 instead of 28
+    if (N * H * (a.y_f32 ? 4 : 2) > kMemoryCache) a.add ? launch(yes, yes) : launch(yes, no);
+    else a.add ? launch(no, yes) : launch(no, no);
   });
   e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -123,6 +123,29 @@ def test_large_vocabularies():
         assert not got.any()
 
 
+def test_many_tokens_added_into_large_vocabularies():
+    """The sorted path's addition over 512 and more classes of words."""
+    import torch
+    import cross_entropy_amd as lm
+    rng = np.random.default_rng(3)
+    for V in (600001, 3000001):
+        log(f"embed_bwd added, V {V}")
+        N, H = 4000, 24
+        ids = rng.integers(0, V, N).astype(np.int32)
+        ids[::3] = ids[0]
+        ids[1], ids[2] = 0, V - 1
+        dy = _values(rng, (N, H), "f32")
+        into = torch.full((V, H), 0.5, device="cuda")
+        lm.embed_backward(dev(ids), dev(dy), dW=into, accumulate=True)
+        rows = np.unique(ids)
+        old = np.full((len(rows), H), 0.5, np.float32)
+        want, e = R.embed_grad(np.searchsorted(rows, ids), dy, len(rows), 1.0, old, "f32")
+        at = torch.from_numpy(rows.astype(np.int64)).cuda()
+        check(into[at].cpu().numpy(), want, e, f"dW {V}")
+        into[at] = 0.5
+        assert bool((into == 0.5).all())
+
+
 def test_rows_past_32_bits():
     """A table and a gradient whose last rows lie beyond 2^32 bytes."""
     import torch
