@@ -614,7 +614,7 @@ __global__ __launch_bounds__(256, ADD ? kAddsPerCU : kRowsPerCU) void embed_rows
 
 // A class's long words; kJoinParts workgroups share their columns. Bound by the
 // longest word's chain of pieces: 11 us for 65536 tokens with a word of 4000,
-// 4.3 for 4096; 81 where 131072 tokens are one word.
+// 4.1 for 4096; 81 where 131072 tokens are one word.
 constexpr int kJoinParts = 8;
 template <bool GF32, bool TAIL>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedBwdArgs a) {
