@@ -229,11 +229,12 @@ __global__ __launch_bounds__(kThreads) void beam_tile_kernel(
 #pragma unroll
         for (int r = 0; r < 4; ++r) z[i][r] = acc[i][j][r];
       }
-      if (ragged) {   // rows past V take no part
+      if (ragged) {   // rows past V take no part, whatever the bits of a mask say there: below every real logit, and
+                      // in statistics that start at kNegBig nothing
 #pragma unroll
         for (int i = 0; i < kNB; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) z[i][r] = (vrow0 + acc_row(i, r, lane) < V) ? z[i][r] : kNegBig;
+          for (int r = 0; r < 4; ++r) z[i][r] = (vrow0 + acc_row(i, r, lane) < V) ? z[i][r] : -INFINITY;
       }
       float mx = z[0][0];
 #pragma unroll

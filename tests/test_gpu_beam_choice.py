@@ -1,0 +1,47 @@
+"""The beam step's choice where float32 does not decide it: masks with bits set
+past the vocabulary. Against float64 (tests/vocab_reference.py)."""
+import numpy as np
+import pytest
+
+import vocab_reference as R
+from gpu_common import dev, dev_bits, log
+from synthetic import bf16_bits_to_f32, f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(h, W, scores, allowed, G, C):
+    import cross_entropy_amd as lm
+    out = lm.beam_step(dev_bits(h), dev_bits(W), dev(scores), G, C, None, dev(allowed))
+    return [x.cpu().numpy() for x in out]
+
+
+def _reference(h, W, scores, allowed, G, C):
+    return R.Beams(bf16_bits_to_f32(h), bf16_bits_to_f32(W), scores, G, C, None, allowed)
+
+
+def _bits(words, N, V):
+    """Masks of N rows that allow the given words."""
+    a = np.zeros((N, -(-V // 32)), np.uint32)
+    np.bitwise_or.at(a, (slice(None), words >> 5), np.uint32(1) << (words & 31).astype(np.uint32))
+    return a.view(np.int32)
+
+
+# the tiles (more than 256 rows) and the streaming kernels; vocabularies that end inside a mask's word
+@pytest.mark.parametrize("B,G,V,C", [(24, 16, 4001, 40), (40, 8, 30011, 20), (2, 16, 4001, 40)])
+@pytest.mark.parametrize("far", [-1e4, -1e9])
+def test_mask_bits_past_the_vocabulary(B, G, V, C, far):
+    """The bits of words that do not exist mean nothing: a row may have them set where its last real words are forbidden."""
+    log(f"mask tail {B} {G} {V} {far}")
+    rng = np.random.default_rng(V + B)
+    N, H = B * G, 64
+    W = f32_to_bf16_bits((0.1 * rng.standard_normal((V, H))).astype(np.float32))
+    h = f32_to_bf16_bits(rng.standard_normal((N, H)).astype(np.float32))
+    scores = np.full((B, G), far, np.float32)
+    scores[:, 0] = -12.0                            # one beam, the others held back at two distances
+    scores[:, 2::3] *= 0.75
+    allowed = np.full((N, -(-V // 32)), -1, np.int32)
+    allowed[::G] = _bits(np.array([3, 1000, 2000]), 1, V)
+    allowed[::G, -1] = np.uint32(0xFFFFFFFF << (V % 32) & 0xFFFFFFFF).view(np.int32)
+    case = (h, W, scores.reshape(N), allowed, G, C)
+    _reference(*case).check(*_run(*case), f"{B} x {G}, V {V}, {far}")
