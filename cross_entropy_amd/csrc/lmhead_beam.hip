@@ -316,9 +316,12 @@ __global__ __launch_bounds__(kThreads) void beam_tile_kernel(
 // swaps; __shfl_xor takes a trip through LDS for each step). Every lane of a
 // group of W ends with the same bits: each step combines the same two values in
 // both of the lanes that exchange them, lower half first where that matters.
+struct Wide;
 template <int CTRL, class T>
 __device__ __forceinline__ T dpp_of(T v) {
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (std::is_same_v<T, Wide>) {
+    return {dpp_of<CTRL>(v.value), dpp_of<CTRL>(v.rest)};
+  } else if constexpr (sizeof(T) == 4) {
     return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
   } else {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -360,7 +363,8 @@ struct Sum {
   __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
 };
 struct Max {
-  __device__ __forceinline__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
+  template <class T>
+  __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
   __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
 };
 struct NanMax {
@@ -381,58 +385,88 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 }
 __device__ __forceinline__ uint32_t index_of(uint64_t key) { return ~(uint32_t)key; }
 
+// The same of a double.
+struct Wide {
+  uint64_t value;
+  uint32_t rest;
+};
+__device__ __forceinline__ bool operator>(const Wide& a, const Wide& b) {
+  return a.value > b.value || (a.value == b.value && a.rest > b.rest);
+}
+__device__ __forceinline__ Wide key_of(double v, uint32_t index) {
+  const uint64_t u = __double_as_longlong(v);
+  return {(u >> 63) != 0 ? ~u : u | 1ull << 63, ~index};
+}
+__device__ __forceinline__ double value_of(const Wide& key) {
+  const uint64_t o = key.value;
+  return __longlong_as_double((o >> 63) != 0 ? o ^ 1ull << 63 : ~o);
+}
+__device__ __forceinline__ uint32_t index_of(const Wide& key) { return ~key.rest; }
+
+// Key{} is none, and lies below all others.
+template <class Key>
+struct Limits;
+template <>
+struct Limits<uint64_t> {
+  static constexpr uint64_t least = 1, above = ~(uint64_t)0;   // of the others; above all of them
+};
+template <>
+struct Limits<Wide> {
+  static constexpr Wide least{0, 1}, above{~(uint64_t)0, ~0u};
+};
+
 constexpr int kSelThreads = 1024;
 constexpr int kSelTeams = 128;    // of 8 threads each
 constexpr int kSelList = 2048;
 constexpr int kSelHeld = 24576;   // items whose values LDS holds (96 KB)
 
 // The `keep` largest keys of items 0 .. n - 1 into kept[0 ..], sorted; returns
-// how many there are (keep, or all that are not 0). key(i) gives an item's key,
-// 0 for none. A thread looks at neighbouring items, a team at those of eight
+// how many there are (keep, or all that are not none). key(i) gives an item's key. A thread looks at neighbouring items, a team at those of eight
 // threads: rows in turn. Every team has a largest key, and the keep-th largest of
 // those is a threshold that at least `keep` items reach, and few more do as a
 // rule: those are ranked. Should more than the list holds reach it (most of the
 // best items lie with few teams), the best are taken one after the other.
 //
 static_assert(kMostKept <= kSelTeams, "a threshold exists");
+template <class Key>
 struct Selection {
-  uint64_t list[kSelList];
-  uint64_t most[kSelTeams];
+  Key list[kSelList];
+  Key most[kSelTeams];
   int rank[kSelTeams];
-  uint64_t kept[kMostKept];
-  uint64_t limit;
+  Key kept[kMostKept];
+  Key limit;
   int count;
 };
-template <class K>
-__device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, K key) {
+template <class Key, class F>
+__device__ __forceinline__ int select_best(Selection<Key>& s, uint32_t n, int keep, F key) {
   const int tid = threadIdx.x;
   constexpr int team = kSelThreads / kSelTeams;
   const uint32_t per = (n + kSelThreads - 1) / kSelThreads;
   const uint32_t i0 = min(n, tid * per), i1 = min(n, i0 + per);
-  auto largest = [&](uint64_t below) {
-    uint64_t most = 0;
+  auto largest = [&](Key below) {
+    Key most{};
 #pragma unroll 4
     for (uint32_t i = i0; i < i1; ++i) {
-      const uint64_t k = key(i);
-      most = k < below ? max(most, k) : most;
+      const Key k = key(i);
+      most = below > k && k > most ? k : most;
     }
     return reduce<team>(most, Max());
   };
-  uint64_t below = ~(uint64_t)0;
+  Key below = Limits<Key>::above;
   int found = 0;
 #pragma unroll 1
   for (int r = 0; r < keep; ++r) {   // once, unless the list runs over
-    const uint64_t most = largest(below);
+    const Key most = largest(below);
     if (tid % team == 0) s.most[tid / team] = most;
     if (tid < kSelTeams) s.rank[tid] = 0;
     if (tid == 0) {
-      s.limit = 1;
+      s.limit = Limits<Key>::least;
       s.count = 0;
     }
     __syncthreads();
     {
       // the teams' ranks, 16 comparisons a thread
-      const uint64_t mine = s.most[tid % kSelTeams];
+      const Key mine = s.most[tid % kSelTeams];
       int rank = 0;
 #pragma unroll
       for (int k = 0; k < kSelTeams / team; ++k) rank += s.most[tid / kSelTeams * (kSelTeams / team) + k] > mine;
@@ -440,9 +474,9 @@ __device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, K
     }
     __syncthreads();
     const int want = found > kSelList ? 0 : keep - 1;
-    if (tid < kSelTeams && s.rank[tid] == want && s.most[tid] > 0) s.limit = s.most[tid];
+    if (tid < kSelTeams && s.rank[tid] == want && s.most[tid] > Key{}) s.limit = s.most[tid];
     __syncthreads();
-    const uint64_t limit = s.limit;
+    const Key limit = s.limit;
     if (found > kSelList) {
       if (tid == 0) s.kept[r] = limit;
       below = limit;
@@ -451,8 +485,8 @@ __device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, K
     }
 #pragma unroll 4
     for (uint32_t i = i0; i < i1; ++i) {
-      const uint64_t k = key(i);
-      if (k < limit) continue;
+      const Key k = key(i);
+      if (limit > k) continue;
       const int at = atomicAdd(&s.count, 1);
       if (at < kSelList) s.list[at] = k;
     }
@@ -464,12 +498,12 @@ __device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, K
   }
   if (found > kSelList) {
     __syncthreads();
-    return keep;   // more than kSelList items are not 0
+    return keep;   // more than kSelList items are not none
   }
 #pragma unroll 1
   for (int first = 0; first < found; first += kSelThreads / 16) {   // 16 threads a candidate
     const int i = first + (tid >> 4);
-    const uint64_t mine = i < found ? s.list[i] : 0;
+    const Key mine = i < found ? s.list[i] : Key{};
     int rank = 0;
 #pragma unroll 2
     for (int k = tid & 15; k < found; k += 16) rank += s.list[k] > mine;
@@ -478,75 +512,6 @@ __device__ __forceinline__ int select_best(Selection& s, uint32_t n, int keep, K
   }
   __syncthreads();
   return min(found, keep);
-}
-
-// Rows whose scores lie far apart (a caller's -1e9 for beams that are to come
-// last): between rows whose items overlap and the next lower ones, all distance
-// but one unit is taken out, so that float32 keys tell items apart everywhere
-// that 64-bit scores do. value(i) gives an item's score and row, -inf for none.
-// 4 to 44 us of select (4 beams at 50257 words, 64 at 151936), taken where
-// float32's steps at the farthest row's distance come near the slack.
-struct Apart {
-  float unit;   // about the largest logit; 0: the rows lie close to each other
-  uint64_t low[kMostBeams], high[kMostBeams];
-  uint32_t order[kMostBeams];
-  double from[kMostBeams], to[kMostBeams];
-};
-// doubles as integers of the same order
-__device__ __forceinline__ uint64_t ordered(double x) {
-  const uint64_t u = __double_as_longlong(x);
-  return (u >> 63) != 0 ? ~u : u | 1ull << 63;
-}
-__device__ __forceinline__ double unordered(uint64_t u) {
-  return __longlong_as_double((u >> 63) != 0 ? u ^ 1ull << 63 : ~u);
-}
-template <class F>
-__device__ __forceinline__ void together(Apart& s, uint32_t G, uint32_t n, F value) {
-  const uint32_t tid = threadIdx.x;
-  __syncthreads();   // the stage before has read them
-  if (tid < kMostBeams) {
-    s.low[tid] = ~(uint64_t)0;
-    s.high[tid] = 0;
-    s.from[tid] = s.to[tid] = 0.0;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (uint32_t i = tid; i < n; i += kSelThreads) {
-    uint32_t index, r;
-    const double x = value(i, index, r);
-    if (x == -INFINITY) continue;
-    atomicMin(reinterpret_cast<unsigned long long*>(&s.low[r]), (unsigned long long)ordered(x));
-    atomicMax(reinterpret_cast<unsigned long long*>(&s.high[r]), (unsigned long long)ordered(x));
-  }
-  __syncthreads();
-  if (tid < G) {
-    uint32_t rank = 0;
-    const uint64_t mine = s.high[tid];
-#pragma unroll 1
-    for (uint32_t r = 0; r < G; ++r) rank += s.high[r] > mine || (s.high[r] == mine && r < tid);
-    s.order[rank] = tid;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    // x goes to x - from + to
-    double from = 0.0, to = 0.0, low = 0.0;
-#pragma unroll 1
-    for (uint32_t k = 0; k < G; ++k) {
-      const uint32_t r = s.order[k];
-      if (s.high[r] == 0) break;   // rows without items come last
-      const double top = unordered(s.high[r]);
-      if (k == 0) {
-        from = low = top;
-      } else if (top < low - s.unit) {
-        to += low - from - s.unit;
-        from = low = top;
-      }
-      low = fmin(low, unordered(s.low[r]));
-      s.from[r] = from;
-      s.to[r] = to;
-    }
-  }
-  __syncthreads();
 }
 
 __device__ __forceinline__ double wave_sum(double v) { return reduce<64>(v, Sum()); }
@@ -560,13 +525,16 @@ __device__ __forceinline__ bool ended_row(const BeamArgs& b, int64_t tok) {
 // 15 for 8 of 8 at 151936, 26 for 64 of 16. One workgroup a group: a group's
 // sections lie within 100 KB or so, and several would need a launch more.
 __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs b) {
-  __shared__ Selection sel;
+  __shared__ union {
+    Selection<uint64_t> narrow;
+    Selection<Wide> wide;
+  } sel;
   __shared__ float held[kSelHeld];
-  __shared__ double base[kMostBeams];
-  __shared__ float size[kMostBeams], shift[kMostBeams];
+  __shared__ double base[kMostBeams], lse64[kMostBeams];
+  __shared__ float size[kMostBeams], shift[kMostBeams], scores[kMostBeams];
   __shared__ uint32_t sec_row[kMostKept], sec_block[kMostKept];
   __shared__ float slack;
-  __shared__ Apart apart;
+  __shared__ bool far;
   __shared__ double rec_sum[kSelThreads];
   __shared__ float rec_max[kSelThreads];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -632,6 +600,8 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
       const bool live = part && finite(lse);
       base[r] = live ? (double)score - lse : -INFINITY;
       size[r] = live ? (float)((double)mx * b.back) : 0.0f;
+      scores[r] = score;
+      lse64[r] = lse;
       b.lse64[tok] = lse;
       b.lse[tok] = part ? (float)lse : 0.0f;
     }
@@ -657,70 +627,63 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     const float most = reduce<64>(fabsf(large), NanMax());
     if (lane < (int)G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
     const float unit = most + b.invT;
-    // where a row lies so far off that its float32 steps reach slack / 8, rows are moved together
-    const bool far = __any(lane < (int)G && finite(mine) && ref - mine > 256.0 * (double)unit);
+    // a row that lies so far off that its float32 steps reach slack / 8
+    const bool any = __any(lane < (int)G && finite(mine) && ref - mine > 256.0 * (double)unit);
     if (lane == 0) {
       slack = unit * 0x1p-13f;   // far more than the tiles' sums are off
-      apart.unit = far ? unit : 0.0f;
+      far = any;
     }
   }
   __syncthreads();
-  const int keep = b.keep;
-  int kept = 0;
+  // key(r, index, z): of an item, by its row, index and largest logit
+  auto choose = [&](auto& sel, auto key) {
+    int kept = 0;
 #pragma unroll 1
-  for (int stage = 0; stage < 2; ++stage) {   // the sections, then the blocks of the best of them
-    const uint32_t n = stage == 0 ? n_a : (uint32_t)kept * per;
-    if (stage == 1) {
-      if (tid < kept) {
-        const uint32_t at = index_of(sel.kept[tid]), r = at / n_sec;
-        sec_row[tid] = r;
-        sec_block[tid] = (at - r * n_sec) * per;
-      }
-      __syncthreads();
+    for (int stage = 0; stage < 2; ++stage) {   // the sections, then the blocks of the best of them
+      const uint32_t n = stage == 0 ? n_a : (uint32_t)kept * per;
+      if (stage == 1) {
+        if (tid < kept) {
+          const uint32_t at = index_of(sel.kept[tid]), r = at / n_sec;
+          sec_row[tid] = r;
+          sec_block[tid] = (at - r * n_sec) * per;
+        }
+        __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {   // kMostKept sections of at most 20 blocks
-        const uint32_t i = tid + kSelThreads * k;
-        if (i >= n) continue;
-        const uint32_t q = quotient(i, by_blocks), blk = sec_block[q] + (i - q * per);
-        held[i] = blk < n_blocks ? b.blocks[(int64_t)blk * b.ld + row0 + sec_row[q]] : -INFINITY;
+        for (int k = 0; k < 2; ++k) {   // kMostKept sections of at most 20 blocks
+          const uint32_t i = tid + kSelThreads * k;
+          if (i >= n) continue;
+          const uint32_t q = quotient(i, by_blocks), blk = sec_block[q] + (i - q * per);
+          held[i] = blk < n_blocks ? b.blocks[(int64_t)blk * b.ld + row0 + sec_row[q]] : -INFINITY;
+        }
+        __syncthreads();
       }
-      __syncthreads();
-    }
-    // an item's row, index and largest logit
-    auto item = [&](uint32_t i, uint32_t& index, float& z) {
-      const uint32_t q = quotient(i, stage == 0 ? by_rows : by_blocks), rest = i - q * (stage == 0 ? G : per);
-      const uint32_t r = stage == 0 ? rest : sec_row[q];
-      index = stage == 0 ? r * n_sec + q : r * n_blocks + sec_block[q] + rest;
-      z = i < kSelHeld ? held[i] : section_at(i);
-      return r;
-    };
-    if (apart.unit == 0.0f) {
-      kept = select_best(sel, n, keep, [&](uint32_t i) {
-        uint32_t index;
-        float z;
-        const float x = shift[item(i, index, z)];
-        return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
-      });
-    } else {
-      auto value = [&](uint32_t i, uint32_t& index, uint32_t& r) {
-        float z;
-        r = item(i, index, z);
-        return z > -INFINITY && base[r] > -INFINITY ? (double)b.scores[row0 + r] + ((double)z * b.rT - b.lse64[row0 + r]) : (double)-INFINITY;
-      };
-      together(apart, G, n, value);
-      kept = select_best(sel, n, keep, [&](uint32_t i) {
-        uint32_t index, r;
-        const double x = value(i, index, r);
-        return x > -INFINITY ? key_of((float)(x - apart.from[r] + apart.to[r]), index) : (uint64_t)0;
+      kept = select_best(sel, n, b.keep, [&](uint32_t i) {
+        const uint32_t q = quotient(i, stage == 0 ? by_rows : by_blocks), rest = i - q * (stage == 0 ? G : per);
+        const uint32_t r = stage == 0 ? rest : sec_row[q];
+        const uint32_t index = stage == 0 ? r * n_sec + q : r * n_blocks + sec_block[q] + rest;
+        return key(r, index, i < kSelHeld ? held[i] : section_at(i));
       });
     }
+    // those of the first C, and of the spare ones that are as good within the slack
+    const bool in = tid < kept && (tid < b.C || value_of(sel.kept[tid]) >= value_of(sel.kept[b.C - 1]) - slack);
+    if (in) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
+    const int used = __syncthreads_count(in);   // values fall, so these are the first ones
+    if (tid == 0) b.used[group] = used;
+  };
+  // Rows whose scores lie far apart (a caller's -1e9 for beams that are to come
+  // last) have keys of 64-bit scores, formed as rank forms them: float32 would not
+  // tell the words of the lower rows apart. Select then takes 4 us longer (4 beams
+  // at 50257 words), 25 (64 groups of 16 at 151936) or 44 (64 beams).
+  if (!far) {
+    choose(sel.narrow, [&](uint32_t r, uint32_t index, float z) {
+      const float x = shift[r];
+      return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
+    });
+  } else {
+    choose(sel.wide, [&](uint32_t r, uint32_t index, float z) {
+      return base[r] > -INFINITY && z > -INFINITY ? key_of((double)scores[r] + ((double)z * b.rT - lse64[r]), index) : Wide{};
+    });
   }
-  const int n2 = kept;
-  // those of the first C, and of the spare ones that are as good within the slack
-  const bool in = tid < n2 && (tid < b.C || value_of(sel.kept[tid]) >= value_of(sel.kept[b.C - 1]) - slack);
-  if (in) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
-  const int used = __syncthreads_count(in);   // values fall, so these are the first ones
-  if (tid == 0) b.used[group] = used;
 }
 
 // A workgroup per chosen block: its 16 logits in 64 bits, four a wave. Products

@@ -1,5 +1,6 @@
 """The beam step's choice where float32 does not decide it: masks with bits set
-past the vocabulary. Against float64 (tests/vocab_reference.py)."""
+past the vocabulary, words of vanishing probability beside beams that are held
+back. Against float64 (tests/vocab_reference.py)."""
 import numpy as np
 import pytest
 
@@ -45,3 +46,25 @@ def test_mask_bits_past_the_vocabulary(B, G, V, C, far):
     allowed[::G, -1] = np.uint32(0xFFFFFFFF << (V % 32) & 0xFFFFFFFF).view(np.int32)
     case = (h, W, scores.reshape(N), allowed, G, C)
     _reference(*case).check(*_run(*case), f"{B} x {G}, V {V}, {far}")
+
+
+@pytest.mark.parametrize("B", [1, 16, 80])
+@pytest.mark.parametrize("far", [-1e6, -1e9])
+def test_words_of_vanishing_probability(B, far):
+    """A leading beam that may take a few words, and others of logit -1e30 (a padded vocabulary): the held-back beams'
+    words lie between the two, and are ordered by their own logits."""
+    log(f"vanishing words {B} {far}")
+    rng = np.random.default_rng(B)
+    G, C, H, V = 4, 20, 64, 8000
+    N = B * G
+    # small whole numbers, whose logits are exact in any order, but for the last 500 words
+    h = rng.integers(-3, 4, (N, H)).astype(np.float32)
+    W = rng.integers(-2, 3, (V, H)).astype(np.float32) / 16
+    h[:, 0], W[:, 0], W[-500:, 0] = 1.0, 0.0, -1e30
+    scores = np.tile(np.array([-5.0, 0.75 * far, far, -np.inf], np.float32), B)
+    allowed = np.full((N, -(-V // 32)), -1, np.int32)
+    allowed[::G] = _bits(np.concatenate([[7, 1500, 3000], np.arange(V - 400, V)]), 1, V)
+    case = (f32_to_bf16_bits(h), f32_to_bf16_bits(W), scores, allowed, G, C)
+    want, got = _reference(*case), _run(*case)
+    # equal logits are equal scores in 64 bits, others at least 1 / 16 apart: the words are the very same ones
+    assert np.array_equal(got[1], want.ids) and np.array_equal(got[2], want.parents)
