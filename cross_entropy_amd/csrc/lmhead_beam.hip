@@ -428,6 +428,7 @@ constexpr int kSelHeld = 24576;   // items whose values LDS holds (96 KB)
 // best items lie with few teams), the best are taken one after the other.
 //
 static_assert(kMostKept <= kSelTeams, "a threshold exists");
+static_assert(kMostKept <= 2 * 64, "two waves look at the kept ones' logits");
 template <class Key>
 struct Selection {
   Key list[kSelList];
@@ -533,7 +534,7 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
   __shared__ double base[kMostBeams], lse64[kMostBeams];
   __shared__ float size[kMostBeams], shift[kMostBeams], scores[kMostBeams];
   __shared__ uint32_t sec_row[kMostKept], sec_block[kMostKept];
-  __shared__ float slack;
+  __shared__ float unit;   // about the largest logit that counts
   __shared__ bool far;
   __shared__ double rec_sum[kSelThreads];
   __shared__ float rec_max[kSelThreads];
@@ -626,17 +627,16 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     const double ref = reduce<64>(mine + (double)large, Max());
     const float most = reduce<64>(fabsf(large), NanMax());
     if (lane < (int)G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
-    const float unit = most + b.invT;
-    // a row that lies so far off that its float32 steps reach slack / 8
-    const bool any = __any(lane < (int)G && finite(mine) && ref - mine > 256.0 * (double)unit);
+    // a row that lies so far off that its float32 steps reach an eighth of the slack below
+    const bool any = __any(lane < (int)G && finite(mine) && ref - mine > 256.0 * (double)(most + b.invT));
     if (lane == 0) {
-      slack = unit * 0x1p-13f;   // far more than the tiles' sums are off
+      unit = most + b.invT;
       far = any;
     }
   }
   __syncthreads();
-  // key(r, index, z): of an item, by its row, index and largest logit
-  auto choose = [&](auto& sel, auto key) {
+  // key(r, index, z): of an item, by its row, index and largest logit; logit(r, value): that logit / T
+  auto choose = [&](auto& sel, auto key, auto logit) {
     int kept = 0;
 #pragma unroll 1
     for (int stage = 0; stage < 2; ++stage) {   // the sections, then the blocks of the best of them
@@ -664,7 +664,15 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
         return key(r, index, i < kSelHeld ? held[i] : section_at(i));
       });
     }
-    // those of the first C, and of the spare ones that are as good within the slack
+    // those of the first C, and of the spare ones that are as good within a slack that is far more than the tiles' sums
+    // are off: a part of the largest logit, or of the kept ones where a mask leaves none as small
+    if (tid < 2 * 64) {
+      const float z = tid < kept ? fabsf(logit(index_of(sel.kept[tid]) / n_blocks, value_of(sel.kept[tid]))) : 0.0f;
+      const float most = reduce<64>(z, [](float a, float b) { return fmaxf(a, b); });
+      if (lane == 0) atomicMax(reinterpret_cast<int*>(&unit), __float_as_int(most + b.invT));   // none is negative
+    }
+    __syncthreads();
+    const float slack = unit * 0x1p-13f;
     const bool in = tid < kept && (tid < b.C || value_of(sel.kept[tid]) >= value_of(sel.kept[b.C - 1]) - slack);
     if (in) b.chosen[group * kMostKept + tid] = index_of(sel.kept[tid]);
     const int used = __syncthreads_count(in);   // values fall, so these are the first ones
@@ -678,11 +686,11 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     choose(sel.narrow, [&](uint32_t r, uint32_t index, float z) {
       const float x = shift[r];
       return x > -INFINITY && z > -INFINITY ? key_of(fmaf(z, b.invT, x), index) : (uint64_t)0;
-    });
+    }, [&](uint32_t r, float value) { return value - shift[r]; });
   } else {
     choose(sel.wide, [&](uint32_t r, uint32_t index, float z) {
       return base[r] > -INFINITY && z > -INFINITY ? key_of((double)scores[r] + ((double)z * b.rT - lse64[r]), index) : Wide{};
-    });
+    }, [&](uint32_t r, double value) { return (float)(value - (double)scores[r] + lse64[r]); });
   }
 }
 

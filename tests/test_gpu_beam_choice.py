@@ -1,6 +1,7 @@
 """The beam step's choice where float32 does not decide it: masks with bits set
 past the vocabulary, words of vanishing probability beside beams that are held
-back. Against float64 (tests/vocab_reference.py)."""
+back, allowed words far below the largest logit. Against float64
+(tests/vocab_reference.py)."""
 import numpy as np
 import pytest
 
@@ -68,3 +69,22 @@ def test_words_of_vanishing_probability(B, far):
     want, got = _reference(*case), _run(*case)
     # equal logits are equal scores in 64 bits, others at least 1 / 16 apart: the words are the very same ones
     assert np.array_equal(got[1], want.ids) and np.array_equal(got[2], want.parents)
+
+
+@pytest.mark.parametrize("N", [16, 64, 300])
+def test_allowed_words_far_below_the_largest_logit(N):
+    """The largest logit lies near 0 and is forbidden; the allowed words lie near -3000, where float32 has steps of
+    2.4e-4, and a few of them within each step: the order is that of 64 bits all the same."""
+    log(f"far below {N}")
+    rng = np.random.default_rng(N)
+    H, V, C = 256, 2000, 8
+    h = (0.05 * rng.standard_normal((N, H))).astype(np.float32)
+    W = (0.01 * rng.standard_normal((V, H))).astype(np.float32)
+    h[:, 0], W[:, 0], W[::2, 0] = 64.0, 0.0, -47.0
+    case = (f32_to_bf16_bits(h), f32_to_bf16_bits(W), np.full(N, -1.0, np.float32), _bits(np.arange(0, V, 2), N, V), 1, C)
+    want, got = _reference(*case), _run(*case)
+    # the reference's logits are sums of products of 16 bits between 2^12 and some 2^-40, off by 2^-41 at most; the best
+    # nine lie further apart than that
+    best = np.sort(want.found, 1)[:, -C - 1:]
+    assert np.diff(best, axis=1).min() > 2.0 ** -38
+    assert np.array_equal(got[1], want.ids)
