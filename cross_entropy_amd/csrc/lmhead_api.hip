@@ -1142,6 +1142,9 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
 // The vocabulary table as an embedding.
 namespace {
 
+// A launch holds less than 2^32 threads: it has fewer workgroups of 256 than this.
+constexpr int64_t kMostBlocks = int64_t(1) << 24;
+
 static_assert(lmh::kMostBeams == LMH_BEAM_MAX_BEAMS && lmh::kMostCandidates == LMH_BEAM_MAX_CANDIDATES, "limits in the header");
 
 int check_embed(const char* who, int64_t N, int64_t H, int64_t V) {
@@ -1203,8 +1206,10 @@ int lmhead_logps_embed_fwd(const void* W, int w_type, const int32_t* ids, int64_
   if (!known_type(w_type) || !known_type(y_type))
     return fail(LMH_ERR_ARGS, "embed_fwd: unknown type among W %d, y %d", w_type, y_type);
   if (!std::isfinite(scale)) return fail(LMH_ERR_ARGS, "embed_fwd: scale must be finite, got %g", (double)scale);
-  if (N * lmh::ceil_div(H, 4) >= (int64_t(1) << 33))
-    return fail(LMH_ERR_UNSUPPORTED, "embed_fwd: N (%lld) times H / 4 (%lld) must stay below 2^33", (long long)N, (long long)H / 4);
+  // outputs that come near this have 512 groups, of four elements or eight, to a workgroup
+  if (lmh::ceil_div(N * lmh::ceil_div(H, 4), 512) >= kMostBlocks)
+    return fail(LMH_ERR_UNSUPPORTED, "embed_fwd: N (%lld) times H / 4, rounded up (%lld), must not exceed 2^33 - 512", (long long)N,
+                (long long)lmh::ceil_div(H, 4));
   if (N == 0) return ok();
   if (!W || !ids || !y) return fail(LMH_ERR_NULL, "embed_fwd: W, ids and y must be non-NULL");
   if (!aligned(W, type_size(w_type)) || !aligned(ids, 4) || !aligned(y, type_size(y_type)))
@@ -1265,9 +1270,6 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
 // ---------------------------------------------------------------------------
 // Beam search on the head.
 namespace {
-
-// A launch holds less than 2^32 threads: workgroups of 256 that it may have.
-constexpr int64_t kMostBlocks = int64_t(1) << 24;
 
 int check_beam(int64_t N, int64_t H, int64_t V, int64_t beams, int64_t candidates) {
   const int rc = check_shape(N, H, V, 1);
@@ -1423,7 +1425,8 @@ int lmhead_logps_beam_reorder(const void* states, void* out, const int32_t* pare
     if (__builtin_mul_overflow(bytes, n, &bytes) || bytes >= (int64_t(1) << 43) || rows >= (int64_t(1) << 31))
       return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: the states hold 2^43 bytes or more");
   const int64_t run = steps * step_bytes;
-  if (run >= (int64_t(1) << 35) || rows >= (int64_t(1) << 30) || lmh::reorder_blocks(planes, rows, beams, runs, run) >= kMostBlocks)
+  if (run >= (int64_t(1) << 35) || rows >= (int64_t(1) << 30) ||
+      lmh::reorder_blocks(planes, rows, beams, runs, run) >= kMostBlocks)
     return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a run of 2^35 bytes or more, 2^30 rows, or more than 2^24 workgroups");
   if (!states || !out || !parents) return fail(LMH_ERR_NULL, "beam_reorder: states, out and parents must be non-NULL");
   if (!aligned(parents, 4) || !aligned(lengths, 4))

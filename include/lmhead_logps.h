@@ -447,9 +447,10 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
  * previous bf16 value being widened first. N = 0: the forward does nothing, the
  * backward writes dW = 0 (unless adding). Errors: LMH_ERR_NULL, LMH_ERR_SHAPE,
  * LMH_ERR_ARGS (unknown type or flag; scale not finite), LMH_ERR_WORKSPACE,
- * LMH_ERR_UNSUPPORTED (a misaligned pointer; a forward of N H / 4 >= 2^33; in the
- * backward and its size query N or V above 2^23 - 256), LMH_ERR_HIP. Outputs must not overlap inputs. Stream
- * semantics as for every call here.
+ * LMH_ERR_UNSUPPORTED (a misaligned pointer; a forward of N times H / 4, rounded up,
+ * above 2^33 - 512; in the backward and its size query N or V above 2^23 - 256),
+ * LMH_ERR_HIP. Outputs must not overlap inputs. Stream semantics as for every call
+ * here.
  */
 int lmhead_logps_embed_workspace_bytes(int64_t N, int64_t H, int64_t V, size_t* bytes_out);   /* the backward's */
 int lmhead_logps_embed_fwd(const void* W, int w_type, const int32_t* ids, int64_t N, int64_t H, int64_t V,
