@@ -1426,8 +1426,8 @@ int lmhead_logps_beam_reorder(const void* states, void* out, const int32_t* pare
       return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: the states hold 2^43 bytes or more");
   const int64_t run = steps * step_bytes;
   if (run >= (int64_t(1) << 35) || rows >= (int64_t(1) << 30) ||
-      lmh::reorder_blocks(planes, rows, beams, runs, run) >= kMostBlocks)
-    return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a run of 2^35 bytes or more, 2^30 rows, or more than 2^24 workgroups");
+      lmh::round_up(lmh::reorder_blocks(planes, rows, beams, runs, run), 8) >= kMostBlocks)   // as launched
+    return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a run of 2^35 bytes or more, 2^30 rows, or more than 2^24 - 8 workgroups");
   if (!states || !out || !parents) return fail(LMH_ERR_NULL, "beam_reorder: states, out and parents must be non-NULL");
   if (!aligned(parents, 4) || !aligned(lengths, 4))
     return fail(LMH_ERR_UNSUPPORTED, "beam_reorder: a pointer is not aligned to its elements");

@@ -511,7 +511,7 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  *            states; below 0 as 0)
  * Errors: LMH_ERR_SHAPE, LMH_ERR_NULL, LMH_ERR_ARGS (an overlap),
  * LMH_ERR_UNSUPPORTED (2^43 bytes or more, 2^35 of a run, 2^30 rows, or more than
- * 2^24 workgroups, of up to 16 beams' 4 KB each: 64 GB of single beams; a
+ * 2^24 - 8 workgroups, of up to 16 beams' 4 KB each: 64 GB of single beams; a
  * misaligned pointer), LMH_ERR_HIP.
  */
 #define LMH_BEAM_MAX_BEAMS 64

@@ -1,6 +1,6 @@
-"""The largest launches of the lookup, on the host: a size whose launch would hold
-2^32 threads is refused, the one below it is not (a null pointer, which is looked
-at next, tells the two apart)."""
+"""The largest launches of the lookup and the reordering, on the host: a size
+whose launch would hold 2^32 threads is refused, the one below it is not (a null
+pointer, which is looked at next, tells the two apart)."""
 import pytest
 
 from cross_entropy_amd import _native as nat
@@ -14,3 +14,9 @@ def test_largest_lookup(N, H, status):
     for w_type in (0, 1):
         for y_type in (0, 1):
             assert nat.raw_embed_fwd(0, w_type, 0x10000, N, H, 300, 1.0, 0x10000, y_type, 0) == status
+
+
+@pytest.mark.parametrize("rows,status", [((1 << 24) - 8, -1), ((1 << 24) - 7, -6), ((1 << 24) - 1, -6), (1 << 24, -6)])
+def test_largest_reordering(rows, status):
+    """A workgroup a row; launches have a multiple of 8 of them."""
+    assert nat.raw_beam_reorder(0, 0x10000, 0x10000, 0, 1, rows, 1, 1, 1, 1, 0) == status
