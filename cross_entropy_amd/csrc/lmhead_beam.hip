@@ -627,8 +627,8 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     const double ref = reduce<64>(mine + (double)large, Max());
     const float most = reduce<64>(fabsf(large), NanMax());
     if (lane < (int)G) shift[lane] = finite(mine) ? (float)(mine - ref) : -INFINITY;
-    // a row that lies so far off that its float32 steps reach an eighth of the slack below
-    const bool any = __any(lane < (int)G && finite(mine) && ref - mine > 256.0 * (double)(most + b.invT));
+    // a row that lies so far off that its float32 steps come near its own logits' sums' errors
+    const bool any = __any(lane < (int)G && finite(mine) && ref - mine > 256.0 * (double)(fabsf(large) + b.invT));
     if (lane == 0) {
       unit = most + b.invT;
       far = any;

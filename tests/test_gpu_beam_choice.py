@@ -1,7 +1,7 @@
 """The beam step's choice where float32 does not decide it: masks with bits set
 past the vocabulary, words of vanishing probability beside beams that are held
-back, allowed words far below the largest logit. Against float64
-(tests/vocab_reference.py)."""
+back or of another row's large logits, allowed words far below the largest one.
+Against float64 (tests/vocab_reference.py)."""
 import numpy as np
 import pytest
 
@@ -68,6 +68,25 @@ def test_words_of_vanishing_probability(B, far):
     case = (f32_to_bf16_bits(h), f32_to_bf16_bits(W), scores, allowed, G, C)
     want, got = _reference(*case), _run(*case)
     # equal logits are equal scores in 64 bits, others at least 1 / 16 apart: the words are the very same ones
+    assert np.array_equal(got[1], want.ids) and np.array_equal(got[2], want.parents)
+
+
+@pytest.mark.parametrize("B", [1, 16, 80])
+def test_far_rows_beside_a_row_of_large_logits(B):
+    """What is far for a row of ordinary logits is not made near by another row's large ones: the leading beam's reach
+    some 5e5, the next ones are held back by 1e8, where float32 has steps of 8."""
+    log(f"far beside large {B}")
+    rng = np.random.default_rng(B)
+    G, C, H, V = 4, 20, 64, 8000
+    N = B * G
+    h = rng.integers(-3, 4, (N, H)).astype(np.float32)
+    W = rng.integers(-2, 3, (V, H)).astype(np.float32) / 16
+    h[::G] *= 2.0 ** 17
+    scores = np.tile(np.array([-5.0, -7.5e7, -1e8, -np.inf], np.float32), B)
+    allowed = np.full((N, -(-V // 32)), -1, np.int32)
+    allowed[::G] = _bits(np.array([7, 1500, 3000]), 1, V)
+    case = (f32_to_bf16_bits(h), f32_to_bf16_bits(W), scores, allowed, G, C)
+    want, got = _reference(*case), _run(*case)
     assert np.array_equal(got[1], want.ids) and np.array_equal(got[2], want.parents)
 
 
