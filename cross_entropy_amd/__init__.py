@@ -830,9 +830,9 @@ def beam_step(hidden, W, scores, beams: int, candidates: Optional[int] = None, e
               temperature: float = 1.0, norm: Optional["Norm"] = None, workspace=None, stream=None) -> Tuple:
     """Allocate outputs and run one step of beam search: (top_scores, top_ids,
     top_parents, lse), the first three [N / beams, candidates]. ``candidates``
-    defaults to 2 * beams, which holds ``beams`` that have not just ended. With
-    ``norm``, hidden is the stream in front of the final norm (bfloat16 or
-    float32)."""
+    defaults to 2 * beams, which holds ``beams`` that have not just ended; it is at
+    most 64, so groups of more than 32 beams have to name it. With ``norm``, hidden
+    is the stream in front of the final norm (bfloat16 or float32)."""
     torch = _torch()
     N, dev = hidden.shape[0], hidden.device
     if candidates is None:
@@ -1060,8 +1060,9 @@ def lmhead_embed(W, ids, scale: float = 1.0, out_dtype=None):
     float32 or bfloat16 and ids int32 [...] of any shape; ids outside [0, V) give
     zeros and no gradient. W's gradient comes whole, in W's dtype (a trainer that
     keeps a tied table's gradient in a buffer of its own adds to the rows that
-    occur alone with ``embed_backward(..., dW=buffer, accumulate=True)``). A
-    second backward, through the gradients, is refused."""
+    occur alone with ``embed_backward(..., dW=buffer, accumulate=True)``). The
+    backward takes up to 2^23 - 256 ids and words. A second backward, through the
+    gradients, is refused."""
     global _EMBED_FN
     if _EMBED_FN is None:
         _EMBED_FN = _embed_function()

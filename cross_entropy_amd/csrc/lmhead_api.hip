@@ -1167,6 +1167,7 @@ struct EmbedPlan {
 EmbedPlan plan_embed(int64_t N, int64_t H, int64_t V, bool add) {
   EmbedPlan p;
   p.few = N <= lmh::kFewIds && (add || V <= lmh::kFewWords);
+  static_assert(int64_t(lmh::kMostClasses) * lmh::kMostClassWords >= int64_t(1) << 23, "classes for the V that check_backward_size lets through");
   while (lmh::ceil_div(V, p.classes) > lmh::kMostClassWords) p.classes *= 2, ++p.shift;
   p.words = (int)lmh::ceil_div(V, p.classes);
   size_t at = 0;

@@ -523,7 +523,7 @@ __device__ __forceinline__ bool ended_row(const BeamArgs& b, int64_t tok) {
 
 // Bound by the chain of its steps (loads, records' sums, two choices of some ten
 // barriers each), not by bytes: 12 us for one group of 4 beams at 50257 words,
-// 15 for 8 of 8 at 151936, 26 for 64 of 16. One workgroup a group: a group's
+// 15 for 8 of 8 at 151936, 28 for 64 of 16. One workgroup a group: a group's
 // sections lie within 100 KB or so, and several would need a launch more.
 __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs b) {
   __shared__ union {

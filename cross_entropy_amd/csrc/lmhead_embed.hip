@@ -5,9 +5,10 @@
 //   dW_v (+)= scale sum_{i: id_i = v} dy_i
 //
 // The gradient's sums run over the tokens of a word in the tokens' order, in
-// pieces of at most kPiece tokens whose sums are then added in order, and no
-// atomics take part in sums: results depend on the arguments alone. Two ways
-// lead there.
+// pieces of at most kPiece tokens. The pieces' sums are added as eight runs of
+// neighbouring ones, each in order, and then run by run. No atomics take part in
+// sums: results depend on the arguments alone. Two ways lead there, with the same
+// bits.
 //
 // Many tokens, sorted by word first (stably):
 //   sort   workgroup c owns the words v with v mod NC = c. Words that follow one
@@ -202,8 +203,10 @@ __device__ __forceinline__ void wave_fence() {
 // or so (65536: 17 us, of 256 CUs that each look at all ids), by a chain of
 // trips to memory and LDS below (4096: 6.8). A sort by digits reads the ids twice
 // or more often, with a launch between, of 2 us at least each. LC: words of a
-// class that LDS counts, 640 (160 KB hold 16 waves' counters and 512
-// found tokens each; up to 163840 words) or kMostClassWords.
+// class that LDS counts, 640 (up to 163840 words; 104 KB with 512 found tokens a
+// wave) or kMostClassWords (152 KB with 192), which takes two words a thread and
+// clears three times the counters: 65536 tokens of 163840 words 21 us, of 163841
+// 37; 4096 tokens 8.7 and 10.0.
 template <int LC>
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const EmbedBwdArgs a) {
   __shared__ int cnt[kSortWaves][LC];   // tokens of the class's word l in the wave's part, then where the wave's next goes
@@ -498,6 +501,7 @@ __device__ __forceinline__ void zero_rows(const EmbedBwdArgs& a, int me, int blo
 // wave's columns, by a workgroup: its waves take runs of neighbouring pieces,
 // whose sums are added in order.
 constexpr int kJoinWaves = 8;
+static_assert(8 * kMostClasses <= 64 << 10, "LDS of embed_rows_kernel's classes");
 template <bool GF32, bool TAIL>
 __device__ __forceinline__ void join_row(const EmbedBwdArgs& a, int first, int tokens, int64_t v, int col, float4 (&xch)[kJoinWaves][64]) {
   constexpr int G = 4;

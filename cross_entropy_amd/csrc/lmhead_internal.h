@@ -302,8 +302,10 @@ struct EmbedFwdArgs {
 
 constexpr int kPiece = 32;             // most tokens of a word that one wave sums
 constexpr int kFewIds = 2048;          // tokens up to which they are counted and not sorted,
-constexpr int kFewWords = 163840;      // and words, where the rows of those that do not occur are zeroed
-constexpr int kMostClasses = 4096;     // workgroups of the sort, a power of two of them
+// and words, where the rows of those that do not occur are zeroed (each zeroing workgroup holds a bit a word, 20 KB, and
+// marks all ids): 256 tokens of 64 columns into 163840 words 9.8 us, sorted (163841) 16.2; 2048 of 256 columns 20.7 and 25.9
+constexpr int kFewWords = 163840;
+constexpr int kMostClasses = 4096;     // workgroups of the sort, a power of two of them, of the most words there may be
 constexpr int kMostClassWords = 2048;  // words of a class
 
 struct EmbedBwdArgs {

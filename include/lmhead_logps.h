@@ -442,8 +442,8 @@ int lmhead_logps_norm_bwd(const void* x, int x_type, const void* weight, int w_t
  *         wrote becomes the table's whole gradient
  * H in [1, 2^20), odd sizes too; every pointer aligned to its elements (the
  * workspace to 16 bytes). Sums are float32, taken over a word's tokens in the
- * order of the tokens (in pieces of 32 whose sums are then added in order), so
- * results depend on the arguments alone; bf16 gradients are rounded once, a
+ * order of the tokens, in pieces of 32; the pieces' sums are added as eight runs of
+ * neighbouring pieces and then run by run. Results so depend on the arguments alone; bf16 gradients are rounded once, a
  * previous bf16 value being widened first. N = 0: the forward does nothing, the
  * backward writes dW = 0 (unless adding). Errors: LMH_ERR_NULL, LMH_ERR_SHAPE,
  * LMH_ERR_ARGS (unknown type or flag; scale not finite), LMH_ERR_WORKSPACE,
@@ -474,7 +474,7 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  *   allowed  int32 [N, ceil(V/32)] or NULL: bit v % 32 of word v / 32 says
  *                     whether the row may take v (lse is that of the whole
  *                     vocabulary all the same); an ended row's bits are not read
- *                     for its candidate
+ *                     for its candidate, and bits from V on mean nothing
  *   temperature       as for the head
  *   top_scores  f32   [N / beams, candidates]  out
  *   top_ids     int32 [N / beams, candidates]  out: the words
@@ -487,12 +487,14 @@ int lmhead_logps_embed_bwd(const int32_t* ids, const void* dy, int y_type, int64
  * of 64-bit scores of logits summed in 64 bits, so it does not depend on the
  * kernels' summation order; lse and the scores carry lse's float32 sums (about 1e-7
  * of them: two candidates of different rows closer than that may change places).
+ * The scores' lse is corrected by what the 64-bit logit of the row's best candidate
+ * changes, the lse that comes out is not: their last bits need not agree.
  * The choice looks at 16 blocks of 16 words more than there are candidates where
  * float32 does not tell their largest logits apart; in a group with more near ties
  * than that it may miss one.
  * The workspace holds 4 N V / 16 bytes of the blocks' largest logits (N rounded
  * up to 64, or to 256 above 128) and smaller arrays;
- * lmhead_logps_beam_workspace_bytes sizes it.
+ * lmhead_logps_beam_workspace_bytes sizes it. Outputs must not overlap inputs.
  * Errors: those of the head's calls, plus LMH_ERR_SHAPE when beams is not in [1,
  * LMH_BEAM_MAX_BEAMS], candidates not in [1, LMH_BEAM_MAX_CANDIDATES] or N not a
  * multiple of beams, and LMH_ERR_UNSUPPORTED where N >= 2^23, beams V >= 2^31 or
